@@ -386,6 +386,138 @@ GB300GEMM_API int gemm_nvfp4_bs_splitk(const void* a, const void* b, const void*
 GB300GEMM_API size_t gemm_nvfp4_bs_splitk_workspace_bytes(int M, int N, int K, int k_splits);
 
 /*
+ * gemm_bf16_nt_xent - linear cross entropy: the softmax cross entropy of the
+ * logits of a language-model head, without storing the logits:
+ *     z[m,v]  = sum_k X[m,k] W[v,k]                     (FP32)
+ *     lse[m]  = log( sum_v exp(z[m,v]) )
+ *     loss[m] = lse[m] - z[m, target[m]]
+ * The logits are formed tile by tile on the tensor cores (as gemm_bf16_nt
+ * forms them, before its rounding) and folded on chip into each row's running
+ * maximum and sum of exponentials, both FP32; the tiles of a row are joined
+ * in a fixed order, so results repeat bit for bit.
+ *
+ * Library extension (the pages define no such call); W has the layout of
+ * gemm_bf16_nt's B.
+ *
+ *   X       bf16 [M][K]  rows (hidden states)                   (read)
+ *   W       bf16 [V][K]  head weights, HuggingFace layout       (read)
+ *   target  int64 [M]    the row's class.  < 0: the row has no loss
+ *                        (loss[m] = 0; lse[m] is computed all the same);
+ *                        >= V: loss[m] = NaN                    (read)
+ *   loss    float [M]    (written)
+ *   lse     float [M]    (written; the backward call reads it)
+ *   workspace  device memory of at least
+ *           gemm_bf16_nt_xent_workspace_bytes(M, V) bytes, 16-byte aligned;
+ *           contents on entry ignored, on return unspecified
+ *   M, V, K >= 1 (any V; at most 2^30 each); K % 8 == 0; X, W 16-byte
+ *   aligned; target 8-byte, loss and lse 4-byte aligned; loss, lse and
+ *   workspace overlap no input and not each other.
+ * A NaN logit, or an infinite maximum, makes the row's loss and lse NaN.
+ * Errors: GEMM_ERR_NULL, _SHAPE (also a workspace that is too small),
+ * _ALIGN, _ALIAS, _ARCH, _LAUNCH, _NO_DEVICE, _CAPTURE.
+ */
+GB300GEMM_API int gemm_bf16_nt_xent(const void* X, const void* W, const long long* target,
+                                    float* loss, float* lse, void* workspace,
+                                    size_t workspace_bytes, int M, int V, int K, void* stream);
+
+/* Workspace bytes gemm_bf16_nt_xent needs (0 for invalid arguments). */
+GB300GEMM_API size_t gemm_bf16_nt_xent_workspace_bytes(int M, int V);
+
+/*
+ * gemm_bf16_nt_xent_backward - gradients of the linear cross entropy:
+ *     G[m,v] = dloss[m] * ( exp(z[m,v] - lse[m]) - [v == target[m]] )
+ *     dX[m,k] = bf16( sum_v G[m,v] W[v,k] ),  dW[v,k] = bf16( sum_m G[m,v] X[m,k] )
+ * The logits are formed again, piece by piece of the vocabulary; a piece's G
+ * is rounded once to BF16 (the operand type of the two products) and lives in
+ * the workspace until both have read it.  Sums are FP32, dX across the pieces
+ * too; every addition has a fixed place, so results repeat bit for bit.
+ *
+ *   X, W, target, M, V, K   as for gemm_bf16_nt_xent
+ *   lse    float [M]   from the forward call on the same X and W  (read)
+ *   dloss  float [M]   gradient of the rows' losses (1 / rows for a mean)
+ *   dX     bf16 [M][K] (written), or NULL: not wanted
+ *   dW     bf16 [V][K] (written), or NULL: not wanted; not both NULL
+ *   workspace  at least gemm_bf16_nt_xent_backward_workspace_bytes(M, V, K)
+ *          bytes, 16-byte aligned; contents on entry ignored, on return
+ *          unspecified
+ * A row with target < 0 has no gradient (dloss[m] is not used); target >= V
+ * makes its row of dX NaN, and with it all of dW.  dX and dW are 16-byte
+ * aligned; the outputs and the workspace overlap no input and not each other.
+ * Errors: as gemm_bf16_nt_xent.
+ */
+GB300GEMM_API int gemm_bf16_nt_xent_backward(const void* X, const void* W,
+                                             const long long* target, const float* lse,
+                                             const float* dloss, void* dX, void* dW,
+                                             void* workspace, size_t workspace_bytes, int M,
+                                             int V, int K, void* stream);
+
+/* Workspace bytes gemm_bf16_nt_xent_backward needs (0 for invalid arguments). */
+GB300GEMM_API size_t gemm_bf16_nt_xent_backward_workspace_bytes(int M, int V, int K);
+
+/*
+ * router_topk - the routing step of a mixture-of-experts layer, on the FP32
+ * logits of gemm_bf16_nt_ordered:
+ *     lse[m]     = log( sum_e exp(l[m,e]) ),   p[m,e] = exp(l[m,e] - lse[m])
+ *     experts[m] = indices of the k largest logits, in falling order (ties:
+ *                  the lower index first)
+ *     weights[m] = p at the experts; with `normalize`, divided by their sum
+ *     T          = rows that take part;  counts[e] = rows that chose e
+ *     probs[e]   = (1/T) sum_m p[m,e]
+ *     losses[0]  = E * sum_e counts[e] / (k T) * probs[e]     (balance loss)
+ *     losses[1]  = (1/T) sum_m lse[m]^2                       (z-loss)
+ * All arithmetic FP32; sums are taken in a fixed order.
+ *
+ * Library extension (the pages define no such call).
+ *
+ *   logits   float [M][ld], ld >= E elements between rows        (read)
+ *   valid    uint8 [M]: 0 = the row (padding) takes no part; NULL = all do
+ *   weights  float [M][k], experts int32 [M][k]                  (written)
+ *   lse      float [M]                                           (written)
+ *   counts   int32 [E + 1]: counts[E] = T                        (written)
+ *   probs    float [E], losses float [2]                         (written)
+ *   workspace  at least router_topk_workspace_bytes(M, E) bytes, 16-byte
+ *            aligned (NULL where that is 0)
+ *   1 <= M <= 2^30, 1 <= E <= 1024, 1 <= k <= min(E, 32).
+ * A logit of -inf closes an expert to its row: it is never chosen, and where
+ * fewer than k are left the remaining places get expert -1, weight 0.  A row
+ * whose logits are all -inf takes no part.  Rows that take no part get expert
+ * -1 and weight 0 everywhere; lse is written for every row.  With T = 0 probs
+ * and losses are 0.  A NaN logit ranks first and makes the row's weights and
+ * lse, probs and losses NaN.
+ * Errors: GEMM_ERR_NULL, _SHAPE, _ALIGN (4 bytes), _ALIAS, _ARCH, _LAUNCH,
+ * _NO_DEVICE, _CAPTURE.
+ */
+GB300GEMM_API int router_topk(const float* logits, const unsigned char* valid, float* weights,
+                              int* experts, float* lse, int* counts, float* probs, float* losses,
+                              void* workspace, size_t workspace_bytes, int M, int E, int ld, int k,
+                              int normalize, void* stream);
+
+/* Workspace bytes router_topk needs (0 for few rows or invalid arguments). */
+GB300GEMM_API size_t router_topk_workspace_bytes(int M, int E);
+
+/*
+ * router_topk_backward - gradient of router_topk with respect to the logits:
+ *     dp[m,e] = dlosses[0] * E * counts[e] / (k T^2)
+ *             + (gradient of p[m,e] through weights, at the chosen experts)
+ *     dl[m,e] = p[m,e] * ( dp[m,e] - sum_f p[m,f] dp[m,f]
+ *                          + dlosses[1] * 2 lse[m] / T )
+ * with, for normalize, the weights' gradient taken through their sum.  The
+ * choice of experts and the counts are constants.
+ *
+ *   logits, M, E, ld, k, normalize   as in the forward call
+ *   experts, lse, counts             the forward call's outputs     (read)
+ *   dweights  float [M][k], or NULL (zero)
+ *   dlosses   float [2] (device): gradients of losses[0], losses[1]; or NULL
+ *   dlogits   [M][E]: float, or bf16 if dlogits_bf16 != 0          (written;
+ *             zero in rows that take no part)
+ * Errors: as router_topk.
+ */
+GB300GEMM_API int router_topk_backward(const float* logits, const int* experts, const float* lse,
+                                       const int* counts, const float* dweights,
+                                       const float* dlosses, void* dlogits, int dlogits_bf16,
+                                       int M, int E, int ld, int k, int normalize, void* stream);
+
+/*
  * bf16_scaled_add - out[i] = bf16( float(out[i]) + scale * float(d[i]) ),
  * product and sum each rounded to FP32.  The second kernel of the unfused
  * LoRA pair (GEMM into a BF16 scratch, then this), kept as the baseline the

@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
+from typing import NamedTuple
 
 import torch
 
@@ -26,6 +27,7 @@ STATUS = {
 }
 EXPORTS = ("gemm_bf16_nt", "gemm_bf16_nn", "gemm_bf16_nt_scaled_acc", "gemm_bf16_nt_ordered", "gemm_nvfp4_bs",
            "gemm_bf16_nt_splitk", "gemm_bf16_nt_streamk", "gemm_nvfp4_bs_splitk", "gemm_w4a16", "gemm_w4a16_t", "gemm_w4a16_ws",
+           "gemm_bf16_nt_xent", "gemm_bf16_nt_xent_backward", "router_topk", "router_topk_backward",
            "bf16_scaled_add", "gemm_get_device_status", "gemm_selftest_wait_timeout",
            "gemm_testing_set_overrides", "gemm_status_string")
 
@@ -73,6 +75,16 @@ def load() -> ctypes.CDLL:
                                                  i, i, i, i, i, vp]
             lib.gemm_nvfp4_bs_splitk_workspace_bytes.argtypes = [i, i, i, i]
             lib.gemm_nvfp4_bs_splitk_workspace_bytes.restype = ctypes.c_size_t
+            lib.gemm_bf16_nt_xent.argtypes = [vp] * 6 + [ctypes.c_size_t] + [i] * 3 + [vp]
+            lib.gemm_bf16_nt_xent_workspace_bytes.argtypes = [i, i]
+            lib.gemm_bf16_nt_xent_workspace_bytes.restype = ctypes.c_size_t
+            lib.gemm_bf16_nt_xent_backward.argtypes = [vp] * 8 + [ctypes.c_size_t] + [i] * 3 + [vp]
+            lib.gemm_bf16_nt_xent_backward_workspace_bytes.argtypes = [i] * 3
+            lib.gemm_bf16_nt_xent_backward_workspace_bytes.restype = ctypes.c_size_t
+            lib.router_topk.argtypes = [vp] * 9 + [ctypes.c_size_t] + [i] * 5 + [vp]
+            lib.router_topk_workspace_bytes.argtypes = [i, i]
+            lib.router_topk_workspace_bytes.restype = ctypes.c_size_t
+            lib.router_topk_backward.argtypes = [vp] * 7 + [i] * 6 + [vp]
             lib.gemm_get_device_status.argtypes = [vp]
             lib.gemm_selftest_wait_timeout.argtypes = [i, vp]
             lib.gemm_testing_set_overrides.argtypes = [i, i]
@@ -368,6 +380,214 @@ def gemm_nvfp4_bs_splitk(a: torch.Tensor, b: torch.Tensor, sfa: torch.Tensor, sf
                                        c.data_ptr(), workspace.data_ptr(), nbytes, L, M, N, K,
                                        int(k_splits), _stream_ptr(stream)), "gemm_nvfp4_bs_splitk")
     return c
+
+
+def _on_device(name: str, like: torch.Tensor, t: torch.Tensor, dtype, shape) -> None:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != like.device:
+        raise ValueError(f"{name} must be on {like.device}, got {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _allocator(device, stream):
+    """torch.empty whose memory belongs to the stream the call runs on, so that
+    the caching allocator does not hand it out again before the call is done."""
+    if stream is None:
+        return lambda shape, dtype: torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(_stream_ptr(stream), device=device)
+
+    def empty(shape, dtype):
+        with torch.cuda.stream(stream):
+            return torch.empty(shape, dtype=dtype, device=device)
+    return empty
+
+
+def _workspace(workspace, need: int, like: torch.Tensor, empty):
+    """(pointer, bytes) of the caller's workspace, or of one allocated here; the
+    third value keeps it alive."""
+    if workspace is None:
+        workspace = empty(max(need, 16), torch.uint8)
+    if not (workspace.device == like.device and workspace.is_contiguous()):
+        raise ValueError(f"workspace must be a contiguous tensor on {like.device}")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+
+def _xent_inputs(X, W, target):
+    _mat(X, torch.bfloat16, "X")
+    _mat(W, torch.bfloat16, "W")
+    if X.shape[1] != W.shape[1]:
+        raise ValueError(f"K mismatch: X {tuple(X.shape)} vs W {tuple(W.shape)}")
+    if W.device != X.device:
+        raise ValueError("X and W must be on one device")
+    M, K = X.shape
+    _on_device("target", X, target, torch.int64, (M,))
+    return M, W.shape[0], K
+
+
+def gemm_bf16_nt_xent_workspace_bytes(M: int, V: int) -> int:
+    return int(load().gemm_bf16_nt_xent_workspace_bytes(M, V))
+
+
+def gemm_bf16_nt_xent(X: torch.Tensor, W: torch.Tensor, target: torch.Tensor,
+                      loss: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                      workspace: torch.Tensor | None = None, stream=None):
+    """(loss [M], lse [M]) of the softmax cross entropy of X W^T, FP32; the logits are not stored.
+
+    X bf16 [M,K]; W bf16 [V,K]; target int64 [M], negative = the row has no
+    loss.  Keep lse for gemm_bf16_nt_xent_backward.
+    """
+    M, V, K = _xent_inputs(X, W, target)
+    empty = _allocator(X.device, stream)
+    loss = empty((M,), torch.float32) if loss is None else loss
+    lse = empty((M,), torch.float32) if lse is None else lse
+    _on_device("loss", X, loss, torch.float32, (M,))
+    _on_device("lse", X, lse, torch.float32, (M,))
+    ws, nbytes, _keep = _workspace(workspace, gemm_bf16_nt_xent_workspace_bytes(M, V), X, empty)
+    with torch.cuda.device(X.device):
+        _check(load().gemm_bf16_nt_xent(X.data_ptr(), W.data_ptr(), target.data_ptr(),
+                                        loss.data_ptr(), lse.data_ptr(), ws, nbytes, M, V, K,
+                                        _stream_ptr(stream)), "gemm_bf16_nt_xent")
+    return loss, lse
+
+
+def gemm_bf16_nt_xent_backward_workspace_bytes(M: int, V: int, K: int) -> int:
+    return int(load().gemm_bf16_nt_xent_backward_workspace_bytes(M, V, K))
+
+
+def gemm_bf16_nt_xent_backward(X: torch.Tensor, W: torch.Tensor, target: torch.Tensor,
+                               lse: torch.Tensor, dloss: torch.Tensor,
+                               dX: torch.Tensor | None = None, dW: torch.Tensor | None = None,
+                               workspace: torch.Tensor | None = None, stream=None,
+                               need_dx: bool = True, need_dw: bool = True):
+    """(dX bf16 [M,K], dW bf16 [V,K]) of gemm_bf16_nt_xent; None for one that is not needed.
+
+    lse: the forward call's; dloss float32 [M]: the rows' loss gradients.
+    """
+    M, V, K = _xent_inputs(X, W, target)
+    _on_device("lse", X, lse, torch.float32, (M,))
+    _on_device("dloss", X, dloss, torch.float32, (M,))
+    need_dx, need_dw = need_dx or dX is not None, need_dw or dW is not None
+    if not (need_dx or need_dw):
+        raise ValueError("neither dX nor dW is needed")
+    empty = _allocator(X.device, stream)
+    if need_dx:
+        dX = empty((M, K), torch.bfloat16) if dX is None else dX
+        _on_device("dX", X, dX, torch.bfloat16, (M, K))
+    if need_dw:
+        dW = empty((V, K), torch.bfloat16) if dW is None else dW
+        _on_device("dW", X, dW, torch.bfloat16, (V, K))
+    ws, nbytes, _keep = _workspace(workspace, gemm_bf16_nt_xent_backward_workspace_bytes(M, V, K),
+                                   X, empty)
+    with torch.cuda.device(X.device):
+        _check(load().gemm_bf16_nt_xent_backward(
+            X.data_ptr(), W.data_ptr(), target.data_ptr(), lse.data_ptr(), dloss.data_ptr(),
+            dX.data_ptr() if need_dx else None, dW.data_ptr() if need_dw else None, ws, nbytes,
+            M, V, K, _stream_ptr(stream)), "gemm_bf16_nt_xent_backward")
+    return dX, dW
+
+
+class RouterTopk(NamedTuple):
+    """What router_topk returns (counts[E] is the number of rows that take part)."""
+    weights: torch.Tensor
+    experts: torch.Tensor
+    lse: torch.Tensor
+    counts: torch.Tensor
+    probs: torch.Tensor
+    losses: torch.Tensor
+
+
+def _logit_rows(logits):
+    """(M, E, ld) of FP32 logits whose rows may lie apart in a wider matrix."""
+    if not isinstance(logits, torch.Tensor):
+        raise TypeError("logits must be a torch.Tensor")
+    if logits.dtype != torch.float32:
+        raise TypeError(f"logits must be torch.float32, got {logits.dtype}")
+    if logits.dim() != 2:
+        raise ValueError(f"logits must be 2-D, got shape {tuple(logits.shape)}")
+    if not logits.is_cuda:
+        raise ValueError("logits must be a CUDA tensor")
+    M, E = logits.shape
+    if E > 1 and logits.stride(1) != 1:
+        raise ValueError("logits must have unit stride within a row")
+    ld = logits.stride(0) if M > 1 else E
+    if ld < E:
+        raise ValueError("rows of logits overlap")
+    return M, E, ld
+
+
+def router_topk_workspace_bytes(M: int, E: int) -> int:
+    return int(load().router_topk_workspace_bytes(M, E))
+
+
+def router_topk(logits: torch.Tensor, k: int, valid: torch.Tensor | None = None,
+                normalize: bool = False, workspace: torch.Tensor | None = None,
+                stream=None) -> RouterTopk:
+    """Softmax, top-k experts, per-expert counts, balance loss and z-loss of FP32 router logits.
+
+    logits float32 [M,E] (row stride >= E); valid uint8 or bool [M], zero = a
+    padding row.  losses = [balance, z].
+    """
+    M, E, ld = _logit_rows(logits)
+    if valid is not None:
+        valid = valid.view(torch.uint8) if valid.dtype == torch.bool else valid
+        _on_device("valid", logits, valid, torch.uint8, (M,))
+    if not 1 <= k <= E:
+        raise ValueError(f"k must be in 1..{E}, got {k}")
+    empty = _allocator(logits.device, stream)
+    f32, i32 = torch.float32, torch.int32
+    out = RouterTopk(empty((M, k), f32), empty((M, k), i32), empty((M,), f32), empty((E + 1,), i32),
+                     empty((E,), f32), empty((2,), f32))
+    ws, nbytes, _keep = _workspace(workspace, router_topk_workspace_bytes(M, E), logits, empty)
+    with torch.cuda.device(logits.device):
+        _check(load().router_topk(logits.data_ptr(), None if valid is None else valid.data_ptr(),
+                                  *(t.data_ptr() for t in out), ws, nbytes, M, E, ld, int(k),
+                                  int(bool(normalize)), _stream_ptr(stream)), "router_topk")
+    return out
+
+
+def router_topk_backward(logits: torch.Tensor, experts: torch.Tensor, lse: torch.Tensor,
+                         counts: torch.Tensor, dweights: torch.Tensor | None = None,
+                         dlosses: torch.Tensor | None = None, normalize: bool = False,
+                         dtype=torch.float32, dlogits: torch.Tensor | None = None, stream=None):
+    """Gradient of router_topk's weights and losses with respect to its logits.
+
+    experts, lse, counts: the forward call's.  dweights float32 [M,k] and
+    dlosses float32 [2] may be None (zero).  dtype: float32, or bfloat16 for a
+    gradient that goes into a BF16 product.
+    """
+    M, E, ld = _logit_rows(logits)
+    if experts.dim() != 2:
+        raise ValueError("experts must be [M, k]")
+    k = experts.shape[1]
+    _on_device("experts", logits, experts, torch.int32, (M, k))
+    _on_device("lse", logits, lse, torch.float32, (M,))
+    _on_device("counts", logits, counts, torch.int32, (E + 1,))
+    if dweights is not None:
+        _on_device("dweights", logits, dweights, torch.float32, (M, k))
+    if dlosses is not None:
+        _on_device("dlosses", logits, dlosses, torch.float32, (2,))
+    if dlogits is not None:
+        dtype = dlogits.dtype
+    if dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"dlogits must be float32 or bfloat16, got {dtype}")
+    if dlogits is None:
+        dlogits = _allocator(logits.device, stream)((M, E), dtype)
+    _on_device("dlogits", logits, dlogits, dtype, (M, E))
+    with torch.cuda.device(logits.device):
+        _check(load().router_topk_backward(
+            logits.data_ptr(), experts.data_ptr(), lse.data_ptr(), counts.data_ptr(),
+            None if dweights is None else dweights.data_ptr(),
+            None if dlosses is None else dlosses.data_ptr(), dlogits.data_ptr(),
+            int(dtype == torch.bfloat16), M, E, ld, k, int(bool(normalize)),
+            _stream_ptr(stream)), "router_topk_backward")
+    return dlogits
 
 
 def bf16_scaled_add(out: torch.Tensor, d: torch.Tensor, scale: float, stream=None):

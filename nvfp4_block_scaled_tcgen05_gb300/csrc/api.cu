@@ -193,6 +193,49 @@ int check_bf16_nt(const void* A, const void* B, const void* C, int M, int N, int
   return GEMM_OK;
 }
 
+inline bool aligned(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+constexpr int kMaxDim = 1 << 30;  // leaves room for rounding a dimension up to whole tiles
+
+// A buffer; n = 0 where the caller passed none.
+struct Span {
+  const void* p;
+  size_t n;
+};
+
+// An output overlaps an input or another output?
+bool any_overlap(const Span* in, int n_in, const Span* out, int n_out) {
+  for (int i = 0; i < n_out; ++i) {
+    if (!out[i].n) continue;
+    for (int j = 0; j < n_in; ++j)
+      if (in[j].n && overlaps(out[i].p, out[i].n, in[j].p, in[j].n)) return true;
+    for (int j = 0; j < i; ++j)
+      if (out[j].n && overlaps(out[i].p, out[i].n, out[j].p, out[j].n)) return true;
+  }
+  return false;
+}
+
+// Shared checks of the routing step (the sizes).
+int check_router(int M, int E, int ld, int k) {
+  if (M <= 0 || M > kMaxDim || E <= 0 || E > kRouterMaxExperts || ld < E) return GEMM_ERR_SHAPE;
+  if (k <= 0 || k > E || k > kRouterMaxTopk) return GEMM_ERR_SHAPE;
+  return GEMM_OK;
+}
+
+// Shared checks of the linear cross entropy (the matrices).
+int check_xent(const void* X, const void* W, int M, int V, int K) {
+  if (!X || !W) return GEMM_ERR_NULL;
+  if (M <= 0 || V <= 0 || K <= 0) return GEMM_ERR_SHAPE;
+  if (M > kMaxDim || V > kMaxDim || K > kMaxDim) return GEMM_ERR_SHAPE;
+  // tiles of every product of the backward pass
+  const long long mb = ((long long)M + 127) / 128, vb = ((long long)V + 127) / 128,
+                  kb = ((long long)K + 255) / 256;
+  if (mb * vb > kMaxTiles || vb * kb > kMaxTiles || mb * kb > kMaxTiles) return GEMM_ERR_SHAPE;
+  if (!aligned16(X) || !aligned16(W)) return GEMM_ERR_ALIGN;
+  if (K % 8 != 0) return GEMM_ERR_ALIGN;  // 16-byte row pitch of X and W
+  return GEMM_OK;
+}
+
 }  // namespace
 }  // namespace gb300
 
@@ -428,6 +471,118 @@ int gemm_nvfp4_bs_splitk(const void* a, const void* b, const void* sfa, const vo
   if (rc != GEMM_OK) return rc;
   return launch_gemm_nvfp4_splitk(a, b, sfa, sfb, c, static_cast<float*>(workspace), L, M, N, K,
                                   k_splits, dev, static_cast<cudaStream_t>(stream));
+}
+
+size_t gemm_bf16_nt_xent_workspace_bytes(int M, int V) {
+  if (M <= 0 || V <= 0 || M > kMaxDim || V > kMaxDim) return 0;
+  return xent_forward_workspace(M, V);
+}
+
+int gemm_bf16_nt_xent(const void* X, const void* W, const long long* target, float* loss,
+                      float* lse, void* workspace, size_t workspace_bytes, int M, int V, int K,
+                      void* stream) {
+  if (!target || !loss || !lse || !workspace) return GEMM_ERR_NULL;
+  int rc = check_xent(X, W, M, V, K);
+  if (rc != GEMM_OK) return rc;
+  if (!aligned(target, 8) || !aligned(loss, 4) || !aligned(lse, 4) || !aligned16(workspace))
+    return GEMM_ERR_ALIGN;
+  const size_t need = xent_forward_workspace(M, V);
+  if (workspace_bytes < need) return GEMM_ERR_SHAPE;
+  const Span in[] = {{X, size_t(M) * K * 2}, {W, size_t(V) * K * 2}, {target, size_t(M) * 8}};
+  const Span out[] = {{loss, size_t(M) * 4}, {lse, size_t(M) * 4}, {workspace, need}};
+  if (any_overlap(in, 3, out, 3)) return GEMM_ERR_ALIAS;
+  DeviceInfo dev;
+  if ((rc = current_device(&dev, stream)) != GEMM_OK) return rc;
+  const XentForward a{X, W, target, loss, lse, workspace, M, V, K};
+  return launch_xent_forward(a, dev, static_cast<cudaStream_t>(stream));
+}
+
+size_t gemm_bf16_nt_xent_backward_workspace_bytes(int M, int V, int K) {
+  if (M <= 0 || V <= 0 || K <= 0 || M > kMaxDim || V > kMaxDim || K > kMaxDim) return 0;
+  return xent_backward_workspace(M, V, K);
+}
+
+int gemm_bf16_nt_xent_backward(const void* X, const void* W, const long long* target,
+                               const float* lse, const float* dloss, void* dX, void* dW,
+                               void* workspace, size_t workspace_bytes, int M, int V, int K,
+                               void* stream) {
+  if (!target || !lse || !dloss || !workspace || (!dX && !dW)) return GEMM_ERR_NULL;
+  int rc = check_xent(X, W, M, V, K);
+  if (rc != GEMM_OK) return rc;
+  if (!aligned(target, 8) || !aligned(lse, 4) || !aligned(dloss, 4) || !aligned16(workspace) ||
+      !aligned16(dX) || !aligned16(dW))
+    return GEMM_ERR_ALIGN;
+  const size_t need = xent_backward_workspace(M, V, K);
+  if (workspace_bytes < need) return GEMM_ERR_SHAPE;
+  const Span in[] = {{X, size_t(M) * K * 2},
+                     {W, size_t(V) * K * 2},
+                     {target, size_t(M) * 8},
+                     {lse, size_t(M) * 4},
+                     {dloss, size_t(M) * 4}};
+  const Span out[] = {
+      {dX, dX ? size_t(M) * K * 2 : 0}, {dW, dW ? size_t(V) * K * 2 : 0}, {workspace, need}};
+  if (any_overlap(in, 5, out, 3)) return GEMM_ERR_ALIAS;
+  DeviceInfo dev;
+  if ((rc = current_device(&dev, stream)) != GEMM_OK) return rc;
+  const XentBackward a{X, W, target, lse, dloss, dX, dW, workspace, M, V, K};
+  return launch_xent_backward(a, dev, static_cast<cudaStream_t>(stream));
+}
+
+size_t router_topk_workspace_bytes(int M, int E) {
+  if (M <= 0 || E <= 0 || E > kRouterMaxExperts) return 0;
+  return router_topk_workspace(M, E);
+}
+
+int router_topk(const float* logits, const unsigned char* valid, float* weights, int* experts,
+                float* lse, int* counts, float* probs, float* losses, void* workspace,
+                size_t workspace_bytes, int M, int E, int ld, int k, int normalize, void* stream) {
+  if (!logits || !weights || !experts || !lse || !counts || !probs || !losses)
+    return GEMM_ERR_NULL;
+  int rc = check_router(M, E, ld, k);
+  if (rc != GEMM_OK) return rc;
+  const size_t need = router_topk_workspace(M, E);
+  if (need && !workspace) return GEMM_ERR_NULL;
+  if (workspace_bytes < need) return GEMM_ERR_SHAPE;
+  if (!aligned(logits, 4) || !aligned(weights, 4) || !aligned(experts, 4) || !aligned(lse, 4) ||
+      !aligned(counts, 4) || !aligned(probs, 4) || !aligned(losses, 4) || !aligned16(workspace))
+    return GEMM_ERR_ALIGN;
+  const size_t rows = size_t(M), mk = rows * size_t(k) * 4;
+  const Span in[] = {{logits, ((rows - 1) * size_t(ld) + E) * 4}, {valid, valid ? rows : 0}};
+  const Span out[] = {{weights, mk},         {experts, mk},       {lse, rows * 4},
+                      {counts, (size_t(E) + 1) * 4}, {probs, size_t(E) * 4}, {losses, 8},
+                      {workspace, need}};
+  if (any_overlap(in, 2, out, 7)) return GEMM_ERR_ALIAS;
+  DeviceInfo dev;
+  if ((rc = current_device(&dev, stream)) != GEMM_OK) return rc;
+  const RouterTopk r{logits, valid, weights, experts, lse, counts, probs, losses,
+                     workspace, M, E, ld, k, normalize != 0};
+  return launch_router_topk(r, dev, static_cast<cudaStream_t>(stream));
+}
+
+int router_topk_backward(const float* logits, const int* experts, const float* lse,
+                         const int* counts, const float* dweights, const float* dlosses,
+                         void* dlogits, int dlogits_bf16, int M, int E, int ld, int k,
+                         int normalize, void* stream) {
+  if (!logits || !experts || !lse || !counts || !dlogits) return GEMM_ERR_NULL;
+  int rc = check_router(M, E, ld, k);
+  if (rc != GEMM_OK) return rc;
+  if (!aligned(logits, 4) || !aligned(experts, 4) || !aligned(lse, 4) || !aligned(counts, 4) ||
+      !aligned(dweights, 4) || !aligned(dlosses, 4) || !aligned(dlogits, dlogits_bf16 ? 2 : 4))
+    return GEMM_ERR_ALIGN;
+  const size_t rows = size_t(M), mk = rows * size_t(k) * 4;
+  const Span in[] = {{logits, ((rows - 1) * size_t(ld) + E) * 4},
+                     {experts, mk},
+                     {lse, rows * 4},
+                     {counts, (size_t(E) + 1) * 4},
+                     {dweights, dweights ? mk : 0},
+                     {dlosses, dlosses ? size_t(8) : 0}};
+  const Span out[] = {{dlogits, rows * size_t(E) * (dlogits_bf16 ? 2 : 4)}};
+  if (any_overlap(in, 6, out, 1)) return GEMM_ERR_ALIAS;
+  DeviceInfo dev;
+  if ((rc = current_device(&dev, stream)) != GEMM_OK) return rc;
+  const RouterTopkBackward r{logits, experts, lse, counts, dweights, dlosses, dlogits,
+                             dlogits_bf16 != 0, M, E, ld, k, normalize != 0};
+  return launch_router_topk_backward(r, dev, static_cast<cudaStream_t>(stream));
 }
 
 int bf16_scaled_add(void* out, const void* d, float scale, long n, void* stream) {

@@ -120,4 +120,54 @@ int launch_splitk_reduce(const float* ws, void* C, size_t n, int splits, const D
 int launch_splitk_reduce_f16(const float* ws, void* C, size_t n, int splits, const DeviceInfo& dev,
                              cudaStream_t stream);
 
+// Linear cross entropy (xent.cu).  Forward: loss and lse [M]; workspace of
+// xent_forward_workspace bytes.  Backward: dX and / or dW (NULL = not wanted).
+struct XentForward {
+  const void *X, *W;
+  const long long* target;
+  float *loss, *lse;
+  void* workspace;
+  int M, V, K;
+};
+struct XentBackward {
+  const void *X, *W;
+  const long long* target;
+  const float *lse, *dloss;
+  void *dX, *dW, *workspace;
+  int M, V, K;
+};
+size_t xent_forward_workspace(int M, int V);
+size_t xent_backward_workspace(int M, int V, int K);
+int launch_xent_forward(const XentForward& a, const DeviceInfo& dev, cudaStream_t stream);
+int launch_xent_backward(const XentBackward& a, const DeviceInfo& dev, cudaStream_t stream);
+
+// Routing step (router_topk.cu); limits: E <= kRouterMaxExperts, k <= 32.
+constexpr int kRouterMaxExperts = 1024;
+constexpr int kRouterMaxTopk = 32;
+struct RouterTopk {
+  const float* logits;  // [M][ld]
+  const unsigned char* valid;
+  float* weights;
+  int* experts;
+  float* lse;
+  int* counts;
+  float *probs, *losses;
+  void* workspace;
+  int M, E, ld, k, normalize;
+};
+struct RouterTopkBackward {
+  const float* logits;  // [M][ld]
+  const int* experts;
+  const float* lse;
+  const int* counts;
+  const float *dweights, *dlosses;
+  void* dlogits;  // [M][E], FP32 or BF16
+  int bf16;
+  int M, E, ld, k, normalize;
+};
+size_t router_topk_workspace(int M, int E);
+int launch_router_topk(const RouterTopk& r, const DeviceInfo& dev, cudaStream_t stream);
+int launch_router_topk_backward(const RouterTopkBackward& r, const DeviceInfo& dev,
+                                cudaStream_t stream);
+
 }  // namespace gb300

@@ -43,12 +43,19 @@ namespace gb300 {
 
 enum class Operand : int { kBF16 = 0, kNVFP4 = 1, kW4A16 = 2 };
 // kScaleBF16: C = bf16(scale * acc), one FP32 multiply then one rounding
+// kAddF32: C (FP32) = acc, or C += acc (p.accumulate)
+// kXentStats: no C; per row and N block the maximum and the sum of
+//   exp(acc - maximum), and the target column's value (linear cross entropy)
+// kXentGradBF16: C = bf16(d_row * (exp(acc - lse_row) - [column = target_row]))
 enum class Epilogue : int {
   kStoreBF16 = 0,
   kScaledAccBF16 = 1,
   kStoreFP16 = 2,
   kStoreF32 = 3,
-  kScaleBF16 = 4
+  kScaleBF16 = 4,
+  kAddF32 = 5,
+  kXentStats = 6,
+  kXentGradBF16 = 7
 };
 
 struct GemmParams {
@@ -64,11 +71,22 @@ struct GemmParams {
   unsigned long long timeout_ns;  // bound on every wait
   int group_m;                    // M blocks per raster group (raster_group_m)
   int sk;                         // stream-K: clusters sharing the tail (0 = off)
+  int accumulate;                 // kAddF32: add to C instead of storing
+  // chained configurations (TileCfg::CHAIN)
+  int late_wait;                  // wait for the previous grid at the end instead of the start
+  int trigger_late;               // let the next grid start only once this one has waited
+  // linear cross entropy (kXent*)
+  const long long* target;        // [M] target column; < 0: the row has no loss
+  const float* row_lse;           // [M] kXentGradBF16
+  const float* row_scale;         // [M] kXentGradBF16: gradient of the row's loss
+  float2* stats;                  // [N blocks][M] kXentStats: maximum, sum of exponentials
+  float* picked;                  // [M] kXentStats: the target column's value
+  int col_offset, col_total;      // first column of this launch, columns in all
 };
 
 template <Operand OP, int CG_, int BN_, int STAGES_, int EPI_WARPS_ = 4, int EPI_BUFS_ = 2,
           bool SFA_REP_ = true, bool SFB_REP_ = false, int KSUB_ = 1, bool B_MN_ = false,
-          bool C_T_ = false>
+          bool C_T_ = false, bool A_MN_ = false, bool CHAIN_ = false>
 struct TileCfg {
   static constexpr Operand kOp = OP;
   static constexpr bool kFP4 = (OP == Operand::kNVFP4);
@@ -94,6 +112,12 @@ struct TileCfg {
   // the CTA's B columns as 64-column atoms (BK rows of 128 bytes each, the
   // TMA's 128-byte swizzle), and the MMA reads B MN-major.
   static constexpr bool B_MN = B_MN_;
+  // A_MN: A is stored [K][M] (M contiguous), staged the same way as 64-row atoms.
+  static constexpr bool A_MN = A_MN_;
+  // CHAIN: the launch may set late_wait / trigger_late, so that a sequence of
+  // grids of which only some depend on their predecessor fills the SMs that
+  // the last round of tiles leaves idle.
+  static constexpr bool CHAIN = CHAIN_;
   // C_T: the output is D transposed (the swapped-operand decode GEMM, whose
   // M role holds the weights and N role the few activation rows)
   static constexpr bool C_T = C_T_;
@@ -144,6 +168,8 @@ struct TileCfg {
   static_assert(KSUB == 1 || (KSUB == 2 && !kFP4), "K sub-tiles: BF16 only");
   static_assert(!B_MN || (!kFP4 && B_ROWS % 64 == 0), "MN-major B: BF16 operands");
   static constexpr int B_ATOM_BYTES = 64 * KSUB * 128;  // one 64-column MN-major atom of a stage
+  static_assert(!A_MN || (!kFP4 && !kW4 && B_MN), "MN-major A: BF16 operands, with MN-major B");
+  static constexpr int A_ATOM_BYTES = B_ATOM_BYTES;
   static_assert(STAGES >= 1, "pipeline stages");
   static_assert(B_ROWS % 8 == 0, "B rows per CTA");
   static_assert(!kFP4 || BN % 128 == 0, "NVFP4 BN must cover whole 128-row scale atoms");
@@ -200,13 +226,14 @@ struct TileCfg {
       64 + 32 * EPI_WARPS + 32 * SF_WARPS + 32 * DQ_WARPS + (kW4 ? 32 : 0);
 
   // Instruction descriptor.  kind::f16: D=F32 (bits 4-5 = 1), A=B=BF16
-  // (bits 7-9 = 1, 10-12 = 1), both K-major, N>>3 in bits 17-22, M>>4 in
-  // bits 24-28.  kind::mxf4nvf4: A=B=E2M1 (1), scale type UE4M3 (bit 23 = 0),
+  // (bits 7-9 = 1, 10-12 = 1), K-major unless bit 15 (A) / 16 (B) is set,
+  // N>>3 in bits 17-22, M>>4 in bits 24-28.  kind::mxf4nvf4: A=B=E2M1 (1), scale type UE4M3 (bit 23 = 0),
   // scale ids 0, dense K=64.
   __host__ __device__ static constexpr uint32_t idesc() {
     return kFP4 ? ((1u << 7) | (1u << 10) | (uint32_t(BN >> 3) << 17) |
                    (uint32_t(TILE_M >> 4) << 24))
-                : ((1u << 4) | (1u << 7) | (1u << 10) | (B_MN ? (1u << 16) : 0u) |
+                : ((1u << 4) | (1u << 7) | (1u << 10) | (A_MN ? (1u << 15) : 0u) |
+                   (B_MN ? (1u << 16) : 0u) |
                    (uint32_t(BN >> 3) << 17) |
                    (uint32_t(TILE_M >> 4) << 24));
   }
@@ -349,6 +376,50 @@ __device__ __forceinline__ void write_box_row_f32(uint8_t* row, int lane, const 
   }
 }
 
+// Linear cross entropy, forward: folds 64 logits of one row into the row's
+// running maximum and sum of exp(z - maximum).  exp(y) = 2^(y log2 e) on the
+// special-function unit (relative error below 2^-21).  A maximum of -inf (no
+// logit yet, or none finite) subtracts 0 instead, so that no inf - inf arises;
+// NaN logits reach the sum.
+__device__ __forceinline__ float fast_exp(float y) { return ptx::ex2(y * 1.4426950408889634f); }
+
+__device__ __forceinline__ void xent_fold(const uint32_t (&a)[32], const uint32_t (&b)[32],
+                                          float& mx, float& sum) {
+  float m4[4] = {mx, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+  for (int i = 0; i < 32; ++i)
+    m4[i & 3] = fmaxf(m4[i & 3], fmaxf(__uint_as_float(a[i]), __uint_as_float(b[i])));
+  const float m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+  const float ref = (m == -INFINITY) ? 0.0f : m;
+  float s4[4] = {sum * fast_exp(mx - ref), 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    s4[i & 3] += fast_exp(__uint_as_float(a[i]) - ref);
+    s4[(i + 2) & 3] += fast_exp(__uint_as_float(b[i]) - ref);
+  }
+  mx = m;
+  sum = (s4[0] + s4[1]) + (s4[2] + s4[3]);
+}
+
+// Linear cross entropy, backward: 32 logits of one row -> gradients
+// d (exp(z - lse) - [column = target]); `rel` is the target's place among
+// them (none if outside 0..31), `live` the columns that exist.  lse = +inf
+// marks a row without a loss (all zeros, whatever the logits).
+__device__ __forceinline__ void xent_grad(uint32_t (&v)[32], float lse, float d, int rel,
+                                          int live) {
+  if (lse == INFINITY && d == 0.0f) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = 0u;
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    float q = fast_exp(__uint_as_float(v[i]) - lse);
+    if (rel == i) q -= 1.0f;
+    v[i] = __float_as_uint(i < live ? d * q : 0.0f);
+  }
+}
+
 // W4A16 weights ("gemm_dense.rs", w4a16_gemm: C = A @ dequant(B), NVFP4
 // weights dequantised to BF16): 16 packed bytes of one weight row (32 e2m1
 // codes, element 2j in the low nibble of byte j) and the row's two e4m3
@@ -470,7 +541,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
   // registers with 16-byte global stores (frees shared memory for stages).
   constexpr bool kDirectStore = (Cfg::EPI_BUFS == 0);
   static_assert(!kDirectStore || EPI == Epilogue::kStoreBF16 || EPI == Epilogue::kStoreFP16 ||
-                    EPI == Epilogue::kScaleBF16 ||
+                    EPI == Epilogue::kScaleBF16 || EPI == Epilogue::kXentStats ||
                     (EPI == Epilogue::kStoreF32 && (Cfg::kRegEpi || Cfg::C_T)),
                 "direct stores serve the plain 16-bit epilogues and FP32 partials");
   static_assert(!Cfg::C_T || EPI == Epilogue::kStoreF32 || EPI == Epilogue::kStoreFP16,
@@ -595,7 +666,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
 #pragma unroll
           for (int sub = 0; sub < Cfg::KSUB; ++sub) {
             const int x = kb * Cfg::KX * Cfg::KSUB + sub * Cfg::KX;
-            ptx::tma_prefetch_3d(&tmap_a, x, a_row, l);
+            if constexpr (!Cfg::A_MN) ptx::tma_prefetch_3d(&tmap_a, x, a_row, l);
             if constexpr (!Cfg::kW4 && !Cfg::B_MN) ptx::tma_prefetch_3d(&tmap_b, x, b_row, l);
           }
           if constexpr (kFP4 && Cfg::SFA_REP)
@@ -607,7 +678,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     // The next grid on the stream (the split-K reduce, the stream-K fixup,
     // or the next GEMM) may be scheduled now: it waits for this grid's end
     // before it touches global memory.
-    ptx::griddep_launch_dependents();
+    if (!Cfg::CHAIN || !p.trigger_late) ptx::griddep_launch_dependents();
   }
   if (warp == 1) {
     ptx::tmem_alloc<CG>(ptx::smem_u32(const_cast<uint32_t*>(tmem_slot)), Cfg::TMEM_COLS);
@@ -620,7 +691,12 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
   const Watch w{abort_flag, p.status, p.timeout_ns};
   // launched as a programmatic dependent: the previous grid on the stream
   // must be complete (and its writes visible) before any global access
-  ptx::griddep_wait();
+  // (late_wait: this grid's inputs were complete before the previous grid
+  // let it start, so it only has to end after that grid)
+  if (!Cfg::CHAIN || !p.late_wait) ptx::griddep_wait();
+  if constexpr (Cfg::CHAIN) {
+    if (p.trigger_late && threadIdx.x == 0) ptx::griddep_launch_dependents();
+  }
 
   // NVFP4: the scale atoms of MMA j of stage s go into the stage's TMEM
   // slot (issued by the scale warp, which then commits sf_full[s]).
@@ -712,7 +788,13 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                 ptx::tma_load_3d_hint(da, &tmap_a, fb, x, a_row, l, pol_ab);
               } else if constexpr (Cfg::B_MN) {
                 // B [K][N]: 64-column atoms of all BK rows, loaded once per stage
-                ptx::tma_load_3d_hint(da, &tmap_a, fb, x, a_row, l, pol_ab);
+                if constexpr (!Cfg::A_MN)
+                  ptx::tma_load_3d_hint(da, &tmap_a, fb, x, a_row, l, pol_ab);
+                else if (sub == 0)
+#pragma unroll
+                  for (int at = 0; at < Cfg::BM / 64; ++at)
+                    ptx::tma_load_3d_hint(stage_a(stage) + at * Cfg::A_ATOM_BYTES, &tmap_a, fb,
+                                          a_row + 64 * at, kb * Cfg::BK, l, pol_ab);
                 if (sub == 0)
 #pragma unroll
                   for (int at = 0; at < Cfg::B_ROWS / 64; ++at)
@@ -755,7 +837,13 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                 (void)db;  // B is written by the dequantisation warps
                 ptx::tma_load_3d_pair_hint(da, &tmap_a, fb, x, a_row, l, pol_ab);
               } else if constexpr (Cfg::B_MN) {
-                ptx::tma_load_3d_pair_hint(da, &tmap_a, fb, x, a_row, l, pol_ab);
+                if constexpr (!Cfg::A_MN)
+                  ptx::tma_load_3d_pair_hint(da, &tmap_a, fb, x, a_row, l, pol_ab);
+                else if (sub == 0)
+#pragma unroll
+                  for (int at = 0; at < Cfg::BM / 64; ++at)
+                    ptx::tma_load_3d_pair_hint(stage_a(stage) + at * Cfg::A_ATOM_BYTES, &tmap_a,
+                                               fb, a_row + 64 * at, kb * Cfg::BK, l, pol_ab);
                 if (sub == 0)
 #pragma unroll
                   for (int at = 0; at < Cfg::B_ROWS / 64; ++at)
@@ -877,8 +965,9 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
       // Stage s, MMA j: start address + s * STAGE_BYTES + offset of j, i.e.
       // the 14-bit start field (address >> 4) grows by that >> 4; shared
       // addresses stay below 2^18 bytes, so the field never carries over.
-      const uint64_t adesc0 = ptx::sw128_kmajor_desc(stage_a(0));
-      // MN-major B: leading offset = atom stride (next 64 columns), stride
+      const uint64_t adesc0 = Cfg::A_MN ? ptx::smem_desc(stage_a(0), Cfg::A_ATOM_BYTES, 1024, 2)
+                                        : ptx::sw128_kmajor_desc(stage_a(0));
+      // MN-major operand: leading offset = atom stride (next 64 columns), stride
       // offset = 8 K rows (1024 bytes)
       const uint64_t bdesc0 = Cfg::B_MN ? ptx::smem_desc(stage_b(0), Cfg::B_ATOM_BYTES, 1024, 2)
                                         : ptx::sw128_kmajor_desc(stage_b(0));
@@ -912,7 +1001,9 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
             if (j < nsteps) {
               // step j: K sub-tile j / 4, 32-byte K slice j % 4 within it
               const uint64_t ad =
-                  adesc0 + soff + uint64_t(((j / 4) * Cfg::A_SUB_BYTES + 32 * (j % 4)) >> 4);
+                  Cfg::A_MN
+                      ? adesc0 + soff + uint64_t((j * 16 * 128) >> 4)
+                      : adesc0 + soff + uint64_t(((j / 4) * Cfg::A_SUB_BYTES + 32 * (j % 4)) >> 4);
               // K-major: sub-tile j / 4, 32-byte K slice j % 4; MN-major: rows 16 j ..
               const uint64_t bd =
                   Cfg::B_MN
@@ -1180,6 +1271,11 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
       if constexpr (kL2Hints) ptx::tma_store_3d_hint(&tmap_c, sbuf, col0, row0, l, pol_c);
       else ptx::tma_store_3d(&tmap_c, sbuf, col0, row0, l);
     };
+    // linear cross entropy: the row block whose per-row values the lane holds
+    int xent_row0 = -1, xent_rel = -1;
+    long long xent_target = -1;
+    float xent_lse = 0.0f, xent_scale = 0.0f;
+    (void)xent_row0, (void)xent_rel, (void)xent_target, (void)xent_lse, (void)xent_scale;
     uint32_t chunk_ctr = 0;
     uint32_t epi_parity = 0;     // bit b: parity of the next wait on epi_bar(e, b)
     uint32_t epi_pending = 0;    // bit b: a load into buffer b has not been waited for
@@ -1245,6 +1341,19 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
       const int row0 = mb * Cfg::TILE_M + int(peer) * Cfg::BM + q * 32;
       const bool rows_live = row0 < p.M;
       const uint32_t tacc = tmem_base + lane_off + uint32_t(acc * BN + col_base);
+      if constexpr (EPI == Epilogue::kXentGradBF16) {
+        if (row0 != xent_row0) {  // this lane's row of the gradient
+          xent_row0 = row0;
+          const int grow = row0 + lane;
+          const long long t = grow < p.M ? p.target[grow] : -1;
+          xent_lse = grow < p.M ? p.row_lse[grow] : 0.0f;
+          // a row without a loss has no gradient; a target past the vocabulary
+          // has no loss to differentiate
+          xent_scale = t < 0 ? 0.0f : (t >= p.col_total ? NAN : p.row_scale[grow]);
+          xent_rel = (t >= p.col_offset && t < p.col_offset + p.N) ? int(t - p.col_offset) : -1;
+          if (t < 0) xent_lse = INFINITY;  // exp(z - inf) = 0 whatever the logits
+        }
+      }
 
       if constexpr (Cfg::C_T) {
         // Transposed output (the swapped-operand decode GEMM: D rows are the
@@ -1437,8 +1546,50 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
             ptx::bulk_commit_group();
           }
         }
-      } else if constexpr (EPI == Epilogue::kStoreF32) {
-        // FP32 partials (split-K): 32-column boxes of 32 rows x 128 bytes.
+      } else if constexpr (EPI == Epilogue::kXentStats) {
+        // Linear cross entropy: each lane owns one row and walks its columns,
+        // 64 at a time, with the running maximum and the running sum of
+        // exponentials in FP32; columns past N take no part.
+        const int grow = row0 + lane;
+        if (row0 != xent_row0) {
+          xent_row0 = row0;
+          xent_target = grow < p.M ? p.target[grow] : -1;
+        }
+        float mx = -INFINITY, sum = 0.0f;
+#pragma unroll 1
+        for (int c = 0; c < Cfg::EPI_COLS / 64; ++c) {
+          const int col0 = nb * BN + col_base + c * 64;
+          uint32_t r0[32], r1[32];
+          const uint32_t taddr = tacc + uint32_t(c * 64);
+          ptx::tmem_ld_32x32b_x32(taddr, r0);
+          ptx::tmem_ld_32x32b_x32(taddr + 32, r1);
+          ptx::tmem_ld_wait_regs(r0);
+          ptx::tmem_ld_wait_regs(r1);
+          if (c == Cfg::EPI_COLS / 64 - 1) release_acc(acc);
+          if (!(rows_live && col0 < p.N)) continue;  // warp-uniform
+          const long long rel = xent_target - (p.col_offset + col0);
+          if (__any_sync(0xffffffffu, rel >= 0 && rel < 64)) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              if (rel == i) p.picked[grow] = __uint_as_float(r0[i]);
+              if (rel == 32 + i) p.picked[grow] = __uint_as_float(r1[i]);
+            }
+          }
+          if (col0 + 64 > p.N) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              if (col0 + i >= p.N) r0[i] = 0xFF800000u;  // -inf
+              if (col0 + 32 + i >= p.N) r1[i] = 0xFF800000u;
+            }
+          }
+          xent_fold(r0, r1, mx, sum);
+        }
+        if (rows_live && grow < p.M)
+          p.stats[(size_t(nb) * (Cfg::EPI_WARPS / 4) + (e >> 2)) * size_t(p.M) + grow] =
+              make_float2(mx, sum);
+      } else if constexpr (EPI == Epilogue::kStoreF32 || EPI == Epilogue::kAddF32) {
+        // FP32 outputs (split-K partials, accumulated gradients): 32-column
+        // boxes of 32 rows x 128 bytes.
 #pragma unroll 1
         for (int c = 0; c < Cfg::EPI_COLS / 32; ++c, ++chunk_ctr) {
           const int b = int(chunk_ctr % Cfg::EPI_BUFS);
@@ -1456,7 +1607,12 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
           ptx::fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
-            store_box(sbuf, col0, row0, l);
+            if constexpr (EPI == Epilogue::kAddF32) {
+              if (p.accumulate) ptx::tma_add_3d(&tmap_c, sbuf, col0, row0, l);
+              else ptx::tma_store_3d(&tmap_c, sbuf, col0, row0, l);
+            } else {
+              store_box(sbuf, col0, row0, l);
+            }
             ptx::bulk_commit_group();
           }
         }
@@ -1619,11 +1775,22 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
               break;
             }
           }
-          write_box_row<EPI>(smem + (sbuf - sbase) + lane * 128, lane, r0, r1, p.scale);
+          if constexpr (EPI == Epilogue::kXentGradBF16) {
+            xent_grad(r0, xent_lse, xent_scale, xent_rel - col0, p.N - col0);
+            xent_grad(r1, xent_lse, xent_scale, xent_rel - col0 - 32, p.N - col0 - 32);
+            write_box_row<Epilogue::kStoreBF16>(smem + (sbuf - sbase) + lane * 128, lane, r0, r1,
+                                                0.0f);
+          } else {
+            write_box_row<EPI>(smem + (sbuf - sbase) + lane * 128, lane, r0, r1, p.scale);
+          }
           ptx::fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
-            store_box(sbuf, col0, row0, l);
+            // the gradient tile is read back by the next launches: no evict-first hint
+            if constexpr (EPI == Epilogue::kXentGradBF16)
+              ptx::tma_store_3d(&tmap_c, sbuf, col0, row0, l);
+            else
+              store_box(sbuf, col0, row0, l);
             ptx::bulk_commit_group();
           }
         }
@@ -1647,6 +1814,9 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
   if (warp == 1) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc<CG>(tmem_base, Cfg::TMEM_COLS);
+  }
+  if constexpr (Cfg::CHAIN) {
+    if (p.late_wait) ptx::griddep_wait();
   }
 }
 

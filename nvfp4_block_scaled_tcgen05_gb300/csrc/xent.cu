@@ -1,0 +1,311 @@
+// Linear cross entropy of a language-model head: for X [M][K], W [V][K]
+//   z[m][v]  = sum_k X[m][k] W[v][k]                 (FP32, never stored)
+//   lse[m]   = log sum_v exp(z[m][v]),   loss[m] = lse[m] - z[m][target[m]]
+// and its gradient, with d[m] = dL/dloss[m]:
+//   G[m][v]  = d[m] (exp(z[m][v] - lse[m]) - [v = target[m]])
+//   dX = G . W,   dW = G^T . X.
+//
+// Forward: the NT GEMM with an epilogue that folds each 256-column tile of a
+// row into (maximum, sum of exponentials); a second kernel joins the tiles of
+// a row in order.  Per row and tile 8 bytes leave the chip instead of 512.
+//
+// Backward: pieces of the vocabulary.  Per piece one GEMM forms the logits
+// again and writes G as BF16 (the operand type of the products that follow:
+// one rounding of relative size 2^-9 per term), one adds G . W into FP32, one
+// computes the piece's rows of dW.  The grids of a piece are chained so that
+// one without a data dependency on its predecessor starts on the SMs the
+// predecessor's last round leaves idle (run_piece).
+#include <algorithm>
+
+#include "launch.cuh"
+
+namespace gb300 {
+
+using XentFwdPair = TileCfg<Operand::kBF16, 2, 256, 3, 4, 0, true, false, 2>;
+using XentFwdSingle = TileCfg<Operand::kBF16, 1, 256, 4, 4, 0>;
+template <int CG, int STAGES, int KSUB, bool BMN, bool AMN>
+using XentCfg =
+    TileCfg<Operand::kBF16, CG, 256, STAGES, 4, 2, true, false, KSUB, BMN, false, AMN, true>;
+using XentGradPair = XentCfg<2, 3, 2, false, false>;
+using XentGradSingle = XentCfg<1, 4, 1, false, false>;
+using XentDxPair = XentCfg<2, 3, 2, true, false>;
+using XentDxSingle = XentCfg<1, 4, 1, true, false>;
+using XentDwPair = XentCfg<2, 3, 2, true, true>;
+
+namespace {
+
+constexpr int kRowsSingle = 128;  // up to this many rows one CTA's 128-row tiles hold them all
+
+// Joins a row's tile statistics in tile order.  One warp per part group and
+// 32 rows per block: lane = row, so each load is one 256-byte line.
+constexpr int kJoinGroups = 16;
+__global__ void __launch_bounds__(32 * kJoinGroups)
+    xent_join_kernel(const float2* __restrict__ stats, const long long* __restrict__ target,
+                     float* __restrict__ loss, float* __restrict__ lse, int M, int V, int parts) {
+  __shared__ float2 part[kJoinGroups][32];
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
+  const int row = int(blockIdx.x) * 32 + lane;
+  const int per = (parts + kJoinGroups - 1) / kJoinGroups;
+  const int p1 = min(parts, (g + 1) * per);
+  float mx = -INFINITY, sum = 0.0f;
+  if (row < M) {
+#pragma unroll 8
+    for (int i = g * per; i < p1; ++i) {
+      const float2 s = __ldcg(stats + size_t(i) * M + row);
+      const float m = fmaxf(mx, s.x);
+      const float ref = (m == -INFINITY) ? 0.0f : m;
+      sum = sum * fast_exp(mx - ref) + s.y * fast_exp(s.x - ref);
+      mx = m;
+    }
+  }
+  part[g][lane] = make_float2(mx, sum);
+  __syncthreads();
+  if (g != 0 || row >= M) return;
+  for (int i = 1; i < kJoinGroups; ++i) {
+    const float2 s = part[i][lane];
+    const float m = fmaxf(mx, s.x);
+    const float ref = (m == -INFINITY) ? 0.0f : m;
+    sum = sum * fast_exp(mx - ref) + s.y * fast_exp(s.x - ref);
+    mx = m;
+  }
+  const float l = ((mx == -INFINITY) ? 0.0f : mx) + logf(sum);
+  lse[row] = l;
+  const long long t = target[row];
+  // loss[row] holds the target's logit, written by the tile that has it
+  loss[row] = t < 0 ? 0.0f : (t >= V ? NAN : l - loss[row]);
+}
+
+template <class Cfg>
+int encode_k_major(CUtensorMap* m, const void* base, int rows, int cols, int box_rows) {
+  return encode_tmap_3d(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, uint64_t(cols),
+                        uint64_t(rows), 1, 64, uint32_t(box_rows), CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+template <class Cfg>
+GemmParams base_params(int M, int N, int K, const DeviceInfo& dev) {
+  GemmParams p{};
+  p.M = M;
+  p.N = N;
+  p.K = K;
+  p.L = 1;
+  p.num_m_blocks = (M + Cfg::TILE_M - 1) / Cfg::TILE_M;
+  p.num_n_blocks = (N + Cfg::BN - 1) / Cfg::BN;
+  p.num_k_blocks = (K + Cfg::BK - 1) / Cfg::BK;
+  p.total_tiles = p.num_m_blocks * p.num_n_blocks;
+  p.group_m = raster_group_m(p.num_m_blocks, (long long)Cfg::TILE_M * K * 2);
+  p.k_splits = 1;
+  p.kb_per_split = p.num_k_blocks;
+  p.status = dev.status;
+  p.timeout_ns = wait_timeout_ns();
+  return p;
+}
+
+template <class Cfg>
+int run_forward(const XentForward& a, const DeviceInfo& dev, cudaStream_t stream) {
+  CUtensorMap tx, tw;
+  int rc = encode_k_major<Cfg>(&tx, a.X, a.M, a.K, Cfg::BM);
+  if (rc == GEMM_OK) rc = encode_k_major<Cfg>(&tw, a.W, a.V, a.K, Cfg::B_ROWS);
+  if (rc != GEMM_OK) return rc;
+  GemmParams p = base_params<Cfg>(a.M, a.V, a.K, dev);
+  p.target = a.target;
+  p.stats = static_cast<float2*>(a.workspace);
+  p.picked = a.loss;
+  p.col_total = a.V;
+  return launch_tcgen05<Cfg, Epilogue::kXentStats>(tx, tw, tx, tx, tx, p, dev, stream);
+}
+
+// How the backward pass is divided.
+struct XentPlan {
+  int piece;      // vocabulary columns per piece
+  int pieces;
+  int splits;     // FP32 slots that dX is summed in (split K of its GEMM)
+  size_t g_bytes; // one piece's G
+  int g_bufs;
+  size_t dx_bytes;
+};
+
+constexpr int kPairs = 76;  // CTA pairs of a GB300
+constexpr long long kPieceBytes = 128ll << 20;
+constexpr int kMinPiece = 4096;
+
+XentPlan make_plan(int M, int V, int K) {
+  XentPlan q{};
+  const int mb = (M + 255) / 256, vb = (V + 255) / 256;
+  long long cols = kPieceBytes / (2ll * M);
+  if (cols < kMinPiece) cols = kMinPiece;
+  int nb = int(std::min<long long>(vb, cols / 256));
+  if (nb < vb) {
+    // equal pieces, then a block count whose tiles fill whole rounds of CTA pairs
+    const int pieces = (vb + nb - 1) / nb;
+    const int even = (vb + pieces - 1) / pieces;
+    int best = nb;
+    double best_cost = 1e300;
+    for (int c = std::max(1, even - even / 8); c <= nb; ++c) {
+      const long long n = (vb + c - 1) / c;
+      const long long last = vb - (n - 1) * c;
+      const double rounds = double(n - 1) * double(((long long)mb * c + kPairs - 1) / kPairs) +
+                            double(((long long)mb * last + kPairs - 1) / kPairs);
+      if (rounds + 0.2 * double(n) < best_cost) {
+        best_cost = rounds + 0.2 * double(n);
+        best = c;
+      }
+    }
+    nb = best;
+  }
+  q.piece = int(std::min<long long>(V, (long long)nb * 256));
+  q.pieces = (V + q.piece - 1) / q.piece;
+  q.g_bytes = size_t(M) * size_t((q.piece + 63) / 64 * 64) * 2;
+  q.g_bytes = (q.g_bytes + 255) / 256 * 256;
+  q.g_bufs = q.pieces > 1 ? 2 : 1;
+  // dX has (M / rows) x (K / 256) tiles; with fewer than the SM groups its K
+  // loop (the vocabulary) is divided and the parts are summed in order
+  const bool single = M <= kRowsSingle;
+  const int units = single ? 2 * kPairs : kPairs;
+  const int tiles = (single ? 1 : mb) * ((K + 255) / 256);
+  const int bk = single ? XentDxSingle::BK : XentDxPair::BK;
+  const int nkb = (q.piece + bk - 1) / bk;
+  int s = tiles >= units ? 1 : units / tiles;
+  s = std::max(1, std::min(s, nkb / 4));
+  const int per = (nkb + s - 1) / s;
+  q.splits = (nkb + per - 1) / per;
+  q.dx_bytes = (q.pieces == 1 && q.splits == 1) ? 0 : size_t(q.splits) * M * size_t(K) * 4;
+  return q;
+}
+
+// G of one piece.
+template <class Cfg>
+int run_grad(const XentBackward& a, void* G, int v0, int vc, bool late, const DeviceInfo& dev,
+             cudaStream_t stream) {
+  CUtensorMap tx, tw, tg;
+  const uint16_t* W = static_cast<const uint16_t*>(a.W) + size_t(v0) * a.K;
+  const int ldg = (vc + 63) / 64 * 64;
+  int rc = encode_k_major<Cfg>(&tx, a.X, a.M, a.K, Cfg::BM);
+  if (rc == GEMM_OK) rc = encode_k_major<Cfg>(&tw, W, vc, a.K, Cfg::B_ROWS);
+  if (rc == GEMM_OK) rc = encode_k_major<Cfg>(&tg, G, a.M, ldg, 32);
+  if (rc != GEMM_OK) return rc;
+  GemmParams p = base_params<Cfg>(a.M, vc, a.K, dev);
+  p.target = a.target;
+  p.row_lse = a.lse;
+  p.row_scale = a.dloss;
+  p.col_offset = v0;
+  p.col_total = a.V;
+  p.late_wait = late;
+  return launch_tcgen05<Cfg, Epilogue::kXentGradBF16>(tx, tw, tg, tx, tx, p, dev, stream);
+}
+
+// One piece's term of dX: G [M][vc] . W_piece [vc][K].
+template <class Cfg>
+int run_dx(const XentBackward& a, const XentPlan& q, const void* G, float* acc, int v0, int vc,
+           const DeviceInfo& dev, cudaStream_t stream) {
+  CUtensorMap tg, tw, tc;
+  const uint16_t* W = static_cast<const uint16_t*>(a.W) + size_t(v0) * a.K;
+  const int ldg = (vc + 63) / 64 * 64;
+  int rc = encode_k_major<Cfg>(&tg, G, a.M, ldg, Cfg::BM);
+  if (rc == GEMM_OK) rc = encode_k_major<Cfg>(&tw, W, vc, a.K, Cfg::BK);
+  if (rc != GEMM_OK) return rc;
+  GemmParams p = base_params<Cfg>(a.M, a.K, vc, dev);
+  p.trigger_late = 1;
+  if (q.dx_bytes == 0) {
+    rc = encode_k_major<Cfg>(&tc, a.dX, a.M, a.K, 32);
+    if (rc != GEMM_OK) return rc;
+    return launch_tcgen05<Cfg, Epilogue::kStoreBF16>(tg, tw, tc, tg, tg, p, dev, stream);
+  }
+  rc = encode_tmap_3d(&tc, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, acc, uint64_t(a.K), uint64_t(a.M),
+                      uint64_t(q.splits), 32, 32, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (rc != GEMM_OK) return rc;
+  // every part holds at least one K block: a shorter last piece may use fewer
+  // slots than the first, whose plain store fills them all
+  const int s = std::min(q.splits, p.num_k_blocks);
+  p.kb_per_split = (p.num_k_blocks + s - 1) / s;
+  p.k_splits = (p.num_k_blocks + p.kb_per_split - 1) / p.kb_per_split;
+  p.L = p.k_splits;
+  p.total_tiles *= p.k_splits;
+  p.accumulate = v0 > 0;
+  return launch_tcgen05<Cfg, Epilogue::kAddF32>(tg, tw, tc, tg, tg, p, dev, stream);
+}
+
+// The piece's rows of dW: G^T [vc][M] . X [M][K].
+int run_dw(const XentBackward& a, const void* G, int v0, int vc, bool after_dx,
+           const DeviceInfo& dev, cudaStream_t stream) {
+  using Cfg = XentDwPair;
+  CUtensorMap tg, tx, tc;
+  uint16_t* dW = static_cast<uint16_t*>(a.dW) + size_t(v0) * a.K;
+  const int ldg = (vc + 63) / 64 * 64;
+  int rc = encode_k_major<Cfg>(&tg, G, a.M, ldg, Cfg::BK);
+  if (rc == GEMM_OK) rc = encode_k_major<Cfg>(&tx, a.X, a.M, a.K, Cfg::BK);
+  if (rc == GEMM_OK) rc = encode_k_major<Cfg>(&tc, dW, vc, a.K, 32);
+  if (rc != GEMM_OK) return rc;
+  GemmParams p = base_params<Cfg>(vc, a.K, a.M, dev);
+  p.late_wait = after_dx;
+  p.trigger_late = !after_dx;
+  return launch_tcgen05<Cfg, Epilogue::kStoreBF16>(tg, tx, tc, tg, tg, p, dev, stream);
+}
+
+}  // namespace
+
+size_t xent_forward_workspace(int M, int V) {
+  return size_t(M) * size_t((V + 255) / 256) * sizeof(float2);
+}
+
+size_t xent_backward_workspace(int M, int V, int K) {
+  const XentPlan q = make_plan(M, V, K);
+  return q.g_bytes * q.g_bufs + q.dx_bytes;
+}
+
+int launch_xent_forward(const XentForward& a, const DeviceInfo& dev, cudaStream_t stream) {
+  const int rc = a.M > kRowsSingle ? run_forward<XentFwdPair>(a, dev, stream)
+                                   : run_forward<XentFwdSingle>(a, dev, stream);
+  if (rc != GEMM_OK) return rc;
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3((a.M + 31) / 32);
+  cfg.blockDim = dim3(32 * kJoinGroups);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, xent_join_kernel, static_cast<const float2*>(a.workspace), a.target,
+                         a.loss, a.lse, a.M, a.V, (a.V + 255) / 256) != cudaSuccess) {
+    cudaGetLastError();
+    return GEMM_ERR_LAUNCH;
+  }
+  return GEMM_OK;
+}
+
+// Order of the grids, and why each may start when it does ("waits" = its
+// programmatic wait for the end of the previous grid comes first):
+//   G_0 waits: everything before the call is complete from here on.
+//   The first product of piece i (dX, or dW if there is no dX) waits: G_i is
+//     complete, and with it, through the late waits below, all of piece i-1.
+//     It lets the next grid start only once it has waited.
+//   dW_i after dX_i reads G_i, complete when it starts, and waits at its end.
+//   G_{i+1} writes the other G buffer, whose readers (piece i-1) are complete
+//     when a product of piece i has started, and waits at its end.
+// A grid that ends after its predecessor keeps the chain: whoever waits for it
+// also has everything before it.
+int launch_xent_backward(const XentBackward& a, const DeviceInfo& dev, cudaStream_t stream) {
+  const XentPlan q = make_plan(a.M, a.V, a.K);
+  const bool single = a.M <= kRowsSingle;
+  uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+  float* acc = reinterpret_cast<float*>(ws + q.g_bytes * q.g_bufs);
+  for (int i = 0; i < q.pieces; ++i) {
+    const int v0 = i * q.piece;
+    const int vc = std::min(q.piece, a.V - v0);
+    void* G = ws + q.g_bytes * (i & (q.g_bufs - 1));
+    int rc = single ? run_grad<XentGradSingle>(a, G, v0, vc, i > 0, dev, stream)
+                    : run_grad<XentGradPair>(a, G, v0, vc, i > 0, dev, stream);
+    if (rc == GEMM_OK && a.dX)
+      rc = single ? run_dx<XentDxSingle>(a, q, G, acc, v0, vc, dev, stream)
+                  : run_dx<XentDxPair>(a, q, G, acc, v0, vc, dev, stream);
+    if (rc == GEMM_OK && a.dW) rc = run_dw(a, G, v0, vc, a.dX != nullptr, dev, stream);
+    if (rc != GEMM_OK) return rc;
+  }
+  if (a.dX && q.dx_bytes)
+    return launch_splitk_reduce(acc, a.dX, size_t(a.M) * a.K, q.splits, dev, stream);
+  return GEMM_OK;
+}
+
+}  // namespace gb300
