@@ -382,57 +382,86 @@ def gemm_nvfp4_bs_splitk(a: torch.Tensor, b: torch.Tensor, sfa: torch.Tensor, sf
     return c
 
 
-def _on_device(name: str, like: torch.Tensor, t: torch.Tensor, dtype, shape) -> None:
+def _on_device(name: str, device, t: torch.Tensor, dtype, shape) -> None:
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and
+            t.device == device and t.is_contiguous()):
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != like.device:
-        raise ValueError(f"{name} must be on {like.device}, got {t.device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _allocator(device, stream):
-    """torch.empty whose memory belongs to the stream the call runs on, so that
-    the caching allocator does not hand it out again before the call is done."""
-    if stream is None:
-        return lambda shape, dtype: torch.empty(shape, dtype=dtype, device=device)
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(_stream_ptr(stream), device=device)
+class _Call:
+    """Device and stream of one call on tensors of `device`: allocates outputs
+    and workspaces on the call's stream, so that the caching allocator does not
+    hand their memory out again before the call is done, and makes the device
+    current while the library runs."""
+    __slots__ = ("device", "stream", "pointer")
 
-    def empty(shape, dtype):
-        with torch.cuda.stream(stream):
-            return torch.empty(shape, dtype=dtype, device=device)
-    return empty
+    def __init__(self, device, stream):
+        self.device = device
+        self.stream = stream
+        if stream is None:
+            self.pointer = torch._C._cuda_getCurrentRawStream(device.index)
+        else:
+            self.pointer = _stream_ptr(stream)
+            if not isinstance(stream, torch.cuda.Stream):
+                self.stream = torch.cuda.ExternalStream(self.pointer, device=device)
+
+    def empty(self, shape, dtype):
+        if self.stream is None:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        with torch.cuda.stream(self.stream):
+            return torch.empty(shape, dtype=dtype, device=self.device)
+
+    def workspace(self, given, need: int):
+        """The caller's workspace, or one allocated here (None where none is needed)."""
+        if given is None:
+            return self.empty((need,), torch.uint8) if need else None
+        if not (given.device == self.device and given.is_contiguous()):
+            raise ValueError(f"workspace must be a contiguous tensor on {self.device}")
+        return given
+
+    def run(self, name: str, *args) -> None:
+        fn = getattr(_lib or load(), name)
+        if torch.cuda.current_device() == self.device.index:
+            rc = fn(*args, self.pointer)
+        else:
+            with torch.cuda.device(self.device):
+                rc = fn(*args, self.pointer)
+        if rc:
+            raise GemmError(rc, name)
 
 
-def _workspace(workspace, need: int, like: torch.Tensor, empty):
-    """(pointer, bytes) of the caller's workspace, or of one allocated here; the
-    third value keeps it alive."""
-    if workspace is None:
-        workspace = empty(max(need, 16), torch.uint8)
-    if not (workspace.device == like.device and workspace.is_contiguous()):
-        raise ValueError(f"workspace must be a contiguous tensor on {like.device}")
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+def _bytes_of(t) -> int:
+    return 0 if t is None else t.numel() * t.element_size()
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
 
 
 def _xent_inputs(X, W, target):
     _mat(X, torch.bfloat16, "X")
     _mat(W, torch.bfloat16, "W")
-    if X.shape[1] != W.shape[1]:
+    M, K = X.shape
+    V, K2 = W.shape
+    if K != K2:
         raise ValueError(f"K mismatch: X {tuple(X.shape)} vs W {tuple(W.shape)}")
     if W.device != X.device:
         raise ValueError("X and W must be on one device")
-    M, K = X.shape
-    _on_device("target", X, target, torch.int64, (M,))
-    return M, W.shape[0], K
+    _on_device("target", X.device, target, torch.int64, (M,))
+    return M, V, K
 
 
 def gemm_bf16_nt_xent_workspace_bytes(M: int, V: int) -> int:
-    return int(load().gemm_bf16_nt_xent_workspace_bytes(M, V))
+    return int((_lib or load()).gemm_bf16_nt_xent_workspace_bytes(M, V))
 
 
 def gemm_bf16_nt_xent(X: torch.Tensor, W: torch.Tensor, target: torch.Tensor,
@@ -444,21 +473,23 @@ def gemm_bf16_nt_xent(X: torch.Tensor, W: torch.Tensor, target: torch.Tensor,
     loss.  Keep lse for gemm_bf16_nt_xent_backward.
     """
     M, V, K = _xent_inputs(X, W, target)
-    empty = _allocator(X.device, stream)
-    loss = empty((M,), torch.float32) if loss is None else loss
-    lse = empty((M,), torch.float32) if lse is None else lse
-    _on_device("loss", X, loss, torch.float32, (M,))
-    _on_device("lse", X, lse, torch.float32, (M,))
-    ws, nbytes, _keep = _workspace(workspace, gemm_bf16_nt_xent_workspace_bytes(M, V), X, empty)
-    with torch.cuda.device(X.device):
-        _check(load().gemm_bf16_nt_xent(X.data_ptr(), W.data_ptr(), target.data_ptr(),
-                                        loss.data_ptr(), lse.data_ptr(), ws, nbytes, M, V, K,
-                                        _stream_ptr(stream)), "gemm_bf16_nt_xent")
+    call = _Call(X.device, stream)
+    if loss is None:
+        loss = call.empty((M,), torch.float32)
+    else:
+        _on_device("loss", X.device, loss, torch.float32, (M,))
+    if lse is None:
+        lse = call.empty((M,), torch.float32)
+    else:
+        _on_device("lse", X.device, lse, torch.float32, (M,))
+    workspace = call.workspace(workspace, gemm_bf16_nt_xent_workspace_bytes(M, V))
+    call.run("gemm_bf16_nt_xent", X.data_ptr(), W.data_ptr(), target.data_ptr(), loss.data_ptr(),
+             lse.data_ptr(), _ptr(workspace), _bytes_of(workspace), M, V, K)
     return loss, lse
 
 
 def gemm_bf16_nt_xent_backward_workspace_bytes(M: int, V: int, K: int) -> int:
-    return int(load().gemm_bf16_nt_xent_backward_workspace_bytes(M, V, K))
+    return int((_lib or load()).gemm_bf16_nt_xent_backward_workspace_bytes(M, V, K))
 
 
 def gemm_bf16_nt_xent_backward(X: torch.Tensor, W: torch.Tensor, target: torch.Tensor,
@@ -471,25 +502,24 @@ def gemm_bf16_nt_xent_backward(X: torch.Tensor, W: torch.Tensor, target: torch.T
     lse: the forward call's; dloss float32 [M]: the rows' loss gradients.
     """
     M, V, K = _xent_inputs(X, W, target)
-    _on_device("lse", X, lse, torch.float32, (M,))
-    _on_device("dloss", X, dloss, torch.float32, (M,))
-    need_dx, need_dw = need_dx or dX is not None, need_dw or dW is not None
-    if not (need_dx or need_dw):
+    device = X.device
+    _on_device("lse", device, lse, torch.float32, (M,))
+    _on_device("dloss", device, dloss, torch.float32, (M,))
+    if not (need_dx or need_dw or dX is not None or dW is not None):
         raise ValueError("neither dX nor dW is needed")
-    empty = _allocator(X.device, stream)
-    if need_dx:
-        dX = empty((M, K), torch.bfloat16) if dX is None else dX
-        _on_device("dX", X, dX, torch.bfloat16, (M, K))
-    if need_dw:
-        dW = empty((V, K), torch.bfloat16) if dW is None else dW
-        _on_device("dW", X, dW, torch.bfloat16, (V, K))
-    ws, nbytes, _keep = _workspace(workspace, gemm_bf16_nt_xent_backward_workspace_bytes(M, V, K),
-                                   X, empty)
-    with torch.cuda.device(X.device):
-        _check(load().gemm_bf16_nt_xent_backward(
-            X.data_ptr(), W.data_ptr(), target.data_ptr(), lse.data_ptr(), dloss.data_ptr(),
-            dX.data_ptr() if need_dx else None, dW.data_ptr() if need_dw else None, ws, nbytes,
-            M, V, K, _stream_ptr(stream)), "gemm_bf16_nt_xent_backward")
+    call = _Call(device, stream)
+    if dX is not None:
+        _on_device("dX", device, dX, torch.bfloat16, (M, K))
+    elif need_dx:
+        dX = call.empty((M, K), torch.bfloat16)
+    if dW is not None:
+        _on_device("dW", device, dW, torch.bfloat16, (V, K))
+    elif need_dw:
+        dW = call.empty((V, K), torch.bfloat16)
+    workspace = call.workspace(workspace, gemm_bf16_nt_xent_backward_workspace_bytes(M, V, K))
+    call.run("gemm_bf16_nt_xent_backward", X.data_ptr(), W.data_ptr(), target.data_ptr(),
+             lse.data_ptr(), dloss.data_ptr(), _ptr(dX), _ptr(dW), _ptr(workspace),
+             _bytes_of(workspace), M, V, K)
     return dX, dW
 
 
@@ -514,16 +544,18 @@ def _logit_rows(logits):
     if not logits.is_cuda:
         raise ValueError("logits must be a CUDA tensor")
     M, E = logits.shape
-    if E > 1 and logits.stride(1) != 1:
+    ld, inner = logits.stride()
+    if E > 1 and inner != 1:
         raise ValueError("logits must have unit stride within a row")
-    ld = logits.stride(0) if M > 1 else E
+    if M <= 1:
+        ld = E
     if ld < E:
         raise ValueError("rows of logits overlap")
     return M, E, ld
 
 
 def router_topk_workspace_bytes(M: int, E: int) -> int:
-    return int(load().router_topk_workspace_bytes(M, E))
+    return int((_lib or load()).router_topk_workspace_bytes(M, E))
 
 
 def router_topk(logits: torch.Tensor, k: int, valid: torch.Tensor | None = None,
@@ -537,19 +569,18 @@ def router_topk(logits: torch.Tensor, k: int, valid: torch.Tensor | None = None,
     M, E, ld = _logit_rows(logits)
     if valid is not None:
         valid = valid.view(torch.uint8) if valid.dtype == torch.bool else valid
-        _on_device("valid", logits, valid, torch.uint8, (M,))
+        _on_device("valid", logits.device, valid, torch.uint8, (M,))
     if not 1 <= k <= E:
         raise ValueError(f"k must be in 1..{E}, got {k}")
-    empty = _allocator(logits.device, stream)
-    f32, i32 = torch.float32, torch.int32
-    out = RouterTopk(empty((M, k), f32), empty((M, k), i32), empty((M,), f32), empty((E + 1,), i32),
-                     empty((E,), f32), empty((2,), f32))
-    ws, nbytes, _keep = _workspace(workspace, router_topk_workspace_bytes(M, E), logits, empty)
-    with torch.cuda.device(logits.device):
-        _check(load().router_topk(logits.data_ptr(), None if valid is None else valid.data_ptr(),
-                                  *(t.data_ptr() for t in out), ws, nbytes, M, E, ld, int(k),
-                                  int(bool(normalize)), _stream_ptr(stream)), "router_topk")
-    return out
+    call = _Call(logits.device, stream)
+    empty, f32, i32 = call.empty, torch.float32, torch.int32
+    weights, experts, lse = empty((M, k), f32), empty((M, k), i32), empty((M,), f32)
+    counts, probs, losses = empty((E + 1,), i32), empty((E,), f32), empty((2,), f32)
+    workspace = call.workspace(workspace, router_topk_workspace_bytes(M, E))
+    call.run("router_topk", logits.data_ptr(), _ptr(valid), weights.data_ptr(), experts.data_ptr(),
+             lse.data_ptr(), counts.data_ptr(), probs.data_ptr(), losses.data_ptr(),
+             _ptr(workspace), _bytes_of(workspace), M, E, ld, k, 1 if normalize else 0)
+    return RouterTopk(weights, experts, lse, counts, probs, losses)
 
 
 def router_topk_backward(logits: torch.Tensor, experts: torch.Tensor, lse: torch.Tensor,
@@ -563,30 +594,29 @@ def router_topk_backward(logits: torch.Tensor, experts: torch.Tensor, lse: torch
     gradient that goes into a BF16 product.
     """
     M, E, ld = _logit_rows(logits)
+    device = logits.device
     if experts.dim() != 2:
         raise ValueError("experts must be [M, k]")
     k = experts.shape[1]
-    _on_device("experts", logits, experts, torch.int32, (M, k))
-    _on_device("lse", logits, lse, torch.float32, (M,))
-    _on_device("counts", logits, counts, torch.int32, (E + 1,))
+    _on_device("experts", device, experts, torch.int32, (M, k))
+    _on_device("lse", device, lse, torch.float32, (M,))
+    _on_device("counts", device, counts, torch.int32, (E + 1,))
     if dweights is not None:
-        _on_device("dweights", logits, dweights, torch.float32, (M, k))
+        _on_device("dweights", device, dweights, torch.float32, (M, k))
     if dlosses is not None:
-        _on_device("dlosses", logits, dlosses, torch.float32, (2,))
+        _on_device("dlosses", device, dlosses, torch.float32, (2,))
     if dlogits is not None:
         dtype = dlogits.dtype
     if dtype not in (torch.float32, torch.bfloat16):
         raise TypeError(f"dlogits must be float32 or bfloat16, got {dtype}")
+    call = _Call(device, stream)
     if dlogits is None:
-        dlogits = _allocator(logits.device, stream)((M, E), dtype)
-    _on_device("dlogits", logits, dlogits, dtype, (M, E))
-    with torch.cuda.device(logits.device):
-        _check(load().router_topk_backward(
-            logits.data_ptr(), experts.data_ptr(), lse.data_ptr(), counts.data_ptr(),
-            None if dweights is None else dweights.data_ptr(),
-            None if dlosses is None else dlosses.data_ptr(), dlogits.data_ptr(),
-            int(dtype == torch.bfloat16), M, E, ld, k, int(bool(normalize)),
-            _stream_ptr(stream)), "router_topk_backward")
+        dlogits = call.empty((M, E), dtype)
+    else:
+        _on_device("dlogits", device, dlogits, dtype, (M, E))
+    call.run("router_topk_backward", logits.data_ptr(), experts.data_ptr(), lse.data_ptr(),
+             counts.data_ptr(), _ptr(dweights), _ptr(dlosses), dlogits.data_ptr(),
+             1 if dtype == torch.bfloat16 else 0, M, E, ld, k, 1 if normalize else 0)
     return dlogits
 
 

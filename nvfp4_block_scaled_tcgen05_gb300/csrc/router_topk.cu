@@ -13,8 +13,10 @@
 // A row takes part if it is valid and has a logit above -inf.  A NaN logit
 // ranks first and makes the row's results NaN.
 //
-// Both kernels read the logits once: one warp per row, the row in registers
-// (element e of a row in lane e % 32), sums and statistics in FP32.
+// Both kernels read the logits once: one warp per row, the row in registers,
+// sums and statistics in FP32.  Each warp keeps the column sums of its rows
+// in registers; blocks add their warps' sums and a second, small grid adds
+// the blocks', both in a fixed order.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -25,12 +27,20 @@
 namespace gb300 {
 namespace {
 
-constexpr int kWarps = 8;            // rows in flight per block
-constexpr int kMaxBlocks = 304;      // two blocks per SM; bounds the partial sums
-constexpr int kFinishThreads = 1024;
+constexpr int kWarps = 16;            // forward: rows in flight per block
+constexpr int kMaxBlocks = 304;       // forward: two blocks per SM; bounds the partial sums
+constexpr int kFinishCtas = 8;        // the cluster that adds the blocks' sums
+constexpr int kFinishGroups = 16;
+constexpr int kFinishThreads = 32 * (kFinishGroups + 1);
+constexpr int kGradWarps = 8;         // backward: rows in flight per block
+constexpr int kGradMaxBlocks = 608;   // four blocks per SM
+constexpr int kOneBlockRows = 2 * kWarps;  // up to this many rows need no second grid
 
 // Partial sums of one block: probabilities [E], z, then the counts [E], T.
-__host__ __device__ constexpr size_t partial_words(int E) { return 2 * size_t(E) + 2; }
+__host__ __device__ constexpr int partial_words(int E) { return 2 * E + 2; }
+
+// e^y, relative error below 2^-21 + 2^-23 |y|
+__device__ __forceinline__ float fast_exp(float y) { return ptx::ex2(y * 1.4426950408889634f); }
 
 // Order-preserving key of a logit: larger key = ranks earlier.  -0 = +0, NaN
 // first; keys up to kNoKey (-inf) are never chosen.
@@ -52,6 +62,31 @@ __device__ __forceinline__ float warp_max(float v) {
   return v;
 }
 
+// Value i of lane `lane` is column column_of(i, lane): groups of four
+// consecutive columns, read and written 16 bytes at a time where kAligned says
+// that rows start on 16 bytes and E % 4 == 0, value by value (through L1)
+// otherwise.  The same columns either way, so results do not depend on it.
+__device__ __forceinline__ int column_of(int i, int lane) {
+  return ((i / 4) * 32 + lane) * 4 + i % 4;
+}
+
+// The lane's NV values of one row; -inf past column E.
+template <int NV, bool kAligned>
+__device__ __forceinline__ void load_row(const float* src, int E, int lane, float (&v)[NV]) {
+#pragma unroll
+  for (int i = 0; i < NV; i += 4) {
+    const int e = column_of(i, lane);
+    if constexpr (kAligned) {
+      float4 q = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+      if (e < E) q = __ldcg(reinterpret_cast<const float4*>(src + e));
+      v[i] = q.x, v[i + 1] = q.y, v[i + 2] = q.z, v[i + 3] = q.w;
+    } else {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) v[i + c] = e + c < E ? src[e + c] : -INFINITY;
+    }
+  }
+}
+
 struct RouteArgs {
   const float* logits;
   const unsigned char* valid;
@@ -65,40 +100,28 @@ struct RouteArgs {
   int M, E, ld, k, normalize;
 };
 
-// balance, z, P and counts from the sums over all rows.  Called by one whole
-// block; prob(e), hits(e) give column e's sums.
-template <class Prob, class Hits>
-__device__ void finish(const RouteArgs& a, float z_sum, int T, Prob prob, Hits hits) {
-  __shared__ float red[32];
-  const float t = float(T > 1 ? T : 1);
-  float dot = 0.0f;
-  for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
-    const float P = prob(e) / t;
-    const int c = hits(e);
-    a.probs[e] = P;
-    a.counts[e] = c;
-    dot += float(c) / (float(a.k) * t) * P;
-  }
-  dot = warp_sum(dot);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = dot;
+__device__ __forceinline__ float at_least_one(int T) { return float(T > 1 ? T : 1); }
+
+// Sum over the block's threads, valid in thread 0; `red` holds one float per warp.
+__device__ __forceinline__ float block_sum(float v, float* red) {
+  v = warp_sum(v);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
   __syncthreads();
-  if (threadIdx.x == 0) {
-    float s = 0.0f;
+  float s = 0.0f;
+  if (threadIdx.x == 0)
     for (int w = 0; w < int(blockDim.x >> 5); ++w) s += red[w];
-    a.losses[0] = float(a.E) * s;
-    a.losses[1] = z_sum / t;
-    a.counts[a.E] = T;
-  }
+  return s;
 }
 
 // NV: values per lane (E <= 32 NV)
-template <int NV>
-__global__ void __launch_bounds__(32 * kWarps) route_kernel(const RouteArgs a) {
+template <int NV, bool kAligned>
+__global__ void __launch_bounds__(32 * kWarps, NV <= 8 ? 2 : 1) route_kernel(const RouteArgs a) {
   extern __shared__ uint32_t sh[];
-  float* sh_prob = reinterpret_cast<float*>(sh);            // [kWarps][E]
-  int* sh_hits = reinterpret_cast<int*>(sh + kWarps * a.E); // [E]
-  __shared__ float sh_z[kWarps];
+  float* sh_prob = reinterpret_cast<float*>(sh);             // [kWarps][E]
+  int* sh_hits = reinterpret_cast<int*>(sh + kWarps * a.E);  // [E]
+  __shared__ float sh_z[kWarps], red[kWarps];
   __shared__ int sh_t[kWarps];
+  __shared__ unsigned long long sh_cand[kWarps][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   for (int e = threadIdx.x; e < a.E; e += blockDim.x) sh_hits[e] = 0;
   __syncthreads();
@@ -107,26 +130,23 @@ __global__ void __launch_bounds__(32 * kWarps) route_kernel(const RouteArgs a) {
 
   float acc[NV];
 #pragma unroll
-  for (int j = 0; j < NV; ++j) acc[j] = 0.0f;
+  for (int i = 0; i < NV; ++i) acc[i] = 0.0f;
   float z = 0.0f;
   int t = 0;
-  for (long long row = (long long)blockIdx.x * kWarps + warp; row < a.M;
-       row += (long long)gridDim.x * kWarps) {
-    const float* src = a.logits + row * a.ld;
-    const bool valid = !a.valid || a.valid[row] != 0;
+  unsigned long long* cand = sh_cand[warp];
+  const long long step = (long long)gridDim.x * kWarps;
+  for (long long row = (long long)blockIdx.x * kWarps + warp; row < a.M; row += step) {
+    const bool valid = !a.valid || __ldcg(a.valid + row) != 0;
     float v[NV];
-    float mx = -INFINITY;
+    load_row<NV, kAligned>(a.logits + row * a.ld, a.E, lane, v);
+    float lane_max = -INFINITY;
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int e = j * 32 + lane;
-      v[j] = e < a.E ? __ldcg(src + e) : -INFINITY;
-      mx = fmaxf(mx, v[j]);
-    }
-    mx = warp_max(mx);
+    for (int i = 0; i < NV; ++i) lane_max = fmaxf(lane_max, v[i]);
+    const float mx = warp_max(lane_max);
     const float ref = mx == -INFINITY ? 0.0f : mx;
     float s = 0.0f, p[NV];
 #pragma unroll
-    for (int j = 0; j < NV; ++j) s += p[j] = expf(v[j] - ref);
+    for (int i = 0; i < NV; ++i) s += p[i] = fast_exp(v[i] - ref);
     s = warp_sum(s);
     const float inv = 1.0f / s;
     const float l = ref + logf(s);
@@ -137,50 +157,106 @@ __global__ void __launch_bounds__(32 * kWarps) route_kernel(const RouteArgs a) {
       z += l * l;
       ++t;
 #pragma unroll
-      for (int j = 0; j < NV; ++j) acc[j] += p[j] * inv;
+      for (int i = 0; i < NV; ++i) acc[i] += p[i] * inv;
     }
-    uint32_t key[NV];
+
+    // Choice.  The k-th largest of the lanes' maxima bounds the k-th largest
+    // value from below, so only values that reach it are candidates: usually
+    // little more than k, which rank themselves against each other.
+    int my_expert = -1, my_rank = lane;
+    float my_weight = 0.0f;
+    bool slow = live && s != s;  // NaN somewhere
+    if (live && !slow) {
+      uint32_t cur = rank_key(lane_max), floor_key = 0u;
+      int n = 0;
+      for (int r = 0; r < a.k && n < a.k; ++r) {
+        floor_key = __reduce_max_sync(0xffffffffu, cur);
+        n += __popc(__ballot_sync(0xffffffffu, cur == floor_key));
+        if (cur == floor_key) cur = 0u;
+      }
+      // fewer than k lanes with a value: every value above -inf is a candidate
+      float bound = -INFINITY;
+      if (n >= a.k && floor_key > kNoKey)
+        bound = __uint_as_float((floor_key & 0x80000000u) ? floor_key & 0x7FFFFFFFu : ~floor_key);
+      n = 0;
+      const uint32_t below = (1u << lane) - 1u;
 #pragma unroll
-    for (int j = 0; j < NV; ++j) key[j] = live ? rank_key(v[j]) : 0u;
-    // k rounds of: the largest key of the warp, lowest index among equals
-    int my_expert = -1;
-    float my_weight = 0.0f, total = 0.0f;
-    for (int r = 0; r < a.k; ++r) {
-      uint32_t best = 0u;
-      int at = 0;
-#pragma unroll
-      for (int j = 0; j < NV; ++j)
-        if (key[j] > best) {
-          best = key[j];
-          at = j * 32 + lane;
+      for (int i = 0; i < NV; ++i) {
+        const bool c = v[i] >= bound && v[i] != -INFINITY;
+        const uint32_t who = __ballot_sync(0xffffffffu, c);
+        const int at = n + __popc(who & below);
+        if (c && at < 32)
+          cand[at] = (static_cast<unsigned long long>(rank_key(v[i])) << 32) |
+                     (0xFFFFFFFFu - uint32_t(column_of(i, lane)));
+        n += __popc(who);
+      }
+      slow = n > 32;
+      if (!slow) {
+        __syncwarp();
+        const unsigned long long mine = lane < n ? cand[lane] : 0ull;
+        int rank = 0;
+    #pragma unroll 4
+        for (int j = 0; j < n; ++j) rank += cand[j] > mine;
+        __syncwarp();
+        if (lane < n) {
+          if (rank < a.k) {
+            const uint32_t key = uint32_t(mine >> 32);
+            const float x = __uint_as_float((key & 0x80000000u) ? key & 0x7FFFFFFFu : ~key);
+            my_expert = int(0xFFFFFFFFu - uint32_t(mine));
+            my_weight = fast_exp(x - ref) * inv;
+          }
+          my_rank = rank;
         }
-      const uint32_t top = __reduce_max_sync(0xffffffffu, best);
-      if (top <= kNoKey) break;
-      const int win = __reduce_min_sync(0xffffffffu, best == top ? at : 0x7FFFFFFF);
-      float w = 0.0f;
-#pragma unroll
-      for (int j = 0; j < NV; ++j)
-        if (j * 32 + lane == win) {
-          key[j] = 0u;
-          w = p[j] * inv;
-        }
-      w = __shfl_sync(0xffffffffu, w, win & 31);
-      total += w;
-      if (lane == r) {
-        my_expert = win;
-        my_weight = w;
       }
     }
-    if (a.normalize && my_expert >= 0) my_weight = my_weight / total;
-    if (lane < a.k) {
-      a.weights[row * a.k + lane] = my_weight;
-      a.experts[row * a.k + lane] = my_expert;
+    if (slow) {  // NaN, or more than 32 candidates (ties): k rounds of the largest key
+      uint32_t key[NV];
+#pragma unroll
+      for (int i = 0; i < NV; ++i) key[i] = rank_key(v[i]);
+      my_rank = lane;
+      for (int r = 0; r < a.k; ++r) {
+        uint32_t best = 0u;
+        int at = 0x7FFFFFFF;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+          if (key[i] > best) {
+            best = key[i];
+            at = column_of(i, lane);
+          }
+        const uint32_t top = __reduce_max_sync(0xffffffffu, best);
+        if (top <= kNoKey) break;
+        const int win = __reduce_min_sync(0xffffffffu, best == top ? at : 0x7FFFFFFF);
+        float w = 0.0f;
+        bool owner = false;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+          if (column_of(i, lane) == win) {
+            key[i] = 0u;
+            w = p[i] * inv;
+            owner = true;
+          }
+        w = __shfl_sync(0xffffffffu, w, __ffs(__ballot_sync(0xffffffffu, owner)) - 1);
+        if (lane == r) {
+          my_expert = win;
+          my_weight = w;
+        }
+      }
+    }
+    if (a.normalize) {
+      const float total = warp_sum(my_expert >= 0 ? my_weight : 0.0f);
+      if (my_expert >= 0) my_weight = my_weight / total;
+    }
+    if (my_rank < a.k) {
+      a.weights[row * a.k + my_rank] = my_weight;
+      a.experts[row * a.k + my_rank] = my_expert;
       if (my_expert >= 0) atomicAdd(sh_hits + my_expert, 1);  // integers: any order
     }
   }
 #pragma unroll
-  for (int j = 0; j < NV; ++j)
-    if (j * 32 + lane < a.E) sh_prob[warp * a.E + j * 32 + lane] = acc[j];
+  for (int i = 0; i < NV; ++i) {
+    const int e = column_of(i, lane);
+    if (e < a.E) sh_prob[warp * a.E + e] = acc[i];
+  }
   if (lane == 0) {
     sh_z[warp] = z;
     sh_t[warp] = t;
@@ -192,51 +268,125 @@ __global__ void __launch_bounds__(32 * kWarps) route_kernel(const RouteArgs a) {
     zb += sh_z[w];
     tb += sh_t[w];
   }
-  auto prob = [&](int e) {
-    float s = 0.0f;
-    for (int w = 0; w < kWarps; ++w) s += sh_prob[w * a.E + e];
-    return s;
-  };
-  if (gridDim.x == 1) {
-    finish(a, zb, tb, prob, [&](int e) { return sh_hits[e]; });
-    return;
-  }
-  uint32_t* out = a.partial + size_t(blockIdx.x) * partial_words(a.E);
+  const bool alone = gridDim.x == 1;
+  const float T = at_least_one(tb);
+  uint32_t* out = alone ? nullptr : a.partial + size_t(blockIdx.x) * partial_words(a.E);
+  float dot = 0.0f;
   for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
-    out[e] = __float_as_uint(prob(e));
-    out[a.E + 1 + e] = uint32_t(sh_hits[e]);
+    float sum = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) sum += sh_prob[w * a.E + e];
+    const int c = sh_hits[e];
+    if (alone) {
+      a.probs[e] = sum / T;
+      a.counts[e] = c;
+      dot += float(c) / (float(a.k) * T) * (sum / T);
+    } else {
+      out[e] = __float_as_uint(sum);
+      out[a.E + 1 + e] = uint32_t(c);
+    }
   }
-  if (threadIdx.x == 0) {
+  if (alone) {
+    dot = block_sum(dot, red);
+    if (threadIdx.x == 0) {
+      a.losses[0] = float(a.E) * dot;
+      a.losses[1] = zb / T;
+      a.counts[a.E] = tb;
+    }
+  } else if (threadIdx.x == 0) {
     out[a.E] = __float_as_uint(zb);
     out[2 * a.E + 1] = uint32_t(tb);
   }
 }
 
-// Adds the blocks' partial sums in block order.
-__global__ void __launch_bounds__(kFinishThreads) route_finish_kernel(const RouteArgs a, int blocks) {
-  extern __shared__ uint32_t sh[];
-  float* sh_prob = reinterpret_cast<float*>(sh);       // [E + 1]
-  int* sh_hits = reinterpret_cast<int*>(sh) + a.E + 1; // [E + 1]
+// Adds the blocks' partial sums: one cluster, each CTA a slice of the columns,
+// then the first CTA adds the slices' parts of the balance loss.  In a CTA,
+// warp g of the first kFinishGroups takes the blocks b = g mod kFinishGroups,
+// lane = column, and the groups are added in order; the last warp adds z and T
+// (column E) meanwhile.  All loads of a thread are independent, so that one
+// memory latency covers them.
+__global__ void __cluster_dims__(kFinishCtas, 1, 1) __launch_bounds__(kFinishThreads)
+    route_finish_kernel(const RouteArgs a, int blocks) {
+  __shared__ float sum[kFinishGroups][33];
+  __shared__ int hit[kFinishGroups][33];
+  __shared__ float z_sum;
+  __shared__ int T_sum;
+  __shared__ float dots[kFinishCtas];
+  ptx::cluster_sync();  // every CTA runs before its shared memory is written remotely
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
-  const size_t words = partial_words(a.E);
-  for (int c = threadIdx.x; c < int(words); c += blockDim.x) {
-    const uint32_t* src = a.partial + c;
-    if (c <= a.E) {
-      float s = 0.0f;
-#pragma unroll 8
-      for (int b = 0; b < blocks; ++b) s += __uint_as_float(__ldcg(src + size_t(b) * words));
-      sh_prob[c] = s;
-    } else {
-      int s = 0;
-#pragma unroll 8
-      for (int b = 0; b < blocks; ++b) s += int(__ldcg(src + size_t(b) * words));
-      sh_hits[c - a.E - 1] = s;
+  const int words = partial_words(a.E);
+  const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
+  const int rank = int(ptx::cluster_ctarank());
+  const int per = (a.E + kFinishCtas - 1) / kFinishCtas;
+  const int e1 = min(a.E, (rank + 1) * per);
+  float dot = 0.0f;
+  for (int e0 = rank * per; e0 == rank * per || e0 < e1; e0 += 32) {
+    const int e = e0 + lane;
+    float fs = 0.0f;
+    int ic = 0;
+    if (g < kFinishGroups) {
+      if (e < e1) {
+        constexpr int kPer = (kMaxBlocks + kFinishGroups - 1) / kFinishGroups;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          const int b = g + i * kFinishGroups;
+          if (b < blocks) {
+            const uint32_t* src = a.partial + size_t(b) * words;
+            fs += __uint_as_float(__ldcg(src + e));
+            ic += int(__ldcg(src + a.E + 1 + e));
+          }
+        }
+      }
+      sum[g][lane] = fs;
+      hit[g][lane] = ic;
+    } else if (e0 == rank * per) {
+      constexpr int kPer = (kMaxBlocks + 31) / 32;
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int b = lane + i * 32;
+        if (b < blocks) {
+          const uint32_t* src = a.partial + size_t(b) * words;
+          fs += __uint_as_float(__ldcg(src + a.E));
+          ic += int(__ldcg(src + 2 * a.E + 1));
+        }
+      }
+      fs = warp_sum(fs);
+      ic = __reduce_add_sync(0xffffffffu, ic);
+      if (lane == 0) {
+        z_sum = fs;
+        T_sum = ic;
+      }
     }
+    __syncthreads();
+    if (g == 0 && e < e1) {
+      float s = 0.0f;
+      int c = 0;
+#pragma unroll
+      for (int i = 0; i < kFinishGroups; ++i) {
+        s += sum[i][lane];
+        c += hit[i][lane];
+      }
+      const float T = at_least_one(T_sum);
+      const float P = s / T;
+      a.probs[e] = P;
+      a.counts[e] = c;
+      dot += float(c) / (float(a.k) * T) * P;
+    }
+    __syncthreads();
   }
-  __syncthreads();
-  finish(a, sh_prob[a.E], sh_hits[a.E], [&](int e) { return sh_prob[e]; },
-         [&](int e) { return sh_hits[e]; });
+  if (g == 0) {
+    dot = warp_sum(dot);
+    if (lane == 0) ptx::st_cluster_f32(ptx::mapa_shared(ptx::smem_u32(&dots[rank]), 0), dot);
+  }
+  ptx::cluster_sync();
+  if (rank == 0 && threadIdx.x == 0) {
+    float d = 0.0f;
+    for (int i = 0; i < kFinishCtas; ++i) d += dots[i];
+    a.losses[0] = float(a.E) * d;
+    a.losses[1] = z_sum / at_least_one(T_sum);
+    a.counts[a.E] = T_sum;
+  }
 }
 
 struct RouteGradArgs {
@@ -250,90 +400,135 @@ struct RouteGradArgs {
   int M, E, ld, k, normalize;
 };
 
-// dl[e] = p[e] (dp[e] - sum_f p[f] dp[f] + 2 d_z lse / T) with
-// dp[e] = d_balance E counts[e] / (k T^2) + (the weight's gradient at a taken
-// expert).  The k entries of the second term go through a zeroed row of
-// shared memory, which every lane reads at its own columns.
-template <int NV, bool kBF16>
-__global__ void __launch_bounds__(32 * kWarps) route_grad_kernel(const RouteGradArgs a) {
-  extern __shared__ uint32_t sh[];
+// With e = exp(l - lse) (lse only has to be near the row's maximum: e is
+// divided by its own sum s, so that p keeps its precision in rows where lse
+// has rounded the sum away) and, over the row, A = the taken experts:
+//   dl[e] = p[e] (dp[e] - sum_f p[f] dp[f] + 2 d_z lse / T)
+//   dp[e] = d_balance E counts[e] / (k T^2) + u[e],   u = 0 outside A
+//   u[e]  = dw[e], or normalised (dw[e] - q) / a with a = sum_A p and
+//           q = sum_A p dw / a; then sum_f p[f] u[f] = 0
+// so one pass of four sums (s, sum e base, sum_A e, sum_A e dw) gives all that
+// a row needs.  The k gradients dw reach the lanes that own their columns
+// through a row of shared memory, kNone elsewhere.
+template <int NV, bool kAligned, bool kBF16>
+__global__ void __launch_bounds__(32 * kGradWarps, NV <= 8 ? 4 : 2)
+    route_grad_kernel(const RouteGradArgs a) {
+  extern __shared__ __align__(16) uint32_t sh[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  float* up = reinterpret_cast<float*>(sh) + warp * a.E;
-  for (int e = lane; e < a.E; e += 32) up[e] = 0.0f;
-  __syncwarp();
+  const float kNone = __uint_as_float(0x7FFFFFFFu);  // a NaN no gradient carries
+  const int up_row = (a.E + 3) / 4 * 4;  // whole 16-byte groups
+  float* base = reinterpret_cast<float*>(sh);  // [up_row] dp's first term
+  float* up = base + (1 + warp) * up_row;
+  for (int e = lane; e < up_row; e += 32) up[e] = kNone;
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
-  const int T = a.counts[a.E];
-  const float t = float(T > 1 ? T : 1);
-  const float db = a.dlosses ? a.dlosses[0] : 0.0f, dz = a.dlosses ? a.dlosses[1] : 0.0f;
+  const float t = at_least_one(a.counts[a.E]);
+  const float db = a.dlosses ? a.dlosses[0] : 0.0f;
+  const float dz = a.dlosses ? a.dlosses[1] : 0.0f;
   const float c0 = db * float(a.E) / (float(a.k) * t) / t;
   const float c1 = 2.0f * dz / t;
-  float base[NV];
-#pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const int e = j * 32 + lane;
-    base[j] = e < a.E ? c0 * float(a.counts[e]) : 0.0f;
-  }
-  for (long long row = (long long)blockIdx.x * kWarps + warp; row < a.M;
-       row += (long long)gridDim.x * kWarps) {
-    const float* src = a.logits + row * a.ld;
-    const float l = a.lse[row];
-    int ex = lane < a.k ? a.experts[row * a.k + lane] : -1;
-    if (ex >= a.E) ex = -1;  // not an expert: takes no part
+  // once per block: read by every row, these few lines of memory are the same
+  // for the whole grid
+  for (int e = threadIdx.x; e < up_row; e += blockDim.x)
+    base[e] = e < a.E ? c0 * float(a.counts[e]) : 0.0f;
+  __syncthreads();
+  const long long step = (long long)gridDim.x * kGradWarps;
+  for (long long row = (long long)blockIdx.x * kGradWarps + warp; row < a.M; row += step) {
+    float p[NV], u[NV];
+    load_row<NV, kAligned>(a.logits + row * a.ld, a.E, lane, p);
+    const float l = __ldcg(a.lse + row);
+    int ex = -1;
+    float g = 0.0f;
+    if (lane < a.k) {
+      ex = __ldcg(a.experts + row * a.k + lane);
+      if (a.dweights) g = __ldcg(a.dweights + row * a.k + lane);
+      if (ex >= a.E) ex = -1;  // not an expert: takes no part
+    }
+    if (__float_as_uint(g) == 0x7FFFFFFFu) g = __uint_as_float(0x7FC00000u);
     const bool live = __shfl_sync(0xffffffffu, ex, 0) >= 0;
-    float p[NV];
-    float mx = -INFINITY;
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int e = j * 32 + lane;
-      p[j] = (live && e < a.E) ? __ldcg(src + e) : -INFINITY;
-      mx = fmaxf(mx, p[j]);
-    }
-    mx = warp_max(mx);
-    const float ref = mx == -INFINITY ? 0.0f : mx;
-    float s = 0.0f;
-#pragma unroll
-    for (int j = 0; j < NV; ++j) s += p[j] = expf(p[j] - ref);
-    s = warp_sum(s);
-    const float inv = s > 0.0f ? 1.0f / s : s;  // 0 in a row that takes no part, NaN stays
-#pragma unroll
-    for (int j = 0; j < NV; ++j) p[j] *= inv;
-    float g = (ex >= 0 && a.dweights) ? a.dweights[row * a.k + lane] : 0.0f;
-    if (a.normalize) {
-      const float q = ex >= 0 ? expf(__ldcg(src + ex) - ref) * inv : 0.0f;
-      const float sum = warp_sum(q);
-      const float gq = warp_sum(g * q);
-      if (ex >= 0) g = (g - gq / sum) / sum;
-    }
     if (ex >= 0) up[ex] = g;
     __syncwarp();
-    float dp[NV];
-    float dot = 0.0f;
+    float s = 0.0f, sb = 0.0f, sa = 0.0f, sg = 0.0f;
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int e = j * 32 + lane;
-      dp[j] = e < a.E ? base[j] + up[e] : 0.0f;
-      dot += p[j] * dp[j];
+    for (int i = 0; i < NV; i += 4) {
+      const int e = column_of(i, lane);
+      float4 q = make_float4(kNone, kNone, kNone, kNone), d = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (e < up_row) {
+        q = *reinterpret_cast<const float4*>(up + e);
+        d = *reinterpret_cast<const float4*>(base + e);
+      }
+      u[i] = q.x, u[i + 1] = q.y, u[i + 2] = q.z, u[i + 3] = q.w;
+      const float b4[4] = {d.x, d.y, d.z, d.w};
+#pragma unroll
+      for (int c = i; c < i + 4; ++c) {
+        p[c] = fast_exp(p[c] - l);
+        s += p[c];
+        sb += p[c] * b4[c - i];
+        const bool taken = __float_as_uint(u[c]) != 0x7FFFFFFFu;
+        sa += taken ? p[c] : 0.0f;
+        sg += taken ? p[c] * u[c] : 0.0f;
+      }
     }
-    dot = warp_sum(dot);
-    const float shift = (live ? c1 * l : 0.0f) - dot;
-    __syncwarp();
-    if (ex >= 0) up[ex] = 0.0f;
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int e = j * 32 + lane;
-      if (e >= a.E) continue;
-      const float d = live ? p[j] * (dp[j] + shift) : 0.0f;
+    for (int o = 16; o; o >>= 1) {
+      s += __shfl_xor_sync(0xffffffffu, s, o);
+      sb += __shfl_xor_sync(0xffffffffu, sb, o);
+      sa += __shfl_xor_sync(0xffffffffu, sa, o);
+      sg += __shfl_xor_sync(0xffffffffu, sg, o);
+    }
+    __syncwarp();
+    if (ex >= 0) up[ex] = kNone;
+    const float inv = 1.0f / s;
+    const float q = a.normalize ? sg / sa : 0.0f;        // sum of the weights times their gradients
+    const float scale = a.normalize ? s / sa : 1.0f;     // 1 / (sum of the taken p)
+    const float shift = c1 * l - (sb + (a.normalize ? 0.0f : sg)) * inv;
+#pragma unroll
+    for (int i = 0; i < NV; i += 4) {
+      const int e = column_of(i, lane);
+      const float4 b = e < up_row ? *reinterpret_cast<const float4*>(base + e)
+                                  : make_float4(0.f, 0.f, 0.f, 0.f);
+      const float b4[4] = {b.x, b.y, b.z, b.w};
+      float d[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const bool taken = __float_as_uint(u[i + c]) != 0x7FFFFFFFu;
+        const float dp = b4[c] + (taken ? (u[i + c] - q) * scale : 0.0f);
+        d[c] = live ? p[i + c] * inv * (dp + shift) : 0.0f;
+      }
       const size_t off = size_t(row) * a.E + e;
       // BF16: one rounding, for a gradient that goes into a BF16 product
-      if constexpr (kBF16) static_cast<__nv_bfloat16*>(a.dlogits)[off] = __float2bfloat16_rn(d);
-      else static_cast<float*>(a.dlogits)[off] = d;
+      if constexpr (kBF16) {
+        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.dlogits) + off;
+        if constexpr (kAligned) {
+          const __nv_bfloat162 lo = __floats2bfloat162_rn(d[0], d[1]);
+          const __nv_bfloat162 hi = __floats2bfloat162_rn(d[2], d[3]);
+          if (e < a.E)
+            *reinterpret_cast<uint2*>(out) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
+                                                        *reinterpret_cast<const uint32_t*>(&hi));
+        } else {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if (e + c < a.E) out[c] = __float2bfloat16_rn(d[c]);
+        }
+      } else {
+        float* out = static_cast<float*>(a.dlogits) + off;
+        if constexpr (kAligned) {
+          if (e < a.E) *reinterpret_cast<float4*>(out) = make_float4(d[0], d[1], d[2], d[3]);
+        } else {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if (e + c < a.E) out[c] = d[c];
+        }
+      }
     }
     __syncwarp();
   }
 }
 
-int route_blocks(int M) { return int(std::min<long long>(kMaxBlocks, ((long long)M + kWarps - 1) / kWarps)); }
+int route_blocks(int M) {
+  if (M <= kOneBlockRows) return 1;
+  return int(std::min<long long>(kMaxBlocks, ((long long)M + kWarps - 1) / kWarps));
+}
 
 template <class Kernel, class... Args>
 int launch(Kernel kernel, int grid, int threads, size_t shared, cudaStream_t stream, Args... args) {
@@ -354,6 +549,47 @@ int launch(Kernel kernel, int grid, int threads, size_t shared, cudaStream_t str
   return GEMM_OK;
 }
 
+template <int NV, bool kAligned>
+int run_route(const RouteArgs& a, int blocks, cudaStream_t stream) {
+  const size_t shared = size_t(kWarps + 1) * a.E * 4;
+  if (shared > 40 * 1024) {  // past the default limit together with the static arrays
+    if (cudaFuncSetAttribute(route_kernel<NV, kAligned>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             int(shared)) != cudaSuccess) {
+      cudaGetLastError();
+      return GEMM_ERR_LAUNCH;
+    }
+  }
+  return launch(route_kernel<NV, kAligned>, blocks, 32 * kWarps, shared, stream, a);
+}
+
+template <int NV, bool kAligned>
+int run_route_grad(const RouteGradArgs& a, bool bf16, cudaStream_t stream) {
+  const int blocks = int(
+      std::min<long long>(kGradMaxBlocks, ((long long)a.M + kGradWarps - 1) / kGradWarps));
+  const size_t shared = size_t(kGradWarps + 1) * ((a.E + 3) / 4 * 4) * 4;
+  return bf16 ? launch(route_grad_kernel<NV, kAligned, true>, blocks, 32 * kGradWarps, shared, stream, a)
+              : launch(route_grad_kernel<NV, kAligned, false>, blocks, 32 * kGradWarps, shared, stream, a);
+}
+
+// The smallest row buffer that holds E columns.
+template <bool kAligned>
+int pick_route(const RouteArgs& a, int blocks, cudaStream_t stream) {
+  if (a.E <= 128) return run_route<4, kAligned>(a, blocks, stream);
+  if (a.E <= 256) return run_route<8, kAligned>(a, blocks, stream);
+  if (a.E <= 512) return run_route<16, kAligned>(a, blocks, stream);
+  return run_route<32, kAligned>(a, blocks, stream);
+}
+
+template <bool kAligned>
+int pick_route_grad(const RouteGradArgs& a, bool bf16, cudaStream_t stream) {
+  if (a.E <= 128) return run_route_grad<4, kAligned>(a, bf16, stream);
+  if (a.E <= 256) return run_route_grad<8, kAligned>(a, bf16, stream);
+  if (a.E <= 512) return run_route_grad<16, kAligned>(a, bf16, stream);
+  return run_route_grad<32, kAligned>(a, bf16, stream);
+}
+
+bool aligned_to(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
 }  // namespace
 
 size_t router_topk_workspace(int M, int E) {
@@ -365,31 +601,20 @@ int launch_router_topk(const RouterTopk& r, const DeviceInfo&, cudaStream_t stre
   const RouteArgs a{r.logits, r.valid, r.weights, r.experts, r.lse, r.counts, r.probs, r.losses,
                     static_cast<uint32_t*>(r.workspace), r.M, r.E, r.ld, r.k, r.normalize};
   const int blocks = route_blocks(r.M);
-  const size_t shared = size_t(kWarps + 1) * r.E * 4;
-  const int threads = 32 * kWarps;
-  int rc;
-  if (r.E <= 64) rc = launch(route_kernel<2>, blocks, threads, shared, stream, a);
-  else if (r.E <= 256) rc = launch(route_kernel<8>, blocks, threads, shared, stream, a);
-  else rc = launch(route_kernel<32>, blocks, threads, shared, stream, a);
+  const bool aligned = r.E % 4 == 0 && (r.ld % 4 == 0 || r.M == 1) && aligned_to(r.logits, 16);
+  const int rc = aligned ? pick_route<true>(a, blocks, stream) : pick_route<false>(a, blocks, stream);
   if (rc != GEMM_OK || blocks == 1) return rc;
-  return launch(route_finish_kernel, 1, kFinishThreads, partial_words(r.E) * 4, stream, a, blocks);
+  return launch(route_finish_kernel, kFinishCtas, kFinishThreads, 0, stream, a, blocks);
 }
 
 int launch_router_topk_backward(const RouterTopkBackward& r, const DeviceInfo&,
                                 cudaStream_t stream) {
   const RouteGradArgs a{r.logits, r.experts, r.lse, r.counts, r.dweights, r.dlosses, r.dlogits,
                         r.M, r.E, r.ld, r.k, r.normalize};
-  const int blocks = route_blocks(r.M);
-  const size_t shared = size_t(kWarps) * r.E * 4;
-  const int threads = 32 * kWarps;
-  if (r.bf16) {
-    if (r.E <= 64) return launch(route_grad_kernel<2, true>, blocks, threads, shared, stream, a);
-    if (r.E <= 256) return launch(route_grad_kernel<8, true>, blocks, threads, shared, stream, a);
-    return launch(route_grad_kernel<32, true>, blocks, threads, shared, stream, a);
-  }
-  if (r.E <= 64) return launch(route_grad_kernel<2, false>, blocks, threads, shared, stream, a);
-  if (r.E <= 256) return launch(route_grad_kernel<8, false>, blocks, threads, shared, stream, a);
-  return launch(route_grad_kernel<32, false>, blocks, threads, shared, stream, a);
+  const bool aligned = r.E % 4 == 0 && (r.ld % 4 == 0 || r.M == 1) && aligned_to(r.logits, 16) &&
+                   aligned_to(r.dlogits, r.bf16 ? 8 : 16);
+  return aligned ? pick_route_grad<true>(a, r.bf16, stream)
+                 : pick_route_grad<false>(a, r.bf16, stream);
 }
 
 }  // namespace gb300
