@@ -44,8 +44,10 @@ namespace gb300 {
 enum class Operand : int { kBF16 = 0, kNVFP4 = 1, kW4A16 = 2 };
 // kScaleBF16: C = bf16(scale * acc), one FP32 multiply then one rounding
 // kAddF32: C (FP32) = acc, or C += acc (p.accumulate)
-// kXentStats: no C; per row and N block the maximum and the sum of
+// kXentStats: no C; per row and column group the maximum and the sum of
 //   exp(acc - maximum), and the target column's value (linear cross entropy)
+// kXentStatsT: the same with the roles swapped (rows of D are the vocabulary,
+//   columns the tokens), one group per CTA and lane quarter
 // kXentGradBF16: C = bf16(d_row * (exp(acc - lse_row) - [column = target_row]))
 enum class Epilogue : int {
   kStoreBF16 = 0,
@@ -55,7 +57,8 @@ enum class Epilogue : int {
   kScaleBF16 = 4,
   kAddF32 = 5,
   kXentStats = 6,
-  kXentGradBF16 = 7
+  kXentGradBF16 = 7,
+  kXentStatsT = 8
 };
 
 struct GemmParams {
@@ -79,9 +82,10 @@ struct GemmParams {
   const long long* target;        // [M] target column; < 0: the row has no loss
   const float* row_lse;           // [M] kXentGradBF16
   const float* row_scale;         // [M] kXentGradBF16: gradient of the row's loss
-  float2* stats;                  // [N blocks][M] kXentStats: maximum, sum of exponentials
+  float2* stats;                  // [groups][tokens] kXentStats*: maximum, sum of exponentials
   float* picked;                  // [M] kXentStats: the target column's value
   int col_offset, col_total;      // first column of this launch, columns in all
+  int k_chunk, chunks;            // CHUNKED: K blocks per chunk, chunks per tile
 };
 
 template <Operand OP, int CG_, int BN_, int STAGES_, int EPI_WARPS_ = 4, int EPI_BUFS_ = 2,
@@ -118,6 +122,9 @@ struct TileCfg {
   // grids of which only some depend on their predecessor fills the SMs that
   // the last round of tiles leaves idle.
   static constexpr bool CHAIN = CHAIN_;
+  // CHUNKED (see ChunkedCfg): a tile's K loop is cut into chunks, each with an
+  // accumulator of its own that the epilogue adds up in registers.
+  static constexpr bool CHUNKED = false;
   // C_T: the output is D transposed (the swapped-operand decode GEMM, whose
   // M role holds the weights and N role the few activation rows)
   static constexpr bool C_T = C_T_;
@@ -239,6 +246,15 @@ struct TileCfg {
   }
 };
 
+// The tensor core adds into its accumulator with truncation, so a long K loop
+// drifts toward zero by about K / 16 half units of the running sum's last
+// place (lse of 4096-deep logits was off by 2.6e-6 of its value).  Chunks of a
+// few hundred K, added with rounding, keep the error at the chunk's length.
+template <class Base>
+struct ChunkedCfg : Base {
+  static constexpr bool CHUNKED = true;
+};
+
 // Work item `tile` -> batch l, M block mb and N block nb, in grouped-M
 // raster order: consecutive items walk group_m M blocks down one N column.
 template <class Cfg>
@@ -274,6 +290,16 @@ struct Seg {
 //    segment partial.
 template <class Cfg>
 __device__ __forceinline__ bool seg_at(const GemmParams& p, int c, int C, int idx, Seg& s) {
+  if constexpr (Cfg::CHUNKED) {
+    const int q = idx / p.chunks;
+    const long long t = (long long)c + (long long)q * C;
+    if (t >= p.total_tiles) return false;
+    s.tile = int(t);
+    s.slot = -1;
+    s.kb0 = (idx - q * p.chunks) * p.k_chunk;
+    s.kb1 = min(p.num_k_blocks, s.kb0 + p.k_chunk);
+    return true;
+  }
   if (!p.sk) {
     const long long t = (long long)c + (long long)idx * C;
     if (t >= p.total_tiles) return false;
@@ -376,29 +402,42 @@ __device__ __forceinline__ void write_box_row_f32(uint8_t* row, int lane, const 
   }
 }
 
-// Linear cross entropy, forward: folds 64 logits of one row into the row's
+// Linear cross entropy, forward: folds 32 logits of one row into the row's
 // running maximum and sum of exp(z - maximum).  exp(y) = 2^(y log2 e) on the
 // special-function unit (relative error below 2^-21).  A maximum of -inf (no
 // logit yet, or none finite) subtracts 0 instead, so that no inf - inf arises;
 // NaN logits reach the sum.
 __device__ __forceinline__ float fast_exp(float y) { return ptx::ex2(y * 1.4426950408889634f); }
 
-__device__ __forceinline__ void xent_fold(const uint32_t (&a)[32], const uint32_t (&b)[32],
-                                          float& mx, float& sum) {
+__device__ __forceinline__ void xent_fold(const float (&x)[32], float& mx, float& sum) {
   float m4[4] = {mx, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-  for (int i = 0; i < 32; ++i)
-    m4[i & 3] = fmaxf(m4[i & 3], fmaxf(__uint_as_float(a[i]), __uint_as_float(b[i])));
+  for (int i = 0; i < 32; ++i) m4[i & 3] = fmaxf(m4[i & 3], x[i]);
   const float m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
   const float ref = (m == -INFINITY) ? 0.0f : m;
   float s4[4] = {sum * fast_exp(mx - ref), 0.0f, 0.0f, 0.0f};
 #pragma unroll
-  for (int i = 0; i < 32; ++i) {
-    s4[i & 3] += fast_exp(__uint_as_float(a[i]) - ref);
-    s4[(i + 2) & 3] += fast_exp(__uint_as_float(b[i]) - ref);
-  }
+  for (int i = 0; i < 32; ++i) s4[i & 3] += fast_exp(x[i] - ref);
   mx = m;
   sum = (s4[0] + s4[1]) + (s4[2] + s4[3]);
+}
+
+// The same of a whole tile row (32 R columns) at once.
+template <int R>
+__device__ __forceinline__ float2 xent_tile(const float (&x)[R][32]) {
+  float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+  for (int i = 0; i < R; ++i)
+#pragma unroll
+    for (int j = 0; j < 32; ++j) m4[j & 3] = fmaxf(m4[j & 3], x[i][j]);
+  const float m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+  const float ref = (m == -INFINITY) ? 0.0f : m;
+  float s4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int i = 0; i < R; ++i)
+#pragma unroll
+    for (int j = 0; j < 32; ++j) s4[j & 3] += fast_exp(x[i][j] - ref);
+  return make_float2(m, (s4[0] + s4[1]) + (s4[2] + s4[3]));
 }
 
 // Linear cross entropy, backward: 32 logits of one row -> gradients
@@ -542,6 +581,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
   constexpr bool kDirectStore = (Cfg::EPI_BUFS == 0);
   static_assert(!kDirectStore || EPI == Epilogue::kStoreBF16 || EPI == Epilogue::kStoreFP16 ||
                     EPI == Epilogue::kScaleBF16 || EPI == Epilogue::kXentStats ||
+                    EPI == Epilogue::kXentStatsT ||
                     (EPI == Epilogue::kStoreF32 && (Cfg::kRegEpi || Cfg::C_T)),
                 "direct stores serve the plain 16-bit epilogues and FP32 partials");
   static_assert(!Cfg::C_T || EPI == Epilogue::kStoreF32 || EPI == Epilogue::kStoreFP16,
@@ -1274,6 +1314,20 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     // linear cross entropy: the row block whose per-row values the lane holds
     int xent_row0 = -1, xent_rel = -1;
     long long xent_target = -1;
+    constexpr bool kXentFwd = EPI == Epilogue::kXentStats || EPI == Epilogue::kXentStatsT;
+    constexpr int XR = kXentFwd ? Cfg::EPI_COLS / 32 : 1;  // 32-column groups per epilogue warp
+    float xr[XR][32];                                      // the tile's sums over the chunks
+    float2 xt[XR];                                         // kXentStatsT: running statistics
+    long long xt_target[XR];
+    (void)xr, (void)xt, (void)xt_target;
+    if constexpr (EPI == Epilogue::kXentStatsT) {
+#pragma unroll
+      for (int i = 0; i < XR; ++i) {
+        xt[i] = make_float2(-INFINITY, 0.0f);
+        const int tok = col_base + 32 * i + lane;
+        xt_target[i] = tok < p.N ? p.target[tok] : -1;
+      }
+    }
     float xent_lse = 0.0f, xent_scale = 0.0f;
     (void)xent_row0, (void)xent_rel, (void)xent_target, (void)xent_lse, (void)xent_scale;
     uint32_t chunk_ctr = 0;
@@ -1546,47 +1600,79 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
             ptx::bulk_commit_group();
           }
         }
-      } else if constexpr (EPI == Epilogue::kXentStats) {
-        // Linear cross entropy: each lane owns one row and walks its columns,
-        // 64 at a time, with the running maximum and the running sum of
-        // exponentials in FP32; columns past N take no part.
-        const int grow = row0 + lane;
-        if (row0 != xent_row0) {
-          xent_row0 = row0;
-          xent_target = grow < p.M ? p.target[grow] : -1;
+      } else if constexpr (kXentFwd) {
+        // Linear cross entropy.  The chunk's accumulator joins the tile's sum
+        // in registers and is handed back at once; the rest overlaps the next
+        // chunks' MMAs.
+        const bool first_chunk = sg.kb0 == 0;
+#pragma unroll
+        for (int i = 0; i < XR; ++i) {
+          uint32_t v[32];
+          ptx::tmem_ld_32x32b_x32(tacc + uint32_t(32 * i), v);
+          ptx::tmem_ld_wait_regs(v);
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            xr[i][j] = first_chunk ? __uint_as_float(v[j]) : xr[i][j] + __uint_as_float(v[j]);
         }
-        float mx = -INFINITY, sum = 0.0f;
-#pragma unroll 1
-        for (int c = 0; c < Cfg::EPI_COLS / 64; ++c) {
-          const int col0 = nb * BN + col_base + c * 64;
-          uint32_t r0[32], r1[32];
-          const uint32_t taddr = tacc + uint32_t(c * 64);
-          ptx::tmem_ld_32x32b_x32(taddr, r0);
-          ptx::tmem_ld_32x32b_x32(taddr + 32, r1);
-          ptx::tmem_ld_wait_regs(r0);
-          ptx::tmem_ld_wait_regs(r1);
-          if (c == Cfg::EPI_COLS / 64 - 1) release_acc(acc);
+        release_acc(acc);
+        if (sg.kb1 < p.num_k_blocks) continue;
+        if constexpr (EPI == Epilogue::kXentStats) {
+          // each lane owns one row: maximum and sum of exponentials over its
+          // columns, in FP32; columns past N take no part
+          const int grow = row0 + lane;
+          if (row0 != xent_row0) {
+            xent_row0 = row0;
+            xent_target = grow < p.M ? p.target[grow] : -1;
+          }
+          const int col0 = nb * BN + col_base;
           if (!(rows_live && col0 < p.N)) continue;  // warp-uniform
-          const long long rel = xent_target - (p.col_offset + col0);
-          if (__any_sync(0xffffffffu, rel >= 0 && rel < 64)) {
+          const long long rel = xent_target - col0;
+          if (__any_sync(0xffffffffu, rel >= 0 && rel < Cfg::EPI_COLS)) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              if (rel == i) p.picked[grow] = __uint_as_float(r0[i]);
-              if (rel == 32 + i) p.picked[grow] = __uint_as_float(r1[i]);
-            }
-          }
-          if (col0 + 64 > p.N) {
+            for (int i = 0; i < XR; ++i)
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              if (col0 + i >= p.N) r0[i] = 0xFF800000u;  // -inf
-              if (col0 + 32 + i >= p.N) r1[i] = 0xFF800000u;
-            }
+              for (int j = 0; j < 32; ++j)
+                if (rel == 32 * i + j) p.picked[grow] = xr[i][j];
           }
-          xent_fold(r0, r1, mx, sum);
+          if (col0 + Cfg::EPI_COLS > p.N) {
+#pragma unroll
+            for (int i = 0; i < XR; ++i)
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (col0 + 32 * i + j >= p.N) xr[i][j] = -INFINITY;
+          }
+          const float2 st = xent_tile(xr);
+          if (grow < p.M)
+            p.stats[(size_t(nb) * (Cfg::EPI_WARPS / 4) + (e >> 2)) * size_t(p.M) + grow] = st;
+        } else {
+          // each lane holds one vocabulary row of 32 tokens: through a 32 x 32
+          // box in shared memory (column j of row t at j ^ t: no bank conflict
+          // either way) every lane gets one token's 32 logits and folds them
+          // into that token's running maximum and sum
+          float* box = reinterpret_cast<float*>(smem + (buf0 - sbase));
+          const int live = p.M - row0;  // vocabulary rows of this warp that exist
+#pragma unroll
+          for (int i = 0; i < XR; ++i) {
+            const int tok = col_base + 32 * i + lane;  // one N block holds all tokens
+            if (col_base + 32 * i >= p.N || live <= 0) break;
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 32; ++j) box[j * 32 + (lane ^ j)] = xr[i][j];
+            __syncwarp();
+            const float* mine = box + lane * 32;
+            float x[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) x[j] = mine[j ^ lane];
+            const long long rel = xt_target[i] - row0;
+            if (rel >= 0 && rel < 32 && tok < p.N) p.picked[tok] = mine[int(rel) ^ lane];
+            if (live < 32) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (j >= live) x[j] = -INFINITY;
+            }
+            xent_fold(x, xt[i].x, xt[i].y);
+          }
         }
-        if (rows_live && grow < p.M)
-          p.stats[(size_t(nb) * (Cfg::EPI_WARPS / 4) + (e >> 2)) * size_t(p.M) + grow] =
-              make_float2(mx, sum);
       } else if constexpr (EPI == Epilogue::kStoreF32 || EPI == Epilogue::kAddF32) {
         // FP32 outputs (split-K partials, accumulated gradients): 32-column
         // boxes of 32 rows x 128 bytes.
@@ -1794,6 +1880,13 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
             ptx::bulk_commit_group();
           }
         }
+      }
+    }
+    if constexpr (EPI == Epilogue::kXentStatsT) {
+#pragma unroll
+      for (int i = 0; i < XR; ++i) {
+        const int tok = col_base + 32 * i + lane;
+        if (tok < p.N) p.stats[(size_t(blockIdx.x) * 4 + (e & 3)) * size_t(p.N) + tok] = xt[i];
       }
     }
     if (lane == 0) {

@@ -21,8 +21,14 @@
 
 namespace gb300 {
 
-using XentFwdPair = TileCfg<Operand::kBF16, 2, 256, 3, 4, 0, true, false, 2>;
-using XentFwdSingle = TileCfg<Operand::kBF16, 1, 256, 4, 4, 0>;
+// Forward, tokens on the MMA's M side: 256 x 256 pair tiles; 8 epilogue warps
+// hold a tile's sums over the K chunks, 128 columns each, in registers.
+using XentFwdPair = ChunkedCfg<TileCfg<Operand::kBF16, 2, 256, 3, 8, 0, true, false, 2>>;
+// Forward of few tokens: the vocabulary on the M side (128 rows per CTA), the
+// tokens on the N side, so that the MMA's time shrinks with the tokens and the
+// kernel streams W.
+template <int BN, int STAGES, int EPI_WARPS>
+using XentFwdT = ChunkedCfg<TileCfg<Operand::kBF16, 1, BN, STAGES, EPI_WARPS, 1, true, false, 2>>;
 template <int CG, int STAGES, int KSUB, bool BMN, bool AMN>
 using XentCfg =
     TileCfg<Operand::kBF16, CG, 256, STAGES, 4, 2, true, false, KSUB, BMN, false, AMN, true>;
@@ -36,45 +42,48 @@ namespace {
 
 constexpr int kRowsSingle = 128;  // up to this many rows one CTA's 128-row tiles hold them all
 
-// Joins a row's tile statistics in tile order.  One warp per part group and
-// 32 rows per block: lane = row, so each load is one 256-byte line.
-constexpr int kJoinGroups = 16;
-__global__ void __launch_bounds__(32 * kJoinGroups)
+constexpr int kChunkK = 512;     // K per accumulator, see ChunkedCfg
+constexpr int kChunkKFew = 256;  // the same where the MMA has time to spare
+
+// Joins the groups' statistics of each row.  A block takes `rows` (a power of
+// two) rows; thread t takes row t % rows and the groups t / rows,
+// t / rows + threads / rows, ...; the threads of a row are then joined
+// pairwise.  The order depends on the sizes alone.
+constexpr int kJoinThreads = 512;
+__device__ __forceinline__ float2 join2(float2 a, float2 b) {
+  const float m = fmaxf(a.x, b.x);
+  const float ref = (m == -INFINITY) ? 0.0f : m;
+  return make_float2(m, a.y * fast_exp(a.x - ref) + b.y * fast_exp(b.x - ref));
+}
+
+__global__ void __launch_bounds__(kJoinThreads)
     xent_join_kernel(const float2* __restrict__ stats, const long long* __restrict__ target,
-                     float* __restrict__ loss, float* __restrict__ lse, int M, int V, int parts) {
-  __shared__ float2 part[kJoinGroups][32];
+                     float* __restrict__ loss, float* __restrict__ lse, int M, int V, int groups,
+                     int rows) {
+  __shared__ float2 part[kJoinThreads];
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
-  const int lane = threadIdx.x & 31, g = threadIdx.x >> 5;
-  const int row = int(blockIdx.x) * 32 + lane;
-  const int per = (parts + kJoinGroups - 1) / kJoinGroups;
-  const int p1 = min(parts, (g + 1) * per);
-  float mx = -INFINITY, sum = 0.0f;
+  const int t = int(threadIdx.x);
+  const int row = int(blockIdx.x) * rows + t % rows;
+  const int per = kJoinThreads / rows;
+  float2 s = make_float2(-INFINITY, 0.0f);
   if (row < M) {
-#pragma unroll 8
-    for (int i = g * per; i < p1; ++i) {
-      const float2 s = __ldcg(stats + size_t(i) * M + row);
-      const float m = fmaxf(mx, s.x);
-      const float ref = (m == -INFINITY) ? 0.0f : m;
-      sum = sum * fast_exp(mx - ref) + s.y * fast_exp(s.x - ref);
-      mx = m;
-    }
+#pragma unroll 4
+    for (int i = t / rows; i < groups; i += per) s = join2(s, __ldcg(stats + size_t(i) * M + row));
   }
-  part[g][lane] = make_float2(mx, sum);
+  part[t] = s;
   __syncthreads();
-  if (g != 0 || row >= M) return;
-  for (int i = 1; i < kJoinGroups; ++i) {
-    const float2 s = part[i][lane];
-    const float m = fmaxf(mx, s.x);
-    const float ref = (m == -INFINITY) ? 0.0f : m;
-    sum = sum * fast_exp(mx - ref) + s.y * fast_exp(s.x - ref);
-    mx = m;
+  for (int h = kJoinThreads / 2; h >= rows; h >>= 1) {
+    if (t < h) part[t] = join2(part[t], part[t + h]);
+    __syncthreads();
   }
-  const float l = ((mx == -INFINITY) ? 0.0f : mx) + logf(sum);
+  if (t >= rows || row >= M) return;
+  s = part[t];
+  const float l = ((s.x == -INFINITY) ? 0.0f : s.x) + logf(s.y);
   lse[row] = l;
-  const long long t = target[row];
+  const long long y = target[row];
   // loss[row] holds the target's logit, written by the tile that has it
-  loss[row] = t < 0 ? 0.0f : (t >= V ? NAN : l - loss[row]);
+  loss[row] = y < 0 ? 0.0f : (y >= V ? NAN : l - loss[row]);
 }
 
 template <class Cfg>
@@ -103,17 +112,45 @@ GemmParams base_params(int M, int N, int K, const DeviceInfo& dev) {
 }
 
 template <class Cfg>
+void set_chunks(GemmParams& p, int k) {
+  p.k_chunk = std::max(1, k / Cfg::BK);
+  p.chunks = (p.num_k_blocks + p.k_chunk - 1) / p.k_chunk;
+}
+
 int run_forward(const XentForward& a, const DeviceInfo& dev, cudaStream_t stream) {
+  using Cfg = XentFwdPair;
   CUtensorMap tx, tw;
   int rc = encode_k_major<Cfg>(&tx, a.X, a.M, a.K, Cfg::BM);
   if (rc == GEMM_OK) rc = encode_k_major<Cfg>(&tw, a.W, a.V, a.K, Cfg::B_ROWS);
   if (rc != GEMM_OK) return rc;
   GemmParams p = base_params<Cfg>(a.M, a.V, a.K, dev);
+  set_chunks<Cfg>(p, kChunkK);
   p.target = a.target;
   p.stats = static_cast<float2*>(a.workspace);
   p.picked = a.loss;
-  p.col_total = a.V;
   return launch_tcgen05<Cfg, Epilogue::kXentStats>(tx, tw, tx, tx, tx, p, dev, stream);
+}
+
+template <class Cfg>
+int run_forward_few(const XentForward& a, int ctas, const DeviceInfo& dev, cudaStream_t stream) {
+  CUtensorMap tx, tw;
+  int rc = encode_k_major<Cfg>(&tw, a.W, a.V, a.K, Cfg::BM);
+  if (rc == GEMM_OK) rc = encode_k_major<Cfg>(&tx, a.X, a.M, a.K, Cfg::B_ROWS);
+  if (rc != GEMM_OK) return rc;
+  GemmParams p = base_params<Cfg>(a.V, a.M, a.K, dev);
+  set_chunks<Cfg>(p, kChunkKFew);
+  p.target = a.target;
+  p.stats = static_cast<float2*>(a.workspace);
+  p.picked = a.loss;
+  return launch_tcgen05<Cfg, Epilogue::kXentStatsT>(tw, tx, tw, tw, tw, p, dev, stream, ctas);
+}
+
+// Column groups that the forward statistics come in: one per 128 columns,
+// or (few rows) four per CTA, of at most kFewCtas CTAs.
+constexpr int kFewCtas = 152;
+int few_ctas(int V) { return std::min(kFewCtas, (V + 127) / 128); }
+int stat_groups(int M, int V) {
+  return M <= kRowsSingle ? 4 * few_ctas(V) : (V + 127) / 128;
 }
 
 // How the backward pass is divided.
@@ -246,7 +283,7 @@ int run_dw(const XentBackward& a, const void* G, int v0, int vc, bool after_dx,
 }  // namespace
 
 size_t xent_forward_workspace(int M, int V) {
-  return size_t(M) * size_t((V + 255) / 256) * sizeof(float2);
+  return size_t(M) * size_t(stat_groups(M, V)) * sizeof(float2);
 }
 
 size_t xent_backward_workspace(int M, int V, int K) {
@@ -255,20 +292,31 @@ size_t xent_backward_workspace(int M, int V, int K) {
 }
 
 int launch_xent_forward(const XentForward& a, const DeviceInfo& dev, cudaStream_t stream) {
-  const int rc = a.M > kRowsSingle ? run_forward<XentFwdPair>(a, dev, stream)
-                                   : run_forward<XentFwdSingle>(a, dev, stream);
+  int groups = stat_groups(a.M, a.V);
+  int rc;
+  if (a.M > kRowsSingle) {
+    rc = run_forward(a, dev, stream);
+  } else {
+    // fewer CTAs where the device has fewer SMs than the workspace allows for
+    const int ctas = std::min(few_ctas(a.V), dev.num_sms);
+    groups = 4 * ctas;
+    rc = a.M <= 64 ? run_forward_few<XentFwdT<64, 4, 4>>(a, ctas, dev, stream)
+                   : run_forward_few<XentFwdT<128, 3, 8>>(a, ctas, dev, stream);
+  }
   if (rc != GEMM_OK) return rc;
+  // few rows: more threads per row
+  const int rows = a.M >= 2048 ? 32 : a.M >= 256 ? 8 : 1;
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3((a.M + 31) / 32);
-  cfg.blockDim = dim3(32 * kJoinGroups);
+  cfg.gridDim = dim3((a.M + rows - 1) / rows);
+  cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   if (cudaLaunchKernelEx(&cfg, xent_join_kernel, static_cast<const float2*>(a.workspace), a.target,
-                         a.loss, a.lse, a.M, a.V, (a.V + 255) / 256) != cudaSuccess) {
+                         a.loss, a.lse, a.M, a.V, groups, rows) != cudaSuccess) {
     cudaGetLastError();
     return GEMM_ERR_LAUNCH;
   }
