@@ -49,6 +49,8 @@ enum class Operand : int { kBF16 = 0, kNVFP4 = 1, kW4A16 = 2 };
 // kXentStatsT: the same with the roles swapped (rows of D are the vocabulary,
 //   columns the tokens), one group per CTA and lane quarter
 // kXentGradBF16: C = bf16(d_row * (exp(acc - lse_row) - [column = target_row]))
+// kXentGradTBF16: the same with the roles swapped (d, lse, target of the
+//   column; the row is the vocabulary's)
 enum class Epilogue : int {
   kStoreBF16 = 0,
   kScaledAccBF16 = 1,
@@ -58,7 +60,8 @@ enum class Epilogue : int {
   kAddF32 = 5,
   kXentStats = 6,
   kXentGradBF16 = 7,
-  kXentStatsT = 8
+  kXentStatsT = 8,
+  kXentGradTBF16 = 9
 };
 
 struct GemmParams {
@@ -125,6 +128,8 @@ struct TileCfg {
   // CHUNKED (see ChunkedCfg): a tile's K loop is cut into chunks, each with an
   // accumulator of its own that the epilogue adds up in registers.
   static constexpr bool CHUNKED = false;
+  // STREAM_A (see StreamedCfg): A is read once and leaves L2 first.
+  static constexpr bool STREAM_A = false;
   // C_T: the output is D transposed (the swapped-operand decode GEMM, whose
   // M role holds the weights and N role the few activation rows)
   static constexpr bool C_T = C_T_;
@@ -253,6 +258,12 @@ struct TileCfg {
 template <class Base>
 struct ChunkedCfg : Base {
   static constexpr bool CHUNKED = true;
+};
+
+// Few tokens: A (the weights) is read once, B (the tokens) by every cluster.
+template <class Base>
+struct StreamedCfg : ChunkedCfg<Base> {
+  static constexpr bool STREAM_A = true;
 };
 
 // Work item `tile` -> batch l, M block mb and N block nb, in grouped-M
@@ -456,6 +467,20 @@ __device__ __forceinline__ void xent_grad(uint32_t (&v)[32], float lse, float d,
     float q = fast_exp(__uint_as_float(v[i]) - lse);
     if (rel == i) q -= 1.0f;
     v[i] = __float_as_uint(i < live ? d * q : 0.0f);
+  }
+}
+
+// The same with the roles swapped: 32 logits of one vocabulary row, one token
+// each; tok[i] = (lse, d, target as int bits) of the tokens, read by every lane
+// at once.
+__device__ __forceinline__ void xent_grad_t(uint32_t (&v)[32], const float4* tok, int row) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    const float4 t = tok[i];
+    float q = fast_exp(__uint_as_float(v[i]) - t.x);
+    if (__float_as_int(t.z) == row) q -= 1.0f;
+    // d = 0 marks a token without a loss: zero whatever the logits
+    v[i] = t.y == 0.0f ? 0u : __float_as_uint(t.y * q);
   }
 }
 
@@ -782,6 +807,8 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     if (lane == 0) {
       const uint64_t pol_ab = ptx::policy_evict_last();
       (void)pol_ab;
+      const uint64_t pol_a = Cfg::STREAM_A ? ptx::policy_evict_first() : pol_ab;
+      (void)pol_a;
       int stage = 0;
       uint32_t phase = 0;
       uint32_t armed = 0, armed_parity = 0;  // bit s: stage s has a load in flight / its parity
@@ -841,7 +868,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                     ptx::tma_load_3d_hint(stage_b(stage) + at * Cfg::B_ATOM_BYTES, &tmap_b, fb,
                                           b_row + 64 * at, kb * Cfg::BK, l, pol_ab);
               } else if constexpr (kHintLoads) {
-                ptx::tma_load_3d_hint(da, &tmap_a, fb, x, a_row, l, pol_ab);
+                ptx::tma_load_3d_hint(da, &tmap_a, fb, x, a_row, l, pol_a);
                 ptx::tma_load_3d_hint(db, &tmap_b, fb, x, b_row, l, pol_ab);
               } else {
                 ptx::tma_load_3d(da, &tmap_a, fb, x, a_row, l);
@@ -890,7 +917,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                     ptx::tma_load_3d_pair_hint(stage_b(stage) + at * Cfg::B_ATOM_BYTES, &tmap_b,
                                                fb, b_row + 64 * at, kb * Cfg::BK, l, pol_ab);
               } else if constexpr (kHintLoads) {
-                ptx::tma_load_3d_pair_hint(da, &tmap_a, fb, x, a_row, l, pol_ab);
+                ptx::tma_load_3d_pair_hint(da, &tmap_a, fb, x, a_row, l, pol_a);
                 ptx::tma_load_3d_pair_hint(db, &tmap_b, fb, x, b_row, l, pol_ab);
               } else {
                 ptx::tma_load_3d_pair(da, &tmap_a, fb, x, a_row, l);
@@ -1320,6 +1347,23 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     float2 xt[XR];                                         // kXentStatsT: running statistics
     long long xt_target[XR];
     (void)xr, (void)xt, (void)xt_target;
+    // kXentGradTBF16: the tokens' values, in the output boxes' place past the
+    // two that the warps use
+    float4* tok_vals = nullptr;
+    if constexpr (EPI == Epilogue::kXentGradTBF16) {
+      static_assert(Cfg::EPI_BUFS >= 3 && Cfg::EPI_WARPS == 4 && Cfg::BN * 16 <= Cfg::EPI_BOX_BYTES,
+                    "a box of its own per warp for the tokens' values");
+      tok_vals = reinterpret_cast<float4*>(smem + (buf0 - sbase) + 2 * Cfg::EPI_BOX_BYTES);
+      for (int i = lane; i < BN; i += 32) {
+        const long long t = i < p.N ? p.target[i] : -1;
+        const int row = (t >= p.col_offset && t < (long long)p.col_offset + p.M)
+                            ? int(t - p.col_offset) : -1;
+        // without a loss: d = 0; a target past the vocabulary: NaN
+        const float d = t < 0 ? 0.0f : (t >= p.col_total ? NAN : p.row_scale[i]);
+        tok_vals[i] = make_float4(i < p.N ? p.row_lse[i] : 0.0f, d, __int_as_float(row), 0.0f);
+      }
+      __syncwarp();
+    }
     if constexpr (EPI == Epilogue::kXentStatsT) {
 #pragma unroll
       for (int i = 0; i < XR; ++i) {
@@ -1797,7 +1841,9 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         }
 #pragma unroll 1
         for (int c = 0; c < Cfg::EPI_COLS / 64; ++c, ++chunk_ctr) {
-          const int b = int(chunk_ctr % Cfg::EPI_BUFS);
+          constexpr int kBoxes =
+              EPI == Epilogue::kXentGradTBF16 ? Cfg::EPI_BUFS - 1 : Cfg::EPI_BUFS;
+          const int b = int(chunk_ctr % kBoxes);
           const uint32_t sbuf =
               last_tile ? sbase + uint32_t(e * (Cfg::EPI_COLS / 64) + c) * Cfg::EPI_BOX_BYTES
                         : buf0 + b * Cfg::EPI_BOX_BYTES;
@@ -1805,7 +1851,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
           const bool live = rows_live && col0 < p.N;
           // The TMA store that last read this buffer must be done with it.
           if (!last_tile) {
-            if (lane == 0) ptx::bulk_wait_group_read<Cfg::EPI_BUFS - 1>();
+            if (lane == 0) ptx::bulk_wait_group_read<kBoxes - 1>();
             __syncwarp();
           }
           if constexpr (EPI == Epilogue::kScaledAccBF16) {
@@ -1866,6 +1912,11 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
             xent_grad(r1, xent_lse, xent_scale, xent_rel - col0 - 32, p.N - col0 - 32);
             write_box_row<Epilogue::kStoreBF16>(smem + (sbuf - sbase) + lane * 128, lane, r0, r1,
                                                 0.0f);
+          } else if constexpr (EPI == Epilogue::kXentGradTBF16) {
+            xent_grad_t(r0, tok_vals + col0, row0 + lane);
+            xent_grad_t(r1, tok_vals + col0 + 32, row0 + lane);
+            write_box_row<Epilogue::kStoreBF16>(smem + (sbuf - sbase) + lane * 128, lane, r0, r1,
+                                                0.0f);
           } else {
             write_box_row<EPI>(smem + (sbuf - sbase) + lane * 128, lane, r0, r1, p.scale);
           }
@@ -1873,7 +1924,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
           __syncwarp();
           if (lane == 0) {
             // the gradient tile is read back by the next launches: no evict-first hint
-            if constexpr (EPI == Epilogue::kXentGradBF16)
+            if constexpr (EPI == Epilogue::kXentGradBF16 || EPI == Epilogue::kXentGradTBF16)
               ptx::tma_store_3d(&tmap_c, sbuf, col0, row0, l);
             else
               store_box(sbuf, col0, row0, l);

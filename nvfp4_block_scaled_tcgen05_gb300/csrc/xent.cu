@@ -24,26 +24,39 @@ namespace gb300 {
 // Forward, tokens on the MMA's M side: 256 x 256 pair tiles; 8 epilogue warps
 // hold a tile's sums over the K chunks, 128 columns each, in registers.
 using XentFwdPair = ChunkedCfg<TileCfg<Operand::kBF16, 2, 256, 3, 8, 0, true, false, 2>>;
-// Forward of few tokens: the vocabulary on the M side (128 rows per CTA), the
-// tokens on the N side, so that the MMA's time shrinks with the tokens and the
-// kernel streams W.
-template <int BN, int STAGES, int EPI_WARPS>
-using XentFwdT = ChunkedCfg<TileCfg<Operand::kBF16, 1, BN, STAGES, EPI_WARPS, 1, true, false, 2>>;
+// Forward of few tokens: the vocabulary on the M side (256 rows per CTA pair),
+// the tokens on the N side, so that the MMA's time shrinks with the tokens and
+// the kernel streams W at the rate of memory (64 x 131072 x 4096: 160 us, 6.7
+// TB/s).  Pairs halve each CTA's share of the tokens; single CTAs took 209 us
+// with one token.
+template <int BN, int STAGES>
+using XentFwdT = StreamedCfg<TileCfg<Operand::kBF16, 2, BN, STAGES, 4, 1, true, false, 2>>;
 template <int CG, int STAGES, int KSUB, bool BMN, bool AMN>
 using XentCfg =
     TileCfg<Operand::kBF16, CG, 256, STAGES, 4, 2, true, false, KSUB, BMN, false, AMN, true>;
 using XentGradPair = XentCfg<2, 3, 2, false, false>;
-using XentGradSingle = XentCfg<1, 4, 1, false, false>;
 using XentDxPair = XentCfg<2, 3, 2, true, false>;
-using XentDxSingle = XentCfg<1, 4, 1, true, false>;
 using XentDwPair = XentCfg<2, 3, 2, true, true>;
+// Few tokens: G is formed transposed ([vocabulary][tokens]) by the roles of
+// XentFwdT, so dX reads it MN-major and dW K-major.
+template <class Base>
+struct StreamAOnce : Base {
+  static constexpr bool STREAM_A = true;
+};
+template <int BN, int STAGES>
+using XentGradT = StreamAOnce<
+    TileCfg<Operand::kBF16, 2, BN, STAGES, 4, 3, true, false, 2, false, false, false, true>>;
+using XentDxFew = XentCfg<1, 4, 1, true, true>;
+// dW of few tokens is bound by writing it: 8 epilogue warps with 4 boxes each
+// keep more of that stream in flight (with 256 tokens the two are even).
+using XentDwFew =
+    TileCfg<Operand::kBF16, 2, 256, 3, 8, 4, true, false, 1, true, false, false, true>;
 
 namespace {
 
-constexpr int kRowsSingle = 128;  // up to this many rows one CTA's 128-row tiles hold them all
+constexpr int kRowsFew = 128;  // up to this many tokens, they take the MMA's N side
 
-constexpr int kChunkK = 512;     // K per accumulator, see ChunkedCfg
-constexpr int kChunkKFew = 256;  // the same where the MMA has time to spare
+constexpr int kChunkK = 512;  // K per accumulator, see ChunkedCfg
 
 // Joins the groups' statistics of each row.  A block takes `rows` (a power of
 // two) rows; thread t takes row t % rows and the groups t / rows,
@@ -132,25 +145,31 @@ int run_forward(const XentForward& a, const DeviceInfo& dev, cudaStream_t stream
 }
 
 template <class Cfg>
-int run_forward_few(const XentForward& a, int ctas, const DeviceInfo& dev, cudaStream_t stream) {
+int run_forward_few(const XentForward& a, int* groups, const DeviceInfo& dev,
+                    cudaStream_t stream) {
   CUtensorMap tx, tw;
   int rc = encode_k_major<Cfg>(&tw, a.W, a.V, a.K, Cfg::BM);
   if (rc == GEMM_OK) rc = encode_k_major<Cfg>(&tx, a.X, a.M, a.K, Cfg::B_ROWS);
   if (rc != GEMM_OK) return rc;
   GemmParams p = base_params<Cfg>(a.V, a.M, a.K, dev);
-  set_chunks<Cfg>(p, kChunkKFew);
+  set_chunks<Cfg>(p, kChunkK);
   p.target = a.target;
   p.stats = static_cast<float2*>(a.workspace);
   p.picked = a.loss;
-  return launch_tcgen05<Cfg, Epilogue::kXentStatsT>(tw, tx, tw, tw, tw, p, dev, stream, ctas);
+  // fewer clusters where the device holds fewer than the workspace allows for
+  const int clusters =
+      std::min(*groups / (4 * Cfg::CLUSTER), tcgen05_cluster_capacity<Cfg, Epilogue::kXentStatsT>(dev));
+  if (clusters <= 0) return GEMM_ERR_LAUNCH;
+  *groups = clusters * 4 * Cfg::CLUSTER;
+  return launch_tcgen05<Cfg, Epilogue::kXentStatsT>(tw, tx, tw, tw, tw, p, dev, stream, clusters);
 }
 
 // Column groups that the forward statistics come in: one per 128 columns,
 // or (few rows) four per CTA, of at most kFewCtas CTAs.
 constexpr int kFewCtas = 152;
-int few_ctas(int V) { return std::min(kFewCtas, (V + 127) / 128); }
+int few_ctas(int V) { return std::min(kFewCtas, 2 * ((V + 255) / 256)); }
 int stat_groups(int M, int V) {
-  return M <= kRowsSingle ? 4 * few_ctas(V) : (V + 127) / 128;
+  return M <= kRowsFew ? 4 * few_ctas(V) : (V + 127) / 128;
 }
 
 // How the backward pass is divided.
@@ -166,6 +185,8 @@ struct XentPlan {
 constexpr int kPairs = 76;  // CTA pairs of a GB300
 constexpr long long kPieceBytes = 128ll << 20;
 constexpr int kMinPiece = 4096;
+
+int round64(int n) { return (n + 63) / 64 * 64; }
 
 XentPlan make_plan(int M, int V, int K) {
   XentPlan q{};
@@ -193,15 +214,16 @@ XentPlan make_plan(int M, int V, int K) {
   }
   q.piece = int(std::min<long long>(V, (long long)nb * 256));
   q.pieces = (V + q.piece - 1) / q.piece;
-  q.g_bytes = size_t(M) * size_t((q.piece + 63) / 64 * 64) * 2;
+  q.g_bytes = M <= kRowsFew ? size_t(q.piece) * size_t(round64(M)) * 2
+                            : size_t(M) * size_t(round64(q.piece)) * 2;
   q.g_bytes = (q.g_bytes + 255) / 256 * 256;
   q.g_bufs = q.pieces > 1 ? 2 : 1;
   // dX has (M / rows) x (K / 256) tiles; with fewer than the SM groups its K
   // loop (the vocabulary) is divided and the parts are summed in order
-  const bool single = M <= kRowsSingle;
-  const int units = single ? 2 * kPairs : kPairs;
-  const int tiles = (single ? 1 : mb) * ((K + 255) / 256);
-  const int bk = single ? XentDxSingle::BK : XentDxPair::BK;
+  const bool few = M <= kRowsFew;
+  const int units = few ? 2 * kPairs : kPairs;
+  const int tiles = (few ? 1 : mb) * ((K + 255) / 256);
+  const int bk = few ? XentDxFew::BK : XentDxPair::BK;
   const int nkb = (q.piece + bk - 1) / bk;
   int s = tiles >= units ? 1 : units / tiles;
   s = std::max(1, std::min(s, nkb / 4));
@@ -211,38 +233,48 @@ XentPlan make_plan(int M, int V, int K) {
   return q;
 }
 
+// A piece of the vocabulary and its G: [M][ld], or with few tokens transposed,
+// [cols][ld].
+struct Piece {
+  void* G;
+  int v0, cols, ld;
+};
+
 // G of one piece.
-template <class Cfg>
-int run_grad(const XentBackward& a, void* G, int v0, int vc, bool late, const DeviceInfo& dev,
+template <class Cfg, bool kT>
+int run_grad(const XentBackward& a, const Piece& pc, bool late, const DeviceInfo& dev,
              cudaStream_t stream) {
   CUtensorMap tx, tw, tg;
-  const uint16_t* W = static_cast<const uint16_t*>(a.W) + size_t(v0) * a.K;
-  const int ldg = (vc + 63) / 64 * 64;
-  int rc = encode_k_major<Cfg>(&tx, a.X, a.M, a.K, Cfg::BM);
-  if (rc == GEMM_OK) rc = encode_k_major<Cfg>(&tw, W, vc, a.K, Cfg::B_ROWS);
-  if (rc == GEMM_OK) rc = encode_k_major<Cfg>(&tg, G, a.M, ldg, 32);
+  const uint16_t* W = static_cast<const uint16_t*>(a.W) + size_t(pc.v0) * a.K;
+  int rc = encode_k_major<Cfg>(&tx, a.X, a.M, a.K, kT ? Cfg::B_ROWS : Cfg::BM);
+  if (rc == GEMM_OK) rc = encode_k_major<Cfg>(&tw, W, pc.cols, a.K, kT ? Cfg::BM : Cfg::B_ROWS);
+  if (rc == GEMM_OK) rc = encode_k_major<Cfg>(&tg, pc.G, kT ? pc.cols : a.M, pc.ld, 32);
   if (rc != GEMM_OK) return rc;
-  GemmParams p = base_params<Cfg>(a.M, vc, a.K, dev);
+  GemmParams p = kT ? base_params<Cfg>(pc.cols, a.M, a.K, dev)
+                    : base_params<Cfg>(a.M, pc.cols, a.K, dev);
   p.target = a.target;
   p.row_lse = a.lse;
   p.row_scale = a.dloss;
-  p.col_offset = v0;
+  p.col_offset = pc.v0;
   p.col_total = a.V;
   p.late_wait = late;
-  return launch_tcgen05<Cfg, Epilogue::kXentGradBF16>(tx, tw, tg, tx, tx, p, dev, stream);
+  if constexpr (kT)
+    return launch_tcgen05<Cfg, Epilogue::kXentGradTBF16>(tw, tx, tg, tw, tw, p, dev, stream);
+  else
+    return launch_tcgen05<Cfg, Epilogue::kXentGradBF16>(tx, tw, tg, tx, tx, p, dev, stream);
 }
 
-// One piece's term of dX: G [M][vc] . W_piece [vc][K].
+// One piece's term of dX: G [M][cols] . W_piece [cols][K].
 template <class Cfg>
-int run_dx(const XentBackward& a, const XentPlan& q, const void* G, float* acc, int v0, int vc,
+int run_dx(const XentBackward& a, const XentPlan& q, const Piece& pc, float* acc,
            const DeviceInfo& dev, cudaStream_t stream) {
   CUtensorMap tg, tw, tc;
-  const uint16_t* W = static_cast<const uint16_t*>(a.W) + size_t(v0) * a.K;
-  const int ldg = (vc + 63) / 64 * 64;
-  int rc = encode_k_major<Cfg>(&tg, G, a.M, ldg, Cfg::BM);
-  if (rc == GEMM_OK) rc = encode_k_major<Cfg>(&tw, W, vc, a.K, Cfg::BK);
+  const uint16_t* W = static_cast<const uint16_t*>(a.W) + size_t(pc.v0) * a.K;
+  int rc = Cfg::A_MN ? encode_k_major<Cfg>(&tg, pc.G, pc.cols, pc.ld, Cfg::BK)
+                     : encode_k_major<Cfg>(&tg, pc.G, a.M, pc.ld, Cfg::BM);
+  if (rc == GEMM_OK) rc = encode_k_major<Cfg>(&tw, W, pc.cols, a.K, Cfg::BK);
   if (rc != GEMM_OK) return rc;
-  GemmParams p = base_params<Cfg>(a.M, a.K, vc, dev);
+  GemmParams p = base_params<Cfg>(a.M, a.K, pc.cols, dev);
   p.trigger_late = 1;
   if (q.dx_bytes == 0) {
     rc = encode_k_major<Cfg>(&tc, a.dX, a.M, a.K, 32);
@@ -259,25 +291,74 @@ int run_dx(const XentBackward& a, const XentPlan& q, const void* G, float* acc, 
   p.k_splits = (p.num_k_blocks + p.kb_per_split - 1) / p.kb_per_split;
   p.L = p.k_splits;
   p.total_tiles *= p.k_splits;
-  p.accumulate = v0 > 0;
+  p.accumulate = pc.v0 > 0;
   return launch_tcgen05<Cfg, Epilogue::kAddF32>(tg, tw, tc, tg, tg, p, dev, stream);
 }
 
-// The piece's rows of dW: G^T [vc][M] . X [M][K].
-int run_dw(const XentBackward& a, const void* G, int v0, int vc, bool after_dx,
-           const DeviceInfo& dev, cudaStream_t stream) {
-  using Cfg = XentDwPair;
+// The piece's rows of dW: G^T [cols][M] . X [M][K].
+template <class Cfg>
+int run_dw(const XentBackward& a, const Piece& pc, bool after_dx, const DeviceInfo& dev,
+           cudaStream_t stream) {
   CUtensorMap tg, tx, tc;
-  uint16_t* dW = static_cast<uint16_t*>(a.dW) + size_t(v0) * a.K;
-  const int ldg = (vc + 63) / 64 * 64;
-  int rc = encode_k_major<Cfg>(&tg, G, a.M, ldg, Cfg::BK);
+  uint16_t* dW = static_cast<uint16_t*>(a.dW) + size_t(pc.v0) * a.K;
+  int rc = Cfg::A_MN ? encode_k_major<Cfg>(&tg, pc.G, a.M, pc.ld, Cfg::BK)
+                     : encode_k_major<Cfg>(&tg, pc.G, pc.cols, pc.ld, Cfg::BM);
   if (rc == GEMM_OK) rc = encode_k_major<Cfg>(&tx, a.X, a.M, a.K, Cfg::BK);
-  if (rc == GEMM_OK) rc = encode_k_major<Cfg>(&tc, dW, vc, a.K, 32);
+  if (rc == GEMM_OK) rc = encode_k_major<Cfg>(&tc, dW, pc.cols, a.K, 32);
   if (rc != GEMM_OK) return rc;
-  GemmParams p = base_params<Cfg>(vc, a.K, a.M, dev);
+  GemmParams p = base_params<Cfg>(pc.cols, a.K, a.M, dev);
   p.late_wait = after_dx;
   p.trigger_late = !after_dx;
   return launch_tcgen05<Cfg, Epilogue::kStoreBF16>(tg, tx, tc, tg, tg, p, dev, stream);
+}
+
+// out[i] = bf16(acc[0][i] + acc[1][i] + ...), FP32 adds in slot order; four
+// outputs per thread, the loads of eight slots in flight at a time.
+constexpr int kSumThreads = 128;
+__global__ void __launch_bounds__(kSumThreads)
+    xent_sum_kernel(const float* __restrict__ acc, uint16_t* __restrict__ out, size_t n, int slots) {
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  const size_t step = size_t(gridDim.x) * kSumThreads;
+  for (size_t i = size_t(blockIdx.x) * kSumThreads + threadIdx.x; i < n / 4; i += step) {
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int b = 0; b < slots; b += 8) {
+      float4 v[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        if (b + u < slots) v[u] = __ldcg(reinterpret_cast<const float4*>(acc + size_t(b + u) * n) + i);
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        if (b + u < slots) {
+          s.x += v[u].x;
+          s.y += v[u].y;
+          s.z += v[u].z;
+          s.w += v[u].w;
+        }
+    }
+    reinterpret_cast<uint2*>(out)[i] =
+        make_uint2(pack_bf16x2(__float_as_uint(s.x), __float_as_uint(s.y)),
+                   pack_bf16x2(__float_as_uint(s.z), __float_as_uint(s.w)));
+  }
+}
+
+template <class Kernel, class... Args>
+int launch_dependent(Kernel kernel, long long grid, int threads, cudaStream_t stream,
+                     Args... args) {
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(unsigned(grid));
+  cfg.blockDim = dim3(threads);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) {
+    cudaGetLastError();
+    return GEMM_ERR_LAUNCH;
+  }
+  return GEMM_OK;
 }
 
 }  // namespace
@@ -294,33 +375,15 @@ size_t xent_backward_workspace(int M, int V, int K) {
 int launch_xent_forward(const XentForward& a, const DeviceInfo& dev, cudaStream_t stream) {
   int groups = stat_groups(a.M, a.V);
   int rc;
-  if (a.M > kRowsSingle) {
-    rc = run_forward(a, dev, stream);
-  } else {
-    // fewer CTAs where the device has fewer SMs than the workspace allows for
-    const int ctas = std::min(few_ctas(a.V), dev.num_sms);
-    groups = 4 * ctas;
-    rc = a.M <= 64 ? run_forward_few<XentFwdT<64, 4, 4>>(a, ctas, dev, stream)
-                   : run_forward_few<XentFwdT<128, 3, 8>>(a, ctas, dev, stream);
-  }
+  if (a.M > kRowsFew) rc = run_forward(a, dev, stream);
+  else if (a.M <= 64) rc = run_forward_few<XentFwdT<64, 4>>(a, &groups, dev, stream);
+  else rc = run_forward_few<XentFwdT<128, 3>>(a, &groups, dev, stream);
   if (rc != GEMM_OK) return rc;
   // few rows: more threads per row
   const int rows = a.M >= 2048 ? 32 : a.M >= 256 ? 8 : 1;
-  cudaLaunchConfig_t cfg{};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3((a.M + rows - 1) / rows);
-  cfg.blockDim = dim3(kJoinThreads);
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, xent_join_kernel, static_cast<const float2*>(a.workspace), a.target,
-                         a.loss, a.lse, a.M, a.V, groups, rows) != cudaSuccess) {
-    cudaGetLastError();
-    return GEMM_ERR_LAUNCH;
-  }
-  return GEMM_OK;
+  return launch_dependent(xent_join_kernel, (a.M + rows - 1) / rows, kJoinThreads, stream,
+                          static_cast<const float2*>(a.workspace), a.target, a.loss, a.lse, a.M,
+                          a.V, groups, rows);
 }
 
 // Order of the grids, and why each may start when it does ("waits" = its
@@ -336,23 +399,36 @@ int launch_xent_forward(const XentForward& a, const DeviceInfo& dev, cudaStream_
 // also has everything before it.
 int launch_xent_backward(const XentBackward& a, const DeviceInfo& dev, cudaStream_t stream) {
   const XentPlan q = make_plan(a.M, a.V, a.K);
-  const bool single = a.M <= kRowsSingle;
+  const bool few = a.M <= kRowsFew;
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   float* acc = reinterpret_cast<float*>(ws + q.g_bytes * q.g_bufs);
   for (int i = 0; i < q.pieces; ++i) {
-    const int v0 = i * q.piece;
-    const int vc = std::min(q.piece, a.V - v0);
-    void* G = ws + q.g_bytes * (i & (q.g_bufs - 1));
-    int rc = single ? run_grad<XentGradSingle>(a, G, v0, vc, i > 0, dev, stream)
-                    : run_grad<XentGradPair>(a, G, v0, vc, i > 0, dev, stream);
+    Piece pc;
+    pc.G = ws + q.g_bytes * (i & (q.g_bufs - 1));
+    pc.v0 = i * q.piece;
+    pc.cols = std::min(q.piece, a.V - pc.v0);
+    pc.ld = round64(few ? a.M : pc.cols);
+    int rc;
+    if (!few) rc = run_grad<XentGradPair, false>(a, pc, i > 0, dev, stream);
+    else if (a.M <= 64) rc = run_grad<XentGradT<64, 4>, true>(a, pc, i > 0, dev, stream);
+    else rc = run_grad<XentGradT<128, 3>, true>(a, pc, i > 0, dev, stream);
     if (rc == GEMM_OK && a.dX)
-      rc = single ? run_dx<XentDxSingle>(a, q, G, acc, v0, vc, dev, stream)
-                  : run_dx<XentDxPair>(a, q, G, acc, v0, vc, dev, stream);
-    if (rc == GEMM_OK && a.dW) rc = run_dw(a, G, v0, vc, a.dX != nullptr, dev, stream);
+      rc = few ? run_dx<XentDxFew>(a, q, pc, acc, dev, stream)
+               : run_dx<XentDxPair>(a, q, pc, acc, dev, stream);
+    if (rc == GEMM_OK && a.dW) {
+      rc = few ? run_dw<XentDwFew>(a, pc, a.dX != nullptr, dev, stream)
+               : run_dw<XentDwPair>(a, pc, a.dX != nullptr, dev, stream);
+    }
     if (rc != GEMM_OK) return rc;
   }
-  if (a.dX && q.dx_bytes)
-    return launch_splitk_reduce(acc, a.dX, size_t(a.M) * a.K, q.splits, dev, stream);
+  if (a.dX && q.dx_bytes) {
+    const size_t n = size_t(a.M) * a.K;
+    const long long grid = std::min<long long>((n / 4 + kSumThreads - 1) / kSumThreads,
+                                               (long long)dev.num_sms * 16);
+    return launch_dependent(xent_sum_kernel, grid, kSumThreads, stream,
+                            static_cast<const float*>(acc), static_cast<uint16_t*>(a.dX), n,
+                            q.splits);
+  }
   return GEMM_OK;
 }
 
