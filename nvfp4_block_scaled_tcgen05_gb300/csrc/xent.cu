@@ -185,6 +185,7 @@ struct XentPlan {
 constexpr int kPairs = 76;  // CTA pairs of a GB300
 constexpr long long kPieceBytes = 128ll << 20;
 constexpr int kMinPiece = 4096;
+constexpr int kMaxSplits = 32;
 
 int round64(int n) { return (n + 63) / 64 * 64; }
 
@@ -218,17 +219,29 @@ XentPlan make_plan(int M, int V, int K) {
                             : size_t(M) * size_t(round64(q.piece)) * 2;
   q.g_bytes = (q.g_bytes + 255) / 256 * 256;
   q.g_bufs = q.pieces > 1 ? 2 : 1;
-  // dX has (M / rows) x (K / 256) tiles; with fewer than the SM groups its K
-  // loop (the vocabulary) is divided and the parts are summed in order
+  // dX has (M / rows) x (K / 256) tiles, often few rounds of CTA pairs with
+  // the last one part empty.  Its K loop (the vocabulary) is divided so that
+  // the rounds fill; the parts are summed in order.  Cost in K blocks (0.68 us
+  // of a pair's MMAs): the rounds' K loops, two more per tile for filling the
+  // pipeline and handing over, and writing and adding the parts at 5 TB/s
+  // (4096 x 131072 x 4096: 256 tiles in 4 rounds took 7406 us, 512 in 7 7217).
   const bool few = M <= kRowsFew;
   const int units = few ? 2 * kPairs : kPairs;
-  const int tiles = (few ? 1 : mb) * ((K + 255) / 256);
+  const long long tiles = (long long)(few ? 1 : mb) * ((K + 255) / 256);
   const int bk = few ? XentDxFew::BK : XentDxPair::BK;
   const int nkb = (q.piece + bk - 1) / bk;
-  int s = tiles >= units ? 1 : units / tiles;
-  s = std::max(1, std::min(s, nkb / 4));
-  const int per = (nkb + s - 1) / s;
-  q.splits = (nkb + per - 1) / per;
+  q.splits = 1;
+  double best = 1e300;
+  for (int want = 1; want <= kMaxSplits && want <= std::max(1, nkb / 4); ++want) {
+    const int per = (nkb + want - 1) / want;
+    const int s = (nkb + per - 1) / per;
+    const double cost = double((tiles * s + units - 1) / units) * (per + 2) +
+                        double(s) * M * double(K) * 8.0 / 3.4e6;
+    if (cost < best) {
+      best = cost;
+      q.splits = s;
+    }
+  }
   q.dx_bytes = (q.pieces == 1 && q.splits == 1) ? 0 : size_t(q.splits) * M * size_t(K) * 4;
   return q;
 }
