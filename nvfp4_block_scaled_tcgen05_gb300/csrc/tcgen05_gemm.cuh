@@ -254,7 +254,7 @@ struct TileCfg {
 // The tensor core adds into its accumulator with truncation, so a long K loop
 // drifts toward zero by about K / 16 half units of the running sum's last
 // place (lse of 4096-deep logits was off by 2.6e-6 of its value).  Chunks of a
-// few hundred K, added with rounding, keep the error at the chunk's length.
+// some hundred K, added with rounding, keep the error at the chunk's length.
 template <class Base>
 struct ChunkedCfg : Base {
   static constexpr bool CHUNKED = true;
@@ -291,7 +291,8 @@ struct Seg {
 };
 
 // Segment `idx` of cluster c among C clusters; false past the end.  Every
-// role of the kernel walks this same sequence.
+// role of the kernel walks this same sequence (CHUNKED: the epilogue, kChunks,
+// takes a tile's chunks one by one, the others whole tiles).
 //  * plain / split-K: tile = c + idx*C; with split-K the batch slot of the
 //    tile selects its K blocks.
 //  * stream-K (p.sk = P): the first floor(tiles/C) rounds are whole tiles
@@ -299,9 +300,9 @@ struct Seg {
 //    are split evenly over clusters 0..P-1, cluster c taking iterations
 //    [T*c/P, T*(c+1)/P) in order, which makes at most its first and last
 //    segment partial.
-template <class Cfg>
+template <class Cfg, bool kChunks = false>
 __device__ __forceinline__ bool seg_at(const GemmParams& p, int c, int C, int idx, Seg& s) {
-  if constexpr (Cfg::CHUNKED) {
+  if constexpr (kChunks) {
     const int q = idx / p.chunks;
     const long long t = (long long)c + (long long)q * C;
     if (t >= p.total_tiles) return false;
@@ -1041,14 +1042,16 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
       Seg sg;
       int it = 0;
       for (int idx = 0; ok && seg_at<Cfg>(p, cluster_id, num_clusters, idx, sg); ++idx, ++it) {
-        const int acc = it % Cfg::NUM_ACC;
+        int acc = it % Cfg::NUM_ACC;
+        int chunk_begin = 0, chunk_end = Cfg::CHUNKED ? p.k_chunk : 0;
+        (void)chunk_begin, (void)chunk_end;
         // the accumulator's previous tile must have been read by the epilogue
         if (!wait_bar(acc_empty(acc), (uint32_t(it / Cfg::NUM_ACC) & 1u) ^ 1u, w, 2)) {
           ok = false;
           break;
         }
         ptx::tc_fence_after();
-        const uint32_t d_tmem = tmem_base + uint32_t(acc * BN);
+        uint32_t d_tmem = tmem_base + uint32_t(acc * BN);
         for (int kb = sg.kb0; kb < sg.kb1; ++kb) {
           if (!ready_wait(stage, phase, w)) {
             ok = false;
@@ -1061,7 +1064,26 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
           const uint64_t soff = uint64_t(uint32_t(stage) * uint32_t(Cfg::STAGE_BYTES >> 4));
           const uint32_t sfa_t = sf_t0 + uint32_t(stage * Cfg::SF_COLS);
           const int nsteps = (kb == tail_kb) ? tail_steps : Cfg::KSTEPS;
-          const bool first_kb = (kb == sg.kb0);
+          if constexpr (Cfg::CHUNKED) {
+            // the next chunk's accumulator, handed back long ago as a rule
+            // (the epilogue reads one in about 1500 cycles, a 512-deep chunk
+            // takes 5200).  In the K loop itself, since a gap of the issuer is
+            // a gap of the tensor pipe.
+            if (kb == chunk_end) {
+              ptx::tc_commit<CG>(acc_full(acc), pair_mask);
+              ++it;
+              acc = it % Cfg::NUM_ACC;
+              if (!wait_bar(acc_empty(acc), (uint32_t(it / Cfg::NUM_ACC) & 1u) ^ 1u, w, 2)) {
+                ok = false;
+                break;
+              }
+              ptx::tc_fence_after();
+              d_tmem = tmem_base + uint32_t(acc * BN);
+              chunk_begin = kb;
+              chunk_end += p.k_chunk;
+            }
+          }
+          const bool first_kb = (kb == (Cfg::CHUNKED ? chunk_begin : sg.kb0));
 #pragma unroll
           for (int j = 0; j < Cfg::KSTEPS; ++j) {
             if constexpr (!Cfg::SF_WARP) copy_scales_for(sfa_t, soff, j);
@@ -1418,7 +1440,8 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
       for (int k = 0; k < LA_SETS - 1; ++k)
         if (seg_at<Cfg>(p, cluster_id, num_clusters, k, sg)) prefetch_out(sg, k);
     }
-    for (int idx = 0; ok && seg_at<Cfg>(p, cluster_id, num_clusters, idx, sg); ++idx, ++it) {
+    for (int idx = 0; ok && seg_at<Cfg, Cfg::CHUNKED>(p, cluster_id, num_clusters, idx, sg);
+         ++idx, ++it) {
       int l, mb, nb;
       decode_tile<Cfg>(sg.tile, p, l, mb, nb);
       const int acc = it % Cfg::NUM_ACC;

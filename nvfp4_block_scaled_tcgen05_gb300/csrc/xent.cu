@@ -56,7 +56,11 @@ namespace {
 
 constexpr int kRowsFew = 128;  // up to this many tokens, they take the MMA's N side
 
-constexpr int kChunkK = 512;  // K per accumulator, see ChunkedCfg
+// K per accumulator, see ChunkedCfg.  8192 x 65536 x 4096 under the power cap:
+// 2530 us with 512, 2470 with 1024 (lse off by 6e-7 of its value, as in plain
+// FP32), 2445 with 2048 (1.3e-6): the extra reads of the accumulators cost
+// power.  Few tokens leave the power to spare.
+constexpr int kChunkK = 1024, kChunkKFew = 512;
 
 // Joins the groups' statistics of each row.  A block takes `rows` (a power of
 // two) rows; thread t takes row t % rows and the groups t / rows,
@@ -152,7 +156,7 @@ int run_forward_few(const XentForward& a, int* groups, const DeviceInfo& dev,
   if (rc == GEMM_OK) rc = encode_k_major<Cfg>(&tx, a.X, a.M, a.K, Cfg::B_ROWS);
   if (rc != GEMM_OK) return rc;
   GemmParams p = base_params<Cfg>(a.V, a.M, a.K, dev);
-  set_chunks<Cfg>(p, kChunkK);
+  set_chunks<Cfg>(p, kChunkKFew);
   p.target = a.target;
   p.stats = static_cast<float2*>(a.workspace);
   p.picked = a.loss;
