@@ -397,46 +397,34 @@ def _on_device(name: str, device, t: torch.Tensor, dtype, shape) -> None:
     raise ValueError(f"{name} must be contiguous")
 
 
-class _Call:
-    """Device and stream of one call on tensors of `device`: allocates outputs
-    and workspaces on the call's stream, so that the caching allocator does not
-    hand their memory out again before the call is done, and makes the device
-    current while the library runs."""
-    __slots__ = ("device", "stream", "pointer")
+def _context(device, stream):
+    """The context that a call on tensors of `device` belongs in: the given
+    stream (its allocations too, so that the caching allocator does not hand
+    their memory out again before the call is done), or the tensors' device
+    where another one is current.  None: it may run as it is."""
+    if stream is not None:
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(_stream_ptr(stream), device=device)
+        return torch.cuda.stream(stream)
+    if torch.cuda.current_device() != device.index:
+        return torch.cuda.device(device)
+    return None
 
-    def __init__(self, device, stream):
-        self.device = device
-        self.stream = stream
-        if stream is None:
-            self.pointer = torch._C._cuda_getCurrentRawStream(device.index)
-        else:
-            self.pointer = _stream_ptr(stream)
-            if not isinstance(stream, torch.cuda.Stream):
-                self.stream = torch.cuda.ExternalStream(self.pointer, device=device)
 
-    def empty(self, shape, dtype):
-        if self.stream is None:
-            return torch.empty(shape, dtype=dtype, device=self.device)
-        with torch.cuda.stream(self.stream):
-            return torch.empty(shape, dtype=dtype, device=self.device)
+def _run(name: str, device, *args) -> None:
+    """The C entry point `name` on the current stream."""
+    rc = getattr(_lib or load(), name)(*args, torch._C._cuda_getCurrentRawStream(device.index))
+    if rc:
+        raise GemmError(rc, name)
 
-    def workspace(self, given, need: int):
-        """The caller's workspace, or one allocated here (None where none is needed)."""
-        if given is None:
-            return self.empty((need,), torch.uint8) if need else None
-        if not (given.device == self.device and given.is_contiguous()):
-            raise ValueError(f"workspace must be a contiguous tensor on {self.device}")
-        return given
 
-    def run(self, name: str, *args) -> None:
-        fn = getattr(_lib or load(), name)
-        if torch.cuda.current_device() == self.device.index:
-            rc = fn(*args, self.pointer)
-        else:
-            with torch.cuda.device(self.device):
-                rc = fn(*args, self.pointer)
-        if rc:
-            raise GemmError(rc, name)
+def _workspace(given, need: int, device):
+    """The caller's workspace, or one allocated here (None where none is needed)."""
+    if given is None:
+        return torch.empty((need,), dtype=torch.uint8, device=device) if need else None
+    if not (given.device == device and given.is_contiguous()):
+        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+    return given
 
 
 def _bytes_of(t) -> int:
@@ -473,18 +461,22 @@ def gemm_bf16_nt_xent(X: torch.Tensor, W: torch.Tensor, target: torch.Tensor,
     loss.  Keep lse for gemm_bf16_nt_xent_backward.
     """
     M, V, K = _xent_inputs(X, W, target)
-    call = _Call(X.device, stream)
+    device, f32 = X.device, torch.float32
+    elsewhere = _context(device, stream)
+    if elsewhere is not None:
+        with elsewhere:
+            return gemm_bf16_nt_xent(X, W, target, loss, lse, workspace)
     if loss is None:
-        loss = call.empty((M,), torch.float32)
+        loss = torch.empty((M,), dtype=f32, device=device)
     else:
-        _on_device("loss", X.device, loss, torch.float32, (M,))
+        _on_device("loss", device, loss, f32, (M,))
     if lse is None:
-        lse = call.empty((M,), torch.float32)
+        lse = torch.empty((M,), dtype=f32, device=device)
     else:
-        _on_device("lse", X.device, lse, torch.float32, (M,))
-    workspace = call.workspace(workspace, gemm_bf16_nt_xent_workspace_bytes(M, V))
-    call.run("gemm_bf16_nt_xent", X.data_ptr(), W.data_ptr(), target.data_ptr(), loss.data_ptr(),
-             lse.data_ptr(), _ptr(workspace), _bytes_of(workspace), M, V, K)
+        _on_device("lse", device, lse, f32, (M,))
+    workspace = _workspace(workspace, gemm_bf16_nt_xent_workspace_bytes(M, V), device)
+    _run("gemm_bf16_nt_xent", device, X.data_ptr(), W.data_ptr(), target.data_ptr(),
+         loss.data_ptr(), lse.data_ptr(), _ptr(workspace), _bytes_of(workspace), M, V, K)
     return loss, lse
 
 
@@ -507,19 +499,23 @@ def gemm_bf16_nt_xent_backward(X: torch.Tensor, W: torch.Tensor, target: torch.T
     _on_device("dloss", device, dloss, torch.float32, (M,))
     if not (need_dx or need_dw or dX is not None or dW is not None):
         raise ValueError("neither dX nor dW is needed")
-    call = _Call(device, stream)
+    elsewhere = _context(device, stream)
+    if elsewhere is not None:
+        with elsewhere:
+            return gemm_bf16_nt_xent_backward(X, W, target, lse, dloss, dX, dW, workspace,
+                                              need_dx=need_dx, need_dw=need_dw)
     if dX is not None:
         _on_device("dX", device, dX, torch.bfloat16, (M, K))
     elif need_dx:
-        dX = call.empty((M, K), torch.bfloat16)
+        dX = torch.empty((M, K), dtype=torch.bfloat16, device=device)
     if dW is not None:
         _on_device("dW", device, dW, torch.bfloat16, (V, K))
     elif need_dw:
-        dW = call.empty((V, K), torch.bfloat16)
-    workspace = call.workspace(workspace, gemm_bf16_nt_xent_backward_workspace_bytes(M, V, K))
-    call.run("gemm_bf16_nt_xent_backward", X.data_ptr(), W.data_ptr(), target.data_ptr(),
-             lse.data_ptr(), dloss.data_ptr(), _ptr(dX), _ptr(dW), _ptr(workspace),
-             _bytes_of(workspace), M, V, K)
+        dW = torch.empty((V, K), dtype=torch.bfloat16, device=device)
+    workspace = _workspace(workspace, gemm_bf16_nt_xent_backward_workspace_bytes(M, V, K), device)
+    _run("gemm_bf16_nt_xent_backward", device, X.data_ptr(), W.data_ptr(), target.data_ptr(),
+         lse.data_ptr(), dloss.data_ptr(), _ptr(dX), _ptr(dW), _ptr(workspace),
+         _bytes_of(workspace), M, V, K)
     return dX, dW
 
 
@@ -567,19 +563,27 @@ def router_topk(logits: torch.Tensor, k: int, valid: torch.Tensor | None = None,
     padding row.  losses = [balance, z].
     """
     M, E, ld = _logit_rows(logits)
+    device, empty, f32, i32 = logits.device, torch.empty, torch.float32, torch.int32
     if valid is not None:
         valid = valid.view(torch.uint8) if valid.dtype == torch.bool else valid
-        _on_device("valid", logits.device, valid, torch.uint8, (M,))
+        _on_device("valid", device, valid, torch.uint8, (M,))
     if not 1 <= k <= E:
         raise ValueError(f"k must be in 1..{E}, got {k}")
-    call = _Call(logits.device, stream)
-    empty, f32, i32 = call.empty, torch.float32, torch.int32
-    weights, experts, lse = empty((M, k), f32), empty((M, k), i32), empty((M,), f32)
-    counts, probs, losses = empty((E + 1,), i32), empty((E,), f32), empty((2,), f32)
-    workspace = call.workspace(workspace, router_topk_workspace_bytes(M, E))
-    call.run("router_topk", logits.data_ptr(), _ptr(valid), weights.data_ptr(), experts.data_ptr(),
-             lse.data_ptr(), counts.data_ptr(), probs.data_ptr(), losses.data_ptr(),
-             _ptr(workspace), _bytes_of(workspace), M, E, ld, k, 1 if normalize else 0)
+    elsewhere = _context(device, stream)
+    if elsewhere is not None:
+        with elsewhere:
+            return router_topk(logits, k, valid, normalize, workspace)
+    weights = empty((M, k), dtype=f32, device=device)
+    experts = empty((M, k), dtype=i32, device=device)
+    lse = empty((M,), dtype=f32, device=device)
+    counts = empty((E + 1,), dtype=i32, device=device)
+    probs = empty((E,), dtype=f32, device=device)
+    losses = empty((2,), dtype=f32, device=device)
+    workspace = _workspace(workspace, router_topk_workspace_bytes(M, E), device)
+    _run("router_topk", device, logits.data_ptr(), _ptr(valid), weights.data_ptr(),
+         experts.data_ptr(), lse.data_ptr(), counts.data_ptr(), probs.data_ptr(),
+         losses.data_ptr(), _ptr(workspace), _bytes_of(workspace), M, E, ld, k,
+         1 if normalize else 0)
     return RouterTopk(weights, experts, lse, counts, probs, losses)
 
 
@@ -609,14 +613,18 @@ def router_topk_backward(logits: torch.Tensor, experts: torch.Tensor, lse: torch
         dtype = dlogits.dtype
     if dtype not in (torch.float32, torch.bfloat16):
         raise TypeError(f"dlogits must be float32 or bfloat16, got {dtype}")
-    call = _Call(device, stream)
+    elsewhere = _context(device, stream)
+    if elsewhere is not None:
+        with elsewhere:
+            return router_topk_backward(logits, experts, lse, counts, dweights, dlosses, normalize,
+                                        dtype, dlogits)
     if dlogits is None:
-        dlogits = call.empty((M, E), dtype)
+        dlogits = torch.empty((M, E), dtype=dtype, device=device)
     else:
         _on_device("dlogits", device, dlogits, dtype, (M, E))
-    call.run("router_topk_backward", logits.data_ptr(), experts.data_ptr(), lse.data_ptr(),
-             counts.data_ptr(), _ptr(dweights), _ptr(dlosses), dlogits.data_ptr(),
-             1 if dtype == torch.bfloat16 else 0, M, E, ld, k, 1 if normalize else 0)
+    _run("router_topk_backward", device, logits.data_ptr(), experts.data_ptr(), lse.data_ptr(),
+         counts.data_ptr(), _ptr(dweights), _ptr(dlosses), dlogits.data_ptr(),
+         1 if dtype == torch.bfloat16 else 0, M, E, ld, k, 1 if normalize else 0)
     return dlogits
 
 

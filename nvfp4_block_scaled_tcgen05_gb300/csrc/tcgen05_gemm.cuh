@@ -81,6 +81,7 @@ struct GemmParams {
   // chained configurations (TileCfg::CHAIN)
   int late_wait;                  // wait for the previous grid at the end instead of the start
   int trigger_late;               // let the next grid start only once this one has waited
+  int early, extra;               // the first `early` clusters start sooner: `extra` more tiles each
   // linear cross entropy (kXent*)
   const long long* target;        // [M] target column; < 0: the row has no loss
   const float* row_lse;           // [M] kXentGradBF16
@@ -311,6 +312,18 @@ __device__ __forceinline__ bool seg_at(const GemmParams& p, int c, int C, int id
     s.kb0 = (idx - q * p.chunks) * p.k_chunk;
     s.kb1 = min(p.num_k_blocks, s.kb0 + p.k_chunk);
     return true;
+  }
+  if constexpr (Cfg::CHAIN) {
+    if (p.extra) {  // tiles 0 .. early * extra - 1 belong to the early clusters
+      long long t = (long long)p.early * p.extra + c + (long long)idx * C;
+      if (c < p.early) t = idx < p.extra ? c + (long long)idx * p.early : t - (long long)p.extra * C;
+      if (t >= p.total_tiles) return false;
+      s.tile = int(t);
+      s.slot = -1;
+      s.kb0 = 0;
+      s.kb1 = p.num_k_blocks;
+      return true;
+    }
   }
   if (!p.sk) {
     const long long t = (long long)c + (long long)idx * C;

@@ -193,6 +193,49 @@ constexpr int kMaxSplits = 32;
 
 int round64(int n) { return (n + 63) / 64 * 64; }
 
+// A grid of the backward chain may start while the last round of its
+// predecessor's tiles runs on part of the SM pairs.  Clusters are started in
+// order, so the first ones get the free pairs: they take `extra` more tiles,
+// chosen so that all end together.  `before`: the predecessor's tiles and the
+// K blocks' time of each; then `tiles` tiles of `tile_kb`; `end`: from the
+// start of the predecessor's last round to the end.  Measured: 2048 x 40000 x
+// 2560 744 -> 700 us, 1024 x 32768 x 2048 253 -> 246 us.  (A start that comes
+// later than assumed costs time, not results.)
+struct GridTiles {
+  long long tiles;
+  double kb;
+};
+struct HeadStart {
+  int early, extra;
+  double end;
+};
+HeadStart head_start(GridTiles before, long long tiles, double tile_kb, int pairs) {
+  const int busy = int(before.tiles % pairs);
+  HeadStart h{0, 0, double((tiles + pairs - 1) / pairs) * tile_kb};
+  if (busy == 0) return h;
+  const int early = pairs - busy;
+  h.end += before.kb;
+  for (int x = 0; double(x) <= before.kb / tile_kb + 1 && (long long)x * early <= tiles; ++x) {
+    const long long rest = tiles - (long long)x * early;
+    const double end_early = double(x + (rest + pairs - 1) / pairs) * tile_kb;
+    const double end_late =
+        before.kb + double(std::max(0ll, (rest - early + pairs - 1) / pairs)) * tile_kb;
+    if (std::max(end_early, end_late) < h.end) h = {early, x, std::max(end_early, end_late)};
+  }
+  return h;
+}
+template <class Cfg, Epilogue EPI>
+void set_head_start(GemmParams& p, GridTiles before, double tile_kb, const DeviceInfo& dev) {
+  const int pairs = tcgen05_cluster_capacity<Cfg, EPI>(dev);
+  if (before.tiles == 0 || pairs <= 0 || p.total_tiles < pairs) return;
+  const HeadStart h = head_start(before, p.total_tiles, tile_kb, pairs);
+  p.early = h.early;
+  p.extra = h.extra;
+}
+
+// A dW tile in K blocks: its K loop, or 2.3 blocks' time to write it.
+double dw_tile_kb(int M) { return std::max((M + 127) / 128 + 0.5, 2.3); }
+
 XentPlan make_plan(int M, int V, int K) {
   XentPlan q{};
   const int mb = (M + 255) / 256, vb = (V + 255) / 256;
@@ -239,8 +282,13 @@ XentPlan make_plan(int M, int V, int K) {
   for (int want = 1; want <= kMaxSplits && want <= std::max(1, nkb / 4); ++want) {
     const int per = (nkb + want - 1) / want;
     const int s = (nkb + per - 1) / per;
-    const double cost = double((tiles * s + units - 1) / units) * (per + 2) +
-                        double(s) * M * double(K) * 8.0 / 3.4e6;
+    const double parts = double(s) * M * double(K) * 8.0 / 3.4e6;
+    double cost = double((tiles * s + units - 1) / units) * (per + 2) + parts;
+    if (!few) {
+      const long long dw_tiles = (long long)((q.piece + 255) / 256) * ((K + 255) / 256);
+      cost = double(tiles * s / units) * (per + 2) + parts +
+             head_start({tiles * s, per + 2.0}, dw_tiles, dw_tile_kb(M), units).end;
+    }
     if (cost < best) {
       best = cost;
       q.splits = s;
@@ -259,8 +307,8 @@ struct Piece {
 
 // G of one piece.
 template <class Cfg, bool kT>
-int run_grad(const XentBackward& a, const Piece& pc, bool late, const DeviceInfo& dev,
-             cudaStream_t stream) {
+int run_grad(const XentBackward& a, const Piece& pc, bool late, GridTiles before,
+             const DeviceInfo& dev, cudaStream_t stream) {
   CUtensorMap tx, tw, tg;
   const uint16_t* W = static_cast<const uint16_t*>(a.W) + size_t(pc.v0) * a.K;
   int rc = encode_k_major<Cfg>(&tx, a.X, a.M, a.K, kT ? Cfg::B_ROWS : Cfg::BM);
@@ -275,16 +323,18 @@ int run_grad(const XentBackward& a, const Piece& pc, bool late, const DeviceInfo
   p.col_offset = pc.v0;
   p.col_total = a.V;
   p.late_wait = late;
+  constexpr Epilogue kEpi = kT ? Epilogue::kXentGradTBF16 : Epilogue::kXentGradBF16;
+  if (late) set_head_start<Cfg, kEpi>(p, before, p.num_k_blocks + 1.0, dev);
   if constexpr (kT)
-    return launch_tcgen05<Cfg, Epilogue::kXentGradTBF16>(tw, tx, tg, tw, tw, p, dev, stream);
+    return launch_tcgen05<Cfg, kEpi>(tw, tx, tg, tw, tw, p, dev, stream);
   else
-    return launch_tcgen05<Cfg, Epilogue::kXentGradBF16>(tx, tw, tg, tx, tx, p, dev, stream);
+    return launch_tcgen05<Cfg, kEpi>(tx, tw, tg, tx, tx, p, dev, stream);
 }
 
 // One piece's term of dX: G [M][cols] . W_piece [cols][K].
 template <class Cfg>
 int run_dx(const XentBackward& a, const XentPlan& q, const Piece& pc, float* acc,
-           const DeviceInfo& dev, cudaStream_t stream) {
+           GridTiles* grid, const DeviceInfo& dev, cudaStream_t stream) {
   CUtensorMap tg, tw, tc;
   const uint16_t* W = static_cast<const uint16_t*>(a.W) + size_t(pc.v0) * a.K;
   int rc = Cfg::A_MN ? encode_k_major<Cfg>(&tg, pc.G, pc.cols, pc.ld, Cfg::BK)
@@ -293,6 +343,7 @@ int run_dx(const XentBackward& a, const XentPlan& q, const Piece& pc, float* acc
   if (rc != GEMM_OK) return rc;
   GemmParams p = base_params<Cfg>(a.M, a.K, pc.cols, dev);
   p.trigger_late = 1;
+  *grid = {p.total_tiles, p.num_k_blocks + 2.0};
   if (q.dx_bytes == 0) {
     rc = encode_k_major<Cfg>(&tc, a.dX, a.M, a.K, 32);
     if (rc != GEMM_OK) return rc;
@@ -308,14 +359,15 @@ int run_dx(const XentBackward& a, const XentPlan& q, const Piece& pc, float* acc
   p.k_splits = (p.num_k_blocks + p.kb_per_split - 1) / p.kb_per_split;
   p.L = p.k_splits;
   p.total_tiles *= p.k_splits;
+  *grid = {p.total_tiles, p.kb_per_split + 2.0};
   p.accumulate = pc.v0 > 0;
   return launch_tcgen05<Cfg, Epilogue::kAddF32>(tg, tw, tc, tg, tg, p, dev, stream);
 }
 
 // The piece's rows of dW: G^T [cols][M] . X [M][K].
 template <class Cfg>
-int run_dw(const XentBackward& a, const Piece& pc, bool after_dx, const DeviceInfo& dev,
-           cudaStream_t stream) {
+int run_dw(const XentBackward& a, const Piece& pc, bool after_dx, GridTiles before,
+           GridTiles* grid, const DeviceInfo& dev, cudaStream_t stream) {
   CUtensorMap tg, tx, tc;
   uint16_t* dW = static_cast<uint16_t*>(a.dW) + size_t(pc.v0) * a.K;
   int rc = Cfg::A_MN ? encode_k_major<Cfg>(&tg, pc.G, a.M, pc.ld, Cfg::BK)
@@ -326,6 +378,8 @@ int run_dw(const XentBackward& a, const Piece& pc, bool after_dx, const DeviceIn
   GemmParams p = base_params<Cfg>(pc.cols, a.K, a.M, dev);
   p.late_wait = after_dx;
   p.trigger_late = !after_dx;
+  if (after_dx) set_head_start<Cfg, Epilogue::kStoreBF16>(p, before, dw_tile_kb(a.M), dev);
+  *grid = p.extra ? GridTiles{0, 0.0} : GridTiles{p.total_tiles, dw_tile_kb(a.M)};
   return launch_tcgen05<Cfg, Epilogue::kStoreBF16>(tg, tx, tc, tg, tg, p, dev, stream);
 }
 
@@ -419,6 +473,7 @@ int launch_xent_backward(const XentBackward& a, const DeviceInfo& dev, cudaStrea
   const bool few = a.M <= kRowsFew;
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   float* acc = reinterpret_cast<float*>(ws + q.g_bytes * q.g_bufs);
+  GridTiles before{0, 0.0};  // the latest grid, for the next one's head start
   for (int i = 0; i < q.pieces; ++i) {
     Piece pc;
     pc.G = ws + q.g_bytes * (i & (q.g_bufs - 1));
@@ -426,16 +481,17 @@ int launch_xent_backward(const XentBackward& a, const DeviceInfo& dev, cudaStrea
     pc.cols = std::min(q.piece, a.V - pc.v0);
     pc.ld = round64(few ? a.M : pc.cols);
     int rc;
-    if (!few) rc = run_grad<XentGradPair, false>(a, pc, i > 0, dev, stream);
-    else if (a.M <= 64) rc = run_grad<XentGradT<64, 4>, true>(a, pc, i > 0, dev, stream);
-    else rc = run_grad<XentGradT<128, 3>, true>(a, pc, i > 0, dev, stream);
+    if (!few) rc = run_grad<XentGradPair, false>(a, pc, i > 0, before, dev, stream);
+    else if (a.M <= 64) rc = run_grad<XentGradT<64, 4>, true>(a, pc, i > 0, before, dev, stream);
+    else rc = run_grad<XentGradT<128, 3>, true>(a, pc, i > 0, before, dev, stream);
     if (rc == GEMM_OK && a.dX)
-      rc = few ? run_dx<XentDxFew>(a, q, pc, acc, dev, stream)
-               : run_dx<XentDxPair>(a, q, pc, acc, dev, stream);
-    if (rc == GEMM_OK && a.dW) {
-      rc = few ? run_dw<XentDwFew>(a, pc, a.dX != nullptr, dev, stream)
-               : run_dw<XentDwPair>(a, pc, a.dX != nullptr, dev, stream);
-    }
+      rc = few ? run_dx<XentDxFew>(a, q, pc, acc, &before, dev, stream)
+               : run_dx<XentDxPair>(a, q, pc, acc, &before, dev, stream);
+    // (the few tokens' dX runs on single CTAs: its last round frees no pairs in order)
+    if (few) before = {0, 0.0};
+    if (rc == GEMM_OK && a.dW)
+      rc = few ? run_dw<XentDwFew>(a, pc, a.dX != nullptr, before, &before, dev, stream)
+               : run_dw<XentDwPair>(a, pc, a.dX != nullptr, before, &before, dev, stream);
     if (rc != GEMM_OK) return rc;
   }
   if (a.dX && q.dx_bytes) {
