@@ -129,8 +129,8 @@ struct TileCfg {
   // CHUNKED (see ChunkedCfg): a tile's K loop is cut into chunks, each with an
   // accumulator of its own that the epilogue adds up in registers.
   static constexpr bool CHUNKED = false;
-  // STREAM_A (see StreamedCfg): A is read once and leaves L2 first.
-  static constexpr bool STREAM_A = false;
+  // STREAM_A, STREAM_B: A or B is not read again and leaves L2 first.
+  static constexpr bool STREAM_A = false, STREAM_B = false;
   // C_T: the output is D transposed (the swapped-operand decode GEMM, whose
   // M role holds the weights and N role the few activation rows)
   static constexpr bool C_T = C_T_;
@@ -292,8 +292,7 @@ struct Seg {
 };
 
 // Segment `idx` of cluster c among C clusters; false past the end.  Every
-// role of the kernel walks this same sequence (CHUNKED: the epilogue, kChunks,
-// takes a tile's chunks one by one, the others whole tiles).
+// role of the kernel walks this same sequence.
 //  * plain / split-K: tile = c + idx*C; with split-K the batch slot of the
 //    tile selects its K blocks.
 //  * stream-K (p.sk = P): the first floor(tiles/C) rounds are whole tiles
@@ -301,18 +300,8 @@ struct Seg {
 //    are split evenly over clusters 0..P-1, cluster c taking iterations
 //    [T*c/P, T*(c+1)/P) in order, which makes at most its first and last
 //    segment partial.
-template <class Cfg, bool kChunks = false>
+template <class Cfg>
 __device__ __forceinline__ bool seg_at(const GemmParams& p, int c, int C, int idx, Seg& s) {
-  if constexpr (kChunks) {
-    const int q = idx / p.chunks;
-    const long long t = (long long)c + (long long)q * C;
-    if (t >= p.total_tiles) return false;
-    s.tile = int(t);
-    s.slot = -1;
-    s.kb0 = (idx - q * p.chunks) * p.k_chunk;
-    s.kb1 = min(p.num_k_blocks, s.kb0 + p.k_chunk);
-    return true;
-  }
   if constexpr (Cfg::CHAIN) {
     if (p.extra) {  // tiles 0 .. early * extra - 1 belong to the early clusters
       long long t = (long long)p.early * p.extra + c + (long long)idx * C;
@@ -427,74 +416,101 @@ __device__ __forceinline__ void write_box_row_f32(uint8_t* row, int lane, const 
   }
 }
 
-// Linear cross entropy, forward: folds 32 logits of one row into the row's
-// running maximum and sum of exp(z - maximum).  exp(y) = 2^(y log2 e) on the
-// special-function unit (relative error below 2^-21).  A maximum of -inf (no
-// logit yet, or none finite) subtracts 0 instead, so that no inf - inf arises;
-// NaN logits reach the sum.
-__device__ __forceinline__ float fast_exp(float y) { return ptx::ex2(y * 1.4426950408889634f); }
+// Linear cross entropy.  exp(x - ref) = 2^(x log2 e - ref log2 e): one fused
+// multiply-add (two columns per instruction) and one special-function
+// operation (relative error below 2^-21).  Rounding ref log2 e shifts all terms
+// of a row alike, by at most the last place of ref.
+constexpr float kLog2e = 1.4426950408889634f;
+__device__ __forceinline__ float fast_exp(float y) { return ptx::ex2(y * kLog2e); }
 
+// Forward: folds 32 logits of one row into the row's running maximum and sum
+// of exp(z - maximum).  A maximum of -inf (no logit yet, or none finite)
+// subtracts 0 instead, so that no inf - inf arises; NaN logits reach the sum.
+__device__ __forceinline__ float xent_max(const float (&x)[32], float m) {
+  float m4[4] = {m, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+  for (int i = 0; i < 32; i += 2) m4[i / 2 & 3] = fmaxf(m4[i / 2 & 3], fmaxf(x[i], x[i + 1]));
+  return fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+}
+__device__ __forceinline__ void xent_add(const float (&x)[32], float ref, float2 (&s)[4]) {
+  const float2 l2 = make_float2(kLog2e, kLog2e), c = make_float2(-ref * kLog2e, -ref * kLog2e);
+#pragma unroll
+  for (int i = 0; i < 32; i += 2) {
+    const float2 y = ptx::fma2(make_float2(x[i], x[i + 1]), l2, c);
+    s[i / 2 & 3] = ptx::add2(s[i / 2 & 3], make_float2(ptx::ex2(y.x), ptx::ex2(y.y)));
+  }
+}
+__device__ __forceinline__ float xent_total(const float2 (&s)[4]) {
+  const float2 t = ptx::add2(ptx::add2(s[0], s[1]), ptx::add2(s[2], s[3]));
+  return t.x + t.y;
+}
 __device__ __forceinline__ void xent_fold(const float (&x)[32], float& mx, float& sum) {
-  float m4[4] = {mx, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-  for (int i = 0; i < 32; ++i) m4[i & 3] = fmaxf(m4[i & 3], x[i]);
-  const float m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+  const float m = xent_max(x, mx);
   const float ref = (m == -INFINITY) ? 0.0f : m;
-  float s4[4] = {sum * fast_exp(mx - ref), 0.0f, 0.0f, 0.0f};
-#pragma unroll
-  for (int i = 0; i < 32; ++i) s4[i & 3] += fast_exp(x[i] - ref);
+  float2 s[4] = {};
+  s[0].x = sum * fast_exp(mx - ref);
+  xent_add(x, ref, s);
   mx = m;
-  sum = (s4[0] + s4[1]) + (s4[2] + s4[3]);
+  sum = xent_total(s);
 }
 
 // The same of a whole tile row (32 R columns) at once.
 template <int R>
 __device__ __forceinline__ float2 xent_tile(const float (&x)[R][32]) {
-  float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+  float m = -INFINITY;
 #pragma unroll
-  for (int i = 0; i < R; ++i)
-#pragma unroll
-    for (int j = 0; j < 32; ++j) m4[j & 3] = fmaxf(m4[j & 3], x[i][j]);
-  const float m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+  for (int i = 0; i < R; ++i) m = xent_max(x[i], m);
   const float ref = (m == -INFINITY) ? 0.0f : m;
-  float s4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  float2 s[4] = {};
 #pragma unroll
-  for (int i = 0; i < R; ++i)
-#pragma unroll
-    for (int j = 0; j < 32; ++j) s4[j & 3] += fast_exp(x[i][j] - ref);
-  return make_float2(m, (s4[0] + s4[1]) + (s4[2] + s4[3]));
+  for (int i = 0; i < R; ++i) xent_add(x[i], ref, s);
+  return make_float2(m, xent_total(s));
 }
 
-// Linear cross entropy, backward: 32 logits of one row -> gradients
-// d (exp(z - lse) - [column = target]); `rel` is the target's place among
-// them (none if outside 0..31), `live` the columns that exist.  lse = +inf
-// marks a row without a loss (all zeros, whatever the logits).
-__device__ __forceinline__ void xent_grad(uint32_t (&v)[32], float lse, float d, int rel,
-                                          int live) {
-  if (lse == INFINITY && d == 0.0f) {
+// Backward: 32 logits of one row -> gradients d (exp(z - lse) - [column =
+// target]); c = -lse log2 e; `rel` is the target's place among them (none if
+// outside 0..31), `live` the columns that exist, `none` marks a row without a
+// loss (all zeros, whatever the logits).  The last three are rare, and looked
+// at once per warp.
+__device__ __forceinline__ void xent_grad(uint32_t (&v)[32], float c, float d, int rel, int live,
+                                          bool none) {
+  const float2 l2 = make_float2(kLog2e, kLog2e), c2 = make_float2(c, c), d2 = make_float2(d, d);
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = 0u;
-    return;
+  for (int i = 0; i < 32; i += 2) {
+    const float2 y =
+        ptx::fma2(make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), l2, c2);
+    const float2 g = ptx::mul2(make_float2(ptx::ex2(y.x), ptx::ex2(y.y)), d2);
+    v[i] = __float_as_uint(g.x);
+    v[i + 1] = __float_as_uint(g.y);
   }
+  if (__any_sync(0xffffffffu, rel >= 0 && rel < 32)) {
 #pragma unroll
-  for (int i = 0; i < 32; ++i) {
-    float q = fast_exp(__uint_as_float(v[i]) - lse);
-    if (rel == i) q -= 1.0f;
-    v[i] = __float_as_uint(i < live ? d * q : 0.0f);
+    for (int i = 0; i < 32; ++i)
+      if (rel == i) v[i] = __float_as_uint(__uint_as_float(v[i]) - d);
+  }
+  if (live < 32) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (i >= live) v[i] = 0u;
+  }
+  if (__any_sync(0xffffffffu, none)) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (none) v[i] = 0u;
   }
 }
 
 // The same with the roles swapped: 32 logits of one vocabulary row, one token
-// each; tok[i] = (lse, d, target as int bits) of the tokens, read by every lane
-// at once.
+// each; tok[i] = (-lse log2 e, d, target as int bits) of the tokens, read by
+// every lane at once.
 __device__ __forceinline__ void xent_grad_t(uint32_t (&v)[32], const float4* tok, int row) {
 #pragma unroll
   for (int i = 0; i < 32; ++i) {
     const float4 t = tok[i];
-    float q = fast_exp(__uint_as_float(v[i]) - t.x);
-    if (__float_as_int(t.z) == row) q -= 1.0f;
+    float g = t.y * ptx::ex2(fmaf(__uint_as_float(v[i]), kLog2e, t.x));
+    if (__float_as_int(t.z) == row) g -= t.y;
     // d = 0 marks a token without a loss: zero whatever the logits
-    v[i] = t.y == 0.0f ? 0u : __float_as_uint(t.y * q);
+    v[i] = t.y == 0.0f ? 0u : __float_as_uint(g);
   }
 }
 
@@ -822,7 +838,8 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
       const uint64_t pol_ab = ptx::policy_evict_last();
       (void)pol_ab;
       const uint64_t pol_a = Cfg::STREAM_A ? ptx::policy_evict_first() : pol_ab;
-      (void)pol_a;
+      const uint64_t pol_b = Cfg::STREAM_B ? ptx::policy_evict_first() : pol_ab;
+      (void)pol_a, (void)pol_b;
       int stage = 0;
       uint32_t phase = 0;
       uint32_t armed = 0, armed_parity = 0;  // bit s: stage s has a load in flight / its parity
@@ -880,7 +897,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
 #pragma unroll
                   for (int at = 0; at < Cfg::B_ROWS / 64; ++at)
                     ptx::tma_load_3d_hint(stage_b(stage) + at * Cfg::B_ATOM_BYTES, &tmap_b, fb,
-                                          b_row + 64 * at, kb * Cfg::BK, l, pol_ab);
+                                          b_row + 64 * at, kb * Cfg::BK, l, pol_b);
               } else if constexpr (kHintLoads) {
                 ptx::tma_load_3d_hint(da, &tmap_a, fb, x, a_row, l, pol_a);
                 ptx::tma_load_3d_hint(db, &tmap_b, fb, x, b_row, l, pol_ab);
@@ -1378,10 +1395,9 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     long long xent_target = -1;
     constexpr bool kXentFwd = EPI == Epilogue::kXentStats || EPI == Epilogue::kXentStatsT;
     constexpr int XR = kXentFwd ? Cfg::EPI_COLS / 32 : 1;  // 32-column groups per epilogue warp
-    float xr[XR][32];                                      // the tile's sums over the chunks
     float2 xt[XR];                                         // kXentStatsT: running statistics
     long long xt_target[XR];
-    (void)xr, (void)xt, (void)xt_target;
+    (void)xt, (void)xt_target;
     // kXentGradTBF16: the tokens' values, in the output boxes' place past the
     // two that the warps use
     float4* tok_vals = nullptr;
@@ -1395,7 +1411,8 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                             ? int(t - p.col_offset) : -1;
         // without a loss: d = 0; a target past the vocabulary: NaN
         const float d = t < 0 ? 0.0f : (t >= p.col_total ? NAN : p.row_scale[i]);
-        tok_vals[i] = make_float4(i < p.N ? p.row_lse[i] : 0.0f, d, __int_as_float(row), 0.0f);
+        tok_vals[i] =
+            make_float4(i < p.N ? -kLog2e * p.row_lse[i] : 0.0f, d, __int_as_float(row), 0.0f);
       }
       __syncwarp();
     }
@@ -1407,8 +1424,9 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         xt_target[i] = tok < p.N ? p.target[tok] : -1;
       }
     }
-    float xent_lse = 0.0f, xent_scale = 0.0f;
-    (void)xent_row0, (void)xent_rel, (void)xent_target, (void)xent_lse, (void)xent_scale;
+    float xent_c = 0.0f, xent_scale = 0.0f;
+    bool xent_none = true;
+    (void)xent_row0, (void)xent_rel, (void)xent_target, (void)xent_c, (void)xent_scale, (void)xent_none;
     uint32_t chunk_ctr = 0;
     uint32_t epi_parity = 0;     // bit b: parity of the next wait on epi_bar(e, b)
     uint32_t epi_pending = 0;    // bit b: a load into buffer b has not been waited for
@@ -1453,8 +1471,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
       for (int k = 0; k < LA_SETS - 1; ++k)
         if (seg_at<Cfg>(p, cluster_id, num_clusters, k, sg)) prefetch_out(sg, k);
     }
-    for (int idx = 0; ok && seg_at<Cfg, Cfg::CHUNKED>(p, cluster_id, num_clusters, idx, sg);
-         ++idx, ++it) {
+    for (int idx = 0; ok && seg_at<Cfg>(p, cluster_id, num_clusters, idx, sg); ++idx, ++it) {
       int l, mb, nb;
       decode_tile<Cfg>(sg.tile, p, l, mb, nb);
       const int acc = it % Cfg::NUM_ACC;
@@ -1480,12 +1497,12 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
           xent_row0 = row0;
           const int grow = row0 + lane;
           const long long t = grow < p.M ? p.target[grow] : -1;
-          xent_lse = grow < p.M ? p.row_lse[grow] : 0.0f;
+          xent_c = grow < p.M ? -kLog2e * p.row_lse[grow] : 0.0f;
           // a row without a loss has no gradient; a target past the vocabulary
           // has no loss to differentiate
           xent_scale = t < 0 ? 0.0f : (t >= p.col_total ? NAN : p.row_scale[grow]);
           xent_rel = (t >= p.col_offset && t < p.col_offset + p.N) ? int(t - p.col_offset) : -1;
-          if (t < 0) xent_lse = INFINITY;  // exp(z - inf) = 0 whatever the logits
+          xent_none = t < 0;
         }
       }
 
@@ -1681,21 +1698,47 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
           }
         }
       } else if constexpr (kXentFwd) {
-        // Linear cross entropy.  The chunk's accumulator joins the tile's sum
+        // Linear cross entropy.  Each chunk's accumulator joins the tile's sum
         // in registers and is handed back at once; the rest overlaps the next
-        // chunks' MMAs.
-        const bool first_chunk = sg.kb0 == 0;
+        // tile's MMAs.
+        float xr[XR][32];
 #pragma unroll
-        for (int i = 0; i < XR; ++i) {
-          uint32_t v[32];
-          ptx::tmem_ld_32x32b_x32(tacc + uint32_t(32 * i), v);
+        for (int i = 0; i < 2 * XR; ++i) {
+          uint32_t v[16];
+          ptx::tmem_ld_32x32b_x16(tacc + uint32_t(16 * i), v);
           ptx::tmem_ld_wait_regs(v);
 #pragma unroll
-          for (int j = 0; j < 32; ++j)
-            xr[i][j] = first_chunk ? __uint_as_float(v[j]) : xr[i][j] + __uint_as_float(v[j]);
+          for (int j = 0; j < 16; ++j) xr[i / 2][16 * (i % 2) + j] = __uint_as_float(v[j]);
         }
         release_acc(acc);
-        if (sg.kb1 < p.num_k_blocks) continue;
+#pragma unroll 1
+        for (int ch = 1; ch < p.chunks; ++ch) {
+          ++it;
+          const int next = it % Cfg::NUM_ACC;
+          ok = __all_sync(0xffffffffu,
+                          wait_bar(acc_full(next), uint32_t(it / Cfg::NUM_ACC) & 1u, w, 4));
+          if (!ok) break;
+          ptx::tc_fence_after();
+          const uint32_t tnext = tmem_base + lane_off + uint32_t(next * BN + col_base);
+#pragma unroll
+          for (int i = 0; i < 2 * XR; ++i) {
+            uint32_t v[16];  // 16 columns at a time: the sums leave few registers
+            ptx::tmem_ld_32x32b_x16(tnext + uint32_t(16 * i), v);
+            ptx::tmem_ld_wait_regs(v);
+#pragma unroll
+            for (int j = 0; j < 16; j += 2) {
+              float& x = xr[i / 2][16 * (i % 2) + j];
+              float& y = xr[i / 2][16 * (i % 2) + j + 1];
+              const float2 t =
+                  ptx::add2(make_float2(x, y),
+                            make_float2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])));
+              x = t.x;
+              y = t.y;
+            }
+          }
+          release_acc(next);
+        }
+        if (!ok) break;
         if constexpr (EPI == Epilogue::kXentStats) {
           // each lane owns one row: maximum and sum of exponentials over its
           // columns, in FP32; columns past N take no part
@@ -1944,8 +1987,10 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
             }
           }
           if constexpr (EPI == Epilogue::kXentGradBF16) {
-            xent_grad(r0, xent_lse, xent_scale, xent_rel - col0, p.N - col0);
-            xent_grad(r1, xent_lse, xent_scale, xent_rel - col0 - 32, p.N - col0 - 32);
+            // a place before this chunk stays negative: -1 marks no target
+            const int rel = xent_rel < 0 ? -1 : xent_rel - col0;
+            xent_grad(r0, xent_c, xent_scale, rel, p.N - col0, xent_none);
+            xent_grad(r1, xent_c, xent_scale, rel - 32, p.N - col0 - 32, xent_none);
             write_box_row<Epilogue::kStoreBF16>(smem + (sbuf - sbase) + lane * 128, lane, r0, r1,
                                                 0.0f);
           } else if constexpr (EPI == Epilogue::kXentGradTBF16) {
