@@ -90,6 +90,7 @@ struct GemmParams {
   float* picked;                  // [M] kXentStats: the target column's value
   int col_offset, col_total;      // first column of this launch, columns in all
   int k_chunk, chunks;            // CHUNKED: K blocks per chunk, chunks per tile
+  int m_rows;                     // VAR_ROWS: rows of A per CTA and tile (a multiple of 32, <= 128)
 };
 
 template <Operand OP, int CG_, int BN_, int STAGES_, int EPI_WARPS_ = 4, int EPI_BUFS_ = 2,
@@ -131,6 +132,8 @@ struct TileCfg {
   static constexpr bool CHUNKED = false;
   // STREAM_A, STREAM_B: A or B is not read again and leaves L2 first.
   static constexpr bool STREAM_A = false, STREAM_B = false;
+  // VAR_ROWS (see FewTokensCfg): tiles of 2 m_rows instead of 256 rows.
+  static constexpr bool VAR_ROWS = false;
   // C_T: the output is D transposed (the swapped-operand decode GEMM, whose
   // M role holds the weights and N role the few activation rows)
   static constexpr bool C_T = C_T_;
@@ -261,10 +264,15 @@ struct ChunkedCfg : Base {
   static constexpr bool CHUNKED = true;
 };
 
-// Few tokens: A (the weights) is read once, B (the tokens) by every cluster.
-template <class Base>
-struct StreamedCfg : ChunkedCfg<Base> {
-  static constexpr bool STREAM_A = true;
+// Few tokens: A is the weights, streamed, and B the tokens.  A tile loads
+// m_rows rows of A per CTA and multiplies all 128 (what earlier tiles left in
+// the rest of the stage gives rows of D that nobody reads): the MMA has time
+// to spare, and shorter tiles share V rows evenly among the SM pairs.
+// kOnce: the weights are not read again.
+template <class Base, bool kOnce>
+struct FewTokensCfg : Base {
+  static constexpr bool STREAM_A = kOnce;
+  static constexpr bool VAR_ROWS = true;
 };
 
 // Work item `tile` -> batch l, M block mb and N block nb, in grouped-M
@@ -726,6 +734,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     *abort_flag = 0u;
     ptx::fence_mbar_init();
   }
+  const int m_rows = Cfg::VAR_ROWS ? p.m_rows : Cfg::BM;  // rows of A per CTA and tile
   // The producer's first segment, found before the dependency wait: the
   // schedule arithmetic run for the first time cost ~0.7 us between the
   // wait and the first load.
@@ -754,7 +763,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
       if (has0) {
         decode_tile<Cfg>(s0.tile, p, l0, mb0, nb0);
         const int l = (p.k_splits > 1) ? l0 / p.k_splits : l0;
-        const int a_row = mb0 * Cfg::TILE_M + int(peer) * Cfg::BM;
+        const int a_row = (mb0 * CG + int(peer)) * m_rows;
         const int b_row = nb0 * BN + int(peer) * Cfg::B_ROWS;
         const int kend = min(s0.kb1, s0.kb0 + STAGES);
         for (int kb = s0.kb0; kb < kend; ++kb) {
@@ -857,12 +866,12 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
           if (!seg_at<Cfg>(p, cluster_id, num_clusters, idx, sg)) break;
           decode_tile<Cfg>(sg.tile, p, l, mb, nb);
         }
-        const int a_row = mb * Cfg::TILE_M + int(peer) * Cfg::BM;
+        const int a_row = (mb * CG + int(peer)) * m_rows;
         const int b_row = nb * BN + int(peer) * Cfg::B_ROWS;
         int sfb_atoms = 0;
         if constexpr (kFP4) sfb_atoms = min(Cfg::SFB_ATOMS, p.rest_n - nb * Cfg::SFB_ATOMS);
         const uint32_t tx =
-            uint32_t(CG) * (Cfg::A_BYTES + (Cfg::kW4 ? 0 : Cfg::B_BYTES) + Cfg::SFA_BYTES +
+            uint32_t(CG) * (uint32_t(m_rows) * 128 * Cfg::KSUB + (Cfg::kW4 ? 0 : Cfg::B_BYTES) + Cfg::SFA_BYTES +
                             uint32_t(sfb_atoms) * Cfg::SFB_ATOM_BYTES);
         // split-K: the batch slot holds batch * k_splits + split
         const int kb_begin = sg.kb0;
@@ -1489,8 +1498,8 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
       ok = __all_sync(0xffffffffu, wait_bar(acc_full(acc), acc_phase, w, 4));
       if (!ok) break;
       ptx::tc_fence_after();
-      const int row0 = mb * Cfg::TILE_M + int(peer) * Cfg::BM + q * 32;
-      const bool rows_live = row0 < p.M;
+      const int row0 = (mb * CG + int(peer)) * m_rows + q * 32;
+      const bool rows_live = row0 < p.M && (!Cfg::VAR_ROWS || q * 32 < m_rows);
       const uint32_t tacc = tmem_base + lane_off + uint32_t(acc * BN + col_base);
       if constexpr (EPI == Epilogue::kXentGradBF16) {
         if (row0 != xent_row0) {  // this lane's row of the gradient
@@ -1773,7 +1782,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
           // either way) every lane gets one token's 32 logits and folds them
           // into that token's running maximum and sum
           float* box = reinterpret_cast<float*>(smem + (buf0 - sbase));
-          const int live = p.M - row0;  // vocabulary rows of this warp that exist
+          const int live = rows_live ? p.M - row0 : 0;  // vocabulary rows of this warp
 #pragma unroll
           for (int i = 0; i < XR; ++i) {
             const int tok = col_base + 32 * i + lane;  // one N block holds all tokens

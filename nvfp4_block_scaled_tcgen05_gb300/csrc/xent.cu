@@ -30,7 +30,8 @@ using XentFwdPair = ChunkedCfg<TileCfg<Operand::kBF16, 2, 256, 3, 8, 0, true, fa
 // TB/s).  Pairs halve each CTA's share of the tokens; single CTAs took 209 us
 // with one token.
 template <int BN, int STAGES>
-using XentFwdT = StreamedCfg<TileCfg<Operand::kBF16, 2, BN, STAGES, 4, 1, true, false, 2>>;
+using XentFwdT = FewTokensCfg<
+    ChunkedCfg<TileCfg<Operand::kBF16, 2, BN, STAGES, 4, 1, true, false, 2>>, true>;
 template <int CG, int STAGES, int KSUB, bool BMN, bool AMN>
 using XentCfg =
     TileCfg<Operand::kBF16, CG, 256, STAGES, 4, 2, true, false, KSUB, BMN, false, AMN, true>;
@@ -42,8 +43,8 @@ using XentDwPair = XentCfg<2, 3, 2, true, true>;
 // Few tokens: G is formed transposed ([vocabulary][tokens]) by the roles of
 // XentFwdT, so dX reads it MN-major and dW K-major.
 template <int BN, int STAGES>
-using XentGradT =
-    TileCfg<Operand::kBF16, 2, BN, STAGES, 4, 3, true, false, 2, false, false, false, true>;
+using XentGradT = FewTokensCfg<
+    TileCfg<Operand::kBF16, 2, BN, STAGES, 4, 3, true, false, 2, false, false, false, true>, false>;
 // The second and last read of the weights (37 x 32768 x 2048: 80 -> 76.5 us
 // with G keeping them in L2 and dX letting them go).
 template <class Base>
@@ -152,21 +153,52 @@ int run_forward(const XentForward& a, const DeviceInfo& dev, cudaStream_t stream
   return launch_tcgen05<Cfg, Epilogue::kXentStats>(tx, tw, tx, tx, tx, p, dev, stream);
 }
 
+// Rows per CTA and tile of the few tokens' kernels (FewTokensCfg): whole
+// rounds of tiles stream at the rate of memory, shared by the pairs; a last
+// round of n tiles takes n / pairs of a round's time, but no less than 0.44,
+// since a pair alone draws no more than about 200 GB/s.  Below 46 (79) rows
+// the MMAs of 64 (128) tokens take longer than the rows; 8 rows' time per
+// tile for its change.
+constexpr int kPairs = 76;  // CTA pairs of a GB300
+int few_rows(int V, int BN) {
+  int best = 128;
+  double best_cost = 1e300;
+  for (int h = 128; h >= 32; h -= 32) {
+    const int tiles = (V + 2 * h - 1) / (2 * h), last = tiles % kPairs;
+    const double rounds = tiles / kPairs + (last ? std::max(double(last) / kPairs, 0.44) : 0.0);
+    const double cost = rounds * (std::max(double(h), BN == 64 ? 46.0 : 79.0) + 8.0);
+    if (cost < best_cost) {
+      best_cost = cost;
+      best = h;
+    }
+  }
+  return best;
+}
+template <class Cfg>
+void set_few_rows(GemmParams& p, int rows) {
+  p.m_rows = rows;
+  p.num_m_blocks = (p.M + 2 * rows - 1) / (2 * rows);
+  p.total_tiles = p.num_m_blocks * p.num_n_blocks;
+}
+
 template <class Cfg>
 int run_forward_few(const XentForward& a, int* groups, const DeviceInfo& dev,
                     cudaStream_t stream) {
   CUtensorMap tx, tw;
-  int rc = encode_k_major<Cfg>(&tw, a.W, a.V, a.K, Cfg::BM);
+  const int rows = few_rows(a.V, Cfg::BN);
+  int rc = encode_k_major<Cfg>(&tw, a.W, a.V, a.K, rows);
   if (rc == GEMM_OK) rc = encode_k_major<Cfg>(&tx, a.X, a.M, a.K, Cfg::B_ROWS);
   if (rc != GEMM_OK) return rc;
   GemmParams p = base_params<Cfg>(a.V, a.M, a.K, dev);
+  set_few_rows<Cfg>(p, rows);
   set_chunks<Cfg>(p, kChunkKFew);
   p.target = a.target;
   p.stats = static_cast<float2*>(a.workspace);
   p.picked = a.loss;
   // fewer clusters where the device holds fewer than the workspace allows for
   const int clusters =
-      std::min(*groups / (4 * Cfg::CLUSTER), tcgen05_cluster_capacity<Cfg, Epilogue::kXentStatsT>(dev));
+      std::min({*groups / (4 * Cfg::CLUSTER), p.total_tiles,
+                tcgen05_cluster_capacity<Cfg, Epilogue::kXentStatsT>(dev)});
   if (clusters <= 0) return GEMM_ERR_LAUNCH;
   *groups = clusters * 4 * Cfg::CLUSTER;
   return launch_tcgen05<Cfg, Epilogue::kXentStatsT>(tw, tx, tw, tw, tw, p, dev, stream, clusters);
@@ -175,7 +207,7 @@ int run_forward_few(const XentForward& a, int* groups, const DeviceInfo& dev,
 // Column groups that the forward statistics come in: one per 128 columns,
 // or (few rows) four per CTA, of at most kFewCtas CTAs.
 constexpr int kFewCtas = 152;
-int few_ctas(int V) { return std::min(kFewCtas, 2 * ((V + 255) / 256)); }
+int few_ctas(int V) { return std::min(kFewCtas, 2 * ((V + 63) / 64)); }
 int stat_groups(int M, int V) {
   return M <= kRowsFew ? 4 * few_ctas(V) : (V + 127) / 128;
 }
@@ -190,7 +222,6 @@ struct XentPlan {
   size_t dx_bytes;
 };
 
-constexpr int kPairs = 76;  // CTA pairs of a GB300
 constexpr long long kPieceBytes = 128ll << 20;
 constexpr int kMinPiece = 4096;
 constexpr int kMaxSplits = 152;
@@ -316,11 +347,13 @@ int run_grad(const XentBackward& a, const Piece& pc, bool late, GridTiles before
   CUtensorMap tx, tw, tg;
   const uint16_t* W = static_cast<const uint16_t*>(a.W) + size_t(pc.v0) * a.K;
   int rc = encode_k_major<Cfg>(&tx, a.X, a.M, a.K, kT ? Cfg::B_ROWS : Cfg::BM);
-  if (rc == GEMM_OK) rc = encode_k_major<Cfg>(&tw, W, pc.cols, a.K, kT ? Cfg::BM : Cfg::B_ROWS);
+  const int rows = kT ? few_rows(pc.cols, Cfg::BN) : 0;
+  if (rc == GEMM_OK) rc = encode_k_major<Cfg>(&tw, W, pc.cols, a.K, kT ? rows : Cfg::B_ROWS);
   if (rc == GEMM_OK) rc = encode_k_major<Cfg>(&tg, pc.G, kT ? pc.cols : a.M, pc.ld, 32);
   if (rc != GEMM_OK) return rc;
   GemmParams p = kT ? base_params<Cfg>(pc.cols, a.M, a.K, dev)
                     : base_params<Cfg>(a.M, pc.cols, a.K, dev);
+  if constexpr (kT) set_few_rows<Cfg>(p, rows);
   p.target = a.target;
   p.row_lse = a.lse;
   p.row_scale = a.dloss;
