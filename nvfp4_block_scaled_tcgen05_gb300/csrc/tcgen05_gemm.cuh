@@ -82,6 +82,10 @@ struct GemmParams {
   int late_wait;                  // wait for the previous grid at the end instead of the start
   int trigger_late;               // let the next grid start only once this one has waited
   int early, extra;               // the first `early` clusters start sooner: `extra` more tiles each
+  const float* sum_src;           // after the late wait: sum_dst[i] = bf16(sum of sum_src's slots)
+  void* sum_dst;                  // (sum_slots; 0 = no such sum)
+  size_t sum_n;
+  int sum_slots;
   // linear cross entropy (kXent*)
   const long long* target;        // [M] target column; < 0: the row has no loss
   const float* row_lse;           // [M] kXentGradBF16
@@ -619,6 +623,47 @@ __device__ __forceinline__ void w4_dequant32(const uint4 raw, uint16_t sc2, uint
       out[4 * i + j] = *reinterpret_cast<const uint32_t*>(&q);
     }
   }
+}
+
+// out[i] = bf16(acc[0][i] + acc[1][i] + ...), FP32 adds in slot order, n % 4 ==
+// 0; thread `at` of `threads`.  S slots of U quadruples are in flight at a time.
+template <int S, int U>
+__device__ __forceinline__ void sum_slots_by(const float* acc, uint16_t* out, size_t n, int slots,
+                                             size_t at, size_t threads) {
+  for (size_t i0 = at; i0 < n / 4; i0 += U * threads) {
+    float4 s[U] = {};
+#pragma unroll 1
+    for (int b = 0; b < slots; b += S) {
+      float4 v[S][U];
+#pragma unroll
+      for (int k = 0; k < S; ++k)
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (b + k < slots && i0 + u * threads < n / 4)
+            v[k][u] = __ldcg(reinterpret_cast<const float4*>(acc + size_t(b + k) * n) + i0 + u * threads);
+#pragma unroll
+      for (int k = 0; k < S; ++k)
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (b + k < slots && i0 + u * threads < n / 4) {
+            s[u].x += v[k][u].x;
+            s[u].y += v[k][u].y;
+            s[u].z += v[k][u].z;
+            s[u].w += v[k][u].w;
+          }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (i0 + u * threads < n / 4)
+        reinterpret_cast<uint2*>(out)[i0 + u * threads] =
+            make_uint2(pack_bf16x2(__float_as_uint(s[u].x), __float_as_uint(s[u].y)),
+                       pack_bf16x2(__float_as_uint(s[u].z), __float_as_uint(s[u].w)));
+  }
+}
+__device__ __forceinline__ void sum_slots(const float* acc, uint16_t* out, size_t n, int slots,
+                                          size_t at, size_t threads) {
+  if (slots <= 2) sum_slots_by<2, 4>(acc, out, n, slots, at, threads);
+  else sum_slots_by<8, 1>(acc, out, n, slots, at, threads);
 }
 
 template <class Cfg, Epilogue EPI>
@@ -2050,7 +2095,13 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     ptx::tmem_dealloc<CG>(tmem_base, Cfg::TMEM_COLS);
   }
   if constexpr (Cfg::CHAIN) {
-    if (p.late_wait) ptx::griddep_wait();
+    if (p.late_wait) {
+      ptx::griddep_wait();
+      if (p.sum_slots)
+        sum_slots(p.sum_src, static_cast<uint16_t*>(p.sum_dst), p.sum_n, p.sum_slots,
+                  size_t(blockIdx.x) * Cfg::THREADS + threadIdx.x,
+                  size_t(gridDim.x) * Cfg::THREADS);
+    }
   }
 }
 

@@ -403,8 +403,8 @@ int run_dx(const XentBackward& a, const XentPlan& q, const Piece& pc, float* acc
 
 // The piece's rows of dW: G^T [cols][M] . X [M][K].
 template <class Cfg>
-int run_dw(const XentBackward& a, const Piece& pc, bool after_dx, GridTiles before,
-           GridTiles* grid, const DeviceInfo& dev, cudaStream_t stream) {
+int run_dw(const XentBackward& a, const Piece& pc, bool after_dx, const float* sum, int slots,
+           GridTiles before, GridTiles* grid, const DeviceInfo& dev, cudaStream_t stream) {
   CUtensorMap tg, tx, tc;
   uint16_t* dW = static_cast<uint16_t*>(a.dW) + size_t(pc.v0) * a.K;
   int rc = Cfg::A_MN ? encode_k_major<Cfg>(&tg, pc.G, a.M, pc.ld, Cfg::BK)
@@ -415,39 +415,26 @@ int run_dw(const XentBackward& a, const Piece& pc, bool after_dx, GridTiles befo
   GemmParams p = base_params<Cfg>(pc.cols, a.K, a.M, dev);
   p.late_wait = after_dx;
   p.trigger_late = !after_dx;
+  p.sum_src = sum;
+  p.sum_dst = a.dX;
+  p.sum_n = size_t(a.M) * a.K;
+  p.sum_slots = slots;
   if (after_dx) set_head_start<Cfg, Epilogue::kStoreBF16>(p, before, dw_tile_kb(a.M), dev);
   *grid = p.extra ? GridTiles{0, 0.0} : GridTiles{p.total_tiles, dw_tile_kb(a.M)};
   return launch_tcgen05<Cfg, Epilogue::kStoreBF16>(tg, tx, tc, tg, tg, p, dev, stream);
 }
 
-// out[i] = bf16(acc[0][i] + acc[1][i] + ...), FP32 adds in slot order; four
-// outputs per thread, the loads of eight slots in flight at a time.
+// The sum of dX's parts as a grid of its own, where no dW follows to do it or
+// its threads would take longer (37 x 32768 x 2048, 1.4 M values: 75.8 us with
+// a grid, 73.2 within dW; 1024 x 32768 x 2048, 4 M values: 247 against 252).
 constexpr int kSumThreads = 128;
+constexpr size_t kSumInDw = size_t(3) << 20;  // values of all parts
 __global__ void __launch_bounds__(kSumThreads)
-    xent_sum_kernel(const float* __restrict__ acc, uint16_t* __restrict__ out, size_t n, int slots) {
+    xent_sum_kernel(const float* acc, uint16_t* out, size_t n, int slots) {
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
-  const size_t step = size_t(gridDim.x) * kSumThreads;
-  for (size_t i = size_t(blockIdx.x) * kSumThreads + threadIdx.x; i < n / 4; i += step) {
-    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int b = 0; b < slots; b += 8) {
-      float4 v[8];
-#pragma unroll
-      for (int u = 0; u < 8; ++u)
-        if (b + u < slots) v[u] = __ldcg(reinterpret_cast<const float4*>(acc + size_t(b + u) * n) + i);
-#pragma unroll
-      for (int u = 0; u < 8; ++u)
-        if (b + u < slots) {
-          s.x += v[u].x;
-          s.y += v[u].y;
-          s.z += v[u].z;
-          s.w += v[u].w;
-        }
-    }
-    reinterpret_cast<uint2*>(out)[i] =
-        make_uint2(pack_bf16x2(__float_as_uint(s.x), __float_as_uint(s.y)),
-                   pack_bf16x2(__float_as_uint(s.z), __float_as_uint(s.w)));
-  }
+  sum_slots(acc, out, n, slots, size_t(blockIdx.x) * kSumThreads + threadIdx.x,
+            size_t(gridDim.x) * kSumThreads);
 }
 
 template <class Kernel, class... Args>
@@ -510,6 +497,8 @@ int launch_xent_backward(const XentBackward& a, const DeviceInfo& dev, cudaStrea
   const bool few = a.M <= kRowsFew;
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   float* acc = reinterpret_cast<float*>(ws + q.g_bytes * q.g_bufs);
+  const bool sum_in_dw =
+      a.dX && a.dW && q.dx_bytes && size_t(a.M) * a.K * q.splits <= kSumInDw;
   GridTiles before{0, 0.0};  // the latest grid, for the next one's head start
   for (int i = 0; i < q.pieces; ++i) {
     Piece pc;
@@ -526,12 +515,14 @@ int launch_xent_backward(const XentBackward& a, const DeviceInfo& dev, cudaStrea
                : run_dx<XentDxPair>(a, q, pc, acc, &before, dev, stream);
     // (the few tokens' dX runs on single CTAs: its last round frees no pairs in order)
     if (few) before = {0, 0.0};
+    // the last dW grid, which ends after dX's, also adds dX's parts
+    const int slots = (sum_in_dw && i + 1 == q.pieces) ? q.splits : 0;
     if (rc == GEMM_OK && a.dW)
-      rc = few ? run_dw<XentDwFew>(a, pc, a.dX != nullptr, before, &before, dev, stream)
-               : run_dw<XentDwPair>(a, pc, a.dX != nullptr, before, &before, dev, stream);
+      rc = few ? run_dw<XentDwFew>(a, pc, a.dX != nullptr, acc, slots, before, &before, dev, stream)
+               : run_dw<XentDwPair>(a, pc, a.dX != nullptr, acc, slots, before, &before, dev, stream);
     if (rc != GEMM_OK) return rc;
   }
-  if (a.dX && q.dx_bytes) {
+  if (a.dX && q.dx_bytes && !sum_in_dw) {
     const size_t n = size_t(a.M) * a.K;
     const long long grid = std::min<long long>((n / 4 + kSumThreads - 1) / kSumThreads,
                                                (long long)dev.num_sms * 16);
