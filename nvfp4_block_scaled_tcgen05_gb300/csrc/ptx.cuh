@@ -153,6 +153,13 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// 1 / x, at most one unit in the last place off.
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // Two FP32 operations in one instruction, each rounded as alone.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   float2 d;

@@ -19,6 +19,8 @@
 // the blocks', both in a fixed order.
 #include <cuda_bf16.h>
 
+#include <float.h>
+
 #include <algorithm>
 
 #include "internal.h"
@@ -49,6 +51,10 @@ __device__ __forceinline__ uint32_t rank_key(float v) {
   const uint32_t b = __float_as_uint(v + 0.0f);
   if (v != v) return 0xFFFFFFFFu;
   return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+
+__device__ __forceinline__ float key_value(uint32_t key) {
+  return __uint_as_float((key & 0x80000000u) ? key & 0x7FFFFFFFu : ~key);
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -116,12 +122,15 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
 // NV: values per lane (E <= 32 NV)
 template <int NV, bool kAligned>
 __global__ void __launch_bounds__(32 * kWarps, NV <= 8 ? 2 : 1) route_kernel(const RouteArgs a) {
-  extern __shared__ uint32_t sh[];
+  extern __shared__ __align__(16) uint32_t sh[];
   float* sh_prob = reinterpret_cast<float*>(sh);             // [kWarps][E]
   int* sh_hits = reinterpret_cast<int*>(sh + kWarps * a.E);  // [E]
+  // each warp's row, 32 NV values, 16-byte aligned
   __shared__ float sh_z[kWarps], red[kWarps];
   __shared__ int sh_t[kWarps];
   __shared__ unsigned long long sh_cand[kWarps][32];
+  float* row_vals = reinterpret_cast<float*>(
+      sh + (kWarps + 1) * ((a.E + 3) / 4 * 4) + (threadIdx.x >> 5) * 32 * NV);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   for (int e = threadIdx.x; e < a.E; e += blockDim.x) sh_hits[e] = 0;
   __syncthreads();
@@ -148,7 +157,7 @@ __global__ void __launch_bounds__(32 * kWarps, NV <= 8 ? 2 : 1) route_kernel(con
 #pragma unroll
     for (int i = 0; i < NV; ++i) s += p[i] = fast_exp(v[i] - ref);
     s = warp_sum(s);
-    const float inv = 1.0f / s;
+    const float inv = ptx::rcp(s);
     const float l = ref + logf(s);
     if (lane == 0) a.lse[row] = l;
     // a sum of 0 is a row of -inf only (a NaN makes the sum NaN)
@@ -160,50 +169,54 @@ __global__ void __launch_bounds__(32 * kWarps, NV <= 8 ? 2 : 1) route_kernel(con
       for (int i = 0; i < NV; ++i) acc[i] += p[i] * inv;
     }
 
-    // Choice.  The k-th largest of the lanes' maxima bounds the k-th largest
-    // value from below, so only values that reach it are candidates: usually
-    // little more than k, which rank themselves against each other.
+    // Choice.  The k-th largest of the lanes' maxima (equal ones counted once)
+    // bounds the k-th largest value from below, so only values that reach it
+    // are candidates: usually little more than k, which rank themselves
+    // against each other.
     int my_expert = -1, my_rank = lane;
     float my_weight = 0.0f;
     bool slow = live && s != s;  // NaN somewhere
     if (live && !slow) {
       uint32_t cur = rank_key(lane_max), floor_key = 0u;
-      int n = 0;
-      for (int r = 0; r < a.k && n < a.k; ++r) {
+      for (int r = 0; r < a.k; ++r) {
         floor_key = __reduce_max_sync(0xffffffffu, cur);
-        n += __popc(__ballot_sync(0xffffffffu, cur == floor_key));
         if (cur == floor_key) cur = 0u;
       }
       // fewer than k lanes with a value: every value above -inf is a candidate
-      float bound = -INFINITY;
-      if (n >= a.k && floor_key > kNoKey)
-        bound = __uint_as_float((floor_key & 0x80000000u) ? floor_key & 0x7FFFFFFFu : ~floor_key);
-      n = 0;
-      const uint32_t below = (1u << lane) - 1u;
+      const float bound = floor_key > kNoKey ? key_value(floor_key) : -FLT_MAX;
+      uint32_t mine = 0u;  // bit i: value i is a candidate
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const bool c = v[i] >= bound && v[i] != -INFINITY;
-        const uint32_t who = __ballot_sync(0xffffffffu, c);
-        const int at = n + __popc(who & below);
-        if (c && at < 32)
-          cand[at] = (static_cast<unsigned long long>(rank_key(v[i])) << 32) |
-                     (0xFFFFFFFFu - uint32_t(column_of(i, lane)));
-        n += __popc(who);
+      for (int i = 0; i < NV; ++i) mine |= v[i] >= bound ? 1u << i : 0u;
+      int n = __popc(mine), at = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int left = __shfl_up_sync(0xffffffffu, at, o);
+        if (lane >= o) at += left;
       }
+      at -= n;                                        // candidates of the lanes before
+      n = __shfl_sync(0xffffffffu, at + n, 31);       // of all lanes
       slow = n > 32;
       if (!slow) {
+        // the row goes through shared memory, where a lane can pick by index
+#pragma unroll
+        for (int i = 0; i < NV; i += 4)
+          *reinterpret_cast<float4*>(row_vals + column_of(i, lane)) =
+              make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+        for (; mine; mine &= mine - 1u, ++at) {
+          const int e = column_of(__ffs(int(mine)) - 1, lane);
+          cand[at] = (static_cast<unsigned long long>(rank_key(row_vals[e])) << 32) |
+                     (0xFFFFFFFFu - uint32_t(e));
+        }
         __syncwarp();
-        const unsigned long long mine = lane < n ? cand[lane] : 0ull;
+        const unsigned long long own = lane < n ? cand[lane] : 0ull;
         int rank = 0;
-    #pragma unroll 4
-        for (int j = 0; j < n; ++j) rank += cand[j] > mine;
+#pragma unroll 4
+        for (int j = 0; j < n; ++j) rank += cand[j] > own;
         __syncwarp();
         if (lane < n) {
           if (rank < a.k) {
-            const uint32_t key = uint32_t(mine >> 32);
-            const float x = __uint_as_float((key & 0x80000000u) ? key & 0x7FFFFFFFu : ~key);
-            my_expert = int(0xFFFFFFFFu - uint32_t(mine));
-            my_weight = fast_exp(x - ref) * inv;
+            my_expert = int(0xFFFFFFFFu - uint32_t(own));
+            my_weight = fast_exp(key_value(uint32_t(own >> 32)) - ref) * inv;
           }
           my_rank = rank;
         }
@@ -244,7 +257,7 @@ __global__ void __launch_bounds__(32 * kWarps, NV <= 8 ? 2 : 1) route_kernel(con
     }
     if (a.normalize) {
       const float total = warp_sum(my_expert >= 0 ? my_weight : 0.0f);
-      if (my_expert >= 0) my_weight = my_weight / total;
+      if (my_expert >= 0) my_weight *= ptx::rcp(total);
     }
     if (my_rank < a.k) {
       a.weights[row * a.k + my_rank] = my_weight;
@@ -408,18 +421,18 @@ struct RouteGradArgs {
 //   u[e]  = dw[e], or normalised (dw[e] - q) / a with a = sum_A p and
 //           q = sum_A p dw / a; then sum_f p[f] u[f] = 0
 // so one pass of four sums (s, sum e base, sum_A e, sum_A e dw) gives all that
-// a row needs.  The k gradients dw reach the lanes that own their columns
-// through a row of shared memory, kNone elsewhere.
+// a row needs.  The k lanes that hold the gradients dw read their e from a row
+// of shared memory and give u back through another, zero elsewhere.
 template <int NV, bool kAligned, bool kBF16>
 __global__ void __launch_bounds__(32 * kGradWarps, NV <= 8 ? 4 : 2)
     route_grad_kernel(const RouteGradArgs a) {
   extern __shared__ __align__(16) uint32_t sh[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const float kNone = __uint_as_float(0x7FFFFFFFu);  // a NaN no gradient carries
   const int up_row = (a.E + 3) / 4 * 4;  // whole 16-byte groups
   float* base = reinterpret_cast<float*>(sh);  // [up_row] dp's first term
-  float* up = base + (1 + warp) * up_row;
-  for (int e = lane; e < up_row; e += 32) up[e] = kNone;
+  float* up = base + (1 + 2 * warp) * up_row;  // [up_row] u
+  float* er = up + up_row;                     // [up_row] e
+  for (int e = lane; e < up_row; e += 32) up[e] = 0.0f;
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   const float t = at_least_one(a.counts[a.E]);
@@ -434,7 +447,7 @@ __global__ void __launch_bounds__(32 * kGradWarps, NV <= 8 ? 4 : 2)
   __syncthreads();
   const long long step = (long long)gridDim.x * kGradWarps;
   for (long long row = (long long)blockIdx.x * kGradWarps + warp; row < a.M; row += step) {
-    float p[NV], u[NV];
+    float p[NV];
     load_row<NV, kAligned>(a.logits + row * a.ld, a.E, lane, p);
     const float l = __ldcg(a.lse + row);
     int ex = -1;
@@ -444,30 +457,26 @@ __global__ void __launch_bounds__(32 * kGradWarps, NV <= 8 ? 4 : 2)
       if (a.dweights) g = __ldcg(a.dweights + row * a.k + lane);
       if (ex >= a.E) ex = -1;  // not an expert: takes no part
     }
-    if (__float_as_uint(g) == 0x7FFFFFFFu) g = __uint_as_float(0x7FC00000u);
     const bool live = __shfl_sync(0xffffffffu, ex, 0) >= 0;
-    if (ex >= 0) up[ex] = g;
-    __syncwarp();
     float s = 0.0f, sb = 0.0f, sa = 0.0f, sg = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; i += 4) {
       const int e = column_of(i, lane);
-      float4 q = make_float4(kNone, kNone, kNone, kNone), d = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (e < up_row) {
-        q = *reinterpret_cast<const float4*>(up + e);
-        d = *reinterpret_cast<const float4*>(base + e);
-      }
-      u[i] = q.x, u[i + 1] = q.y, u[i + 2] = q.z, u[i + 3] = q.w;
-      const float b4[4] = {d.x, d.y, d.z, d.w};
 #pragma unroll
       for (int c = i; c < i + 4; ++c) {
         p[c] = fast_exp(p[c] - l);
         s += p[c];
-        sb += p[c] * b4[c - i];
-        const bool taken = __float_as_uint(u[c]) != 0x7FFFFFFFu;
-        sa += taken ? p[c] : 0.0f;
-        sg += taken ? p[c] * u[c] : 0.0f;
       }
+      if (e < up_row) {
+        const float4 b = *reinterpret_cast<const float4*>(base + e);
+        sb += p[i] * b.x + p[i + 1] * b.y + p[i + 2] * b.z + p[i + 3] * b.w;
+        *reinterpret_cast<float4*>(er + e) = make_float4(p[i], p[i + 1], p[i + 2], p[i + 3]);
+      }
+    }
+    __syncwarp();
+    if (ex >= 0) {
+      sa = er[ex];
+      sg = sa * g;
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
@@ -476,24 +485,26 @@ __global__ void __launch_bounds__(32 * kGradWarps, NV <= 8 ? 4 : 2)
       sa += __shfl_xor_sync(0xffffffffu, sa, o);
       sg += __shfl_xor_sync(0xffffffffu, sg, o);
     }
+    const float inv = ptx::rcp(s);
+    if (ex >= 0) {
+      // q = sg / sa: the sum of the weights times their gradients; s / sa: 1 /
+      // (the sum of the taken p)
+      const float a1 = ptx::rcp(sa);
+      up[ex] = a.normalize ? (g - sg * a1) * (s * a1) : g;
+    }
     __syncwarp();
-    if (ex >= 0) up[ex] = kNone;
-    const float inv = 1.0f / s;
-    const float q = a.normalize ? sg / sa : 0.0f;        // sum of the weights times their gradients
-    const float scale = a.normalize ? s / sa : 1.0f;     // 1 / (sum of the taken p)
     const float shift = c1 * l - (sb + (a.normalize ? 0.0f : sg)) * inv;
 #pragma unroll
     for (int i = 0; i < NV; i += 4) {
       const int e = column_of(i, lane);
-      const float4 b = e < up_row ? *reinterpret_cast<const float4*>(base + e)
-                                  : make_float4(0.f, 0.f, 0.f, 0.f);
-      const float b4[4] = {b.x, b.y, b.z, b.w};
-      float d[4];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const bool taken = __float_as_uint(u[i + c]) != 0x7FFFFFFFu;
-        const float dp = b4[c] + (taken ? (u[i + c] - q) * scale : 0.0f);
-        d[c] = live ? p[i + c] * inv * (dp + shift) : 0.0f;
+      float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      if (live && e < up_row) {
+        const float4 b = *reinterpret_cast<const float4*>(base + e);
+        const float4 u = *reinterpret_cast<const float4*>(up + e);
+        d[0] = p[i] * inv * (b.x + u.x + shift);
+        d[1] = p[i + 1] * inv * (b.y + u.y + shift);
+        d[2] = p[i + 2] * inv * (b.z + u.z + shift);
+        d[3] = p[i + 3] * inv * (b.w + u.w + shift);
       }
       const size_t off = size_t(row) * a.E + e;
       // BF16: one rounding, for a gradient that goes into a BF16 product
@@ -522,6 +533,7 @@ __global__ void __launch_bounds__(32 * kGradWarps, NV <= 8 ? 4 : 2)
       }
     }
     __syncwarp();
+    if (ex >= 0) up[ex] = 0.0f;
   }
 }
 
@@ -549,16 +561,22 @@ int launch(Kernel kernel, int grid, int threads, size_t shared, cudaStream_t str
   return GEMM_OK;
 }
 
+// Past the default limit (together with the static arrays) a kernel has to be
+// allowed its dynamic shared memory.
+template <class Kernel>
+bool allow_shared(Kernel kernel, size_t bytes) {
+  if (bytes <= 40 * 1024) return true;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes)) ==
+      cudaSuccess)
+    return true;
+  cudaGetLastError();
+  return false;
+}
+
 template <int NV, bool kAligned>
 int run_route(const RouteArgs& a, int blocks, cudaStream_t stream) {
-  const size_t shared = size_t(kWarps + 1) * a.E * 4;
-  if (shared > 40 * 1024) {  // past the default limit together with the static arrays
-    if (cudaFuncSetAttribute(route_kernel<NV, kAligned>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             int(shared)) != cudaSuccess) {
-      cudaGetLastError();
-      return GEMM_ERR_LAUNCH;
-    }
-  }
+  const size_t shared = (size_t(kWarps + 1) * ((a.E + 3) / 4 * 4) + size_t(kWarps) * 32 * NV) * 4;
+  if (!allow_shared(route_kernel<NV, kAligned>, shared)) return GEMM_ERR_LAUNCH;
   return launch(route_kernel<NV, kAligned>, blocks, 32 * kWarps, shared, stream, a);
 }
 
@@ -566,9 +584,10 @@ template <int NV, bool kAligned>
 int run_route_grad(const RouteGradArgs& a, bool bf16, cudaStream_t stream) {
   const int blocks = int(
       std::min<long long>(kGradMaxBlocks, ((long long)a.M + kGradWarps - 1) / kGradWarps));
-  const size_t shared = size_t(kGradWarps + 1) * ((a.E + 3) / 4 * 4) * 4;
-  return bf16 ? launch(route_grad_kernel<NV, kAligned, true>, blocks, 32 * kGradWarps, shared, stream, a)
-              : launch(route_grad_kernel<NV, kAligned, false>, blocks, 32 * kGradWarps, shared, stream, a);
+  const size_t shared = size_t(2 * kGradWarps + 1) * ((a.E + 3) / 4 * 4) * 4;
+  auto kernel = bf16 ? route_grad_kernel<NV, kAligned, true> : route_grad_kernel<NV, kAligned, false>;
+  if (!allow_shared(kernel, shared)) return GEMM_ERR_LAUNCH;
+  return launch(kernel, blocks, 32 * kGradWarps, shared, stream, a);
 }
 
 // The smallest row buffer that holds E columns.
