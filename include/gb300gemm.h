@@ -1,5 +1,6 @@
 /*
- * gb300gemm.h - C ABI of the GB300 (sm_103a) dense NT GEMM library.
+ * gb300gemm.h - C ABI of the GB300 (sm_103a) dense NT GEMM library, and of the
+ * losses that a mixture-of-experts language model trains on.
  *
  * All entry points:
  *  - take plain pointers and sizes; no framework types cross this boundary;

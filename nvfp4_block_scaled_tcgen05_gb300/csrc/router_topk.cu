@@ -17,6 +17,12 @@
 // sums and statistics in FP32.  Each warp keeps the column sums of its rows
 // in registers; blocks add their warps' sums and a second, small grid adds
 // the blocks', both in a fixed order.
+//
+// Measured (top-8 of 256): one row 3.4 us forward, 1.7 us backward; 4510 rows
+// 9.1 and 3.1 us; 65536 rows 39 us forward (bound by issuing, about 350
+// instructions a row) and 26.5 us backward (5.1 TB/s of logits and gradients).
+// A row is a chain of reductions about 2 us long, so small calls are bound by
+// latency; up to kOneBlockRows rows one block does without the second grid.
 #include <cuda_bf16.h>
 
 #include <float.h>

@@ -22,7 +22,9 @@
 //                 ("register-staged") every accumulator column is read into
 //                 registers before the accumulator is released, so the
 //                 epilogue still overlaps the next tile's MMAs; with two
-//                 accumulators 8 warps take half of the columns each;
+//                 accumulators 8 warps take half of the columns each
+//                 (linear cross entropy: statistics of the logits, or their
+//                 gradient, instead of the logits);
 //   W4A16 only    8 conversion warps (packed codes -> BF16 B stages) and
 //                 one warp TMA-loading the codes and scales into a ring.
 // Every wait is bounded (globaltimer); a timeout records a code in the

@@ -5,16 +5,24 @@
 //   G[m][v]  = d[m] (exp(z[m][v] - lse[m]) - [v = target[m]])
 //   dX = G . W,   dW = G^T . X.
 //
-// Forward: the NT GEMM with an epilogue that folds each 256-column tile of a
-// row into (maximum, sum of exponentials); a second kernel joins the tiles of
-// a row in order.  Per row and tile 8 bytes leave the chip instead of 512.
+// Forward: the NT GEMM with an epilogue that folds a row's 128 columns of a
+// tile into (maximum, sum of exponentials); a second kernel joins the groups of
+// a row in a fixed order.  Per row and 128 logits 8 bytes leave the chip
+// instead of 256.  Bound by the MMAs (8192 x 65536 x 4096: 2219 us in a burst,
+// 1982 TFLOP/s; 2400-2470 under the power cap) or, with few tokens, by reading
+// W (64 x 131072 x 4096: 160 us, 6.7 TB/s).  Rows whose pitch is not a multiple
+// of 32 bytes cost a fifth sector per 128 bytes on the way from L2: 1016 x
+// 32003 x 2056 takes 100 us where 1024 x 32768 x 2048 takes 78.
 //
 // Backward: pieces of the vocabulary.  Per piece one GEMM forms the logits
 // again and writes G as BF16 (the operand type of the products that follow:
 // one rounding of relative size 2^-9 per term), one adds G . W into FP32, one
-// computes the piece's rows of dW.  The grids of a piece are chained so that
-// one without a data dependency on its predecessor starts on the SMs the
-// predecessor's last round leaves idle (run_piece).
+// computes the piece's rows of dW: three times the forward's products, since
+// the logits are not kept.  The grids of a piece are chained so that one
+// without a data dependency on its predecessor starts on the SMs the
+// predecessor's last round leaves idle (launch_xent_backward).  4096 x 131072 x
+// 4096: 7220 us in a burst (1828 TFLOP/s), 7730 under the power cap; 37 x 32768
+// x 2048: 73 us, of which reading W twice and writing dW take 60.
 #include <algorithm>
 
 #include "launch.cuh"
@@ -64,8 +72,10 @@ constexpr int kRowsFew = 128;  // up to this many tokens, they take the MMA's N 
 // K per accumulator, see ChunkedCfg.  8192 x 65536 x 4096 under the power cap:
 // 2530 us with 512, 2470 with 1024 (lse off by 6e-7 of its value, as in plain
 // FP32), 2445 with 2048 (1.3e-6): the extra reads of the accumulators cost
-// power.  Few tokens leave the power to spare.
-constexpr int kChunkK = 1024, kChunkKFew = 512;
+// power.  Few tokens have it to spare, and a single row's loss lse - z[target]
+// cancels: 37 x 32768 x 2048 takes 27.0 us with 512, 27.3 with 256, 28.2 with
+// 128.
+constexpr int kChunkK = 1024, kChunkKFew = 256;
 
 // Joins the groups' statistics of each row.  A block takes `rows` (a power of
 // two) rows; thread t takes row t % rows and the groups t / rows,
