@@ -239,7 +239,6 @@ struct XentPlan {
 // additions hidden behind the MMAs.
 constexpr long long kPieceBytes = 128ll << 20;
 constexpr int kMinPiece = 4096;
-constexpr int kMaxSplits = 152;
 
 int round64(int n) { return (n + 63) / 64 * 64; }
 
@@ -265,12 +264,17 @@ HeadStart head_start(GridTiles before, long long tiles, double tile_kb, int pair
   if (busy == 0) return h;
   const int early = pairs - busy;
   h.end += before.kb;
-  for (int x = 0; double(x) <= before.kb / tile_kb + 1 && (long long)x * early <= tiles; ++x) {
-    const long long rest = tiles - (long long)x * early;
+  // the early clusters' end grows with x and the others' falls; they meet near
+  // the head start's worth of tiles
+  const long long even =
+      std::min(static_cast<long long>(before.kb / tile_kb), tiles / early);
+  for (long long x = std::max(0ll, even - 1); x <= even + 1 && x * early <= tiles; ++x) {
+    const long long rest = tiles - x * early;
     const double end_early = double(x + (rest + pairs - 1) / pairs) * tile_kb;
     const double end_late =
         before.kb + double(std::max(0ll, (rest - early + pairs - 1) / pairs)) * tile_kb;
-    if (std::max(end_early, end_late) < h.end) h = {early, x, std::max(end_early, end_late)};
+    if (std::max(end_early, end_late) < h.end)
+      h = {early, int(x), std::max(end_early, end_late)};
   }
   return h;
 }
@@ -329,7 +333,9 @@ XentPlan make_plan(int M, int V, int K) {
   const int nkb = (q.piece + bk - 1) / bk;
   q.splits = 1;
   double best = 1e300;
-  for (int want = 1; want <= kMaxSplits && want <= std::max(1, nkb / 4); ++want) {
+  // (more than two rounds of parts fill no better)
+  const int most = std::max<int>(4, int(2 * units / std::min<long long>(tiles, units)));
+  for (int want = 1; want <= most && want <= std::max(1, nkb / 4); ++want) {
     const int per = (nkb + want - 1) / want;
     const int s = (nkb + per - 1) / per;
     const double parts = double(s) * M * double(K) * 8.0 / 3.4e6;
