@@ -419,16 +419,16 @@ def _run(name: str, device, *args) -> None:
 
 
 def _workspace(given, need: int, device):
-    """The caller's workspace, or one allocated here (None where none is needed)."""
+    """(pointer, bytes, tensor) of the caller's workspace, or of one allocated
+    here (None where none is needed); the tensor has to live through the call."""
     if given is None:
-        return torch.empty((need,), dtype=torch.uint8, device=device) if need else None
+        if not need:
+            return None, 0, None
+        given = torch.empty((need,), dtype=torch.uint8, device=device)
+        return given.data_ptr(), need, given
     if not (given.device == device and given.is_contiguous()):
         raise ValueError(f"workspace must be a contiguous tensor on {device}")
-    return given
-
-
-def _bytes_of(t) -> int:
-    return 0 if t is None else t.numel() * t.element_size()
+    return given.data_ptr(), given.numel() * given.element_size(), given
 
 
 def _ptr(t):
@@ -474,9 +474,9 @@ def gemm_bf16_nt_xent(X: torch.Tensor, W: torch.Tensor, target: torch.Tensor,
         lse = torch.empty((M,), dtype=f32, device=device)
     else:
         _on_device("lse", device, lse, f32, (M,))
-    workspace = _workspace(workspace, gemm_bf16_nt_xent_workspace_bytes(M, V), device)
+    ws, nbytes, _alive = _workspace(workspace, gemm_bf16_nt_xent_workspace_bytes(M, V), device)
     _run("gemm_bf16_nt_xent", device, X.data_ptr(), W.data_ptr(), target.data_ptr(),
-         loss.data_ptr(), lse.data_ptr(), _ptr(workspace), _bytes_of(workspace), M, V, K)
+         loss.data_ptr(), lse.data_ptr(), ws, nbytes, M, V, K)
     return loss, lse
 
 
@@ -512,10 +512,9 @@ def gemm_bf16_nt_xent_backward(X: torch.Tensor, W: torch.Tensor, target: torch.T
         _on_device("dW", device, dW, torch.bfloat16, (V, K))
     elif need_dw:
         dW = torch.empty((V, K), dtype=torch.bfloat16, device=device)
-    workspace = _workspace(workspace, gemm_bf16_nt_xent_backward_workspace_bytes(M, V, K), device)
+    ws, nbytes, _alive = _workspace(workspace, gemm_bf16_nt_xent_backward_workspace_bytes(M, V, K), device)
     _run("gemm_bf16_nt_xent_backward", device, X.data_ptr(), W.data_ptr(), target.data_ptr(),
-         lse.data_ptr(), dloss.data_ptr(), _ptr(dX), _ptr(dW), _ptr(workspace),
-         _bytes_of(workspace), M, V, K)
+         lse.data_ptr(), dloss.data_ptr(), _ptr(dX), _ptr(dW), ws, nbytes, M, V, K)
     return dX, dW
 
 
@@ -579,10 +578,10 @@ def router_topk(logits: torch.Tensor, k: int, valid: torch.Tensor | None = None,
     counts = empty((E + 1,), dtype=i32, device=device)
     probs = empty((E,), dtype=f32, device=device)
     losses = empty((2,), dtype=f32, device=device)
-    workspace = _workspace(workspace, router_topk_workspace_bytes(M, E), device)
+    ws, nbytes, _alive = _workspace(workspace, router_topk_workspace_bytes(M, E), device)
     _run("router_topk", device, logits.data_ptr(), _ptr(valid), weights.data_ptr(),
          experts.data_ptr(), lse.data_ptr(), counts.data_ptr(), probs.data_ptr(),
-         losses.data_ptr(), _ptr(workspace), _bytes_of(workspace), M, E, ld, k,
+         losses.data_ptr(), ws, nbytes, M, E, ld, k,
          1 if normalize else 0)
     return RouterTopk(weights, experts, lse, counts, probs, losses)
 

@@ -196,6 +196,20 @@ def test_backward_against_differences(g, norm):
         assert (num - (got.to(F64) * u).sum()).abs() <= (tol * u.abs()).sum() + 1e-6
 
 
+@pytest.mark.parametrize("E,k", [(256, 8), (64, 32), (1024, 5), (33, 33 - 1)])
+def test_all_equal_logits_take_the_lowest_indices(g, E, k):
+    # every value is a candidate: more than 32 of them go the long way
+    l = torch.full((70, E), 0.25, device="cuda")
+    out = g.router_topk(l, k, normalize=True)
+    assert (out.experts == torch.arange(k, device="cuda")).all()
+    assert ((out.weights.to(F64) - 1 / k).abs() <= 1e-6 / k).all()
+    assert (out.counts[:k] == 70).all() and (out.counts[k:-1] == 0).all()
+    l[:, E - 1] = 1.0                      # one value above the ties
+    out = g.router_topk(l, k)
+    assert (out.experts[:, 0] == E - 1).all()
+    assert (out.experts[:, 1:] == torch.arange(k - 1, device="cuda")).all()
+
+
 def test_row_stride(g):
     l, valid = logits_of(333, 48, 3, closed=0.2)
     wide = torch.full((333, 131), float("nan"), device="cuda")

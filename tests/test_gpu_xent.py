@@ -127,6 +127,73 @@ def test_pieces_of_the_vocabulary(g, M, V, K):
     assert torch.equal(again[0], dX) and torch.equal(again[1], dW)   # fixed order of sums
 
 
+@pytest.mark.parametrize("M,V,K", [
+    (1, 1849, 72), (64, 1849, 328),       # tiles of 64 vocabulary rows
+    (3, 4902, 136), (64, 4865, 40),       # of 128
+    (17, 23300, 64), (128, 9000, 264),    # of 192
+    (33, 32769, 24), (100, 19456, 1032),  # of 256
+])
+def test_tile_heights_of_few_tokens(g, M, V, K):
+    X, W, t, d = problem(M, V, K, 31 + V)
+    loss, lse = g.gemm_bf16_nt_xent(X, W, t)
+    check_forward(loss, lse, reference(X, W, t))
+    dX, dW = g.gemm_bf16_nt_xent_backward(X, W, t, lse, d)
+    rX, rW, eX, eW = gradients(X, W, t, lse, d)
+    assert ((dX.to(F64) - rX).abs() <= eX).all()
+    assert ((dW.to(F64) - rW).abs() <= eW).all()
+
+
+@pytest.mark.parametrize("M,V,K", [
+    (1000, 20000, 520),    # dW's first clusters take more tiles than the others
+    (300, 30011, 1032),    # many parts of dX, more than one round of dW
+    (16411, 20001, 72),    # six pieces, whose G grids start early too
+])
+def test_grids_that_start_early(g, M, V, K):
+    X, W, t, d = problem(M, V, K, 37)
+    loss, lse = g.gemm_bf16_nt_xent(X, W, t)
+    dX, dW = g.gemm_bf16_nt_xent_backward(X, W, t, lse, d)
+    rX, rW, eX, eW = gradients(X, W, t, lse, d)
+    assert ((dX.to(F64) - rX).abs() <= eX).all()
+    assert ((dW.to(F64) - rW).abs() <= eW).all()
+    for _ in range(5):
+        again = g.gemm_bf16_nt_xent_backward(X, W, t, lse, d)
+        assert torch.equal(again[0], dX) and torch.equal(again[1], dW)
+
+
+def test_concurrent_streams_and_threads(g):
+    # two host threads, a stream and a workspace each, on the same weights
+    import threading
+    cases = [problem(M, 6000, 256, 41 + M) for M in (50, 300)]
+    want = []
+    for X, W, t, d in cases:
+        loss, lse = g.gemm_bf16_nt_xent(X, W, t)
+        want.append((loss, lse, *g.gemm_bf16_nt_xent_backward(X, W, t, lse, d)))
+    torch.cuda.synchronize()
+    got, errors = [[], []], []
+
+    def work(i):
+        try:
+            X, W, t, d = cases[i]
+            s = torch.cuda.Stream()
+            for _ in range(20):
+                loss, lse = g.gemm_bf16_nt_xent(X, W, t, stream=s)
+                got[i].append((loss, lse, *g.gemm_bf16_nt_xent_backward(X, W, t, lse, d, stream=s)))
+            s.synchronize()
+        except Exception as e:  # noqa: BLE001 (reported by the main thread)
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    assert not errors
+    for i in range(2):
+        assert len(got[i]) == 20
+        for res in got[i]:
+            assert all(torch.equal(a, b) for a, b in zip(res, want[i]))
+
+
 @pytest.mark.parametrize("M", [100, 300])
 def test_gradients_against_differences(g, M):
     V, K = 600, 64
