@@ -524,7 +524,7 @@ int gemm_bf16_nt_xent_backward(const void* X, const void* W, const long long* ta
   if (any_overlap(in, 5, out, 3)) return GEMM_ERR_ALIAS;
   DeviceInfo dev;
   if ((rc = current_device(&dev, stream)) != GEMM_OK) return rc;
-  const XentBackward a{X, W, target, lse, dloss, dX, dW, workspace, M, V, K};
+  const XentBackward a{X, W, target, lse, dloss, dX, dW, workspace, M, V, K, K};
   return launch_xent_backward(a, dev, static_cast<cudaStream_t>(stream));
 }
 

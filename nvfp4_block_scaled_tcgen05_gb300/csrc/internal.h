@@ -135,6 +135,7 @@ struct XentBackward {
   const float *lse, *dloss;
   void *dX, *dW, *workspace;
   int M, V, K;
+  int ldx;  // set by the launcher: X's row pitch
 };
 size_t xent_forward_workspace(int M, int V);
 size_t xent_backward_workspace(int M, int V, int K);

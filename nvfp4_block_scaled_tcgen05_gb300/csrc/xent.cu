@@ -118,6 +118,30 @@ __global__ void __launch_bounds__(kJoinThreads)
   loss[row] = y < 0 ? 0.0f : (y >= V ? NAN : l - loss[row]);
 }
 
+// X's rows with a pitch that is a multiple of 32 bytes, K + 8 elements: see
+// pads_x.  One 16-byte piece per thread.
+constexpr int kPadThreads = 128;
+__global__ void __launch_bounds__(kPadThreads)
+    xent_pad_kernel(const uint4* X, uint4* out, int M, int pieces) {
+  ptx::griddep_launch_dependents();
+  ptx::griddep_wait();
+  for (int row = int(blockIdx.y); row < M; row += int(gridDim.y)) {
+    const uint4* src = X + size_t(row) * pieces;
+    uint4* dst = out + size_t(row) * (pieces + 1);
+    const int i = int(blockIdx.x) * kPadThreads + int(threadIdx.x);
+    if (i < pieces) dst[i] = __ldcg(src + i);
+  }
+}
+
+// The matrix of X [rows][cols] with pitch ld.
+template <class Cfg>
+int encode_x(CUtensorMap* m, const void* base, int rows, int cols, int ld, int box_rows) {
+  return encode_tmap_3d_strided(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, uint64_t(cols),
+                                uint64_t(rows), 1, uint64_t(ld) * 2,
+                                uint64_t(ld) * 2 * uint64_t(rows), 64, uint32_t(box_rows), 1,
+                                CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
 template <class Cfg>
 int encode_k_major(CUtensorMap* m, const void* base, int rows, int cols, int box_rows) {
   return encode_tmap_3d(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, uint64_t(cols),
@@ -367,7 +391,7 @@ int run_grad(const XentBackward& a, const Piece& pc, bool late, GridTiles before
              const DeviceInfo& dev, cudaStream_t stream) {
   CUtensorMap tx, tw, tg;
   const uint16_t* W = static_cast<const uint16_t*>(a.W) + size_t(pc.v0) * a.K;
-  int rc = encode_k_major<Cfg>(&tx, a.X, a.M, a.K, kT ? Cfg::B_ROWS : Cfg::BM);
+  int rc = encode_x<Cfg>(&tx, a.X, a.M, a.K, a.ldx, kT ? Cfg::B_ROWS : Cfg::BM);
   const int rows = kT ? few_rows(pc.cols, Cfg::BN) : 0;
   if (rc == GEMM_OK) rc = encode_k_major<Cfg>(&tw, W, pc.cols, a.K, kT ? rows : Cfg::B_ROWS);
   if (rc == GEMM_OK) rc = encode_k_major<Cfg>(&tg, pc.G, kT ? pc.cols : a.M, pc.ld, 32);
@@ -430,7 +454,7 @@ int run_dw(const XentBackward& a, const Piece& pc, bool after_dx, const float* s
   uint16_t* dW = static_cast<uint16_t*>(a.dW) + size_t(pc.v0) * a.K;
   int rc = Cfg::A_MN ? encode_k_major<Cfg>(&tg, pc.G, a.M, pc.ld, Cfg::BK)
                      : encode_k_major<Cfg>(&tg, pc.G, pc.cols, pc.ld, Cfg::BM);
-  if (rc == GEMM_OK) rc = encode_k_major<Cfg>(&tx, a.X, a.M, a.K, Cfg::BK);
+  if (rc == GEMM_OK) rc = encode_x<Cfg>(&tx, a.X, a.M, a.K, a.ldx, Cfg::BK);
   if (rc == GEMM_OK) rc = encode_k_major<Cfg>(&tc, dW, pc.cols, a.K, 32);
   if (rc != GEMM_OK) return rc;
   GemmParams p = base_params<Cfg>(pc.cols, a.K, a.M, dev);
@@ -459,13 +483,13 @@ __global__ void __launch_bounds__(kSumThreads)
 }
 
 template <class Kernel, class... Args>
-int launch_dependent(Kernel kernel, long long grid, int threads, cudaStream_t stream,
+int launch_dependent(Kernel kernel, dim3 grid, int threads, cudaStream_t stream,
                      Args... args) {
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3(unsigned(grid));
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
   cfg.stream = stream;
   cfg.attrs = attr;
@@ -477,6 +501,27 @@ int launch_dependent(Kernel kernel, long long grid, int threads, cudaStream_t st
   return GEMM_OK;
 }
 
+// Rows whose pitch is an odd multiple of 16 bytes (K % 16 == 8) take five
+// 32-byte sectors per 128 bytes on the way from L2, which then paces the MMAs.
+// The backward pass first copies X to rows of K + 8 elements, where the
+// vocabulary is long enough to repay it: 1016 x 32003 x 2056 283.6 -> 276 us,
+// 2048 x 40000 x 4104 1262 -> 1202, 300 x 32003 x 2056 159 -> 154, but 1016 x
+// 9000 x 2056 90.8 -> 92.5.  (W would cost more than it gains.)
+constexpr int kPadColumns = 12288;
+bool pads_x(int M, int V, int K) { return K % 16 != 0 && M > kRowsFew && V >= kPadColumns; }
+size_t pad_bytes(int M, int V, int K) {
+  return pads_x(M, V, K) ? (size_t(M) * (size_t(K) + 8) * 2 + 255) / 256 * 256 : 0;
+}
+int pad_x(XentBackward& a, void* to, cudaStream_t stream) {
+  const int pieces = a.K / 8;
+  const int rc = launch_dependent(
+      xent_pad_kernel, dim3((pieces + kPadThreads - 1) / kPadThreads, std::min(a.M, 4096)),
+      kPadThreads, stream, static_cast<const uint4*>(a.X), static_cast<uint4*>(to), a.M, pieces);
+  a.X = to;
+  a.ldx = a.K + 8;
+  return rc;
+}
+
 }  // namespace
 
 size_t xent_forward_workspace(int M, int V) {
@@ -485,7 +530,7 @@ size_t xent_forward_workspace(int M, int V) {
 
 size_t xent_backward_workspace(int M, int V, int K) {
   const XentPlan q = make_plan(M, V, K);
-  return q.g_bytes * q.g_bufs + q.dx_bytes;
+  return pad_bytes(M, V, K) + q.g_bytes * q.g_bufs + q.dx_bytes;
 }
 
 int launch_xent_forward(const XentForward& a, const DeviceInfo& dev, cudaStream_t stream) {
@@ -497,7 +542,7 @@ int launch_xent_forward(const XentForward& a, const DeviceInfo& dev, cudaStream_
   if (rc != GEMM_OK) return rc;
   // few rows: more threads per row
   const int rows = a.M >= 2048 ? 32 : a.M >= 256 ? 8 : 1;
-  return launch_dependent(xent_join_kernel, (a.M + rows - 1) / rows, kJoinThreads, stream,
+  return launch_dependent(xent_join_kernel, dim3((a.M + rows - 1) / rows), kJoinThreads, stream,
                           static_cast<const float2*>(a.workspace), a.target, a.loss, a.lse, a.M,
                           a.V, groups, rows);
 }
@@ -513,7 +558,14 @@ int launch_xent_forward(const XentForward& a, const DeviceInfo& dev, cudaStream_
 //     when a product of piece i has started, and waits at its end.
 // A grid that ends after its predecessor keeps the chain: whoever waits for it
 // also has everything before it.
-int launch_xent_backward(const XentBackward& a, const DeviceInfo& dev, cudaStream_t stream) {
+int launch_xent_backward(const XentBackward& args, const DeviceInfo& dev, cudaStream_t stream) {
+  XentBackward a = args;
+  a.ldx = a.K;
+  if (const size_t pad = pad_bytes(a.M, a.V, a.K)) {
+    const int rc = pad_x(a, a.workspace, stream);
+    if (rc != GEMM_OK) return rc;
+    a.workspace = static_cast<uint8_t*>(a.workspace) + pad;
+  }
   const XentPlan q = make_plan(a.M, a.V, a.K);
   const bool few = a.M <= kRowsFew;
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
@@ -547,7 +599,7 @@ int launch_xent_backward(const XentBackward& a, const DeviceInfo& dev, cudaStrea
     const size_t n = size_t(a.M) * a.K;
     const long long grid = std::min<long long>((n / 4 + kSumThreads - 1) / kSumThreads,
                                                (long long)dev.num_sms * 16);
-    return launch_dependent(xent_sum_kernel, grid, kSumThreads, stream,
+    return launch_dependent(xent_sum_kernel, dim3(unsigned(grid)), kSumThreads, stream,
                             static_cast<const float*>(acc), static_cast<uint16_t*>(a.dX), n,
                             q.splits);
   }
