@@ -96,6 +96,7 @@ struct GemmParams {
   float* picked;                  // [M] kXentStats: the target column's value
   int col_offset, col_total;      // first column of this launch, columns in all
   int k_chunk, chunks;            // CHUNKED: K blocks per chunk, chunks per tile
+  int n_last;                     // TRIM_N: columns of the last N block, rounded up to 32
   int m_rows;                     // VAR_ROWS: rows of A per CTA and tile (a multiple of 32, <= 128)
 };
 
@@ -140,6 +141,8 @@ struct TileCfg {
   static constexpr bool STREAM_A = false, STREAM_B = false;
   // VAR_ROWS (see FewTokensCfg): tiles of 2 m_rows instead of 256 rows.
   static constexpr bool VAR_ROWS = false;
+  // TRIM_N (see TrimCfg): the last N block's MMAs are n_last columns wide.
+  static constexpr bool TRIM_N = false;
   // C_T: the output is D transposed (the swapped-operand decode GEMM, whose
   // M role holds the weights and N role the few activation rows)
   static constexpr bool C_T = C_T_;
@@ -279,6 +282,17 @@ template <class Base, bool kOnce>
 struct FewTokensCfg : Base {
   static constexpr bool STREAM_A = kOnce;
   static constexpr bool VAR_ROWS = true;
+};
+
+// A last N block of few columns costs a whole block's MMAs (2056 columns: 9
+// blocks for 8.03).  Trimmed, its MMAs take n_last columns, the first half from
+// the first CTA's part of B and the second from the other's, so that the
+// accumulator's columns stay those of C (4096 x 40000 x 1096, dX and dW: 771 ->
+// 747 us).
+template <class Base>
+struct TrimCfg : Base {
+  static constexpr bool TRIM_N = true;
+  static_assert(Base::CG == 2 && Base::B_MN, "CTA pairs, MN-major B");
 };
 
 // Work item `tile` -> batch l, M block mb and N block nb, in grouped-M
@@ -782,6 +796,10 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     ptx::fence_mbar_init();
   }
   const int m_rows = Cfg::VAR_ROWS ? p.m_rows : Cfg::BM;  // rows of A per CTA and tile
+  // columns of N block nb's MMAs
+  auto tile_n = [&](int nb) {
+    return Cfg::TRIM_N && nb + 1 == p.num_n_blocks ? p.n_last : BN;
+  };
   // The producer's first segment, found before the dependency wait: the
   // schedule arithmetic run for the first time cost ~0.7 us between the
   // wait and the first load.
@@ -914,12 +932,16 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
           decode_tile<Cfg>(sg.tile, p, l, mb, nb);
         }
         const int a_row = (mb * CG + int(peer)) * m_rows;
-        const int b_row = nb * BN + int(peer) * Cfg::B_ROWS;
+        const int b_row = nb * BN + int(peer) * (Cfg::TRIM_N ? tile_n(nb) / 2 : Cfg::B_ROWS);
+        // TRIM_N: 64-column atoms of B that the tile needs
+        const int b_atoms = Cfg::TRIM_N ? (tile_n(nb) / 2 + 63) / 64 : Cfg::B_ROWS / 64;
+        const uint32_t b_bytes =
+            Cfg::TRIM_N ? uint32_t(b_atoms) * Cfg::B_ATOM_BYTES : uint32_t(Cfg::B_BYTES);
         int sfb_atoms = 0;
         if constexpr (kFP4) sfb_atoms = min(Cfg::SFB_ATOMS, p.rest_n - nb * Cfg::SFB_ATOMS);
         const uint32_t tx =
-            uint32_t(CG) * (uint32_t(m_rows) * 128 * Cfg::KSUB + (Cfg::kW4 ? 0 : Cfg::B_BYTES) + Cfg::SFA_BYTES +
-                            uint32_t(sfb_atoms) * Cfg::SFB_ATOM_BYTES);
+            uint32_t(CG) * (uint32_t(m_rows) * 128 * Cfg::KSUB + (Cfg::kW4 ? 0u : b_bytes) +
+                            Cfg::SFA_BYTES + uint32_t(sfb_atoms) * Cfg::SFB_ATOM_BYTES);
         // split-K: the batch slot holds batch * k_splits + split
         const int kb_begin = sg.kb0;
         const int kb_end = sg.kb1;
@@ -1001,8 +1023,9 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                 if (sub == 0)
 #pragma unroll
                   for (int at = 0; at < Cfg::B_ROWS / 64; ++at)
-                    ptx::tma_load_3d_pair_hint(stage_b(stage) + at * Cfg::B_ATOM_BYTES, &tmap_b,
-                                               fb, b_row + 64 * at, kb * Cfg::BK, l, pol_ab);
+                    if (!Cfg::TRIM_N || at < b_atoms)
+                      ptx::tma_load_3d_pair_hint(stage_b(stage) + at * Cfg::B_ATOM_BYTES, &tmap_b,
+                                                 fb, b_row + 64 * at, kb * Cfg::BK, l, pol_ab);
               } else if constexpr (kHintLoads) {
                 ptx::tma_load_3d_pair_hint(da, &tmap_a, fb, x, a_row, l, pol_a);
                 ptx::tma_load_3d_pair_hint(db, &tmap_b, fb, x, b_row, l, pol_ab);
@@ -1097,7 +1120,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0 && leader) {
-      constexpr uint32_t idesc = Cfg::idesc();
+      uint32_t idesc = Cfg::idesc();
       // The tensor pipe takes the next MMA only shortly before the one it
       // is executing ends, so whatever this thread does between a stage's
       // last MMA and the next stage's first leaves the pipe idle.  The loop
@@ -1137,6 +1160,11 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
           break;
         }
         ptx::tc_fence_after();
+        if constexpr (Cfg::TRIM_N) {
+          int l, mb, nb;
+          decode_tile<Cfg>(sg.tile, p, l, mb, nb);
+          idesc = (Cfg::idesc() & ~(0x3Fu << 17)) | (uint32_t(tile_n(nb) >> 3) << 17);
+        }
         uint32_t d_tmem = tmem_base + uint32_t(acc * BN);
         for (int kb = sg.kb0; kb < sg.kb1; ++kb) {
           if (!ready_wait(stage, phase, w)) {

@@ -46,8 +46,9 @@ using XentCfg =
 // G: 8 epilogue warps (one box each), since an exponential per logit takes
 // longer than the MMAs of a short K loop.
 using XentGradPair = TileCfg<Operand::kBF16, 2, 256, 3, 8, 1, true, false, 2, false, false, false, true>;
-using XentDxPair = XentCfg<2, 3, 2, true, false>;
-using XentDwPair = XentCfg<2, 3, 2, true, true>;
+// dX and dW have K columns, often few tiles of 256: the last one is trimmed.
+using XentDxPair = TrimCfg<XentCfg<2, 3, 2, true, false>>;
+using XentDwPair = TrimCfg<XentCfg<2, 3, 2, true, true>>;
 // Few tokens: G is formed transposed ([vocabulary][tokens]) by the roles of
 // XentFwdT, so dX reads it MN-major and dW K-major.
 template <int BN, int STAGES>
@@ -162,6 +163,7 @@ GemmParams base_params(int M, int N, int K, const DeviceInfo& dev) {
   p.group_m = raster_group_m(p.num_m_blocks, (long long)Cfg::TILE_M * K * 2);
   p.k_splits = 1;
   p.kb_per_split = p.num_k_blocks;
+  p.n_last = (N - (p.num_n_blocks - 1) * Cfg::BN + 31) / 32 * 32;
   p.status = dev.status;
   p.timeout_ns = wait_timeout_ns();
   return p;
