@@ -1511,6 +1511,10 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     float xent_c = 0.0f, xent_scale = 0.0f;
     bool xent_none = true;
     (void)xent_row0, (void)xent_rel, (void)xent_target, (void)xent_c, (void)xent_scale, (void)xent_none;
+    // Boxes stored so far; box b of the next one is chunk_ctr % boxes.  It counts
+    // stores, not chunks: the wait before a box is reused allows as many
+    // committed groups as there are other boxes, so a chunk without a store
+    // (columns past N) must not advance it.
     uint32_t chunk_ctr = 0;
     uint32_t epi_parity = 0;     // bit b: parity of the next wait on epi_bar(e, b)
     uint32_t epi_pending = 0;    // bit b: a load into buffer b has not been waited for
@@ -1722,7 +1726,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
             last_tile = sg.slot < 0 && !seg_at<Cfg>(p, cluster_id, num_clusters, idx + 1, nx);
           }
 #pragma unroll
-        for (int c = 0; c < NCH; ++c, ++chunk_ctr) {
+        for (int c = 0; c < NCH; ++c) {
           const int b = int(chunk_ctr % Cfg::EPI_BUFS);
           const uint32_t sbuf =
               last_tile ? sbase + uint32_t(e * NCH + c) * Cfg::EPI_BOX_BYTES
@@ -1744,6 +1748,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
             store_box(sbuf, col0, row0, l);
             ptx::bulk_commit_group();
           }
+          ++chunk_ctr;
         }
         }
       } else if constexpr (kLookahead) {
@@ -1884,7 +1889,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         // FP32 outputs (split-K partials, accumulated gradients): 32-column
         // boxes of 32 rows x 128 bytes.
 #pragma unroll 1
-        for (int c = 0; c < Cfg::EPI_COLS / 32; ++c, ++chunk_ctr) {
+        for (int c = 0; c < Cfg::EPI_COLS / 32; ++c) {
           const int b = int(chunk_ctr % Cfg::EPI_BUFS);
           const uint32_t sbuf = buf0 + b * Cfg::EPI_BOX_BYTES;
           const int col0 = nb * BN + col_base + c * 32;
@@ -1908,6 +1913,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
             }
             ptx::bulk_commit_group();
           }
+          ++chunk_ctr;
         }
       } else if constexpr (kDirectStore) {
         // 64 columns per chunk: each lane converts its row and writes eight
@@ -2003,7 +2009,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
           last_tile = sg.slot < 0 && !seg_at<Cfg>(p, cluster_id, num_clusters, idx + 1, nx);
         }
 #pragma unroll 1
-        for (int c = 0; c < Cfg::EPI_COLS / 64; ++c, ++chunk_ctr) {
+        for (int c = 0; c < Cfg::EPI_COLS / 64; ++c) {
           constexpr int kBoxes =
               EPI == Epilogue::kXentGradTBF16 ? Cfg::EPI_BUFS - 1 : Cfg::EPI_BUFS;
           const int b = int(chunk_ctr % kBoxes);
@@ -2058,6 +2064,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                 ptx::tma_store_3d(&tmap_sfa, sbuf2, sx + 32, sy, sz);
                 ptx::bulk_commit_group();
               }
+              ++chunk_ctr;
               continue;
             }
           }
@@ -2095,6 +2102,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
               store_box(sbuf, col0, row0, l);
             ptx::bulk_commit_group();
           }
+          ++chunk_ctr;
         }
       }
     }
