@@ -45,7 +45,8 @@ using XentCfg =
     TileCfg<Operand::kBF16, CG, 256, STAGES, 4, 2, true, false, KSUB, BMN, false, AMN, true>;
 // G: 8 epilogue warps (one box each), since an exponential per logit takes
 // longer than the MMAs of a short K loop.
-using XentGradPair = TileCfg<Operand::kBF16, 2, 256, 3, 8, 1, true, false, 2, false, false, false, true>;
+using XentGradPair =
+    TileCfg<Operand::kBF16, 2, 256, 3, 8, 1, true, false, 2, false, false, false, true>;
 // dX and dW have K columns, often few tiles of 256: the last one is trimmed.
 using XentDxPair = TrimCfg<XentCfg<2, 3, 2, true, false>>;
 using XentDwPair = TrimCfg<XentCfg<2, 3, 2, true, true>>;
@@ -134,19 +135,16 @@ __global__ void __launch_bounds__(kPadThreads)
   }
 }
 
-// The matrix of X [rows][cols] with pitch ld.
-template <class Cfg>
-int encode_x(CUtensorMap* m, const void* base, int rows, int cols, int ld, int box_rows) {
+// Tensor map of a BF16 matrix [rows][cols] with row pitch ld (all in
+// elements): boxes of 64 columns and box_rows rows, 128-byte swizzle.
+int encode_rows(CUtensorMap* m, const void* base, int rows, int cols, int ld, int box_rows) {
   return encode_tmap_3d_strided(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, uint64_t(cols),
                                 uint64_t(rows), 1, uint64_t(ld) * 2,
                                 uint64_t(ld) * 2 * uint64_t(rows), 64, uint32_t(box_rows), 1,
                                 CU_TENSOR_MAP_SWIZZLE_128B);
 }
-
-template <class Cfg>
-int encode_k_major(CUtensorMap* m, const void* base, int rows, int cols, int box_rows) {
-  return encode_tmap_3d(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, uint64_t(cols),
-                        uint64_t(rows), 1, 64, uint32_t(box_rows), CU_TENSOR_MAP_SWIZZLE_128B);
+int encode_rows(CUtensorMap* m, const void* base, int rows, int cols, int box_rows) {
+  return encode_rows(m, base, rows, cols, cols, box_rows);
 }
 
 template <class Cfg>
@@ -178,8 +176,8 @@ void set_chunks(GemmParams& p, int k) {
 int run_forward(const XentForward& a, const DeviceInfo& dev, cudaStream_t stream) {
   using Cfg = XentFwdPair;
   CUtensorMap tx, tw;
-  int rc = encode_k_major<Cfg>(&tx, a.X, a.M, a.K, Cfg::BM);
-  if (rc == GEMM_OK) rc = encode_k_major<Cfg>(&tw, a.W, a.V, a.K, Cfg::B_ROWS);
+  int rc = encode_rows(&tx, a.X, a.M, a.K, Cfg::BM);
+  if (rc == GEMM_OK) rc = encode_rows(&tw, a.W, a.V, a.K, Cfg::B_ROWS);
   if (rc != GEMM_OK) return rc;
   GemmParams p = base_params<Cfg>(a.M, a.V, a.K, dev);
   set_chunks<Cfg>(p, kChunkK);
@@ -210,7 +208,6 @@ int few_rows(int V, int BN) {
   }
   return best;
 }
-template <class Cfg>
 void set_few_rows(GemmParams& p, int rows) {
   p.m_rows = rows;
   p.num_m_blocks = (p.M + 2 * rows - 1) / (2 * rows);
@@ -222,11 +219,11 @@ int run_forward_few(const XentForward& a, int* groups, const DeviceInfo& dev,
                     cudaStream_t stream) {
   CUtensorMap tx, tw;
   const int rows = few_rows(a.V, Cfg::BN);
-  int rc = encode_k_major<Cfg>(&tw, a.W, a.V, a.K, rows);
-  if (rc == GEMM_OK) rc = encode_k_major<Cfg>(&tx, a.X, a.M, a.K, Cfg::B_ROWS);
+  int rc = encode_rows(&tw, a.W, a.V, a.K, rows);
+  if (rc == GEMM_OK) rc = encode_rows(&tx, a.X, a.M, a.K, Cfg::B_ROWS);
   if (rc != GEMM_OK) return rc;
   GemmParams p = base_params<Cfg>(a.V, a.M, a.K, dev);
-  set_few_rows<Cfg>(p, rows);
+  set_few_rows(p, rows);
   set_chunks<Cfg>(p, kChunkKFew);
   p.target = a.target;
   p.stats = static_cast<float2*>(a.workspace);
@@ -393,14 +390,14 @@ int run_grad(const XentBackward& a, const Piece& pc, bool late, GridTiles before
              const DeviceInfo& dev, cudaStream_t stream) {
   CUtensorMap tx, tw, tg;
   const uint16_t* W = static_cast<const uint16_t*>(a.W) + size_t(pc.v0) * a.K;
-  int rc = encode_x<Cfg>(&tx, a.X, a.M, a.K, a.ldx, kT ? Cfg::B_ROWS : Cfg::BM);
+  int rc = encode_rows(&tx, a.X, a.M, a.K, a.ldx, kT ? Cfg::B_ROWS : Cfg::BM);
   const int rows = kT ? few_rows(pc.cols, Cfg::BN) : 0;
-  if (rc == GEMM_OK) rc = encode_k_major<Cfg>(&tw, W, pc.cols, a.K, kT ? rows : Cfg::B_ROWS);
-  if (rc == GEMM_OK) rc = encode_k_major<Cfg>(&tg, pc.G, kT ? pc.cols : a.M, pc.ld, 32);
+  if (rc == GEMM_OK) rc = encode_rows(&tw, W, pc.cols, a.K, kT ? rows : Cfg::B_ROWS);
+  if (rc == GEMM_OK) rc = encode_rows(&tg, pc.G, kT ? pc.cols : a.M, pc.ld, 32);
   if (rc != GEMM_OK) return rc;
   GemmParams p = kT ? base_params<Cfg>(pc.cols, a.M, a.K, dev)
                     : base_params<Cfg>(a.M, pc.cols, a.K, dev);
-  if constexpr (kT) set_few_rows<Cfg>(p, rows);
+  if constexpr (kT) set_few_rows(p, rows);
   p.target = a.target;
   p.row_lse = a.lse;
   p.row_scale = a.dloss;
@@ -421,15 +418,15 @@ int run_dx(const XentBackward& a, const XentPlan& q, const Piece& pc, float* acc
            GridTiles* grid, const DeviceInfo& dev, cudaStream_t stream) {
   CUtensorMap tg, tw, tc;
   const uint16_t* W = static_cast<const uint16_t*>(a.W) + size_t(pc.v0) * a.K;
-  int rc = Cfg::A_MN ? encode_k_major<Cfg>(&tg, pc.G, pc.cols, pc.ld, Cfg::BK)
-                     : encode_k_major<Cfg>(&tg, pc.G, a.M, pc.ld, Cfg::BM);
-  if (rc == GEMM_OK) rc = encode_k_major<Cfg>(&tw, W, pc.cols, a.K, Cfg::BK);
+  int rc = Cfg::A_MN ? encode_rows(&tg, pc.G, pc.cols, pc.ld, Cfg::BK)
+                     : encode_rows(&tg, pc.G, a.M, pc.ld, Cfg::BM);
+  if (rc == GEMM_OK) rc = encode_rows(&tw, W, pc.cols, a.K, Cfg::BK);
   if (rc != GEMM_OK) return rc;
   GemmParams p = base_params<Cfg>(a.M, a.K, pc.cols, dev);
   p.trigger_late = 1;
   *grid = {p.total_tiles, p.num_k_blocks + 2.0};
   if (q.dx_bytes == 0) {
-    rc = encode_k_major<Cfg>(&tc, a.dX, a.M, a.K, 32);
+    rc = encode_rows(&tc, a.dX, a.M, a.K, 32);
     if (rc != GEMM_OK) return rc;
     return launch_tcgen05<Cfg, Epilogue::kStoreBF16>(tg, tw, tc, tg, tg, p, dev, stream);
   }
@@ -454,10 +451,10 @@ int run_dw(const XentBackward& a, const Piece& pc, bool after_dx, const float* s
            GridTiles before, GridTiles* grid, const DeviceInfo& dev, cudaStream_t stream) {
   CUtensorMap tg, tx, tc;
   uint16_t* dW = static_cast<uint16_t*>(a.dW) + size_t(pc.v0) * a.K;
-  int rc = Cfg::A_MN ? encode_k_major<Cfg>(&tg, pc.G, a.M, pc.ld, Cfg::BK)
-                     : encode_k_major<Cfg>(&tg, pc.G, pc.cols, pc.ld, Cfg::BM);
-  if (rc == GEMM_OK) rc = encode_x<Cfg>(&tx, a.X, a.M, a.K, a.ldx, Cfg::BK);
-  if (rc == GEMM_OK) rc = encode_k_major<Cfg>(&tc, dW, pc.cols, a.K, 32);
+  int rc = Cfg::A_MN ? encode_rows(&tg, pc.G, a.M, pc.ld, Cfg::BK)
+                     : encode_rows(&tg, pc.G, pc.cols, pc.ld, Cfg::BM);
+  if (rc == GEMM_OK) rc = encode_rows(&tx, a.X, a.M, a.K, a.ldx, Cfg::BK);
+  if (rc == GEMM_OK) rc = encode_rows(&tc, dW, pc.cols, a.K, 32);
   if (rc != GEMM_OK) return rc;
   GemmParams p = base_params<Cfg>(pc.cols, a.K, a.M, dev);
   p.late_wait = after_dx;
@@ -485,8 +482,7 @@ __global__ void __launch_bounds__(kSumThreads)
 }
 
 template <class Kernel, class... Args>
-int launch_dependent(Kernel kernel, dim3 grid, int threads, cudaStream_t stream,
-                     Args... args) {
+int launch_dependent(Kernel kernel, dim3 grid, int threads, cudaStream_t stream, Args... args) {
   cudaLaunchConfig_t cfg{};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
