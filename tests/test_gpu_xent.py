@@ -147,6 +147,7 @@ def test_tile_heights_of_few_tokens(g, M, V, K):
     (1000, 20000, 520),    # dW's first clusters take more tiles than the others
     (300, 30011, 1032),    # many parts of dX, more than one round of dW
     (16411, 20001, 72),    # six pieces, whose G grids start early too
+    (128, 530001, 40),     # few tokens in two pieces
 ])
 def test_grids_that_start_early(g, M, V, K):
     X, W, t, d = problem(M, V, K, 37)
