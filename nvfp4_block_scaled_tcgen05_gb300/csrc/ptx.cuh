@@ -153,6 +153,13 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// The largest of a full warp's values, NaN left out.
+__device__ __forceinline__ float redux_max(float v) {
+  float y;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(v));
+  return y;
+}
+
 // 1 / x, at most one unit in the last place off.
 __device__ __forceinline__ float rcp(float x) {
   float y;

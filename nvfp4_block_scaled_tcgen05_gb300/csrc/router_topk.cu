@@ -18,9 +18,10 @@
 // in registers; blocks add their warps' sums and a second, small grid adds
 // the blocks', both in a fixed order.
 //
-// Measured (top-8 of 256): one row 3.4 us forward, 1.7 us backward; 4510 rows
-// 9.1 and 3.1 us; 65536 rows 39 us forward (bound by issuing, about 350
-// instructions a row) and 26.5 us backward (5.1 TB/s of logits and gradients).
+// Measured (top-8 of 256): one row 3.3 us forward, 1.7 us backward; 4510 rows
+// 8.8 and 3.1 us; 65536 rows 37.5 us forward (bound by issuing, about 330
+// instructions a row; 39.2 with the maxima by shuffles and integer keys) and
+// 26.5 us backward (5.1 TB/s of logits and gradients).
 // A row is a chain of reductions about 2 us long, so small calls are bound by
 // latency; up to kOneBlockRows rows one block does without the second grid.
 #include <cuda_bf16.h>
@@ -66,11 +67,6 @@ __device__ __forceinline__ float key_value(uint32_t key) {
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
-__device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
   return v;
 }
 
@@ -134,7 +130,7 @@ __global__ void __launch_bounds__(32 * kWarps, NV <= 8 ? 2 : 1) route_kernel(con
   // each warp's row, 32 NV values, 16-byte aligned
   __shared__ float sh_z[kWarps], red[kWarps];
   __shared__ int sh_t[kWarps];
-  __shared__ unsigned long long sh_cand[kWarps][32];
+  __shared__ __align__(16) unsigned long long sh_cand[kWarps][32];
   float* row_vals = reinterpret_cast<float*>(
       sh + (kWarps + 1) * ((a.E + 3) / 4 * 4) + (threadIdx.x >> 5) * 32 * NV);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -157,7 +153,7 @@ __global__ void __launch_bounds__(32 * kWarps, NV <= 8 ? 2 : 1) route_kernel(con
     float lane_max = -INFINITY;
 #pragma unroll
     for (int i = 0; i < NV; ++i) lane_max = fmaxf(lane_max, v[i]);
-    const float mx = warp_max(lane_max);
+    const float mx = ptx::redux_max(lane_max);
     const float ref = mx == -INFINITY ? 0.0f : mx;
     float s = 0.0f, p[NV];
 #pragma unroll
@@ -183,13 +179,13 @@ __global__ void __launch_bounds__(32 * kWarps, NV <= 8 ? 2 : 1) route_kernel(con
     float my_weight = 0.0f;
     bool slow = live && s != s;  // NaN somewhere
     if (live && !slow) {
-      uint32_t cur = rank_key(lane_max), floor_key = 0u;
-      for (int r = 0; r < a.k; ++r) {
-        floor_key = __reduce_max_sync(0xffffffffu, cur);
-        if (cur == floor_key) cur = 0u;
+      float bound = mx, cur = lane_max;
+      for (int r = 1; r < a.k; ++r) {
+        if (cur == bound) cur = -INFINITY;
+        bound = ptx::redux_max(cur);
       }
       // fewer than k lanes with a value: every value above -inf is a candidate
-      const float bound = floor_key > kNoKey ? key_value(floor_key) : -FLT_MAX;
+      bound = fmaxf(bound, -FLT_MAX);
       uint32_t mine = 0u;  // bit i: value i is a candidate
 #pragma unroll
       for (int i = 0; i < NV; ++i) mine |= v[i] >= bound ? 1u << i : 0u;
@@ -213,11 +209,15 @@ __global__ void __launch_bounds__(32 * kWarps, NV <= 8 ? 2 : 1) route_kernel(con
           cand[at] = (static_cast<unsigned long long>(rank_key(row_vals[e])) << 32) |
                      (0xFFFFFFFFu - uint32_t(e));
         }
+        if (lane == 0 && n % 2) cand[n] = 0ull;  // read in pairs below
         __syncwarp();
         const unsigned long long own = lane < n ? cand[lane] : 0ull;
         int rank = 0;
 #pragma unroll 4
-        for (int j = 0; j < n; ++j) rank += cand[j] > own;
+        for (int j = 0; j < n; j += 2) {
+          const ulonglong2 other = *reinterpret_cast<const ulonglong2*>(cand + j);
+          rank += int(other.x > own) + int(other.y > own);
+        }
         __syncwarp();
         if (lane < n) {
           if (rank < a.k) {
