@@ -266,8 +266,12 @@ struct TileCfg {
 
 // The tensor core adds into its accumulator with truncation, so a long K loop
 // drifts toward zero by about K / 16 half units of the running sum's last
-// place (lse of 4096-deep logits was off by 2.6e-6 of its value).  Chunks of a
+// place (lse of 4096-deep logits was off by 2.6e-6 of its value).  Chunks of
 // some hundred K, added with rounding, keep the error at the chunk's length.
+// The gradient's epilogue adds the same chunks as the statistics': with equal
+// logits in both passes their error cancels in exp(z - lse) - 1 of a row whose
+// target is nearly certain (K = 4096, z of 22 to 30: p off by 8e-5 on average
+// without chunks there, by 2e-7 with them).
 template <class Base>
 struct ChunkedCfg : Base {
   static constexpr bool CHUNKED = true;
@@ -500,13 +504,12 @@ __device__ __forceinline__ float2 xent_tile(const float (&x)[R][32]) {
 // outside 0..31), `live` the columns that exist, `none` marks a row without a
 // loss (all zeros, whatever the logits).  The last three are rare, and looked
 // at once per warp.
-__device__ __forceinline__ void xent_grad(uint32_t (&v)[32], float c, float d, int rel, int live,
-                                          bool none) {
+__device__ __forceinline__ void xent_grad(const float (&x)[32], uint32_t (&v)[32], float c, float d,
+                                          int rel, int live, bool none) {
   const float2 l2 = make_float2(kLog2e, kLog2e), c2 = make_float2(c, c), d2 = make_float2(d, d);
 #pragma unroll
   for (int i = 0; i < 32; i += 2) {
-    const float2 y =
-        ptx::fma2(make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), l2, c2);
+    const float2 y = ptx::fma2(make_float2(x[i], x[i + 1]), l2, c2);
     const float2 g = ptx::mul2(make_float2(ptx::ex2(y.x), ptx::ex2(y.y)), d2);
     v[i] = __float_as_uint(g.x);
     v[i + 1] = __float_as_uint(g.y);
@@ -531,11 +534,12 @@ __device__ __forceinline__ void xent_grad(uint32_t (&v)[32], float c, float d, i
 // The same with the roles swapped: 32 logits of one vocabulary row, one token
 // each; tok[i] = (-lse log2 e, d, target as int bits) of the tokens, read by
 // every lane at once.
-__device__ __forceinline__ void xent_grad_t(uint32_t (&v)[32], const float4* tok, int row) {
+__device__ __forceinline__ void xent_grad_t(const float (&x)[32], uint32_t (&v)[32],
+                                            const float4* tok, int row) {
 #pragma unroll
   for (int i = 0; i < 32; ++i) {
     const float4 t = tok[i];
-    float g = t.y * ptx::ex2(fmaf(__uint_as_float(v[i]), kLog2e, t.x));
+    float g = t.y * ptx::ex2(fmaf(x[i], kLog2e, t.x));
     if (__float_as_int(t.z) == row) g -= t.y;
     // d = 0 marks a token without a loss: zero whatever the logits
     v[i] = t.y == 0.0f ? 0u : __float_as_uint(g);
@@ -1477,9 +1481,14 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     // linear cross entropy: the row block whose per-row values the lane holds
     int xent_row0 = -1, xent_rel = -1;
     long long xent_target = -1;
-    constexpr bool kXentFwd = EPI == Epilogue::kXentStats || EPI == Epilogue::kXentStatsT;
-    constexpr int XR = kXentFwd ? Cfg::EPI_COLS / 32 : 1;  // 32-column groups per epilogue warp
-    float2 xt[XR];                                         // kXentStatsT: running statistics
+    constexpr bool kXentGrad =
+        EPI == Epilogue::kXentGradBF16 || EPI == Epilogue::kXentGradTBF16;
+    static_assert(!Cfg::CHUNKED || kXentGrad || EPI == Epilogue::kXentStats ||
+                      EPI == Epilogue::kXentStatsT,
+                  "the epilogues that add a tile's chunks");
+    // 32-column groups per epilogue warp
+    constexpr int XR = Cfg::CHUNKED ? Cfg::EPI_COLS / 32 : 1;
+    float2 xt[XR];  // kXentStatsT: running statistics
     long long xt_target[XR];
     (void)xt, (void)xt_target;
     // kXentGradTBF16: the tokens' values, in the output boxes' place past the
@@ -1511,6 +1520,23 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     float xent_c = 0.0f, xent_scale = 0.0f;
     bool xent_none = true;
     (void)xent_row0, (void)xent_rel, (void)xent_target, (void)xent_c, (void)xent_scale, (void)xent_none;
+    // Linear cross entropy: 64 logits of the lane's row, columns col0.., become
+    // gradients in its row of a box.
+    auto write_grad_row = [&](const float (&x0)[32], const float (&x1)[32], uint32_t sbuf, int row,
+                              int col0) {
+      uint32_t r0[32], r1[32];
+      if constexpr (EPI == Epilogue::kXentGradBF16) {
+        // a place before this chunk stays negative: -1 marks no target
+        const int rel = xent_rel < 0 ? -1 : xent_rel - col0;
+        xent_grad(x0, r0, xent_c, xent_scale, rel, p.N - col0, xent_none);
+        xent_grad(x1, r1, xent_c, xent_scale, rel - 32, p.N - col0 - 32, xent_none);
+      } else if constexpr (EPI == Epilogue::kXentGradTBF16) {
+        xent_grad_t(x0, r0, tok_vals + col0, row);
+        xent_grad_t(x1, r1, tok_vals + col0 + 32, row);
+      }
+      write_box_row<Epilogue::kStoreBF16>(smem + (sbuf - sbase) + lane * 128, lane, r0, r1, 0.0f);
+    };
+    (void)write_grad_row;
     // Boxes stored so far; box b of the next one is chunk_ctr % boxes.  It counts
     // stores, not chunks: the wait before a box is reused allows as many
     // committed groups as there are other boxes, so a chunk without a store
@@ -1786,7 +1812,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
             ptx::bulk_commit_group();
           }
         }
-      } else if constexpr (kXentFwd) {
+      } else if constexpr (Cfg::CHUNKED) {
         // Linear cross entropy.  Each chunk's accumulator joins the tile's sum
         // in registers and is handed back at once; the rest overlaps the next
         // tile's MMAs.
@@ -1856,7 +1882,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
           const float2 st = xent_tile(xr);
           if (grow < p.M)
             p.stats[(size_t(nb) * (Cfg::EPI_WARPS / 4) + (e >> 2)) * size_t(p.M) + grow] = st;
-        } else {
+        } else if constexpr (EPI == Epilogue::kXentStatsT) {
           // each lane holds one vocabulary row of 32 tokens: through a 32 x 32
           // box in shared memory (column j of row t at j ^ t: no bank conflict
           // either way) every lane gets one token's 32 logits and folds them
@@ -1883,6 +1909,46 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                 if (j >= live) x[j] = -INFINITY;
             }
             xent_fold(x, xt[i].x, xt[i].y);
+          }
+        } else {
+          // gradients, one box of 64 columns after the other; the CTA's last
+          // tile puts each in a place of its own in the freed stage memory (as
+          // in the other epilogues).  The loop stays rolled and the sums move
+          // down to the first 64 columns: twice the code cost more in cold
+          // instruction fetches (1024 x 32768 x 256: 62.9 against 58.9 us).
+          constexpr int NCH = Cfg::EPI_COLS / 64;
+          static_assert(Cfg::EPI_WARPS * NCH * Cfg::EPI_BOX_BYTES <= Cfg::STAGES * Cfg::STAGE_BYTES,
+                        "the last tile's boxes fit the stages");
+          constexpr int kBoxes =
+              EPI == Epilogue::kXentGradTBF16 ? Cfg::EPI_BUFS - 1 : Cfg::EPI_BUFS;
+          Seg nx;
+          const bool last_tile = !seg_at<Cfg>(p, cluster_id, num_clusters, idx + 1, nx);
+#pragma unroll 1
+          for (int c = 0; c < NCH; ++c) {
+            const int col0 = nb * BN + col_base + c * 64;
+            if (!(rows_live && col0 < p.N)) break;  // warp-uniform
+            const int b = int(chunk_ctr % kBoxes);
+            const uint32_t sbuf = last_tile
+                                      ? sbase + uint32_t(e * NCH + c) * Cfg::EPI_BOX_BYTES
+                                      : buf0 + b * Cfg::EPI_BOX_BYTES;
+            // the TMA store that last read this box must be done with it
+            if (!last_tile) {
+              if (lane == 0) ptx::bulk_wait_group_read<kBoxes - 1>();
+              __syncwarp();
+            }
+            write_grad_row(xr[0], xr[1], sbuf, row0 + lane, col0);
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              // read back by the next launches: no evict-first hint
+              ptx::tma_store_3d(&tmap_c, sbuf, col0, row0, l);
+              ptx::bulk_commit_group();
+            }
+            ++chunk_ctr;
+#pragma unroll
+            for (int i = 0; i + 2 < XR; ++i)
+#pragma unroll
+              for (int j = 0; j < 32; ++j) xr[i][j] = xr[i + 2][j];
           }
         }
       } else if constexpr (EPI == Epilogue::kStoreF32 || EPI == Epilogue::kAddF32) {
@@ -2010,9 +2076,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         }
 #pragma unroll 1
         for (int c = 0; c < Cfg::EPI_COLS / 64; ++c) {
-          constexpr int kBoxes =
-              EPI == Epilogue::kXentGradTBF16 ? Cfg::EPI_BUFS - 1 : Cfg::EPI_BUFS;
-          const int b = int(chunk_ctr % kBoxes);
+          const int b = int(chunk_ctr % Cfg::EPI_BUFS);
           const uint32_t sbuf =
               last_tile ? sbase + uint32_t(e * (Cfg::EPI_COLS / 64) + c) * Cfg::EPI_BOX_BYTES
                         : buf0 + b * Cfg::EPI_BOX_BYTES;
@@ -2020,7 +2084,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
           const bool live = rows_live && col0 < p.N;
           // The TMA store that last read this buffer must be done with it.
           if (!last_tile) {
-            if (lane == 0) ptx::bulk_wait_group_read<kBoxes - 1>();
+            if (lane == 0) ptx::bulk_wait_group_read<Cfg::EPI_BUFS - 1>();
             __syncwarp();
           }
           if constexpr (EPI == Epilogue::kScaledAccBF16) {
@@ -2077,18 +2141,14 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
               break;
             }
           }
-          if constexpr (EPI == Epilogue::kXentGradBF16) {
-            // a place before this chunk stays negative: -1 marks no target
-            const int rel = xent_rel < 0 ? -1 : xent_rel - col0;
-            xent_grad(r0, xent_c, xent_scale, rel, p.N - col0, xent_none);
-            xent_grad(r1, xent_c, xent_scale, rel - 32, p.N - col0 - 32, xent_none);
-            write_box_row<Epilogue::kStoreBF16>(smem + (sbuf - sbase) + lane * 128, lane, r0, r1,
-                                                0.0f);
-          } else if constexpr (EPI == Epilogue::kXentGradTBF16) {
-            xent_grad_t(r0, tok_vals + col0, row0 + lane);
-            xent_grad_t(r1, tok_vals + col0 + 32, row0 + lane);
-            write_box_row<Epilogue::kStoreBF16>(smem + (sbuf - sbase) + lane * 128, lane, r0, r1,
-                                                0.0f);
+          if constexpr (kXentGrad) {
+            float x0[32], x1[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              x0[j] = __uint_as_float(r0[j]);
+              x1[j] = __uint_as_float(r1[j]);
+            }
+            write_grad_row(x0, x1, sbuf, row0 + lane, col0);
           } else {
             write_box_row<EPI>(smem + (sbuf - sbase) + lane * 128, lane, r0, r1, p.scale);
           }
@@ -2096,10 +2156,8 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
           __syncwarp();
           if (lane == 0) {
             // the gradient tile is read back by the next launches: no evict-first hint
-            if constexpr (EPI == Epilogue::kXentGradBF16 || EPI == Epilogue::kXentGradTBF16)
-              ptx::tma_store_3d(&tmap_c, sbuf, col0, row0, l);
-            else
-              store_box(sbuf, col0, row0, l);
+            if constexpr (kXentGrad) ptx::tma_store_3d(&tmap_c, sbuf, col0, row0, l);
+            else store_box(sbuf, col0, row0, l);
             ptx::bulk_commit_group();
           }
           ++chunk_ctr;

@@ -44,9 +44,11 @@ template <int CG, int STAGES, int KSUB, bool BMN, bool AMN>
 using XentCfg =
     TileCfg<Operand::kBF16, CG, 256, STAGES, 4, 2, true, false, KSUB, BMN, false, AMN, true>;
 // G: 8 epilogue warps (one box each), since an exponential per logit takes
-// longer than the MMAs of a short K loop.
-using XentGradPair =
+// longer than the MMAs of a short K loop.  One chunk of K needs no sum in
+// registers, and streams (1024 x 32768 x 256: 55.9 us, through the sums 58.9).
+using XentGradStream =
     TileCfg<Operand::kBF16, 2, 256, 3, 8, 1, true, false, 2, false, false, false, true>;
+using XentGradPair = ChunkedCfg<XentGradStream>;
 // dX and dW have K columns, often few tiles of 256: the last one is trimmed.
 using XentDxPair = TrimCfg<XentCfg<2, 3, 2, true, false>>;
 using XentDwPair = TrimCfg<XentCfg<2, 3, 2, true, true>>;
@@ -54,7 +56,9 @@ using XentDwPair = TrimCfg<XentCfg<2, 3, 2, true, true>>;
 // XentFwdT, so dX reads it MN-major and dW K-major.
 template <int BN, int STAGES>
 using XentGradT = FewTokensCfg<
-    TileCfg<Operand::kBF16, 2, BN, STAGES, 4, 3, true, false, 2, false, false, false, true>, false>;
+    ChunkedCfg<
+        TileCfg<Operand::kBF16, 2, BN, STAGES, 4, 3, true, false, 2, false, false, false, true>>,
+    false>;
 // The second and last read of the weights (37 x 32768 x 2048: 80 -> 76.5 us
 // with G keeping them in L2 and dX letting them go).
 template <class Base>
@@ -398,6 +402,8 @@ int run_grad(const XentBackward& a, const Piece& pc, bool late, GridTiles before
   GemmParams p = kT ? base_params<Cfg>(pc.cols, a.M, a.K, dev)
                     : base_params<Cfg>(a.M, pc.cols, a.K, dev);
   if constexpr (kT) set_few_rows(p, rows);
+  // the forward pass's chunks, see ChunkedCfg
+  if constexpr (Cfg::CHUNKED) set_chunks<Cfg>(p, kT ? kChunkKFew : kChunkK);
   p.target = a.target;
   p.row_lse = a.lse;
   p.row_scale = a.dloss;
@@ -578,7 +584,8 @@ int launch_xent_backward(const XentBackward& args, const DeviceInfo& dev, cudaSt
     pc.cols = std::min(q.piece, a.V - pc.v0);
     pc.ld = round64(few ? a.M : pc.cols);
     int rc;
-    if (!few) rc = run_grad<XentGradPair, false>(a, pc, i > 0, before, dev, stream);
+    if (!few && a.K <= kChunkK) rc = run_grad<XentGradStream, false>(a, pc, i > 0, before, dev, stream);
+    else if (!few) rc = run_grad<XentGradPair, false>(a, pc, i > 0, before, dev, stream);
     else if (a.M <= 64) rc = run_grad<XentGradT<64, 4>, true>(a, pc, i > 0, before, dev, stream);
     else rc = run_grad<XentGradT<128, 3>, true>(a, pc, i > 0, before, dev, stream);
     if (rc == GEMM_OK && a.dX)
