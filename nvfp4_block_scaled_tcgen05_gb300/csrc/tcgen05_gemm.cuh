@@ -448,10 +448,11 @@ __device__ __forceinline__ void write_box_row_f32(uint8_t* row, int lane, const 
   }
 }
 
-// Linear cross entropy.  exp(x - ref) = 2^(x log2 e - ref log2 e): one fused
-// multiply-add (two columns per instruction) and one special-function
-// operation (relative error below 2^-21).  Rounding ref log2 e shifts all terms
-// of a row alike, by at most the last place of ref.
+// Linear cross entropy.  exp(x - ref) = 2^((x - ref) log2 e): a subtraction and
+// a multiplication (two columns per instruction each) and one special-function
+// operation (relative error below 2^-21).  The subtraction comes first: ref
+// log2 e passes the FP32 range where ref is still finite, and the difference of
+// near values is exact.
 constexpr float kLog2e = 1.4426950408889634f;
 __device__ __forceinline__ float fast_exp(float y) { return ptx::ex2(y * kLog2e); }
 
@@ -465,10 +466,10 @@ __device__ __forceinline__ float xent_max(const float (&x)[32], float m) {
   return fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
 }
 __device__ __forceinline__ void xent_add(const float (&x)[32], float ref, float2 (&s)[4]) {
-  const float2 l2 = make_float2(kLog2e, kLog2e), c = make_float2(-ref * kLog2e, -ref * kLog2e);
+  const float2 l2 = make_float2(kLog2e, kLog2e), r2 = make_float2(-ref, -ref);
 #pragma unroll
   for (int i = 0; i < 32; i += 2) {
-    const float2 y = ptx::fma2(make_float2(x[i], x[i + 1]), l2, c);
+    const float2 y = ptx::mul2(ptx::add2(make_float2(x[i], x[i + 1]), r2), l2);
     s[i / 2 & 3] = ptx::add2(s[i / 2 & 3], make_float2(ptx::ex2(y.x), ptx::ex2(y.y)));
   }
 }
@@ -500,16 +501,16 @@ __device__ __forceinline__ float2 xent_tile(const float (&x)[R][32]) {
 }
 
 // Backward: 32 logits of one row -> gradients d (exp(z - lse) - [column =
-// target]); c = -lse log2 e; `rel` is the target's place among them (none if
-// outside 0..31), `live` the columns that exist, `none` marks a row without a
-// loss (all zeros, whatever the logits).  The last three are rare, and looked
-// at once per warp.
-__device__ __forceinline__ void xent_grad(const float (&x)[32], uint32_t (&v)[32], float c, float d,
-                                          int rel, int live, bool none) {
-  const float2 l2 = make_float2(kLog2e, kLog2e), c2 = make_float2(c, c), d2 = make_float2(d, d);
+// target]); `rel` is the target's place among them (none if outside 0..31),
+// `live` the columns that exist, `none` marks a row without a loss (all zeros,
+// whatever the logits).  The last three are rare, and looked at once per warp.
+__device__ __forceinline__ void xent_grad(const float (&x)[32], uint32_t (&v)[32], float lse,
+                                          float d, int rel, int live, bool none) {
+  const float2 l2 = make_float2(kLog2e, kLog2e), r2 = make_float2(-lse, -lse),
+               d2 = make_float2(d, d);
 #pragma unroll
   for (int i = 0; i < 32; i += 2) {
-    const float2 y = ptx::fma2(make_float2(x[i], x[i + 1]), l2, c2);
+    const float2 y = ptx::mul2(ptx::add2(make_float2(x[i], x[i + 1]), r2), l2);
     const float2 g = ptx::mul2(make_float2(ptx::ex2(y.x), ptx::ex2(y.y)), d2);
     v[i] = __float_as_uint(g.x);
     v[i + 1] = __float_as_uint(g.y);
@@ -532,14 +533,14 @@ __device__ __forceinline__ void xent_grad(const float (&x)[32], uint32_t (&v)[32
 }
 
 // The same with the roles swapped: 32 logits of one vocabulary row, one token
-// each; tok[i] = (-lse log2 e, d, target as int bits) of the tokens, read by
-// every lane at once.
+// each; tok[i] = (lse, d, target as int bits) of the tokens, read by every lane
+// at once.
 __device__ __forceinline__ void xent_grad_t(const float (&x)[32], uint32_t (&v)[32],
                                             const float4* tok, int row) {
 #pragma unroll
   for (int i = 0; i < 32; ++i) {
     const float4 t = tok[i];
-    float g = t.y * ptx::ex2(fmaf(x[i], kLog2e, t.x));
+    float g = t.y * fast_exp(x[i] - t.x);
     if (__float_as_int(t.z) == row) g -= t.y;
     // d = 0 marks a token without a loss: zero whatever the logits
     v[i] = t.y == 0.0f ? 0u : __float_as_uint(g);
@@ -1505,7 +1506,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         // without a loss: d = 0; a target past the vocabulary: NaN
         const float d = t < 0 ? 0.0f : (t >= p.col_total ? NAN : p.row_scale[i]);
         tok_vals[i] =
-            make_float4(i < p.N ? -kLog2e * p.row_lse[i] : 0.0f, d, __int_as_float(row), 0.0f);
+            make_float4(i < p.N ? p.row_lse[i] : 0.0f, d, __int_as_float(row), 0.0f);
       }
       __syncwarp();
     }
@@ -1517,9 +1518,9 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         xt_target[i] = tok < p.N ? p.target[tok] : -1;
       }
     }
-    float xent_c = 0.0f, xent_scale = 0.0f;
+    float xent_lse = 0.0f, xent_scale = 0.0f;
     bool xent_none = true;
-    (void)xent_row0, (void)xent_rel, (void)xent_target, (void)xent_c, (void)xent_scale, (void)xent_none;
+    (void)xent_row0, (void)xent_rel, (void)xent_target, (void)xent_lse, (void)xent_scale, (void)xent_none;
     // Linear cross entropy: 64 logits of the lane's row, columns col0.., become
     // gradients in its row of a box.
     auto write_grad_row = [&](const float (&x0)[32], const float (&x1)[32], uint32_t sbuf, int row,
@@ -1528,8 +1529,8 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
       if constexpr (EPI == Epilogue::kXentGradBF16) {
         // a place before this chunk stays negative: -1 marks no target
         const int rel = xent_rel < 0 ? -1 : xent_rel - col0;
-        xent_grad(x0, r0, xent_c, xent_scale, rel, p.N - col0, xent_none);
-        xent_grad(x1, r1, xent_c, xent_scale, rel - 32, p.N - col0 - 32, xent_none);
+        xent_grad(x0, r0, xent_lse, xent_scale, rel, p.N - col0, xent_none);
+        xent_grad(x1, r1, xent_lse, xent_scale, rel - 32, p.N - col0 - 32, xent_none);
       } else if constexpr (EPI == Epilogue::kXentGradTBF16) {
         xent_grad_t(x0, r0, tok_vals + col0, row);
         xent_grad_t(x1, r1, tok_vals + col0 + 32, row);
@@ -1611,7 +1612,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
           xent_row0 = row0;
           const int grow = row0 + lane;
           const long long t = grow < p.M ? p.target[grow] : -1;
-          xent_c = grow < p.M ? -kLog2e * p.row_lse[grow] : 0.0f;
+          xent_lse = grow < p.M ? p.row_lse[grow] : 0.0f;
           // a row without a loss has no gradient; a target past the vocabulary
           // has no loss to differentiate
           xent_scale = t < 0 ? 0.0f : (t >= p.col_total ? NAN : p.row_scale[grow]);
