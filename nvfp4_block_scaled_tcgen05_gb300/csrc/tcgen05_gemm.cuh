@@ -534,7 +534,8 @@ __device__ __forceinline__ void xent_grad(const float (&x)[32], uint32_t (&v)[32
 
 // The same with the roles swapped: 32 logits of one vocabulary row, one token
 // each; tok[i] = (lse, d, target as int bits) of the tokens, read by every lane
-// at once.
+// at once; the target is -1 outside these rows, kNoLoss for a token without one.
+constexpr int kNoLoss = -2;
 __device__ __forceinline__ void xent_grad_t(const float (&x)[32], uint32_t (&v)[32],
                                             const float4* tok, int row) {
 #pragma unroll
@@ -542,8 +543,9 @@ __device__ __forceinline__ void xent_grad_t(const float (&x)[32], uint32_t (&v)[
     const float4 t = tok[i];
     float g = t.y * fast_exp(x[i] - t.x);
     if (__float_as_int(t.z) == row) g -= t.y;
-    // d = 0 marks a token without a loss: zero whatever the logits
-    v[i] = t.y == 0.0f ? 0u : __float_as_uint(g);
+    // zero whatever the logits; d = 0 of a token with a loss is an ordinary
+    // factor, and 0 times NaN is NaN as in xent_grad
+    v[i] = __float_as_int(t.z) == kNoLoss ? 0u : __float_as_uint(g);
   }
 }
 
@@ -1502,11 +1504,10 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
       for (int i = lane; i < BN; i += 32) {
         const long long t = i < p.N ? p.target[i] : -1;
         const int row = (t >= p.col_offset && t < (long long)p.col_offset + p.M)
-                            ? int(t - p.col_offset) : -1;
-        // without a loss: d = 0; a target past the vocabulary: NaN
+                            ? int(t - p.col_offset) : (t < 0 ? kNoLoss : -1);
+        // a target past the vocabulary: NaN
         const float d = t < 0 ? 0.0f : (t >= p.col_total ? NAN : p.row_scale[i]);
-        tok_vals[i] =
-            make_float4(i < p.N ? p.row_lse[i] : 0.0f, d, __int_as_float(row), 0.0f);
+        tok_vals[i] = make_float4(i < p.N ? p.row_lse[i] : 0.0f, d, __int_as_float(row), 0.0f);
       }
       __syncwarp();
     }
