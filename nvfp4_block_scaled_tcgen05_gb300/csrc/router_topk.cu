@@ -29,6 +29,7 @@
 #include <float.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "internal.h"
 #include "ptx.cuh"
@@ -567,50 +568,67 @@ int launch(Kernel kernel, int grid, int threads, size_t shared, cudaStream_t str
   return GEMM_OK;
 }
 
+// Dynamic shared memory of a launch.
+constexpr size_t route_shared(int E, int NV) {
+  return (size_t(kWarps + 1) * ((E + 3) / 4 * 4) + size_t(kWarps) * 32 * NV) * 4;
+}
+constexpr size_t route_grad_shared(int E) {
+  return size_t(2 * kGradWarps + 1) * ((E + 3) / 4 * 4) * 4;
+}
+
 // Past the default limit (together with the static arrays) a kernel has to be
-// allowed its dynamic shared memory.
-template <class Kernel>
-bool allow_shared(Kernel kernel, size_t bytes) {
-  if (bytes <= 40 * 1024) return true;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes)) ==
-      cudaSuccess)
-    return true;
-  cudaGetLastError();
-  return false;
+// allowed its dynamic shared memory.  The attribute belongs to the kernel and
+// its last value counts, so it is set once per device, to the most that any E
+// of the kernel needs: a value per call could be lowered by another host thread
+// before the launch.
+template <auto kKernel, size_t kMost>
+bool allow_shared(const DeviceInfo& dev) {
+  if constexpr (kMost > 40 * 1024) {
+    static std::atomic<bool> allowed[64];
+    std::atomic<bool>& done = allowed[dev.device & 63];
+    if (done.load()) return true;
+    if (cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kMost)) !=
+        cudaSuccess) {
+      cudaGetLastError();
+      return false;
+    }
+    done.store(true);
+  }
+  return true;
 }
 
 template <int NV, bool kAligned>
-int run_route(const RouteArgs& a, int blocks, cudaStream_t stream) {
-  const size_t shared = (size_t(kWarps + 1) * ((a.E + 3) / 4 * 4) + size_t(kWarps) * 32 * NV) * 4;
-  if (!allow_shared(route_kernel<NV, kAligned>, shared)) return GEMM_ERR_LAUNCH;
-  return launch(route_kernel<NV, kAligned>, blocks, 32 * kWarps, shared, stream, a);
+int run_route(const RouteArgs& a, int blocks, const DeviceInfo& dev, cudaStream_t stream) {
+  if (!allow_shared<route_kernel<NV, kAligned>, route_shared(32 * NV, NV)>(dev))
+    return GEMM_ERR_LAUNCH;
+  return launch(route_kernel<NV, kAligned>, blocks, 32 * kWarps, route_shared(a.E, NV), stream, a);
 }
 
-template <int NV, bool kAligned>
-int run_route_grad(const RouteGradArgs& a, bool bf16, cudaStream_t stream) {
+template <int NV, bool kAligned, bool kBF16>
+int run_route_grad(const RouteGradArgs& a, const DeviceInfo& dev, cudaStream_t stream) {
+  if (!allow_shared<route_grad_kernel<NV, kAligned, kBF16>, route_grad_shared(32 * NV)>(dev))
+    return GEMM_ERR_LAUNCH;
   const int blocks = int(
       std::min<long long>(kGradMaxBlocks, ((long long)a.M + kGradWarps - 1) / kGradWarps));
-  const size_t shared = size_t(2 * kGradWarps + 1) * ((a.E + 3) / 4 * 4) * 4;
-  auto kernel = bf16 ? route_grad_kernel<NV, kAligned, true> : route_grad_kernel<NV, kAligned, false>;
-  if (!allow_shared(kernel, shared)) return GEMM_ERR_LAUNCH;
-  return launch(kernel, blocks, 32 * kGradWarps, shared, stream, a);
+  return launch(route_grad_kernel<NV, kAligned, kBF16>, blocks, 32 * kGradWarps,
+                route_grad_shared(a.E), stream, a);
 }
 
 // The smallest row buffer that holds E columns.
 template <bool kAligned>
-int pick_route(const RouteArgs& a, int blocks, cudaStream_t stream) {
-  if (a.E <= 128) return run_route<4, kAligned>(a, blocks, stream);
-  if (a.E <= 256) return run_route<8, kAligned>(a, blocks, stream);
-  if (a.E <= 512) return run_route<16, kAligned>(a, blocks, stream);
-  return run_route<32, kAligned>(a, blocks, stream);
+int pick_route(const RouteArgs& a, int blocks, const DeviceInfo& dev, cudaStream_t stream) {
+  if (a.E <= 128) return run_route<4, kAligned>(a, blocks, dev, stream);
+  if (a.E <= 256) return run_route<8, kAligned>(a, blocks, dev, stream);
+  if (a.E <= 512) return run_route<16, kAligned>(a, blocks, dev, stream);
+  return run_route<32, kAligned>(a, blocks, dev, stream);
 }
 
-template <bool kAligned>
-int pick_route_grad(const RouteGradArgs& a, bool bf16, cudaStream_t stream) {
-  if (a.E <= 128) return run_route_grad<4, kAligned>(a, bf16, stream);
-  if (a.E <= 256) return run_route_grad<8, kAligned>(a, bf16, stream);
-  if (a.E <= 512) return run_route_grad<16, kAligned>(a, bf16, stream);
-  return run_route_grad<32, kAligned>(a, bf16, stream);
+template <bool kAligned, bool kBF16>
+int pick_route_grad(const RouteGradArgs& a, const DeviceInfo& dev, cudaStream_t stream) {
+  if (a.E <= 128) return run_route_grad<4, kAligned, kBF16>(a, dev, stream);
+  if (a.E <= 256) return run_route_grad<8, kAligned, kBF16>(a, dev, stream);
+  if (a.E <= 512) return run_route_grad<16, kAligned, kBF16>(a, dev, stream);
+  return run_route_grad<32, kAligned, kBF16>(a, dev, stream);
 }
 
 bool aligned_to(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
@@ -622,24 +640,28 @@ size_t router_topk_workspace(int M, int E) {
   return b > 1 ? size_t(b) * partial_words(E) * 4 : 0;
 }
 
-int launch_router_topk(const RouterTopk& r, const DeviceInfo&, cudaStream_t stream) {
+int launch_router_topk(const RouterTopk& r, const DeviceInfo& dev, cudaStream_t stream) {
   const RouteArgs a{r.logits, r.valid, r.weights, r.experts, r.lse, r.counts, r.probs, r.losses,
                     static_cast<uint32_t*>(r.workspace), r.M, r.E, r.ld, r.k, r.normalize};
   const int blocks = route_blocks(r.M);
   const bool aligned = r.E % 4 == 0 && (r.ld % 4 == 0 || r.M == 1) && aligned_to(r.logits, 16);
-  const int rc = aligned ? pick_route<true>(a, blocks, stream) : pick_route<false>(a, blocks, stream);
+  const int rc = aligned ? pick_route<true>(a, blocks, dev, stream)
+                         : pick_route<false>(a, blocks, dev, stream);
   if (rc != GEMM_OK || blocks == 1) return rc;
   return launch(route_finish_kernel, kFinishCtas, kFinishThreads, 0, stream, a, blocks);
 }
 
-int launch_router_topk_backward(const RouterTopkBackward& r, const DeviceInfo&,
+int launch_router_topk_backward(const RouterTopkBackward& r, const DeviceInfo& dev,
                                 cudaStream_t stream) {
   const RouteGradArgs a{r.logits, r.experts, r.lse, r.counts, r.dweights, r.dlosses, r.dlogits,
                         r.M, r.E, r.ld, r.k, r.normalize};
   const bool aligned = r.E % 4 == 0 && (r.ld % 4 == 0 || r.M == 1) && aligned_to(r.logits, 16) &&
                    aligned_to(r.dlogits, r.bf16 ? 8 : 16);
-  return aligned ? pick_route_grad<true>(a, r.bf16, stream)
-                 : pick_route_grad<false>(a, r.bf16, stream);
+  if (r.bf16)
+    return aligned ? pick_route_grad<true, true>(a, dev, stream)
+                   : pick_route_grad<false, true>(a, dev, stream);
+  return aligned ? pick_route_grad<true, false>(a, dev, stream)
+                 : pick_route_grad<false, false>(a, dev, stream);
 }
 
 }  // namespace gb300
