@@ -114,6 +114,11 @@ def _check(rc: int, where: str) -> None:
         raise GemmError(rc, where)
 
 
+# The C ABI's sizes are 32-bit int, and ctypes passes the lower 32 bits of a
+# larger number without a word.
+_INT_MAX = (1 << 31) - 1
+
+
 def _mat(t: torch.Tensor, dtype, name: str, ndim: int = 2) -> None:
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -125,6 +130,8 @@ def _mat(t: torch.Tensor, dtype, name: str, ndim: int = 2) -> None:
         raise ValueError(f"{name} must be a CUDA tensor")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous (row-major)")
+    if t.numel() > _INT_MAX and max(t.shape) > _INT_MAX:
+        raise ValueError(f"{name} has a dimension past 2^31 - 1: {tuple(t.shape)}")
 
 
 def gemm_bf16_nt(A: torch.Tensor, B: torch.Tensor, C: torch.Tensor | None = None, stream=None):
@@ -444,11 +451,15 @@ def _xent_inputs(X, W, target):
         raise ValueError(f"K mismatch: X {tuple(X.shape)} vs W {tuple(W.shape)}")
     if W.device != X.device:
         raise ValueError("X and W must be on one device")
+    if M > _INT_MAX or V > _INT_MAX or K > _INT_MAX:
+        raise ValueError(f"sizes past 2^31 - 1: M {M}, V {V}, K {K}")
     _on_device("target", X.device, target, torch.int64, (M,))
     return M, V, K
 
 
 def gemm_bf16_nt_xent_workspace_bytes(M: int, V: int) -> int:
+    if not (0 <= M <= _INT_MAX and 0 <= V <= _INT_MAX):
+        return 0
     return int((_lib or load()).gemm_bf16_nt_xent_workspace_bytes(M, V))
 
 
@@ -481,6 +492,8 @@ def gemm_bf16_nt_xent(X: torch.Tensor, W: torch.Tensor, target: torch.Tensor,
 
 
 def gemm_bf16_nt_xent_backward_workspace_bytes(M: int, V: int, K: int) -> int:
+    if not (0 <= M <= _INT_MAX and 0 <= V <= _INT_MAX and 0 <= K <= _INT_MAX):
+        return 0
     return int((_lib or load()).gemm_bf16_nt_xent_backward_workspace_bytes(M, V, K))
 
 
@@ -546,10 +559,14 @@ def _logit_rows(logits):
         ld = E
     if ld < E:
         raise ValueError("rows of logits overlap")
+    if ld > _INT_MAX or M > _INT_MAX:
+        raise ValueError(f"logits {M} x {E} with row stride {ld}: past 2^31 - 1")
     return M, E, ld
 
 
 def router_topk_workspace_bytes(M: int, E: int) -> int:
+    if not (0 <= M <= _INT_MAX and 0 <= E <= _INT_MAX):
+        return 0
     return int((_lib or load()).router_topk_workspace_bytes(M, E))
 
 
