@@ -74,7 +74,8 @@ int launch_tcgen05(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorM
   // Programmatic dependent launch: the kernel's prologue (barrier set-up,
   // TMEM allocation, tensor-map prefetch) may overlap the end of the
   // previous kernel on the stream; every thread waits for that kernel's
-  // completion before touching global memory.
+  // completion before touching global memory, except in the chained grids
+  // that set late_wait (their order stands above launch_xent_backward).
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.numAttrs = 2;

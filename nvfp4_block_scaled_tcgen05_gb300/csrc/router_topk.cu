@@ -18,10 +18,10 @@
 // in registers; blocks add their warps' sums and a second, small grid adds
 // the blocks', both in a fixed order.
 //
-// Measured (top-8 of 256): one row 3.3 us forward, 1.7 us backward; 4510 rows
-// 8.8 and 3.1 us; 65536 rows 37.5 us forward (bound by issuing, about 330
-// instructions a row; 39.2 with the maxima by shuffles and integer keys) and
-// 26.5 us backward (5.1 TB/s of logits and gradients).
+// Measured (top-8 of 256): one row 3.1 us forward, 1.8 us backward; 4510 rows
+// 8.6 and 3.5 us; 65536 rows 37.4 us forward (40.0 with closed experts and
+// padding rows; bound by issuing, 447 instructions a row there) and 26.6 us
+// backward (5.2 TB/s of logits and gradients).
 // A row is a chain of reductions about 2 us long, so small calls are bound by
 // latency; up to kOneBlockRows rows one block does without the second grid.
 #include <cuda_bf16.h>

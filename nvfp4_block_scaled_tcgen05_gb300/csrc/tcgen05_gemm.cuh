@@ -267,7 +267,8 @@ struct TileCfg {
 // The tensor core adds into its accumulator with truncation, so a long K loop
 // drifts toward zero by about K / 16 half units of the running sum's last
 // place (lse of 4096-deep logits was off by 2.6e-6 of its value).  Chunks of
-// some hundred K, added with rounding, keep the error at the chunk's length.
+// 1024 K (few tokens: 256), added with rounding, keep the error at the chunk's
+// length.
 // The gradient's epilogue adds the same chunks as the statistics': with equal
 // logits in both passes their error cancels in exp(z - lse) - 1 of a row whose
 // target is nearly certain (K = 4096, z of 22 to 30: p off by 8e-5 on average
@@ -853,7 +854,10 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     }
     // The next grid on the stream (the split-K reduce, the stream-K fixup,
     // or the next GEMM) may be scheduled now: it waits for this grid's end
-    // before it touches global memory.
+    // before it touches global memory.  A chained grid with late_wait does not:
+    // what it reads and writes before that wait was complete, or had been read,
+    // when its predecessor let it start (trigger_late; the order of such a
+    // chain stands above launch_xent_backward).
     if (!Cfg::CHAIN || !p.trigger_late) ptx::griddep_launch_dependents();
   }
   if (warp == 1) {
@@ -1186,10 +1190,11 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
           const uint32_t sfa_t = sf_t0 + uint32_t(stage * Cfg::SF_COLS);
           const int nsteps = (kb == tail_kb) ? tail_steps : Cfg::KSTEPS;
           if constexpr (Cfg::CHUNKED) {
-            // the next chunk's accumulator, handed back long ago as a rule
-            // (the epilogue reads one in about 1500 cycles, a 512-deep chunk
-            // takes 5200).  In the K loop itself, since a gap of the issuer is
-            // a gap of the tensor pipe.
+            // the next chunk's accumulator, handed back long ago as a rule:
+            // the epilogue reads one in about 1500 cycles, a chunk of 1024 K
+            // takes 10000, and the few tokens' chunks of 256 take as long as
+            // their weights need from memory.  In the K loop itself, since a
+            // gap of the issuer is a gap of the tensor pipe.
             if (kb == chunk_end) {
               ptx::tc_commit<CG>(acc_full(acc), pair_mask);
               ++it;

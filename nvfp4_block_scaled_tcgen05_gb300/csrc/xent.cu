@@ -8,21 +8,23 @@
 // Forward: the NT GEMM with an epilogue that folds a row's 128 columns of a
 // tile into (maximum, sum of exponentials); a second kernel joins the groups of
 // a row in a fixed order.  Per row and 128 logits 8 bytes leave the chip
-// instead of 256.  Bound by the MMAs (8192 x 65536 x 4096: 2219 us in a burst,
-// 1982 TFLOP/s; 2400-2470 under the power cap) or, with few tokens, by reading
-// W (64 x 131072 x 4096: 160 us, 6.7 TB/s).  Rows whose pitch is not a multiple
-// of 32 bytes cost a fifth sector per 128 bytes on the way from L2: 1016 x
-// 32003 x 2056 takes 100 us where 1024 x 32768 x 2048 takes 78.
+// instead of 256.  Bound by the MMAs (8192 x 65536 x 4096: 2220 us in a burst,
+// 1981 TFLOP/s; 2390-2470 under the power cap) or, with few tokens, by reading
+// W (64 x 131072 x 4096: 158 us, 6.8 TB/s; one token and 32768 x 2048, where
+// the grids' ramps weigh more: 26.4 us, 5.1 TB/s).  Rows whose pitch is not a
+// multiple of 32 bytes cost a fifth sector per 128 bytes on the way from L2:
+// 1016 x 32003 x 2056 takes 103 us where 1024 x 32768 x 2048 takes 82.
 //
 // Backward: pieces of the vocabulary.  Per piece one GEMM forms the logits
-// again and writes G as BF16 (the operand type of the products that follow:
-// one rounding of relative size 2^-9 per term), one adds G . W into FP32, one
-// computes the piece's rows of dW: three times the forward's products, since
-// the logits are not kept.  The grids of a piece are chained so that one
+// again, in the forward pass's chunks of K, and writes G as BF16 (the operand
+// type of the products that follow: one rounding of relative size at most 2^-8
+// per term), one adds G . W into FP32, one computes the piece's rows of dW:
+// three times the forward's products, since the logits are not kept.  The grids of a piece are chained so that one
 // without a data dependency on its predecessor starts on the SMs the
 // predecessor's last round leaves idle (launch_xent_backward).  4096 x 131072 x
-// 4096: 7220 us in a burst (1828 TFLOP/s), 7730 under the power cap; 37 x 32768
-// x 2048: 73 us, of which reading W twice and writing dW take 60.
+// 4096: 6850-7260 us in a burst (1818-1927 TFLOP/s), 7660-7710 under the power
+// cap; 37 x 32768 x 2048: 75.5 us, of which reading W twice and writing dW take
+// 60.
 #include <algorithm>
 
 #include "launch.cuh"
@@ -76,11 +78,11 @@ namespace {
 constexpr int kRowsFew = 128;  // up to this many tokens, they take the MMA's N side
 
 // K per accumulator, see ChunkedCfg.  8192 x 65536 x 4096 under the power cap:
-// 2530 us with 512, 2470 with 1024 (lse off by 6e-7 of its value, as in plain
-// FP32), 2445 with 2048 (1.3e-6): the extra reads of the accumulators cost
-// power.  Few tokens have it to spare, and a single row's loss lse - z[target]
-// cancels: 37 x 32768 x 2048 takes 27.0 us with 512, 27.3 with 256, 28.2 with
-// 128.
+// 2530 us with 512 (lse off by 3e-7 of its value), 2470 with 1024 (6e-7; a plain
+// FP32 evaluation is off by 4e-7 to 6e-7), 2445 with 2048 (1.3e-6): the extra
+// reads of the accumulators cost power.  Few tokens have it to spare, and a
+// single row's loss lse - z[target] cancels: 37 x 32768 x 2048 takes 27.0 us
+// with 512, 27.3 with 256, 28.2 with 128.
 constexpr int kChunkK = 1024, kChunkKFew = 256;
 
 // Joins the groups' statistics of each row.  A block takes `rows` (a power of
