@@ -413,7 +413,9 @@ GB300GEMM_API size_t gemm_nvfp4_bs_splitk_workspace_bytes(int M, int N, int K, i
  *   M, V, K >= 1 (any V; at most 2^30 each); K % 8 == 0; X, W 16-byte
  *   aligned; target 8-byte, loss and lse 4-byte aligned; loss, lse and
  *   workspace overlap no input and not each other.
- * A NaN logit, or an infinite maximum, makes the row's loss and lse NaN.
+ * A NaN logit, or a maximum of +inf, makes the row's loss and lse NaN; where
+ * every logit is -inf, lse is -inf and the loss NaN.  Finite logits give finite
+ * results, up to the end of the FP32 range.
  * Errors: GEMM_ERR_NULL, _SHAPE (also a workspace that is too small),
  * _ALIGN, _ALIAS, _ARCH, _LAUNCH, _NO_DEVICE, _CAPTURE.
  */
@@ -428,9 +430,10 @@ GB300GEMM_API size_t gemm_bf16_nt_xent_workspace_bytes(int M, int V);
  * gemm_bf16_nt_xent_backward - gradients of the linear cross entropy:
  *     G[m,v] = dloss[m] * ( exp(z[m,v] - lse[m]) - [v == target[m]] )
  *     dX[m,k] = bf16( sum_v G[m,v] W[v,k] ),  dW[v,k] = bf16( sum_m G[m,v] X[m,k] )
- * The logits are formed again, piece by piece of the vocabulary; a piece's G
- * is rounded once to BF16 (the operand type of the two products) and lives in
- * the workspace until both have read it.  Sums are FP32, dX across the pieces
+ * The logits are formed again, piece by piece of the vocabulary, with the sums
+ * of the forward call on the same sizes; a piece's G is rounded once to BF16
+ * (the operand type of the two products) and lives in the workspace until both
+ * have read it.  Sums are FP32, dX across the pieces
  * too; every addition has a fixed place, so results repeat bit for bit.
  *
  *   X, W, target, M, V, K   as for gemm_bf16_nt_xent
@@ -441,7 +444,8 @@ GB300GEMM_API size_t gemm_bf16_nt_xent_workspace_bytes(int M, int V);
  *   workspace  at least gemm_bf16_nt_xent_backward_workspace_bytes(M, V, K)
  *          bytes, 16-byte aligned; contents on entry ignored, on return
  *          unspecified
- * A row with target < 0 has no gradient (dloss[m] is not used); target >= V
+ * A row with target < 0 has no gradient (dloss[m] is not used; dloss[m] = 0 of
+ * another row is an ordinary factor, so 0 beside a NaN gives NaN); target >= V
  * makes its row of dX NaN, and with it all of dW.  dX and dW are 16-byte
  * aligned; the outputs and the workspace overlap no input and not each other.
  * Errors: as gemm_bf16_nt_xent.
