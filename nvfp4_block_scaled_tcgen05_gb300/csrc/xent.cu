@@ -78,11 +78,11 @@ namespace {
 constexpr int kRowsFew = 128;  // up to this many tokens, they take the MMA's N side
 
 // K per accumulator, see ChunkedCfg.  8192 x 65536 x 4096 under the power cap:
-// 2530 us with 512 (lse off by 3e-7 of its value), 2470 with 1024 (6e-7; a plain
-// FP32 evaluation is off by 4e-7 to 6e-7), 2445 with 2048 (1.3e-6): the extra
-// reads of the accumulators cost power.  Few tokens have it to spare, and a
-// single row's loss lse - z[target] cancels: 37 x 32768 x 2048 takes 27.0 us
-// with 512, 27.3 with 256, 28.2 with 128.
+// 2530 us with 512 (lse off by 3e-7 of its value), 2470 with 1024 (6e-7, 1e-6 in
+// well-learned rows; a plain FP32 evaluation is off by 3e-7 to 6e-7), 2445 with
+// 2048 (1.3e-6): the extra reads of the accumulators cost power.  Few tokens
+// have it to spare, and a single row's loss lse - z[target] cancels: 37 x 32768
+// x 2048 takes 27.0 us with 512, 27.3 with 256, 28.2 with 128.
 constexpr int kChunkK = 1024, kChunkKFew = 256;
 
 // Joins the groups' statistics of each row.  A block takes `rows` (a power of
