@@ -523,6 +523,76 @@ GB300GEMM_API int router_topk_backward(const float* logits, const int* experts, 
                                        int M, int E, int ld, int k, int normalize, void* stream);
 
 /*
+ * gemm_bf16_nt_gated - the gated projection of a feed-forward block, both
+ * products, the activation and their product in one kernel:
+ *     G = X . Wg^T,  U = X . Wu^T            (FP32, as gemm_bf16_nt forms them)
+ *     H = bf16( act(G) * U )
+ *   act = GEMM_ACT_SILU:       g / (1 + exp(-g))
+ *         GEMM_ACT_GELU_TANH:  g/2 (1 + tanh( sqrt(2/pi) (g + 0.044715 g^3) ))
+ * Both weight matrices have the layout of gemm_bf16_nt's B; two halves of one
+ * [2F][K] matrix are two pointers into it.
+ *
+ * Library extension (the pages define no such call).
+ *
+ *   X      bf16 [M][K], Wg, Wu bf16 [F][K]                       (read)
+ *   H      bf16 [M][F]                                           (written)
+ *   gates  bf16 [2][M][F], or NULL: G and U rounded, for the backward call
+ *   M, F, K >= 1, at most 2^30; F % 8 == 0 and K % 8 == 0; every pointer 16-byte
+ *   aligned; the outputs overlap no input and not each other.
+ * A gate of -inf gives NaN, as the formula does.
+ * Errors: GEMM_ERR_NULL, _SHAPE (also an unknown act), _ALIGN, _ALIAS, _ARCH,
+ * _LAUNCH, _NO_DEVICE, _CAPTURE.
+ */
+#define GEMM_ACT_SILU       0
+#define GEMM_ACT_GELU_TANH  1
+GB300GEMM_API int gemm_bf16_nt_gated(const void* X, const void* Wg, const void* Wu, void* H,
+                                     void* gates, int act, int M, int F, int K, void* stream);
+
+/*
+ * gemm_bf16_nt_gated_backward - gradients of the gated projection:
+ *     dG = bf16( dH * U * act'(G) ),   dU = bf16( dH * act(G) )
+ *     dX = bf16( dG . Wg + dU . Wu ),  dWg = bf16( dG^T . X ),  dWu = bf16( dU^T . X )
+ * with G and U from the forward call's gates, or formed again from X (FP32, no
+ * gates kept: activation checkpointing).  Sums are FP32 and every addition has a
+ * fixed place, so results repeat bit for bit.
+ *
+ *   X, Wg, Wu, act, M, F, K   as in the forward call
+ *   dH     bf16 [M][F]                                           (read)
+ *   gates  bf16 [2][M][F] of the forward call, or NULL           (read)
+ *   dX     bf16 [M][K] (written), or NULL: not wanted
+ *   dWg, dWu  bf16 [F][K] (written), or both NULL: not wanted; not all three NULL
+ *   workspace  at least gemm_bf16_nt_gated_backward_workspace_bytes(M, F, K)
+ *          bytes, 16-byte aligned; contents on entry ignored, on return unspecified
+ *   Every pointer 16-byte aligned; the outputs and the workspace overlap no input
+ *   and not each other.
+ * Errors: as gemm_bf16_nt_gated; GEMM_ERR_SHAPE also for a workspace that is too
+ * small.
+ */
+GB300GEMM_API int gemm_bf16_nt_gated_backward(const void* X, const void* Wg, const void* Wu,
+                                              const void* dH, const void* gates, void* dX,
+                                              void* dWg, void* dWu, void* workspace,
+                                              size_t workspace_bytes, int act, int M, int F,
+                                              int K, void* stream);
+
+/* Workspace bytes gemm_bf16_nt_gated_backward needs (0 for invalid arguments). */
+GB300GEMM_API size_t gemm_bf16_nt_gated_backward_workspace_bytes(int M, int F, int K);
+
+/*
+ * gemm_bf16_tn - C[M,N] = bf16( A[K,M]^T . B[K,N] ), FP32 accumulation: the weight
+ * gradient dW = dY^T . X of a product Y = X . W^T (K is then the tokens).
+ *
+ * Library extension (the pages define no such call).
+ *
+ *   A bf16 [K][M], B bf16 [K][N] (read), C bf16 [M][N] (written), row-major;
+ *   M, N, K >= 1; M % 8 == 0 and N % 8 == 0 (16-byte row pitches; any K); every
+ *   pointer 16-byte aligned; C must not overlap A or B.
+ * Errors: GEMM_ERR_NULL, _SHAPE, _ALIGN, _ALIAS, _ARCH, _LAUNCH, _NO_DEVICE,
+ * _CAPTURE.
+ */
+GB300GEMM_API int gemm_bf16_tn(const void* A, const void* B, void* C, int M, int N, int K,
+                               void* stream);
+
+/*
  * bf16_scaled_add - out[i] = bf16( float(out[i]) + scale * float(d[i]) ),
  * product and sum each rounded to FP32.  The second kernel of the unfused
  * LoRA pair (GEMM into a BF16 scratch, then this), kept as the baseline the

@@ -28,6 +28,7 @@ STATUS = {
 EXPORTS = ("gemm_bf16_nt", "gemm_bf16_nn", "gemm_bf16_nt_scaled_acc", "gemm_bf16_nt_ordered", "gemm_nvfp4_bs",
            "gemm_bf16_nt_splitk", "gemm_bf16_nt_streamk", "gemm_nvfp4_bs_splitk", "gemm_w4a16", "gemm_w4a16_t", "gemm_w4a16_ws",
            "gemm_bf16_nt_xent", "gemm_bf16_nt_xent_backward", "router_topk", "router_topk_backward",
+           "gemm_bf16_nt_gated", "gemm_bf16_nt_gated_backward", "gemm_bf16_tn",
            "bf16_scaled_add", "gemm_get_device_status", "gemm_selftest_wait_timeout",
            "gemm_testing_set_overrides", "gemm_status_string")
 
@@ -85,6 +86,11 @@ def load() -> ctypes.CDLL:
             lib.router_topk_workspace_bytes.argtypes = [i, i]
             lib.router_topk_workspace_bytes.restype = ctypes.c_size_t
             lib.router_topk_backward.argtypes = [vp] * 7 + [i] * 6 + [vp]
+            lib.gemm_bf16_nt_gated.argtypes = [vp] * 5 + [i] * 4 + [vp]
+            lib.gemm_bf16_nt_gated_backward.argtypes = [vp] * 9 + [ctypes.c_size_t] + [i] * 4 + [vp]
+            lib.gemm_bf16_nt_gated_backward_workspace_bytes.argtypes = [i] * 3
+            lib.gemm_bf16_nt_gated_backward_workspace_bytes.restype = ctypes.c_size_t
+            lib.gemm_bf16_tn.argtypes = [vp] * 3 + [i] * 3 + [vp]
             lib.gemm_get_device_status.argtypes = [vp]
             lib.gemm_selftest_wait_timeout.argtypes = [i, vp]
             lib.gemm_testing_set_overrides.argtypes = [i, i]
@@ -642,6 +648,131 @@ def router_topk_backward(logits: torch.Tensor, experts: torch.Tensor, lse: torch
          counts.data_ptr(), _ptr(dweights), _ptr(dlosses), dlogits.data_ptr(),
          1 if dtype == torch.bfloat16 else 0, M, E, ld, k, 1 if normalize else 0)
     return dlogits
+
+
+ACTIVATIONS = {"silu": 0, "gelu_tanh": 1}
+
+
+def _activation(act: str) -> int:
+    if act not in ACTIVATIONS:
+        raise ValueError(f"act must be one of {sorted(ACTIVATIONS)}, got {act!r}")
+    return ACTIVATIONS[act]
+
+
+def _gated_inputs(X, Wg, Wu):
+    _mat(X, torch.bfloat16, "X")
+    _mat(Wg, torch.bfloat16, "Wg")
+    M, K = X.shape
+    F, K2 = Wg.shape
+    if K != K2:
+        raise ValueError(f"K mismatch: X {tuple(X.shape)} vs Wg {tuple(Wg.shape)}")
+    if Wg.device != X.device:
+        raise ValueError("X and Wg must be on one device")
+    if M > _INT_MAX or F > _INT_MAX or K > _INT_MAX:
+        raise ValueError(f"sizes past 2^31 - 1: M {M}, F {F}, K {K}")
+    _on_device("Wu", X.device, Wu, torch.bfloat16, (F, K))
+    return M, F, K
+
+
+def gemm_bf16_nt_gated(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, act: str = "silu",
+                       H: torch.Tensor | None = None, gates: torch.Tensor | None = None,
+                       stream=None, save_gates: bool = False):
+    """(H bf16 [M,F], gates): H = act(X Wg^T) * (X Wu^T) in one kernel.
+
+    X bf16 [M,K]; Wg, Wu bf16 [F,K]; act "silu" or "gelu_tanh".  gates is
+    None, or with save_gates (or a tensor given for it) both products as bf16
+    [2,M,F], which gemm_bf16_nt_gated_backward reads.
+    """
+    M, F, K = _gated_inputs(X, Wg, Wu)
+    kind, device, bf16 = _activation(act), X.device, torch.bfloat16
+    elsewhere = _context(device, stream)
+    if elsewhere is not None:
+        with elsewhere:
+            return gemm_bf16_nt_gated(X, Wg, Wu, act, H, gates, save_gates=save_gates)
+    if H is None:
+        H = torch.empty((M, F), dtype=bf16, device=device)
+    else:
+        _on_device("H", device, H, bf16, (M, F))
+    if gates is not None:
+        _on_device("gates", device, gates, bf16, (2, M, F))
+    elif save_gates:
+        gates = torch.empty((2, M, F), dtype=bf16, device=device)
+    _run("gemm_bf16_nt_gated", device, X.data_ptr(), Wg.data_ptr(), Wu.data_ptr(), H.data_ptr(),
+         _ptr(gates), kind, M, F, K)
+    return H, gates
+
+
+def gemm_bf16_nt_gated_backward_workspace_bytes(M: int, F: int, K: int) -> int:
+    if not (0 <= M <= _INT_MAX and 0 <= F <= _INT_MAX and 0 <= K <= _INT_MAX):
+        return 0
+    return int((_lib or load()).gemm_bf16_nt_gated_backward_workspace_bytes(M, F, K))
+
+
+def gemm_bf16_nt_gated_backward(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor,
+                                dH: torch.Tensor, act: str = "silu",
+                                gates: torch.Tensor | None = None,
+                                dX: torch.Tensor | None = None, dWg: torch.Tensor | None = None,
+                                dWu: torch.Tensor | None = None,
+                                workspace: torch.Tensor | None = None, stream=None,
+                                need_dx: bool = True, need_dw: bool = True):
+    """(dX bf16 [M,K], dWg, dWu bf16 [F,K]) of gemm_bf16_nt_gated; None for what is not needed.
+
+    dH bf16 [M,F]; gates: the forward call's, or None to form them again from X.
+    """
+    M, F, K = _gated_inputs(X, Wg, Wu)
+    kind, device, bf16 = _activation(act), X.device, torch.bfloat16
+    _on_device("dH", device, dH, bf16, (M, F))
+    if gates is not None:
+        _on_device("gates", device, gates, bf16, (2, M, F))
+    if (dWg is None) != (dWu is None):
+        raise ValueError("give both of dWg and dWu, or neither")
+    if not (need_dx or need_dw or dX is not None or dWg is not None):
+        raise ValueError("neither dX nor the weight gradients are needed")
+    elsewhere = _context(device, stream)
+    if elsewhere is not None:
+        with elsewhere:
+            return gemm_bf16_nt_gated_backward(X, Wg, Wu, dH, act, gates, dX, dWg, dWu, workspace,
+                                               need_dx=need_dx, need_dw=need_dw)
+    if dX is not None:
+        _on_device("dX", device, dX, bf16, (M, K))
+    elif need_dx:
+        dX = torch.empty((M, K), dtype=bf16, device=device)
+    if dWg is not None:
+        _on_device("dWg", device, dWg, bf16, (F, K))
+        _on_device("dWu", device, dWu, bf16, (F, K))
+    elif need_dw:
+        dWg = torch.empty((F, K), dtype=bf16, device=device)
+        dWu = torch.empty((F, K), dtype=bf16, device=device)
+    ws, nbytes, _alive = _workspace(workspace, gemm_bf16_nt_gated_backward_workspace_bytes(M, F, K),
+                                    device)
+    _run("gemm_bf16_nt_gated_backward", device, X.data_ptr(), Wg.data_ptr(), Wu.data_ptr(),
+         dH.data_ptr(), _ptr(gates), _ptr(dX), _ptr(dWg), _ptr(dWu), ws, nbytes, kind, M, F, K)
+    return dX, dWg, dWu
+
+
+def gemm_bf16_tn(A: torch.Tensor, B: torch.Tensor, C: torch.Tensor | None = None, stream=None):
+    """C[M,N] = bf16(A[K,M]^T . B[K,N]), FP32 accumulation: a weight gradient dY^T X."""
+    _mat(A, torch.bfloat16, "A")
+    _mat(B, torch.bfloat16, "B")
+    K, M = A.shape
+    K2, N = B.shape
+    if K != K2:
+        raise ValueError(f"K mismatch: A {tuple(A.shape)} vs B {tuple(B.shape)}")
+    device = A.device
+    if B.device != device:
+        raise ValueError("A and B must be on one device")
+    if M > _INT_MAX or N > _INT_MAX or K > _INT_MAX:
+        raise ValueError(f"sizes past 2^31 - 1: M {M}, N {N}, K {K}")
+    elsewhere = _context(device, stream)
+    if elsewhere is not None:
+        with elsewhere:
+            return gemm_bf16_tn(A, B, C)
+    if C is None:
+        C = torch.empty((M, N), dtype=torch.bfloat16, device=device)
+    else:
+        _on_device("C", device, C, torch.bfloat16, (M, N))
+    _run("gemm_bf16_tn", device, A.data_ptr(), B.data_ptr(), C.data_ptr(), M, N, K)
+    return C
 
 
 def bf16_scaled_add(out: torch.Tensor, d: torch.Tensor, scale: float, stream=None):

@@ -236,6 +236,21 @@ int check_xent(const void* X, const void* W, int M, int V, int K) {
   return GEMM_OK;
 }
 
+// Shared checks of the gated projection (the inputs).
+int check_gated(const void* X, const void* Wg, const void* Wu, int act, int M, int F, int K) {
+  if (!X || !Wg || !Wu) return GEMM_ERR_NULL;
+  if (M <= 0 || F <= 0 || K <= 0) return GEMM_ERR_SHAPE;
+  if (M > kMaxDim || F > kMaxDim || K > kMaxDim) return GEMM_ERR_SHAPE;
+  if (act != GEMM_ACT_SILU && act != GEMM_ACT_GELU_TANH) return GEMM_ERR_SHAPE;
+  // tiles of every product, both directions; K blocks of dX's loop over 2 F
+  const long long mb = ((long long)M + 127) / 128, fb = ((long long)F + 63) / 64,
+                  kb = ((long long)K + 255) / 256;
+  if (mb * fb > kMaxTiles || fb * kb > kMaxTiles || mb * kb > kMaxTiles) return GEMM_ERR_SHAPE;
+  if (!aligned16(X) || !aligned16(Wg) || !aligned16(Wu)) return GEMM_ERR_ALIGN;
+  if (F % 8 != 0 || K % 8 != 0) return GEMM_ERR_ALIGN;  // 16-byte row pitches
+  return GEMM_OK;
+}
+
 }  // namespace
 }  // namespace gb300
 
@@ -583,6 +598,66 @@ int router_topk_backward(const float* logits, const int* experts, const float* l
   const RouterTopkBackward r{logits, experts, lse, counts, dweights, dlosses, dlogits,
                              dlogits_bf16 != 0, M, E, ld, k, normalize != 0};
   return launch_router_topk_backward(r, dev, static_cast<cudaStream_t>(stream));
+}
+
+int gemm_bf16_nt_gated(const void* X, const void* Wg, const void* Wu, void* H, void* gates, int act,
+                       int M, int F, int K, void* stream) {
+  if (!H) return GEMM_ERR_NULL;
+  int rc = check_gated(X, Wg, Wu, act, M, F, K);
+  if (rc != GEMM_OK) return rc;
+  if (!aligned16(H) || !aligned16(gates)) return GEMM_ERR_ALIGN;
+  const size_t mk = size_t(M) * K * 2, fk = size_t(F) * K * 2, mf = size_t(M) * F * 2;
+  const Span in[] = {{X, mk}, {Wg, fk}, {Wu, fk}};
+  const Span out[] = {{H, mf}, {gates, gates ? 2 * mf : 0}};
+  if (any_overlap(in, 3, out, 2)) return GEMM_ERR_ALIAS;
+  DeviceInfo dev;
+  if ((rc = current_device(&dev, stream)) != GEMM_OK) return rc;
+  const GatedForward a{X, Wg, Wu, H, gates, act, M, F, K};
+  return launch_gated_forward(a, dev, static_cast<cudaStream_t>(stream));
+}
+
+size_t gemm_bf16_nt_gated_backward_workspace_bytes(int M, int F, int K) {
+  if (M <= 0 || F <= 0 || K <= 0 || M > kMaxDim || F > kMaxDim || K > kMaxDim) return 0;
+  return gated_backward_workspace(M, F, K);
+}
+
+int gemm_bf16_nt_gated_backward(const void* X, const void* Wg, const void* Wu, const void* dH,
+                                const void* gates, void* dX, void* dWg, void* dWu,
+                                void* workspace, size_t workspace_bytes, int act, int M, int F,
+                                int K, void* stream) {
+  if (!dH || !workspace || !dWg != !dWu || (!dX && !dWg)) return GEMM_ERR_NULL;
+  int rc = check_gated(X, Wg, Wu, act, M, F, K);
+  if (rc != GEMM_OK) return rc;
+  if (!aligned16(dH) || !aligned16(gates) || !aligned16(dX) || !aligned16(dWg) ||
+      !aligned16(dWu) || !aligned16(workspace))
+    return GEMM_ERR_ALIGN;
+  const size_t need = gated_backward_workspace(M, F, K);
+  if (workspace_bytes < need) return GEMM_ERR_SHAPE;
+  const size_t mk = size_t(M) * K * 2, fk = size_t(F) * K * 2, mf = size_t(M) * F * 2;
+  const Span in[] = {{X, mk}, {Wg, fk}, {Wu, fk}, {dH, mf}, {gates, gates ? 2 * mf : 0}};
+  const Span out[] = {
+      {dX, dX ? mk : 0}, {dWg, dWg ? fk : 0}, {dWu, dWu ? fk : 0}, {workspace, need}};
+  if (any_overlap(in, 5, out, 4)) return GEMM_ERR_ALIAS;
+  DeviceInfo dev;
+  if ((rc = current_device(&dev, stream)) != GEMM_OK) return rc;
+  const GatedBackward a{X, Wg, Wu, dH, gates, dX, dWg, dWu, workspace, act, M, F, K};
+  return launch_gated_backward(a, dev, static_cast<cudaStream_t>(stream));
+}
+
+int gemm_bf16_tn(const void* A, const void* B, void* C, int M, int N, int K, void* stream) {
+  if (!A || !B || !C) return GEMM_ERR_NULL;
+  if (M <= 0 || N <= 0 || K <= 0) return GEMM_ERR_SHAPE;
+  if (M > kMaxDim || N > kMaxDim || K > kMaxDim) return GEMM_ERR_SHAPE;
+  const long long tiles = ((long long)M + 127) / 128 * (((long long)N + 63) / 64);
+  if (tiles > kMaxTiles) return GEMM_ERR_SHAPE;
+  if (!aligned16(A) || !aligned16(B) || !aligned16(C)) return GEMM_ERR_ALIGN;
+  if (M % 8 != 0 || N % 8 != 0) return GEMM_ERR_ALIGN;  // 16-byte row pitch of A, B and C
+  const size_t sa = size_t(K) * M * 2, sb = size_t(K) * N * 2, sc = size_t(M) * N * 2;
+  if (overlaps(C, sc, A, sa) || overlaps(C, sc, B, sb)) return GEMM_ERR_ALIAS;
+  DeviceInfo dev;
+  const int rc = current_device(&dev, stream);
+  if (rc != GEMM_OK) return rc;
+  return launch_gemm_bf16_tn(A, B, C, M, N, K, dev, static_cast<cudaStream_t>(stream));
 }
 
 int bf16_scaled_add(void* out, const void* d, float scale, long n, void* stream) {

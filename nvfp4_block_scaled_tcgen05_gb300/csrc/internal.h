@@ -142,6 +142,25 @@ size_t xent_backward_workspace(int M, int V, int K);
 int launch_xent_forward(const XentForward& a, const DeviceInfo& dev, cudaStream_t stream);
 int launch_xent_backward(const XentBackward& a, const DeviceInfo& dev, cudaStream_t stream);
 
+// Gated projection (gated.cu).  Forward: H, and with gates both factors
+// [2][M][F].  Backward: from gates, or with NULL from X; dX and / or both weight
+// gradients (NULL = not wanted).  launch_gemm_bf16_tn: C = A^T B.
+struct GatedForward {
+  const void *X, *Wg, *Wu;
+  void *H, *gates;
+  int act, M, F, K;
+};
+struct GatedBackward {
+  const void *X, *Wg, *Wu, *dH, *gates;
+  void *dX, *dWg, *dWu, *workspace;
+  int act, M, F, K;
+};
+size_t gated_backward_workspace(int M, int F, int K);
+int launch_gated_forward(const GatedForward& a, const DeviceInfo& dev, cudaStream_t stream);
+int launch_gated_backward(const GatedBackward& a, const DeviceInfo& dev, cudaStream_t stream);
+int launch_gemm_bf16_tn(const void* A, const void* B, void* C, int M, int N, int K,
+                        const DeviceInfo& dev, cudaStream_t stream);
+
 // Routing step (router_topk.cu); limits: E <= kRouterMaxExperts, k <= 32.
 constexpr int kRouterMaxExperts = 1024;
 constexpr int kRouterMaxTopk = 32;

@@ -38,6 +38,7 @@
 #include <stdint.h>
 
 #include "epilogue_math.cuh"
+#include "gate_act.cuh"
 #include "ptx.cuh"
 #include "watchdog.cuh"
 
@@ -53,6 +54,9 @@ enum class Operand : int { kBF16 = 0, kNVFP4 = 1, kW4A16 = 2 };
 // kXentGradBF16: C = bf16(d_row * (exp(acc - lse_row) - [column = target_row]))
 // kXentGradTBF16: the same with the roles swapped (d, lse, target of the
 //   column; the row is the vocabulary's)
+// kGatedBF16 (GATED tiles): C = bf16(act(gate) * up), and with p.gates_out both
+//   factors as BF16 through the A-scale map
+// kGatedGradBF16: C[0] = bf16(dH * up * act'(gate)), C[1] = bf16(dH * act(gate))
 enum class Epilogue : int {
   kStoreBF16 = 0,
   kScaledAccBF16 = 1,
@@ -63,7 +67,9 @@ enum class Epilogue : int {
   kXentStats = 6,
   kXentGradBF16 = 7,
   kXentStatsT = 8,
-  kXentGradTBF16 = 9
+  kXentGradTBF16 = 9,
+  kGatedBF16 = 10,
+  kGatedGradBF16 = 11
 };
 
 struct GemmParams {
@@ -98,6 +104,11 @@ struct GemmParams {
   int k_chunk, chunks;            // CHUNKED: K blocks per chunk, chunks per tile
   int n_last;                     // TRIM_N: columns of the last N block, rounded up to 32
   int m_rows;                     // VAR_ROWS: rows of A per CTA and tile (a multiple of 32, <= 128)
+  // gated projection (kGated*)
+  int act;                        // GEMM_ACT_*
+  int gates_out;                  // kGatedBF16: store the factors too
+  const uint16_t* dh;             // kGatedGradBF16: gradient of the output, [M][N]
+  int k_half;                     // DUAL_K: K blocks of the first pair of operands
 };
 
 template <Operand OP, int CG_, int BN_, int STAGES_, int EPI_WARPS_ = 4, int EPI_BUFS_ = 2,
@@ -143,6 +154,8 @@ struct TileCfg {
   static constexpr bool VAR_ROWS = false;
   // TRIM_N (see TrimCfg): the last N block's MMAs are n_last columns wide.
   static constexpr bool TRIM_N = false;
+  // GATED, DUAL_K, DUAL_OUT: see GatedCfg, DualKCfg, DualOutCfg.
+  static constexpr bool GATED = false, DUAL_K = false, DUAL_OUT = false;
   // C_T: the output is D transposed (the swapped-operand decode GEMM, whose
   // M role holds the weights and N role the few activation rows)
   static constexpr bool C_T = C_T_;
@@ -298,6 +311,33 @@ template <class Base>
 struct TrimCfg : Base {
   static constexpr bool TRIM_N = true;
   static_assert(Base::CG == 2 && Base::B_MN, "CTA pairs, MN-major B");
+};
+
+// Two weight matrices share a tile: the first CTA of the pair stages BN / 2 rows
+// of B (gate), the second the same rows of another matrix (up, the B-scale map),
+// so that column c of the accumulator's first half and of its second belong to
+// one output.
+template <class Base>
+struct GatedCfg : Base {
+  static constexpr bool GATED = true;
+  static_assert(Base::CG == 2 && !Base::B_MN && !Base::kFP4 && !Base::kW4, "CTA pairs, NT layout");
+};
+
+// One K loop over two products, A0 B0 + A1 B1: K blocks from k_half on come from
+// the scale maps' operands.  A block that passes the first one's end is filled
+// with zeros.
+template <class Base>
+struct DualKCfg : Base {
+  static constexpr bool DUAL_K = true;
+  static_assert(Base::CG == 2 && Base::B_MN && !Base::kFP4 && !Base::kW4, "CTA pairs, NN layout");
+};
+
+// Two outputs in one grid: batch l = 0, 1 of A against one B, stored through
+// the output's map and the A-scale map.
+template <class Base>
+struct DualOutCfg : Base {
+  static constexpr bool DUAL_OUT = true;
+  static_assert(Base::CG == 2 && Base::A_MN, "CTA pairs, both operands MN-major");
 };
 
 // Work item `tile` -> batch l, M block mb and N block nb, in grouped-M
@@ -548,6 +588,36 @@ __device__ __forceinline__ void xent_grad_t(const float (&x)[32], uint32_t (&v)[
     // factor, and 0 times NaN is NaN as in xent_grad
     v[i] = __float_as_int(t.z) == kNoLoss ? 0u : __float_as_uint(g);
   }
+}
+
+// Gated projection: 32 columns of a row, FP32 bits.  g <- act(g) u.
+__device__ __forceinline__ void gated_product(int act, uint32_t (&g)[32], const uint32_t (&u)[32]) {
+  auto all = [&](auto kind) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      const float x = __uint_as_float(g[i]);
+      g[i] = __float_as_uint(gate_act<decltype(kind)::value>(x) * __uint_as_float(u[i]));
+    }
+  };
+  if (act == GEMM_ACT_SILU) all(ActKind<GEMM_ACT_SILU>{});
+  else all(ActKind<GEMM_ACT_GELU_TANH>{});
+}
+
+// g <- dh u act'(g), u <- dh act(g); dh: the 32 values of the output's gradient.
+__device__ __forceinline__ void gated_gradient(int act, uint32_t (&g)[32], uint32_t (&u)[32],
+                                               const uint4 (&dh)[4]) {
+  auto all = [&](auto kind) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      const uint32_t w = (&dh[i / 8].x)[(i % 8) / 2];
+      const float d = i % 2 ? bf16_hi(w) : bf16_lo(w);
+      const float2 a = gate_act_slope<decltype(kind)::value>(__uint_as_float(g[i]));
+      g[i] = __float_as_uint(d * __uint_as_float(u[i]) * a.y);
+      u[i] = __float_as_uint(d * a.x);
+    }
+  };
+  if (act == GEMM_ACT_SILU) all(ActKind<GEMM_ACT_SILU>{});
+  else all(ActKind<GEMM_ACT_GELU_TANH>{});
 }
 
 // W4A16 weights ("gemm_dense.rs", w4a16_gemm: C = A @ dequant(B), NVFP4
@@ -823,9 +893,10 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
       ptx::prefetch_tmap(&tmap_sfb);
     } else if constexpr (Cfg::kW4) {
       ptx::prefetch_tmap(&tmap_sfb);  // the block scales (tmap_b: the codes)
-    } else if (p.sk) {
-      ptx::prefetch_tmap(&tmap_sfa);  // the stream-K workspace
+    } else if (p.sk || Cfg::DUAL_K || Cfg::DUAL_OUT || p.gates_out) {
+      ptx::prefetch_tmap(&tmap_sfa);  // the stream-K workspace, or a second matrix
     }
+    if constexpr (Cfg::GATED || Cfg::DUAL_K) ptx::prefetch_tmap(&tmap_sfb);
     {
       // The operand tiles of this CTA's first stages are pulled into L2
       // while the previous grid on the stream finishes.  A prefetch moves
@@ -837,14 +908,16 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         decode_tile<Cfg>(s0.tile, p, l0, mb0, nb0);
         const int l = (p.k_splits > 1) ? l0 / p.k_splits : l0;
         const int a_row = (mb0 * CG + int(peer)) * m_rows;
-        const int b_row = nb0 * BN + int(peer) * Cfg::B_ROWS;
+        const int b_row = Cfg::GATED ? nb0 * Cfg::B_ROWS : nb0 * BN + int(peer) * Cfg::B_ROWS;
+        const void* map_b = Cfg::GATED && peer ? &tmap_sfb : &tmap_b;
+        (void)map_b, (void)b_row;
         const int kend = min(s0.kb1, s0.kb0 + STAGES);
         for (int kb = s0.kb0; kb < kend; ++kb) {
 #pragma unroll
           for (int sub = 0; sub < Cfg::KSUB; ++sub) {
             const int x = kb * Cfg::KX * Cfg::KSUB + sub * Cfg::KX;
-            if constexpr (!Cfg::A_MN) ptx::tma_prefetch_3d(&tmap_a, x, a_row, l);
-            if constexpr (!Cfg::kW4 && !Cfg::B_MN) ptx::tma_prefetch_3d(&tmap_b, x, b_row, l);
+            if constexpr (!Cfg::A_MN && !Cfg::DUAL_K) ptx::tma_prefetch_3d(&tmap_a, x, a_row, l);
+            if constexpr (!Cfg::kW4 && !Cfg::B_MN) ptx::tma_prefetch_3d(map_b, x, b_row, l);
           }
           if constexpr (kFP4 && Cfg::SFA_REP)
             ptx::tma_prefetch_3d(&tmap_sfa, 0, 0,
@@ -943,7 +1016,8 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
           decode_tile<Cfg>(sg.tile, p, l, mb, nb);
         }
         const int a_row = (mb * CG + int(peer)) * m_rows;
-        const int b_row = nb * BN + int(peer) * (Cfg::TRIM_N ? tile_n(nb) / 2 : Cfg::B_ROWS);
+        const int b_row = Cfg::GATED ? nb * Cfg::B_ROWS
+                                     : nb * BN + int(peer) * (Cfg::TRIM_N ? tile_n(nb) / 2 : Cfg::B_ROWS);
         // TRIM_N: 64-column atoms of B that the tile needs
         const int b_atoms = Cfg::TRIM_N ? (tile_n(nb) / 2 + 63) / 64 : Cfg::B_ROWS / 64;
         const uint32_t b_bytes =
@@ -1015,9 +1089,16 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
             }
           } else {
             const uint32_t fb = ptx::mapa_shared(full_bar(stage), pair_leader);  // the leader's barrier
+            // two weight matrices, or two products in one K loop
+            const bool second = Cfg::GATED ? peer != 0 : Cfg::DUAL_K && kb >= p.k_half;
+            const void* map_a = Cfg::DUAL_K && second ? &tmap_sfa : &tmap_a;
+            const void* map_b = (Cfg::GATED || Cfg::DUAL_K) && second ? &tmap_sfb : &tmap_b;
+            const int kb_x = Cfg::DUAL_K && second ? kb - p.k_half : kb;
+            const int l_b = Cfg::DUAL_OUT ? 0 : l;
+            (void)map_a, (void)map_b, (void)l_b;
 #pragma unroll
             for (int sub = 0; sub < Cfg::KSUB; ++sub) {
-              const int x = kb * Cfg::KX * Cfg::KSUB + sub * Cfg::KX;
+              const int x = kb_x * Cfg::KX * Cfg::KSUB + sub * Cfg::KX;
               const uint32_t da = stage_a(stage) + sub * Cfg::A_SUB_BYTES;
               const uint32_t db = stage_b(stage) + sub * Cfg::B_SUB_BYTES;
               if constexpr (Cfg::kW4) {
@@ -1025,7 +1106,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                 ptx::tma_load_3d_pair_hint(da, &tmap_a, fb, x, a_row, l, pol_ab);
               } else if constexpr (Cfg::B_MN) {
                 if constexpr (!Cfg::A_MN)
-                  ptx::tma_load_3d_pair_hint(da, &tmap_a, fb, x, a_row, l, pol_ab);
+                  ptx::tma_load_3d_pair_hint(da, map_a, fb, x, a_row, l, pol_ab);
                 else if (sub == 0)
 #pragma unroll
                   for (int at = 0; at < Cfg::BM / 64; ++at)
@@ -1035,11 +1116,11 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
 #pragma unroll
                   for (int at = 0; at < Cfg::B_ROWS / 64; ++at)
                     if (!Cfg::TRIM_N || at < b_atoms)
-                      ptx::tma_load_3d_pair_hint(stage_b(stage) + at * Cfg::B_ATOM_BYTES, &tmap_b,
-                                                 fb, b_row + 64 * at, kb * Cfg::BK, l, pol_ab);
+                      ptx::tma_load_3d_pair_hint(stage_b(stage) + at * Cfg::B_ATOM_BYTES, map_b,
+                                                 fb, b_row + 64 * at, kb_x * Cfg::BK, l_b, pol_ab);
               } else if constexpr (kHintLoads) {
                 ptx::tma_load_3d_pair_hint(da, &tmap_a, fb, x, a_row, l, pol_a);
-                ptx::tma_load_3d_pair_hint(db, &tmap_b, fb, x, b_row, l, pol_ab);
+                ptx::tma_load_3d_pair_hint(db, map_b, fb, x, b_row, l, pol_ab);
               } else {
                 ptx::tma_load_3d_pair(da, &tmap_a, fb, x, a_row, l);
                 ptx::tma_load_3d_pair(db, &tmap_b, fb, x, b_row, l);
@@ -1483,6 +1564,10 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     const uint64_t pol_c = ptx::policy_evict_first();
     (void)pol_c;
     auto store_box = [&](uint32_t sbuf, int col0, int row0, int l) {
+      if constexpr (Cfg::DUAL_OUT) {
+        ptx::tma_store_3d_hint(l ? &tmap_sfa : &tmap_c, sbuf, col0, row0, 0, pol_c);
+        return;
+      }
       if constexpr (kL2Hints) ptx::tma_store_3d_hint(&tmap_c, sbuf, col0, row0, l, pol_c);
       else ptx::tma_store_3d(&tmap_c, sbuf, col0, row0, l);
     };
@@ -1956,6 +2041,87 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
             for (int i = 0; i + 2 < XR; ++i)
 #pragma unroll
               for (int j = 0; j < 32; ++j) xr[i][j] = xr[i + 2][j];
+          }
+        }
+      } else if constexpr (EPI == Epilogue::kGatedBF16 || EPI == Epilogue::kGatedGradBF16) {
+        // Gated projection: 64 outputs at a time from 64 columns of each half.
+        // The CTA's last tile puts each box in a place of its own in the freed
+        // stage memory (as in the other epilogues).
+        static_assert(Cfg::EPI_COLS == 256, "one warp holds both halves");
+        constexpr int NCH = Cfg::BN / 128;     // 64-column chunks of a tile's outputs
+        constexpr int kBoxesMost = EPI == Epilogue::kGatedBF16 ? 3 : 2;  // per chunk
+        static_assert(Cfg::EPI_WARPS * NCH * kBoxesMost * Cfg::EPI_BOX_BYTES <=
+                          Cfg::STAGES * Cfg::STAGE_BYTES,
+                      "the last tile's boxes fit the stages");
+        Seg nx;
+        const bool last_tile = !seg_at<Cfg>(p, cluster_id, num_clusters, idx + 1, nx);
+        int boxes = 0;  // of this tile
+        // the place of the warp's next box
+        auto next_box = [&]() {
+          if (last_tile) return sbase + uint32_t(e * NCH * kBoxesMost + boxes++) * Cfg::EPI_BOX_BYTES;
+          if (lane == 0) ptx::bulk_wait_group_read<Cfg::EPI_BUFS - 1>();
+          __syncwarp();
+          return buf0 + uint32_t(chunk_ctr++ % Cfg::EPI_BUFS) * Cfg::EPI_BOX_BYTES;
+        };
+        auto send = [&](const CUtensorMap* map, uint32_t sbuf, int col0, int z) {
+          ptx::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            // read back by the next launches: no evict-first hint
+            ptx::tma_store_3d(map, sbuf, col0, row0, z);
+            ptx::bulk_commit_group();
+          }
+        };
+#pragma unroll 1
+        for (int c = 0; c < NCH; ++c) {
+          const int col0 = nb * (BN / 2) + c * 64;
+          const bool live = rows_live && col0 < p.N;  // warp-uniform
+          uint4 dh[8];
+          if constexpr (EPI == Epilogue::kGatedGradBF16) {
+            // the lane's 64 values of dH (N % 8 == 0: a piece of 8 is whole)
+            const uint16_t* src = p.dh + size_t(row0 + lane) * p.N + col0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              dh[j] = live && row0 + lane < p.M && col0 + 8 * j < p.N
+                          ? __ldcg(reinterpret_cast<const uint4*>(src) + j)
+                          : make_uint4(0, 0, 0, 0);
+          }
+          uint32_t g0[32], g1[32], u0[32], u1[32];
+          const uint32_t tg = tacc + uint32_t(c * 64), tu = tg + BN / 2;
+          ptx::tmem_ld_32x32b_x32(tg, g0);
+          ptx::tmem_ld_32x32b_x32(tg + 32, g1);
+          ptx::tmem_ld_32x32b_x32(tu, u0);
+          ptx::tmem_ld_32x32b_x32(tu + 32, u1);
+          ptx::tmem_ld_wait_regs(g0);
+          ptx::tmem_ld_wait_regs(g1);
+          ptx::tmem_ld_wait_regs(u0);
+          ptx::tmem_ld_wait_regs(u1);
+          if (c == NCH - 1) release_acc(acc);
+          if (!live) continue;
+          if constexpr (EPI == Epilogue::kGatedBF16) {
+            if (p.gates_out) {
+              uint32_t sbuf = next_box();
+              write_box_row<Epilogue::kStoreBF16>(smem + (sbuf - sbase) + lane * 128, lane, g0, g1, 0.0f);
+              send(&tmap_sfa, sbuf, col0, 0);
+              sbuf = next_box();
+              write_box_row<Epilogue::kStoreBF16>(smem + (sbuf - sbase) + lane * 128, lane, u0, u1, 0.0f);
+              send(&tmap_sfa, sbuf, col0, 1);
+            }
+            gated_product(p.act, g0, u0);
+            gated_product(p.act, g1, u1);
+            const uint32_t sbuf = next_box();
+            write_box_row<Epilogue::kStoreBF16>(smem + (sbuf - sbase) + lane * 128, lane, g0, g1, 0.0f);
+            send(&tmap_c, sbuf, col0, 0);
+          } else {
+            const uint4 lo[4] = {dh[0], dh[1], dh[2], dh[3]}, hi[4] = {dh[4], dh[5], dh[6], dh[7]};
+            gated_gradient(p.act, g0, u0, lo);
+            gated_gradient(p.act, g1, u1, hi);
+            uint32_t sbuf = next_box();
+            write_box_row<Epilogue::kStoreBF16>(smem + (sbuf - sbase) + lane * 128, lane, g0, g1, 0.0f);
+            send(&tmap_c, sbuf, col0, 0);
+            sbuf = next_box();
+            write_box_row<Epilogue::kStoreBF16>(smem + (sbuf - sbase) + lane * 128, lane, u0, u1, 0.0f);
+            send(&tmap_c, sbuf, col0, 1);
           }
         }
       } else if constexpr (EPI == Epilogue::kStoreF32 || EPI == Epilogue::kAddF32) {
