@@ -593,6 +593,119 @@ GB300GEMM_API int gemm_bf16_tn(const void* A, const void* B, void* C, int M, int
                                void* stream);
 
 /*
+ * residual_norm - the residual step between two blocks of a transformer: the norm
+ * after a block, its gate and residual scale, and the norm before the next block,
+ * one pass over the rows.  With r(v) = 1 / sqrt( mean(v^2) + eps ) of a row:
+ *     c = block * r(block) * w_post     (c = block without w_post)
+ *     y = x + scale * gate * c          (gate = 1 without one), in the stream's type
+ *     n = bf16( y * r(y) * w_pre )      (of y as it is stored)
+ * Arithmetic and sums are FP32; sums are taken in a fixed order.
+ *
+ * Library extension (the pages define no such call).
+ *
+ *   x        [M][D], the residual stream: bf16, or float if x_f32 != 0  (read)
+ *   block    bf16 [M][D], the block's output, or NULL: no block yet (then y = x:
+ *            w_post, gate, y and rstd_post have to be NULL)             (read)
+ *   w_post   bf16 [D], or NULL: no norm after the block                 (read)
+ *   gate     bf16 [M / rows_per_gate][D], or NULL: row m has gate row
+ *            m / rows_per_gate (M: one gate for all rows; a sequence's length;
+ *            1: a gate per row)                                         (read)
+ *   w_pre    bf16 [D], or NULL: no norm before the next block (then n and rstd_pre
+ *            have to be NULL); not both block and w_pre NULL            (read)
+ *   y        [M][D] of x's type; may be x itself                        (written)
+ *   n        bf16 [M][D]                                                (written)
+ *   rstd_post, rstd_pre  float [M], r(block) and r(y) for the backward call, or
+ *            NULL: not wanted                                           (written)
+ *   M >= 1, at most 2^30; 8 <= D <= 16384, D % 8 == 0; eps >= 0; rows_per_gate >= 1
+ *   divides M (used with a gate); matrices and weights 16-byte, rstd 4-byte aligned;
+ *   an output overlaps no input (but y == x) and no other output.
+ * A row whose values are all zero has r = 1 / sqrt(eps), and NaN for eps = 0.
+ * Errors: GEMM_ERR_NULL, _SHAPE, _ALIGN, _ALIAS, _ARCH, _LAUNCH, _NO_DEVICE,
+ * _CAPTURE.
+ */
+GB300GEMM_API int residual_norm(const void* x, const void* block, const void* w_post,
+                                const void* gate, const void* w_pre, void* y, void* n,
+                                float* rstd_post, float* rstd_pre, float scale, float eps,
+                                int x_f32, int M, int D, int rows_per_gate, void* stream);
+
+/*
+ * residual_norm_backward - gradient of residual_norm, from dy (at y) and dn (at n),
+ * with yh = y * r(y), bh = block * r(block), and mean over a row:
+ *     t      = dy + r(y) ( dn w_pre - yh mean(dn w_pre yh) )
+ *     dx     = t,   q = scale * gate * t  (at c)
+ *     dblock = r(block) ( q w_post - bh mean(q w_post bh) )   (q without w_post)
+ *     dw_pre = sum_m dn yh,   dw_post = sum_m q bh,   dgate = sum over the gate's
+ *              rows of scale * t * c
+ * t is rounded only where it is stored as dx.  Sums over rows are FP32 in a fixed
+ * order: results repeat bit for bit.
+ *
+ *   dy        [M][D] of the stream's type, or NULL: zero               (read)
+ *   dn        bf16 [M][D] and y, the stream that the forward call wrote (x where it
+ *             had no block): both required with w_pre, else dn NULL    (read)
+ *   block     as in the forward call, or NULL                          (read)
+ *   rstd_post, rstd_pre  the forward call's, required with w_post, w_pre
+ *   w_post, gate, w_pre, scale, x_f32, M, D, rows_per_gate   as in the forward call
+ *   dx        [M][D] of the stream's type                              (written)
+ *   dblock    bf16 [M][D]; required with block, else NULL              (written)
+ *   dw_post, dw_pre  float [D], dgate float [M / rows_per_gate][D], or NULL: not
+ *             wanted (NULL also where there is no such input)          (written)
+ *   workspace at least residual_norm_backward_workspace_bytes(M, D, rows_per_gate,
+ *             weights, gates) bytes, with weights the number of dw_post and dw_pre
+ *             that are wanted and gates 1 if dgate is; 16-byte aligned (NULL where
+ *             that is 0); contents on entry ignored, on return unspecified
+ *   dx may be dy itself; otherwise the outputs and the workspace overlap no input and
+ *   not each other.
+ * Errors: as residual_norm; GEMM_ERR_SHAPE also for a workspace that is too small.
+ */
+GB300GEMM_API int residual_norm_backward(const void* dy, const void* dn, const void* y,
+                                         const void* block, const float* rstd_post,
+                                         const float* rstd_pre, const void* w_post,
+                                         const void* gate, const void* w_pre, void* dx,
+                                         void* dblock, float* dw_post, float* dgate,
+                                         float* dw_pre, void* workspace, size_t workspace_bytes,
+                                         float scale, int x_f32, int M, int D,
+                                         int rows_per_gate, void* stream);
+
+/* Workspace bytes residual_norm_backward needs (0 for none or invalid arguments). */
+GB300GEMM_API size_t residual_norm_backward_workspace_bytes(int M, int D, int rows_per_gate,
+                                                            int weights, int gates);
+
+/*
+ * gemv_w4a16 - gemm_w4a16 for few tokens (decoding), bound by reading the weights
+ * once:
+ *     C[m,n] = bf16( scale2 * sum_k A[m,k] * w[n,k] ),  w = e2m1(b) * e4m3(sfb)
+ * The same weights, exact products and FP32 sums as gemm_w4a16's; the order of the
+ * sums differs (fixed for given sizes), so results may differ in the last BF16 bit.
+ *
+ * Defined by: as gemm_w4a16 (the operation); the few-token form is a library
+ * extension.
+ *
+ *   A bf16 [M][K], b uint8 [N][K/2], sfb uint8 [N][K/16] e4m3, scale2: as for
+ *   gemm_w4a16 (read);  C bf16 [M][N] (written; must not overlap A, b or sfb)
+ *   1 <= M <= 16; N >= 1 (any N), K >= 1, K % 256 == 0, at most 2^30 each; A, b and
+ *   sfb 16-byte, C 2-byte aligned.
+ * Errors: GEMM_ERR_NULL, _SHAPE, _ALIGN (also K % 256), _ALIAS, _ARCH, _LAUNCH,
+ * _NO_DEVICE, _CAPTURE.
+ */
+GB300GEMM_API int gemv_w4a16(const void* A, const void* b, const void* sfb, float scale2, void* C,
+                             int M, int N, int K, void* stream);
+
+/*
+ * gemv_w4a16_gated - the gated projection of few tokens with NVFP4 weights, both
+ * products, the activation and their product in one kernel:
+ *     H[m,f] = bf16( act( scale2_g sum_k A wg ) * ( scale2_u sum_k A wu ) )
+ *   with act as for gemm_bf16_nt_gated.
+ *
+ *   bg, sfg, scale2_g and bu, sfu, scale2_u: two weight matrices of [F][K] as for
+ *   gemv_w4a16 (read);  H bf16 [M][F] (written; must not overlap the inputs);
+ *   otherwise as gemv_w4a16 with N = F.
+ * Errors: as gemv_w4a16; GEMM_ERR_SHAPE also for an unknown act.
+ */
+GB300GEMM_API int gemv_w4a16_gated(const void* A, const void* bg, const void* sfg, float scale2_g,
+                                   const void* bu, const void* sfu, float scale2_u, void* H,
+                                   int act, int M, int F, int K, void* stream);
+
+/*
  * bf16_scaled_add - out[i] = bf16( float(out[i]) + scale * float(d[i]) ),
  * product and sum each rounded to FP32.  The second kernel of the unfused
  * LoRA pair (GEMM into a BF16 scratch, then this), kept as the baseline the

@@ -29,6 +29,7 @@ EXPORTS = ("gemm_bf16_nt", "gemm_bf16_nn", "gemm_bf16_nt_scaled_acc", "gemm_bf16
            "gemm_bf16_nt_splitk", "gemm_bf16_nt_streamk", "gemm_nvfp4_bs_splitk", "gemm_w4a16", "gemm_w4a16_t", "gemm_w4a16_ws",
            "gemm_bf16_nt_xent", "gemm_bf16_nt_xent_backward", "router_topk", "router_topk_backward",
            "gemm_bf16_nt_gated", "gemm_bf16_nt_gated_backward", "gemm_bf16_tn",
+           "residual_norm", "residual_norm_backward", "gemv_w4a16", "gemv_w4a16_gated",
            "bf16_scaled_add", "gemm_get_device_status", "gemm_selftest_wait_timeout",
            "gemm_testing_set_overrides", "gemm_status_string")
 
@@ -91,6 +92,12 @@ def load() -> ctypes.CDLL:
             lib.gemm_bf16_nt_gated_backward_workspace_bytes.argtypes = [i] * 3
             lib.gemm_bf16_nt_gated_backward_workspace_bytes.restype = ctypes.c_size_t
             lib.gemm_bf16_tn.argtypes = [vp] * 3 + [i] * 3 + [vp]
+            lib.residual_norm.argtypes = [vp] * 9 + [f] * 2 + [i] * 4 + [vp]
+            lib.residual_norm_backward.argtypes = [vp] * 15 + [ctypes.c_size_t, f] + [i] * 4 + [vp]
+            lib.residual_norm_backward_workspace_bytes.argtypes = [i] * 5
+            lib.residual_norm_backward_workspace_bytes.restype = ctypes.c_size_t
+            lib.gemv_w4a16.argtypes = [vp, vp, vp, f, vp, i, i, i, vp]
+            lib.gemv_w4a16_gated.argtypes = [vp, vp, vp, f, vp, vp, f, vp, i, i, i, i, vp]
             lib.gemm_get_device_status.argtypes = [vp]
             lib.gemm_selftest_wait_timeout.argtypes = [i, vp]
             lib.gemm_testing_set_overrides.argtypes = [i, i]
@@ -773,6 +780,230 @@ def gemm_bf16_tn(A: torch.Tensor, B: torch.Tensor, C: torch.Tensor | None = None
         _on_device("C", device, C, torch.bfloat16, (M, N))
     _run("gemm_bf16_tn", device, A.data_ptr(), B.data_ptr(), C.data_ptr(), M, N, K)
     return C
+
+
+class ResidualNorm(NamedTuple):
+    """What residual_norm returns; None for what the call has no use for."""
+    y: torch.Tensor
+    n: torch.Tensor | None
+    rstd_post: torch.Tensor | None
+    rstd_pre: torch.Tensor | None
+
+
+class ResidualNormGrads(NamedTuple):
+    """What residual_norm_backward returns; None for what it was not asked for."""
+    dx: torch.Tensor
+    dblock: torch.Tensor | None
+    dw_pre: torch.Tensor | None
+    dw_post: torch.Tensor | None
+    dgate: torch.Tensor | None
+
+
+def _stream_rows(t, name: str):
+    """(M, D, 1 if FP32) of the residual stream or its gradient."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"{name} must be bfloat16 or float32, got {t.dtype}")
+    _mat(t, t.dtype, name)
+    M, D = t.shape
+    if M > _INT_MAX or D > _INT_MAX:
+        raise ValueError(f"sizes past 2^31 - 1: M {M}, D {D}")
+    return M, D, 1 if t.dtype == torch.float32 else 0
+
+
+def _norm_inputs(M, D, device, block, w_post, gate, w_pre):
+    """Checks what residual_norm and its gradient share; rows per gate (M without one)."""
+    bf16 = torch.bfloat16
+    if block is None and (w_post is not None or gate is not None):
+        raise ValueError("w_post and gate belong to a block: give block")
+    if block is None and w_pre is None:
+        raise ValueError("neither a block nor w_pre: nothing to do")
+    if block is not None:
+        _on_device("block", device, block, bf16, (M, D))
+    if w_post is not None:
+        _on_device("w_post", device, w_post, bf16, (D,))
+    if w_pre is not None:
+        _on_device("w_pre", device, w_pre, bf16, (D,))
+    if gate is None:
+        return M
+    groups = 1
+    if isinstance(gate, torch.Tensor) and gate.dim() == 2:
+        groups = gate.shape[0]
+        if groups == 0 or M % groups:
+            raise ValueError(f"gate has {groups} rows, which do not divide {M}")
+    _on_device("gate", device, gate, bf16, (D,) if groups == 1 and gate.dim() == 1 else (groups, D))
+    return M // groups
+
+
+def residual_norm(x: torch.Tensor, block: torch.Tensor | None = None,
+                  w_post: torch.Tensor | None = None, gate: torch.Tensor | None = None,
+                  w_pre: torch.Tensor | None = None, scale: float = 1.0, eps: float = 1e-6,
+                  y: torch.Tensor | None = None, n: torch.Tensor | None = None,
+                  stream=None) -> ResidualNorm:
+    """The residual step between two blocks: y = x + scale * gate * norm(block, w_post) and
+    n = norm(y, w_pre), root-mean-square norms, in one pass.
+
+    x [M,D], the stream, bf16 or float32; block bf16 [M,D], or None: no block
+    yet (y is x); gate bf16 [D], or [G,D] with G a divisor of M: row m has gate
+    row m // (M // G); w_post, w_pre bf16 [D], or None: no such norm.  y may be
+    x: the stream is updated in place.
+    """
+    M, D, f32 = _stream_rows(x, "x")
+    device = x.device
+    rows = _norm_inputs(M, D, device, block, w_post, gate, w_pre)
+    if y is not None:
+        if block is None:
+            raise ValueError("without a block there is no y to write")
+        _on_device("y", device, y, x.dtype, (M, D))
+    if n is not None:
+        if w_pre is None:
+            raise ValueError("n needs w_pre")
+        _on_device("n", device, n, torch.bfloat16, (M, D))
+    elsewhere = _context(device, stream)
+    if elsewhere is not None:
+        with elsewhere:
+            return residual_norm(x, block, w_post, gate, w_pre, scale, eps, y, n)
+    empty, F32 = torch.empty, torch.float32
+    if y is None and block is not None:
+        y = empty((M, D), dtype=x.dtype, device=device)
+    if n is None and w_pre is not None:
+        n = empty((M, D), dtype=torch.bfloat16, device=device)
+    rstd_post = None if w_post is None else empty((M,), dtype=F32, device=device)
+    rstd_pre = None if w_pre is None else empty((M,), dtype=F32, device=device)
+    _run("residual_norm", device, x.data_ptr(), _ptr(block), _ptr(w_post), _ptr(gate), _ptr(w_pre),
+         _ptr(y), _ptr(n), _ptr(rstd_post), _ptr(rstd_pre), float(scale), float(eps), f32, M, D, rows)
+    return ResidualNorm(x if block is None else y, n, rstd_post, rstd_pre)
+
+
+def residual_norm_backward_workspace_bytes(M: int, D: int, rows_per_gate: int, weights: int,
+                                           gates: int) -> int:
+    if not (0 <= M <= _INT_MAX and 0 <= D <= _INT_MAX and 0 <= rows_per_gate <= _INT_MAX):
+        return 0
+    return int((_lib or load()).residual_norm_backward_workspace_bytes(M, D, rows_per_gate, weights,
+                                                                       gates))
+
+
+def residual_norm_backward(dy: torch.Tensor | None, dn: torch.Tensor | None,
+                           y: torch.Tensor | None, block: torch.Tensor | None = None,
+                           rstd_post: torch.Tensor | None = None,
+                           rstd_pre: torch.Tensor | None = None,
+                           w_post: torch.Tensor | None = None, gate: torch.Tensor | None = None,
+                           w_pre: torch.Tensor | None = None, scale: float = 1.0,
+                           dx: torch.Tensor | None = None, dblock: torch.Tensor | None = None,
+                           workspace: torch.Tensor | None = None, stream=None,
+                           need_dw: bool = True) -> ResidualNormGrads:
+    """Gradients of residual_norm from those of y (dy, None: zero) and n (dn, with w_pre).
+
+    y, rstd_post, rstd_pre: the forward call's; block, w_post, gate, w_pre and
+    scale as there.  The gradients of the weights and the gate are float32 of
+    the weights' and the gate's shape (need_dw False: none).  dx may be dy.
+    """
+    first = dy if dy is not None else y
+    M, D, f32 = _stream_rows(first, "dy" if dy is not None else "y")
+    device, bf16, F32 = first.device, torch.bfloat16, torch.float32
+    rows = _norm_inputs(M, D, device, block, w_post, gate, w_pre)
+    if (dn is None) != (w_pre is None):
+        raise ValueError("dn and w_pre belong together")
+    if dy is None and dn is None:
+        raise ValueError("neither dy nor dn: nothing to do")
+    if w_pre is not None:
+        _on_device("dn", device, dn, bf16, (M, D))
+        _on_device("y", device, y, first.dtype, (M, D))
+        _on_device("rstd_pre", device, rstd_pre, F32, (M,))
+    if w_post is not None:
+        _on_device("rstd_post", device, rstd_post, F32, (M,))
+    if dx is not None:
+        _on_device("dx", device, dx, first.dtype, (M, D))
+    if dblock is not None:
+        if block is None:
+            raise ValueError("without a block there is no dblock")
+        _on_device("dblock", device, dblock, bf16, (M, D))
+    elsewhere = _context(device, stream)
+    if elsewhere is not None:
+        with elsewhere:
+            return residual_norm_backward(dy, dn, y, block, rstd_post, rstd_pre, w_post, gate, w_pre,
+                                          scale, dx, dblock, workspace, need_dw=need_dw)
+    empty = torch.empty
+    if dx is None:
+        dx = empty((M, D), dtype=first.dtype, device=device)
+    if dblock is None and block is not None:
+        dblock = empty((M, D), dtype=bf16, device=device)
+    dw_post = empty((D,), dtype=F32, device=device) if need_dw and w_post is not None else None
+    dw_pre = empty((D,), dtype=F32, device=device) if need_dw and w_pre is not None else None
+    dgate = empty(gate.shape, dtype=F32, device=device) if need_dw and gate is not None else None
+    need = residual_norm_backward_workspace_bytes(M, D, rows, (dw_post is not None) + (dw_pre is not None),
+                                                  1 if dgate is not None else 0)
+    ws, nbytes, _alive = _workspace(workspace, need, device)
+    _run("residual_norm_backward", device, _ptr(dy), _ptr(dn), _ptr(y), _ptr(block),
+         _ptr(rstd_post) if w_post is not None else None, _ptr(rstd_pre) if w_pre is not None else None,
+         _ptr(w_post), _ptr(gate), _ptr(w_pre), dx.data_ptr(), _ptr(dblock), _ptr(dw_post),
+         _ptr(dgate), _ptr(dw_pre), ws, nbytes, float(scale), f32, M, D, rows)
+    return ResidualNormGrads(dx, dblock, dw_pre, dw_post, dgate)
+
+
+def _gemv_inputs(A, *weights):
+    """(M, N, K) of few tokens A and NVFP4 weight matrices of one shape: (b, sfb, names)."""
+    _mat(A, torch.bfloat16, "A")
+    M, K = A.shape
+    first = weights[0][0]
+    _mat(first, torch.uint8, weights[0][2])
+    N = first.shape[0]
+    if M > _INT_MAX or N > _INT_MAX or K > _INT_MAX:
+        raise ValueError(f"sizes past 2^31 - 1: M {M}, N {N}, K {K}")
+    if K % 256:
+        raise ValueError(f"K must be a multiple of 256, got {K}")
+    if not 1 <= M <= 16:
+        raise ValueError(f"1 to 16 tokens, got {M}: gemm_w4a16 takes more")
+    for b, sf, name_b, name_sf in weights:
+        _on_device(name_b, A.device, b, torch.uint8, (N, K // 2))
+        _on_device(name_sf, A.device, sf, torch.uint8, (N, K // 16))
+    return M, N, K
+
+
+def gemv_w4a16(A: torch.Tensor, b: torch.Tensor, sfb: torch.Tensor, scale2: float,
+               C: torch.Tensor | None = None, stream=None):
+    """gemm_w4a16 for 1 to 16 tokens: C = bf16(scale2 * (A . w^T)), w = e2m1(b) * e4m3(sfb).
+
+    A bf16 [M,K]; b uint8 [N,K/2] (low nibble = even k); sfb uint8 [N,K/16]; K a
+    multiple of 256, any N.
+    """
+    M, N, K = _gemv_inputs(A, (b, sfb, "b", "sfb"))
+    device = A.device
+    elsewhere = _context(device, stream)
+    if elsewhere is not None:
+        with elsewhere:
+            return gemv_w4a16(A, b, sfb, scale2, C)
+    if C is None:
+        C = torch.empty((M, N), dtype=torch.bfloat16, device=device)
+    else:
+        _on_device("C", device, C, torch.bfloat16, (M, N))
+    _run("gemv_w4a16", device, A.data_ptr(), b.data_ptr(), sfb.data_ptr(), float(scale2),
+         C.data_ptr(), M, N, K)
+    return C
+
+
+def gemv_w4a16_gated(A: torch.Tensor, bg: torch.Tensor, sfg: torch.Tensor, scale2_g: float,
+                     bu: torch.Tensor, sfu: torch.Tensor, scale2_u: float, act: str = "silu",
+                     H: torch.Tensor | None = None, stream=None):
+    """The gated projection of 1 to 16 tokens with NVFP4 weights, in one kernel:
+    H = bf16(act(scale2_g * (A . wg^T)) * (scale2_u * (A . wu^T))).
+
+    Both matrices as for gemv_w4a16, of one shape; act "silu" or "gelu_tanh".
+    """
+    M, F, K = _gemv_inputs(A, (bg, sfg, "bg", "sfg"), (bu, sfu, "bu", "sfu"))
+    kind, device = _activation(act), A.device
+    elsewhere = _context(device, stream)
+    if elsewhere is not None:
+        with elsewhere:
+            return gemv_w4a16_gated(A, bg, sfg, scale2_g, bu, sfu, scale2_u, act, H)
+    if H is None:
+        H = torch.empty((M, F), dtype=torch.bfloat16, device=device)
+    else:
+        _on_device("H", device, H, torch.bfloat16, (M, F))
+    _run("gemv_w4a16_gated", device, A.data_ptr(), bg.data_ptr(), sfg.data_ptr(), float(scale2_g),
+         bu.data_ptr(), sfu.data_ptr(), float(scale2_u), H.data_ptr(), kind, M, F, K)
+    return H
 
 
 def bf16_scaled_add(out: torch.Tensor, d: torch.Tensor, scale: float, stream=None):

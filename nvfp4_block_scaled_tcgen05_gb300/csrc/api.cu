@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <initializer_list>
 #include <mutex>
 
 #include "internal.h"
@@ -249,6 +250,36 @@ int check_gated(const void* X, const void* Wg, const void* Wu, int act, int M, i
   if (!aligned16(X) || !aligned16(Wg) || !aligned16(Wu)) return GEMM_ERR_ALIGN;
   if (F % 8 != 0 || K % 8 != 0) return GEMM_ERR_ALIGN;  // 16-byte row pitches
   return GEMM_OK;
+}
+
+// Shared checks of the residual step (the sizes; rows_per_gate where there is a gate).
+int check_norm(int M, int D, int rows_per_gate, bool gate) {
+  if (M <= 0 || M > kMaxDim || D <= 0 || D > kNormMaxD) return GEMM_ERR_SHAPE;
+  if (gate && (rows_per_gate <= 0 || M % rows_per_gate != 0)) return GEMM_ERR_SHAPE;
+  if (D % 8 != 0) return GEMM_ERR_ALIGN;  // 16-byte row pitches
+  return GEMM_OK;
+}
+
+// Shared checks of the few-token products; b[1] is NULL for a single matrix.
+int check_gemv(const GemvW4& a) {
+  const int n = a.b[1] || a.sf[1] ? 2 : 1;
+  if (!a.A || !a.C) return GEMM_ERR_NULL;
+  for (int i = 0; i < n; ++i)
+    if (!a.b[i] || !a.sf[i]) return GEMM_ERR_NULL;
+  if (a.M <= 0 || a.N <= 0 || a.K <= 0 || a.M > kGemvMaxM) return GEMM_ERR_SHAPE;
+  if (a.N > kMaxDim || a.K > kMaxDim) return GEMM_ERR_SHAPE;
+  if (n == 2 && a.act != GEMM_ACT_SILU && a.act != GEMM_ACT_GELU_TANH) return GEMM_ERR_SHAPE;
+  if (a.K % 256 != 0) return GEMM_ERR_ALIGN;  // 16-byte rows of the block scales
+  if (!aligned16(a.A) || !aligned(a.C, 2)) return GEMM_ERR_ALIGN;
+  const size_t rows = size_t(a.N), codes = rows * (size_t(a.K) / 2), scales = rows * (size_t(a.K) / 16);
+  Span in[5] = {{a.A, size_t(a.M) * a.K * 2}};
+  for (int i = 0; i < n; ++i) {
+    if (!aligned16(a.b[i]) || !aligned16(a.sf[i])) return GEMM_ERR_ALIGN;
+    in[1 + 2 * i] = {a.b[i], codes};
+    in[2 + 2 * i] = {a.sf[i], scales};
+  }
+  const Span out[] = {{a.C, size_t(a.M) * rows * 2}};
+  return any_overlap(in, 1 + 2 * n, out, 1) ? GEMM_ERR_ALIAS : GEMM_OK;
 }
 
 }  // namespace
@@ -658,6 +689,155 @@ int gemm_bf16_tn(const void* A, const void* B, void* C, int M, int N, int K, voi
   const int rc = current_device(&dev, stream);
   if (rc != GEMM_OK) return rc;
   return launch_gemm_bf16_tn(A, B, C, M, N, K, dev, static_cast<cudaStream_t>(stream));
+}
+
+int residual_norm(const void* x, const void* block, const void* w_post, const void* gate,
+                  const void* w_pre, void* y, void* n, float* rstd_post, float* rstd_pre,
+                  float scale, float eps, int x_f32, int M, int D, int rows_per_gate,
+                  void* stream) {
+  if (!x || (!block && !w_pre) || !block != !y || !w_pre != !n) return GEMM_ERR_NULL;
+  if ((!block && (w_post || gate)) || (!w_post && rstd_post) || (!w_pre && rstd_pre))
+    return GEMM_ERR_NULL;
+  int rc = check_norm(M, D, rows_per_gate, gate != nullptr);
+  if (rc != GEMM_OK) return rc;
+  if (!(eps >= 0.0f)) return GEMM_ERR_SHAPE;
+  for (const void* p : {x, block, w_post, gate, w_pre, static_cast<const void*>(y),
+                        static_cast<const void*>(n)})
+    if (!aligned16(p)) return GEMM_ERR_ALIGN;
+  if (!aligned(rstd_post, 4) || !aligned(rstd_pre, 4)) return GEMM_ERR_ALIGN;
+  const size_t md = size_t(M) * D, stream_bytes = md * (x_f32 ? 4 : 2), d2 = size_t(D) * 2;
+  const bool in_place = y == x;
+  const Span in[] = {{x, in_place ? 0 : stream_bytes},
+                     {block, block ? md * 2 : 0},
+                     {w_post, w_post ? d2 : 0},
+                     {gate, gate ? size_t(M / rows_per_gate) * d2 : 0},
+                     {w_pre, w_pre ? d2 : 0}};
+  const Span out[] = {{y, y ? stream_bytes : 0},
+                      {n, n ? md * 2 : 0},
+                      {rstd_post, rstd_post ? size_t(M) * 4 : 0},
+                      {rstd_pre, rstd_pre ? size_t(M) * 4 : 0}};
+  if (any_overlap(in, 5, out, 4)) return GEMM_ERR_ALIAS;
+  DeviceInfo dev;
+  if ((rc = current_device(&dev, stream)) != GEMM_OK) return rc;
+  const ResidualNorm a{x,     block, w_post,      gate, w_pre, y, n, rstd_post, rstd_pre,
+                       scale, eps,   x_f32 != 0,  M,    D,     gate ? rows_per_gate : M};
+  return launch_residual_norm(a, dev, static_cast<cudaStream_t>(stream));
+}
+
+size_t residual_norm_backward_workspace_bytes(int M, int D, int rows_per_gate, int weights,
+                                              int gates) {
+  if (check_norm(M, D, rows_per_gate, gates != 0) != GEMM_OK || weights < 0 || weights > 2) return 0;
+  return residual_norm_backward_workspace(M, D, gates ? rows_per_gate : M, weights, gates != 0);
+}
+
+int residual_norm_backward(const void* dy, const void* dn, const void* y, const void* block,
+                           const float* rstd_post, const float* rstd_pre, const void* w_post,
+                           const void* gate, const void* w_pre, void* dx, void* dblock,
+                           float* dw_post, float* dgate, float* dw_pre, void* workspace,
+                           size_t workspace_bytes, float scale, int x_f32, int M, int D,
+                           int rows_per_gate, void* stream) {
+  if (!dx || (!dy && !dn) || !block != !dblock || !w_pre != !dn) return GEMM_ERR_NULL;
+  if ((w_pre && (!y || !rstd_pre)) || (w_post && !rstd_post)) return GEMM_ERR_NULL;
+  if (!block && (w_post || gate)) return GEMM_ERR_NULL;
+  if ((dw_post && !w_post) || (dgate && !gate) || (dw_pre && !w_pre)) return GEMM_ERR_NULL;
+  int rc = check_norm(M, D, rows_per_gate, gate != nullptr);
+  if (rc != GEMM_OK) return rc;
+  const int weights = (dw_post != nullptr) + (dw_pre != nullptr);
+  const int per_gate = gate ? rows_per_gate : M;
+  const size_t need = residual_norm_backward_workspace(M, D, per_gate, weights, dgate != nullptr);
+  if (need && !workspace) return GEMM_ERR_NULL;
+  if (workspace_bytes < need) return GEMM_ERR_SHAPE;
+  if (!w_pre) y = nullptr;
+  for (const void* p : {dy, dn, y, block, w_post, gate, w_pre, static_cast<const void*>(dx),
+                        static_cast<const void*>(dblock), static_cast<const void*>(workspace),
+                        static_cast<const void*>(dw_post), static_cast<const void*>(dgate),
+                        static_cast<const void*>(dw_pre)})
+    if (!aligned16(p)) return GEMM_ERR_ALIGN;
+  if (!aligned(rstd_post, 4) || !aligned(rstd_pre, 4)) return GEMM_ERR_ALIGN;
+  const size_t md = size_t(M) * D, stream_bytes = md * (x_f32 ? 4 : 2), d2 = size_t(D) * 2;
+  const size_t groups = gate ? size_t(M / rows_per_gate) : 0;
+  const Span in[] = {{dy, dy && dy != dx ? stream_bytes : 0},
+                     {dn, dn ? md * 2 : 0},
+                     {y, y ? stream_bytes : 0},
+                     {block, block ? md * 2 : 0},
+                     {rstd_post, w_post ? size_t(M) * 4 : 0},
+                     {rstd_pre, w_pre ? size_t(M) * 4 : 0},
+                     {w_post, w_post ? d2 : 0},
+                     {gate, groups * d2},
+                     {w_pre, w_pre ? d2 : 0}};
+  const Span out[] = {{dx, stream_bytes},
+                      {dblock, dblock ? md * 2 : 0},
+                      {dw_post, dw_post ? d2 * 2 : 0},
+                      {dgate, dgate ? groups * d2 * 2 : 0},
+                      {dw_pre, dw_pre ? d2 * 2 : 0},
+                      {workspace, need}};
+  if (any_overlap(in, 9, out, 6)) return GEMM_ERR_ALIAS;
+  DeviceInfo dev;
+  if ((rc = current_device(&dev, stream)) != GEMM_OK) return rc;
+  ResidualNormBackward a{};
+  a.dy = dy;
+  a.dn = dn;
+  a.y = y;
+  a.block = block;
+  a.rstd_post = rstd_post;
+  a.rstd_pre = rstd_pre;
+  a.w_post = w_post;
+  a.gate = gate;
+  a.w_pre = w_pre;
+  a.dx = dx;
+  a.dblock = dblock;
+  a.dw_post = dw_post;
+  a.dgate = dgate;
+  a.dw_pre = dw_pre;
+  a.parts = static_cast<float*>(workspace);
+  a.scale = scale;
+  a.x_f32 = x_f32 != 0;
+  a.M = M;
+  a.D = D;
+  a.rows_per_gate = per_gate;
+  return launch_residual_norm_backward(a, dev, static_cast<cudaStream_t>(stream));
+}
+
+int gemv_w4a16(const void* A, const void* b, const void* sfb, float scale2, void* C, int M, int N,
+               int K, void* stream) {
+  GemvW4 a{};
+  a.A = A;
+  a.b[0] = static_cast<const uint8_t*>(b);
+  a.sf[0] = static_cast<const uint8_t*>(sfb);
+  a.scale2[0] = scale2;
+  a.C = C;
+  a.M = M;
+  a.N = N;
+  a.K = K;
+  int rc = check_gemv(a);
+  if (rc != GEMM_OK) return rc;
+  DeviceInfo dev;
+  if ((rc = current_device(&dev, stream)) != GEMM_OK) return rc;
+  return launch_gemv_w4a16(a, dev, static_cast<cudaStream_t>(stream));
+}
+
+int gemv_w4a16_gated(const void* A, const void* bg, const void* sfg, float scale2_g,
+                     const void* bu, const void* sfu, float scale2_u, void* H, int act, int M,
+                     int F, int K, void* stream) {
+  if (!bu || !sfu) return GEMM_ERR_NULL;
+  GemvW4 a{};
+  a.A = A;
+  a.b[0] = static_cast<const uint8_t*>(bg);
+  a.b[1] = static_cast<const uint8_t*>(bu);
+  a.sf[0] = static_cast<const uint8_t*>(sfg);
+  a.sf[1] = static_cast<const uint8_t*>(sfu);
+  a.scale2[0] = scale2_g;
+  a.scale2[1] = scale2_u;
+  a.C = H;
+  a.act = act;
+  a.M = M;
+  a.N = F;
+  a.K = K;
+  int rc = check_gemv(a);
+  if (rc != GEMM_OK) return rc;
+  DeviceInfo dev;
+  if ((rc = current_device(&dev, stream)) != GEMM_OK) return rc;
+  return launch_gemv_w4a16(a, dev, static_cast<cudaStream_t>(stream));
 }
 
 int bf16_scaled_add(void* out, const void* d, float scale, long n, void* stream) {

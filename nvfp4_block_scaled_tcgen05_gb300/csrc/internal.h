@@ -161,6 +161,45 @@ int launch_gated_backward(const GatedBackward& a, const DeviceInfo& dev, cudaStr
 int launch_gemm_bf16_tn(const void* A, const void* B, void* C, int M, int N, int K,
                         const DeviceInfo& dev, cudaStream_t stream);
 
+// Few tokens times NVFP4 weights (gemv_w4a16.cu), M <= kGemvMaxM; with b[1] the
+// gated form, act(scale2[0] A b0^T) * (scale2[1] A b1^T).
+constexpr int kGemvMaxM = 16;
+struct GemvW4 {
+  const void* A;
+  const uint8_t *b[2], *sf[2];
+  float scale2[2];
+  void* C;
+  int act, M, N, K;
+};
+int launch_gemv_w4a16(const GemvW4& a, const DeviceInfo& dev, cudaStream_t stream);
+
+// Residual step (residual_norm.cu): norm after a block, gate, residual scale, norm
+// before the next block.  D <= kNormMaxD, D % 8 == 0; rows_per_gate divides M.
+constexpr int kNormMaxD = 16384;
+struct ResidualNorm {
+  const void *x, *block, *w_post, *gate, *w_pre;  // all but x may be NULL
+  void *y, *n;
+  float *rstd_post, *rstd_pre;
+  float scale, eps;
+  int x_f32, M, D, rows_per_gate;
+};
+struct ResidualNormBackward {
+  const void *dy, *dn, *y, *block;
+  const float *rstd_post, *rstd_pre;
+  const void *w_post, *gate, *w_pre;
+  void *dx, *dblock;
+  float *dw_post, *dgate, *dw_pre;
+  float* parts;  // workspace
+  float scale;
+  int x_f32, M, D, rows_per_gate;
+  // set by the launcher: runs of rows, their parts' kinds, runs per gate group
+  int runs, rows_per_run, kinds, parts_per_gate;
+};
+size_t residual_norm_backward_workspace(int M, int D, int rows_per_gate, int weights, bool gates);
+int launch_residual_norm(const ResidualNorm& a, const DeviceInfo& dev, cudaStream_t stream);
+int launch_residual_norm_backward(const ResidualNormBackward& a, const DeviceInfo& dev,
+                                  cudaStream_t stream);
+
 // Routing step (router_topk.cu); limits: E <= kRouterMaxExperts, k <= 32.
 constexpr int kRouterMaxExperts = 1024;
 constexpr int kRouterMaxTopk = 32;

@@ -90,3 +90,122 @@ def check(got, want, bound, what):
         at = tuple(torch.nonzero(bad)[0].tolist())
         raise AssertionError(f"{what}: {int(bad.sum())} of {bad.numel()} out of bounds; first {at}: "
                              f"{float(got[at])} instead of {float(want[at])}, allowed {float(bound[at])}")
+
+
+# ------------------------------------------------------------------ residual step
+# A row's sum: a thread adds at most 32 terms, a warp's tree 5, the warps 16, all
+# FP32: below 2^-18 of the sum of magnitudes, products and a division included.
+ROW_SUM = 2.0 ** -18
+
+
+def half_step(dtype):
+    return torch.finfo(dtype).eps / 2
+
+
+def rows_of(gate, M):
+    g = gate.to(F64).reshape(-1, gate.shape[-1])
+    return g.repeat_interleave(M // g.shape[0], dim=0)
+
+
+def norm(x, block, w_post, gate, w_pre, scale, eps, stored):
+    """y, n, rstd_post, rstd_pre and the bounds of y, n; n is of the stream as `stored`."""
+    b, y, ey, r_post = None, x.to(F64), torch.zeros_like(x, dtype=F64), None
+    if block is not None:
+        c = block.to(F64)
+        if w_post is not None:
+            r_post = torch.rsqrt((c * c).mean(dim=1) + eps)
+            c = c * r_post[:, None] * w_post.to(F64)
+        if gate is not None:
+            c = c * rows_of(gate, x.shape[0])
+        # the norm's scale, then four products and a sum in FP32, then the stored type
+        y = y + scale * c
+        ey = (ROW_SUM + 2.0 ** -21) * (scale * c).abs() + (2.0 ** -24 + half_step(x.dtype)) * (y.abs() + (scale * c).abs() * 2.0 ** -17)
+    n = en = r_pre = None
+    if w_pre is not None:
+        s = stored.to(F64)
+        r_pre = torch.rsqrt((s * s).mean(dim=1) + eps)
+        n = s * r_pre[:, None] * w_pre.to(F64)
+        en = (ROW_SUM + 2.0 ** -22 + BF16_HALF) * n.abs()
+    return y, n, r_post, r_pre, ey, en
+
+
+def norm_backward(dy, dn, y, block, r_post, r_pre, w_post, gate, w_pre, scale, dtype):
+    """{name: (value, bound)} of residual_norm_backward."""
+    like = dy if dy is not None else y
+    M, D = like.shape
+    t = torch.zeros(M, D, dtype=F64, device=like.device) if dy is None else dy.to(F64)
+    mag, et, out = t.abs(), torch.zeros_like(t), {}
+    sums = (M / 300 + 64) * 2.0 ** -24  # rows of a run, the runs that a warp joins, the warps
+    e, yh, m1 = torch.zeros_like(t), torch.zeros_like(t), torch.zeros_like(t[:, :1])
+    abs_eyh = m1
+    if w_pre is not None:
+        r = r_pre.to(F64)[:, None]
+        yh, d = y.to(F64) * r, dn.to(F64)
+        out["dw_pre"] = ((d * yh).sum(dim=0), (sums + 2.0 ** -22) * (d * yh).abs().sum(dim=0))
+        e = d * w_pre.to(F64)
+        m1 = (e * yh).mean(dim=1, keepdim=True)
+        abs_eyh = (e * yh).abs().mean(dim=1, keepdim=True)
+        t = t + r * (e - yh * m1)
+        mag = mag + r * e.abs()
+        et = 2.0 ** -20 * (mag + r * (yh * m1).abs()) + r * yh.abs() * ROW_SUM * abs_eyh
+        e, m1, abs_eyh = r * e, r * m1, r * abs_eyh
+    out["dx"] = (t, et + half_step(dtype) * (t.abs() + et))
+    if block is None:
+        return out
+    g = torch.ones_like(t) if gate is None else rows_of(gate, M)
+    q = scale * g * t
+    eq = (scale * g).abs() * et + 2.0 ** -21 * q.abs()
+    bh, w = block.to(F64), torch.ones_like(t[0])
+    if w_post is not None:
+        r, w = r_post.to(F64)[:, None], w_post.to(F64)
+        bh = bh * r
+        p = (scale * g * w * bh).abs()
+        m2 = (q * w * bh).mean(dim=1, keepdim=True)
+        e_m2 = 2 * ROW_SUM * ((p * mag).mean(dim=1, keepdim=True) +
+                              (m1.abs() + abs_eyh) * (p * yh.abs()).mean(dim=1, keepdim=True))
+        db = r * (q * w - bh * m2)
+        edb = r * (w.abs() * eq + bh.abs() * e_m2) + 2.0 ** -20 * r * ((q * w).abs() + (bh * m2).abs())
+        out["dw_post"] = ((q * bh).sum(dim=0), (sums + 2.0 ** -21) * (q * bh).abs().sum(dim=0) + (bh.abs() * eq).sum(dim=0))
+    else:
+        db, edb = q, eq
+    out["dblock"] = (db, edb + BF16_HALF * (db.abs() + edb))
+    if gate is not None:
+        c = bh * w
+        groups = gate.reshape(-1, D).shape[0]
+        shape = (groups, M // groups, D)
+        v = scale * t * c
+        ev = (sums + 2.0 ** -21) * v.abs() + abs(scale) * c.abs() * et
+        # a group whole within a run: its rows are added one after the other
+        ev = ev + M / groups * 2.0 ** -24 * v.abs() if groups > 1 else ev
+        out["dgate"] = (v.reshape(shape).sum(dim=1).reshape(gate.shape), ev.reshape(shape).sum(dim=1).reshape(gate.shape))
+    return out
+
+
+# ------------------------------------------------------------------ 4-bit weights
+def nvfp4_weights(b, sf):
+    """e2m1 * e4m3 in 64 bits, decoded from the formats' fields."""
+    codes = torch.stack([b % 16, b // 16], dim=2).reshape(b.shape[0], -1).long()
+    m, e, s = codes % 2, codes // 2 % 4, 1 - 2 * (codes // 8)
+    value = s.to(F64) * torch.where(e > 0, (1 + m.to(F64) / 2) * 2.0 ** (e.to(F64) - 1), m.to(F64) / 2)
+    f = sf.long()
+    fm, fe, fs = f % 8, f // 8 % 16, 1 - 2 * (f // 128)
+    scale = fs.to(F64) * torch.where(fe > 0, (1 + fm.to(F64) / 8) * 2.0 ** (fe.to(F64) - 7), fm.to(F64) * 2.0 ** -9)
+    scale = torch.where(f % 128 == 127, torch.full_like(scale, float("nan")), scale)
+    return value * scale.repeat_interleave(16, dim=1)
+
+
+def few_tokens(A, b, sf, scale2):
+    """(scale2 A w^T, error bound of its FP32 form)."""
+    w, a = nvfp4_weights(b, sf), A.to(F64)
+    v = scale2 * (a @ w.T)
+    # the accumulator, the halves and splits of K, the scale
+    return v, acc_bound(A.shape[1] + 16 * 20, abs(scale2) * (a.abs() @ w.abs().T)) + 2.0 ** -23 * v.abs()
+
+
+def few_tokens_gated(A, bg, sfg, s_g, bu, sfu, s_u, kind):
+    (G, eg), (U, eu) = few_tokens(A, bg, sfg, s_g), few_tokens(A, bu, sfu, s_u)
+    a, _ = act(G, kind)
+    ea = SLOPE_MAX * eg + ACT_REL * G.abs()
+    H = a * U
+    eh = ea * (U.abs() + eu) + a.abs() * eu + 2.0 ** -23 * H.abs()
+    return H, eh * (1 + BF16_HALF) + BF16_HALF * H.abs()

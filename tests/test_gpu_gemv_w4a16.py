@@ -1,0 +1,84 @@
+"""Products of 1 to 16 tokens with NVFP4 weights, plain and gated, against 64-bit
+references and against gemm_w4a16."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+import feed_forward_ref as ref
+
+pytestmark = pytest.mark.gpu
+BF16 = torch.bfloat16
+
+
+@pytest.fixture(scope="module")
+def g():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import __graft_entry__
+    __graft_entry__.build()
+    import nvfp4_block_scaled_tcgen05_gb300 as g
+    yield g
+    assert g.gemm_get_device_status() == 0
+
+
+def weights(N, K, seed):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    b = torch.randint(0, 256, (N, K // 2), generator=gen, device="cuda", dtype=torch.uint8)
+    # every e4m3 value but NaN, both signs
+    sf = torch.randint(0, 127, (N, K // 16), generator=gen, device="cuda", dtype=torch.uint8)
+    sf += 128 * torch.randint(0, 2, (N, K // 16), generator=gen, device="cuda", dtype=torch.uint8)
+    return b, sf
+
+
+def tokens(M, K, seed):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randn(M, K, generator=gen, device="cuda").to(BF16)
+
+
+# rows: one, a tile's edges, more than a wave of blocks; K: the least, odd multiples, past a chunk
+SIZES = [(1, 1, 256), (1, 8, 256), (2, 15, 512), (3, 16, 768), (5, 17, 256), (7, 63, 1280), (8, 64, 2048), (9, 65, 2304), (1, 2048, 11008),
+         (16, 127, 16384), (11, 130, 3328), (15, 1000, 4096), (4, 10008, 512), (16, 20000, 768), (12, 33, 256)]
+
+
+@pytest.mark.parametrize("M,N,K", SIZES)
+def test_plain(g, M, N, K):
+    A, (b, sf) = tokens(M, K, 1), weights(N, K, 2)
+    want, e = ref.few_tokens(A, b, sf, 0.37)
+    ref.check(g.gemv_w4a16(A, b, sf, 0.37), want, e * (1 + ref.BF16_HALF) + ref.BF16_HALF * want.abs(), "C")
+
+
+@pytest.mark.parametrize("kind", ["silu", "gelu_tanh"])
+@pytest.mark.parametrize("M,F,K", SIZES)
+def test_gated(g, M, F, K, kind):
+    A, (bg, sfg), (bu, sfu) = tokens(M, K, 3), weights(F, K, 4), weights(F, K, 5)
+    s_g, s_u = 0.01 / K ** 0.5, -0.02 / K ** 0.5
+    want, e = ref.few_tokens_gated(A, bg, sfg, s_g, bu, sfu, s_u, kind)
+    ref.check(g.gemv_w4a16_gated(A, bg, sfg, s_g, bu, sfu, s_u, act=kind), want, e, "H")
+
+
+@pytest.mark.parametrize("M", range(1, 17))
+def test_exact_sums(g, M):
+    """Small whole numbers: every sum is exact, so the result is the rounded one."""
+    K, N = 1536, 200
+    gen = torch.Generator(device="cuda").manual_seed(M)
+    A = torch.randint(-4, 5, (M, K), generator=gen, device="cuda").to(BF16)
+    b = torch.randint(0, 256, (N, K // 2), generator=gen, device="cuda", dtype=torch.uint8)
+    sf = torch.randint(5, 9, (N, K // 16), generator=gen, device="cuda", dtype=torch.uint8) * 8  # 2^-2 .. 2
+    want = (A.to(ref.F64) @ ref.nvfp4_weights(b, sf).T).to(torch.float32).to(BF16)
+    got = g.gemv_w4a16(A, b, sf, 1.0)
+    assert torch.equal(got, want)
+    if N % 8 == 0:
+        assert torch.equal(g.gemm_w4a16(A, b, sf, 1.0), want)
+
+
+def test_nonfinite_values_stay_in_their_rows(g):
+    A, (b, sf) = tokens(3, 512, 6), weights(40, 512, 7)
+    clean = g.gemv_w4a16(A, b, sf, 1.0)
+    A[1, 7] = float("inf")
+    sf[5, 3] = 0x7F
+    got = g.gemv_w4a16(A, b, sf, 1.0)
+    assert got[:, 5].isnan().all()
+    keep = [n for n in range(40) if n != 5]
+    assert torch.equal(got[0, keep], clean[0, keep]) and torch.equal(got[2, keep], clean[2, keep])
+    assert not got[1].isfinite().any()
