@@ -192,8 +192,8 @@ struct ResidualNormBackward {
   float* parts;  // workspace
   float scale;
   int x_f32, M, D, rows_per_gate;
-  // set by the launcher: runs of rows, their parts' kinds, runs per gate group
-  int runs, rows_per_run, kinds, parts_per_gate;
+  // set by the launcher: rows of a unit's run, parts' kinds, blocks per gate group
+  int rows_per_run, kinds, parts_per_gate;
 };
 size_t residual_norm_backward_workspace(int M, int D, int rows_per_gate, int weights, bool gates);
 int launch_residual_norm(const ResidualNorm& a, const DeviceInfo& dev, cudaStream_t stream);

@@ -2,432 +2,751 @@
 //   c = b * r(b) * w_post      (norm after the block; c = b without w_post)
 //   y = x + scale * gate * c   (rounded to the stream's type)
 //   n = y * r(y) * w_pre       (norm before the next block, of y as it is stored)
-// and its gradient, from dy (at y) and dn (at n):
-//   t  = dy + r_y (dn w_pre - yh mean(dn w_pre yh)),   yh = y r_y      dx = t
-//   q  = scale * gate * t * w_post,                    bh = b r_b
-//   db = r_b (q - bh mean(q bh))
+// and its gradient, from dy (at y) and dn (at n), with yh = y r_y, bh = b r_b:
+//   t  = dy + r_y (dn w_pre - yh mean(dn w_pre yh)),                  dx = t
+//   db = r_b (p t - bh mean(p t bh)),  p = scale * gate * w_post
 //   dw_pre = sum dn yh,  dw_post = sum scale gate t bh,  dgate = sum scale t bh w_post
-// The second mean needs t, which needs the first: with q = p t, p = scale gate w_post,
-//   sum q bh = sum p bh (dy + r_y dn w_pre) - r_y mean(dn w_pre yh) sum p bh yh,
-// so one joint reduction of three sums serves both.
+// The second mean needs t, which needs the first; with u = dy + r_y dn w_pre,
+//   sum p t bh = sum p bh u - r_y mean(dn w_pre yh) sum p bh yh,
+// so one joint reduction of three sums serves both.  dw_post and dgate are both
+// multiples of T = sum t bh over a gate group's rows, the one sum that is kept.
 //
 // Bound by memory: forward x, b read and y, n written once, backward dy, dn, y, b
-// read and dx, db written once; a row lives in registers between its read and its
-// write.  Sums are FP32 in a fixed order (results repeat bit for bit).
+// read and dx, db written once.  A unit of warps takes a row at a time; the rows
+// ahead are on their way into its ring in shared memory by bulk copies, so that the
+// bytes in flight do not depend on how many threads wait.  Sums are FP32 in a fixed
+// order (results repeat bit for bit).
 #include <algorithm>
 
-#include "epilogue_math.cuh"
 #include "chain.cuh"
+#include "epilogue_math.cuh"
 
 namespace gb300 {
 
 namespace {
 
-// Eight values of a row.
+// Eight values of a row, two FP32 operations per instruction.
 struct Vec8 {
-  float v[8];
+  float2 v[4];
 };
-
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ Vec8 zero8() {
+  Vec8 r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r.v[i] = make_float2(0.0f, 0.0f);
+  return r;
+}
 __device__ __forceinline__ Vec8 unpack8(uint4 a) {
   Vec8 r;
   const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    r.v[2 * i] = bf16_lo(w[i]);
-    r.v[2 * i + 1] = bf16_hi(w[i]);
-  }
+  for (int i = 0; i < 4; ++i) r.v[i] = make_float2(bf16_lo(w[i]), bf16_hi(w[i]));
   return r;
 }
 __device__ __forceinline__ uint4 pack8(const Vec8& a) {
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    w[i] = pack_bf16x2(__float_as_uint(a.v[2 * i]), __float_as_uint(a.v[2 * i + 1]));
+    w[i] = pack_bf16x2(__float_as_uint(a.v[i].x), __float_as_uint(a.v[i].y));
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// What a thread has read of eight values of the stream (BF16 or FP32).
+// Eight values of the stream, BF16 or FP32, as they lie in memory.
 template <bool kF32>
 struct Raw8;
 template <>
 struct Raw8<false> {
   uint4 a;
-  __device__ __forceinline__ void load(const void* p, size_t i) {
-    a = __ldcg(reinterpret_cast<const uint4*>(p) + i);
+  __device__ __forceinline__ void read(const uint8_t* row, int c) {
+    a = reinterpret_cast<const uint4*>(row)[c];
   }
   __device__ __forceinline__ Vec8 get() const { return unpack8(a); }
 };
 template <>
 struct Raw8<true> {
-  float4 a, b;
-  __device__ __forceinline__ void load(const void* p, size_t i) {
-    a = __ldcg(reinterpret_cast<const float4*>(p) + 2 * i);
-    b = __ldcg(reinterpret_cast<const float4*>(p) + 2 * i + 1);
+  Vec8 a;
+  __device__ __forceinline__ void read(const uint8_t* row, int c) {
+    const float4 lo = reinterpret_cast<const float4*>(row)[2 * c];
+    const float4 hi = reinterpret_cast<const float4*>(row)[2 * c + 1];
+    a.v[0] = make_float2(lo.x, lo.y);
+    a.v[1] = make_float2(lo.z, lo.w);
+    a.v[2] = make_float2(hi.x, hi.y);
+    a.v[3] = make_float2(hi.z, hi.w);
   }
-  __device__ __forceinline__ Vec8 get() const { return {{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}}; }
+  __device__ __forceinline__ Vec8 get() const { return a; }
 };
-// Stores eight values and returns them as they are stored.
+// Stores piece i of eight values and returns them as they are stored.
 template <bool kF32>
 __device__ __forceinline__ Vec8 store8(void* p, size_t i, const Vec8& v) {
   if constexpr (kF32) {
-    reinterpret_cast<float4*>(p)[2 * i] = make_float4(v.v[0], v.v[1], v.v[2], v.v[3]);
-    reinterpret_cast<float4*>(p)[2 * i + 1] = make_float4(v.v[4], v.v[5], v.v[6], v.v[7]);
+    float4* q = static_cast<float4*>(p) + 2 * i;
+    q[0] = make_float4(v.v[0].x, v.v[0].y, v.v[1].x, v.v[1].y);
+    q[1] = make_float4(v.v[2].x, v.v[2].y, v.v[3].x, v.v[3].y);
     return v;
   } else {
     const uint4 w = pack8(v);
-    reinterpret_cast<uint4*>(p)[i] = w;
+    static_cast<uint4*>(p)[i] = w;
     return unpack8(w);
   }
 }
-
-// Sums of N values over the block's threads; every thread gets them.  `part`
-// holds N floats per warp and is free again after the next barrier.
-template <int N>
-__device__ __forceinline__ void block_sum(float (&s)[N], float* part) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-    for (int k = 0; k < N; ++k) s[k] += __shfl_xor_sync(0xffffffffu, s[k], o);
-  const int warps = int(blockDim.x) >> 5;
-  if (warps == 1) return;
-  const int warp = int(threadIdx.x) >> 5;
-  if ((threadIdx.x & 31) == 0)
-#pragma unroll
-    for (int k = 0; k < N; ++k) part[warp * N + k] = s[k];
-  __syncthreads();
-#pragma unroll
-  for (int k = 0; k < N; ++k) s[k] = 0.0f;
-  for (int w = 0; w < warps; ++w)
-#pragma unroll
-    for (int k = 0; k < N; ++k) s[k] += part[w * N + k];
+__device__ __forceinline__ Vec8 weights8(const void* w, size_t i) {
+  return unpack8(__ldg(static_cast<const uint4*>(w) + i));
 }
 
 __device__ __forceinline__ float inverse_rms(float sum, int D, float eps) {
   return 1.0f / sqrtf(sum / float(D) + eps);
 }
 
+// How a kernel's blocks are laid out: `units` of `warps` warps each, a unit with a
+// ring of `stages` rows of stage_bytes; a thread has V pieces of eight values.
+struct Shape {
+  int V, warps, units, stages, ctas;
+  int stage_bytes;
+  int threads() const { return 32 * warps * units; }
+  int smem() const { return 128 + units * stages * (stage_bytes + 8); }
+};
+
+constexpr int kMaxWarps = 16;  // of a unit: D = 16384 with V = 4
+
+// Rows of up to four matrices through a unit's ring.
+struct Source {
+  const void* p;
+  uint32_t bytes;  // per row; 0: no such matrix
+};
+template <int N>
+struct Ring {
+  Source src[N];
+  uint8_t* mem;
+  uint32_t bars, base;
+  int stage_bytes, stages, unit, warps, tid;
+  int next_stage, stage;
+  uint32_t phase;
+  Watch w;
+
+  // `smem`: the block's dynamic shared memory.  Every thread of the block calls it.
+  __device__ __forceinline__ void init(uint8_t* smem, const Shape& s, unsigned int* status,
+                                       unsigned long long timeout_ns) {
+    volatile uint32_t* abort = reinterpret_cast<volatile uint32_t*>(smem);
+    warps = s.warps;
+    stages = s.stages;
+    stage_bytes = s.stage_bytes;
+    unit = int(threadIdx.x) / (32 * warps);
+    tid = int(threadIdx.x) - unit * 32 * warps;
+    const uint32_t at = ptx::smem_u32(smem);
+    mem = smem + 128 + size_t(unit) * stages * stage_bytes;
+    base = ptx::smem_u32(mem);
+    bars = at + 128 + s.units * stages * stage_bytes + unit * stages * 8;
+    if (tid == 0)
+      for (int i = 0; i < stages; ++i) ptx::mbar_init(bars + 8 * i, 1);
+    if (threadIdx.x == 0) *abort = 0u;
+    ptx::fence_mbar_init();
+    __syncthreads();
+    w = Watch{abort, status, timeout_ns};
+    next_stage = stage = 0;
+    phase = 0;
+  }
+  // The unit's first thread: the row's copies into the next stage.
+  __device__ __forceinline__ void fill(int row) {
+    uint32_t total = 0, dst = base + uint32_t(next_stage) * stage_bytes;
+#pragma unroll
+    for (int i = 0; i < N; ++i) total += src[i].bytes;
+    const uint32_t bar = bars + 8 * next_stage;
+    ptx::mbar_arrive_expect_tx(bar, total);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (src[i].bytes) {
+        ptx::bulk_load(dst, static_cast<const uint8_t*>(src[i].p) + size_t(row) * src[i].bytes,
+                       src[i].bytes, bar);
+        dst += src[i].bytes;
+      }
+    if (++next_stage == stages) next_stage = 0;
+  }
+  // Waits for the current stage.  A wait that runs out is recorded and the kernel
+  // goes on over what is there (every thread makes the same steps either way).
+  __device__ __forceinline__ const uint8_t* wait() {
+    wait_bar(bars + 8 * stage, phase, w, 12);
+    return mem + size_t(stage) * stage_bytes;
+  }
+  __device__ __forceinline__ void advance() {
+    if (++stage == stages) {
+      stage = 0;
+      phase ^= 1u;
+    }
+  }
+  // After a wait that ran out: time for the copies in flight to land.
+  __device__ __forceinline__ void settle() const {
+    if (*w.abort) spin_ns(2000000ull);
+  }
+  __device__ __forceinline__ void sync() const {
+    if (warps == 1) __syncwarp();
+    else ptx::named_barrier(1 + unit, 32 * warps);
+  }
+  // Sums of K values over the unit; every thread gets them.  A barrier of the unit's
+  // threads lies within.  `part`: K floats per warp, free again two calls later.
+  template <int K>
+  __device__ __forceinline__ void sum(float (&s)[K], float* part) const {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+      for (int k = 0; k < K; ++k) s[k] += __shfl_xor_sync(0xffffffffu, s[k], o);
+    if (warps == 1) {
+      __syncwarp();
+      return;
+    }
+    if ((tid & 31) == 0)
+#pragma unroll
+      for (int k = 0; k < K; ++k) part[k * kMaxWarps + (tid >> 5)] = s[k];
+    sync();
+    // every warp adds the parts in the same tree
+    const int lane = tid & 31;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      s[k] = lane < warps ? part[k * kMaxWarps + lane] : 0.0f;
+#pragma unroll
+      for (int o = kMaxWarps / 2; o > 0; o >>= 1) s[k] += __shfl_xor_sync(0xffffffffu, s[k], o);
+      s[k] = __shfl_sync(0xffffffffu, s[k], 0);
+    }
+  }
+};
+
 // ---------------------------------------------------------------- forward
-template <bool kF32, int V>
-__global__ void __launch_bounds__(512)
-    residual_norm_kernel(const ResidualNorm a) {
-  __shared__ float part[2][32];
+template <bool kF32, int V, int kThreads>
+__global__ void __launch_bounds__(kThreads, kThreads <= 288 ? 2 : 1)
+    residual_norm_kernel(const ResidualNorm a, const Shape shape, unsigned int* status,
+                         unsigned long long timeout_ns) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ float parts[8][2][2][kMaxWarps];
+  Ring<2> ring;
+  ring.src[0] = {a.x, uint32_t(a.D) * (kF32 ? 4u : 2u)};
+  ring.src[1] = {a.block, a.block ? uint32_t(a.D) * 2u : 0u};
+  ring.init(smem, shape, status, timeout_ns);
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
-  const int pieces = a.D / 8;
-  for (int row = int(blockIdx.x); row < a.M; row += int(gridDim.x)) {
-    const size_t base = size_t(row) * pieces;
-    Vec8 y[V];
-    uint4 b[V];
+  const int pieces = a.D / 8, step = int(gridDim.x) * shape.units, threads = 32 * shape.warps;
+  const int first = int(blockIdx.x) * shape.units + ring.unit;
+  if (ring.tid == 0)
+    for (int i = 0, row = first; i < shape.stages && row < a.M; ++i, row += step) ring.fill(row);
+  uint4 w_post[V], w_pre[V], gate[V];
+  auto read_weights = [&](const void* p, uint4 (&w)[V]) {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int c = int(threadIdx.x) + i * int(blockDim.x);
-      y[i] = Vec8{};
+      const int c = ring.tid + i * threads;
+      w[i] = p && c < pieces ? __ldg(static_cast<const uint4*>(p) + c) : make_uint4(0, 0, 0, 0);
+    }
+  };
+  read_weights(a.w_post, w_post);
+  read_weights(a.w_pre, w_pre);
+  int gate_row = -1;
+  float(*part)[2][kMaxWarps] = parts[ring.unit];
+  int odd = 0;
+  for (int row = first; row < a.M; row += step, odd ^= 1) {
+    const size_t base = size_t(row) * pieces;
+    if (a.gate && row / a.rows_per_gate != gate_row) {
+      gate_row = row / a.rows_per_gate;
+      read_weights(static_cast<const uint16_t*>(a.gate) + size_t(gate_row) * a.D, gate);
+    }
+    const uint8_t* mem = ring.wait();
+    Vec8 y[V];
+    uint4 b[V];
+    float2 s2 = both(0.0f);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = ring.tid + i * threads;
+      y[i] = zero8();
       b[i] = make_uint4(0, 0, 0, 0);
       if (c < pieces) {
         Raw8<kF32> x;
-        x.load(a.x, base + c);
-        if (a.block) b[i] = __ldcg(static_cast<const uint4*>(a.block) + base + c);
+        x.read(mem, c);
         y[i] = x.get();
+        if (a.block) b[i] = reinterpret_cast<const uint4*>(mem + ring.src[0].bytes)[c];
       }
+      const Vec8 v = unpack8(b[i]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s2 = ptx::fma2(v.v[j], v.v[j], s2);
     }
+    // the row is in registers: after the next barrier its stage takes another
+    ptx::fence_proxy_async_smem();
+    const int ahead = row + shape.stages * step;
+    const bool refill = ring.tid == 0 && ahead < a.M && ahead > row;
     float r = 1.0f;
     if (a.w_post) {
-      float s[1] = {0.0f};
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const Vec8 v = unpack8(b[i]);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) s[0] += v.v[j] * v.v[j];
-      }
-      block_sum(s, part[0]);
+      float s[1] = {s2.x + s2.y};
+      ring.sum(s, part[odd][0]);
+      if (refill) ring.fill(ahead);
       r = inverse_rms(s[0], a.D, a.eps);
-      if (threadIdx.x == 0 && a.rstd_post) a.rstd_post[row] = r;
+      if (ring.tid == 0 && a.rstd_post) a.rstd_post[row] = r;
     }
-    float s[1] = {0.0f};
+    s2 = both(0.0f);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int c = int(threadIdx.x) + i * int(blockDim.x);
+      const int c = ring.tid + i * threads;
       if (c >= pieces) break;
       if (a.block) {
-        const Vec8 v = unpack8(b[i]);
-        const Vec8 w = a.w_post ? unpack8(__ldg(static_cast<const uint4*>(a.w_post) + c)) : Vec8{};
-        const Vec8 g = a.gate ? unpack8(__ldg(static_cast<const uint4*>(a.gate) +
-                                              size_t(row / a.rows_per_gate) * pieces + c))
-                              : Vec8{};
+        Vec8 v = unpack8(b[i]);
+        if (a.w_post) {
+          const Vec8 w = unpack8(w_post[i]);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          float u = v.v[j];
-          if (a.w_post) u *= r * w.v[j];
-          if (a.gate) u *= g.v[j];
-          y[i].v[j] += a.scale * u;
+          for (int j = 0; j < 4; ++j) v.v[j] = ptx::mul2(ptx::mul2(v.v[j], both(r)), w.v[j]);
         }
+        if (a.gate) {
+          const Vec8 w = unpack8(gate[i]);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v.v[j] = ptx::mul2(v.v[j], w.v[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[i].v[j] = ptx::fma2(both(a.scale), v.v[j], y[i].v[j]);
         y[i] = store8<kF32>(a.y, base + c, y[i]);
       }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) s[0] += y[i].v[j] * y[i].v[j];
+      for (int j = 0; j < 4; ++j) s2 = ptx::fma2(y[i].v[j], y[i].v[j], s2);
     }
     if (a.w_pre) {
-      block_sum(s, part[1]);
+      float s[1] = {s2.x + s2.y};
+      ring.sum(s, part[odd][1]);
+      if (refill && !a.w_post) ring.fill(ahead);
       const float ry = inverse_rms(s[0], a.D, a.eps);
-      if (threadIdx.x == 0 && a.rstd_pre) a.rstd_pre[row] = ry;
+      if (ring.tid == 0 && a.rstd_pre) a.rstd_pre[row] = ry;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        const int c = int(threadIdx.x) + i * int(blockDim.x);
+        const int c = ring.tid + i * threads;
         if (c >= pieces) break;
-        const Vec8 w = unpack8(__ldg(static_cast<const uint4*>(a.w_pre) + c));
-        Vec8 n;
+        const Vec8 w = unpack8(w_pre[i]);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) n.v[j] = y[i].v[j] * ry * w.v[j];
-        static_cast<uint4*>(a.n)[base + c] = pack8(n);
+        for (int j = 0; j < 4; ++j) y[i].v[j] = ptx::mul2(ptx::mul2(y[i].v[j], both(ry)), w.v[j]);
+        static_cast<uint4*>(a.n)[base + c] = pack8(y[i]);
       }
+    } else if (!a.w_post) {
+      ring.sync();
+      if (refill) ring.fill(ahead);
     }
-    __syncthreads();  // `part` is free for the next row
+    ring.advance();
   }
+  ring.settle();
 }
 
 // ---------------------------------------------------------------- backward
-// Rows are divided among the blocks in runs; a run lies within one gate group, or
-// holds whole groups.  A thread keeps its columns' weight gradients of the run in
-// registers and writes them to the block's place in the workspace; dgate of groups
-// that lie within a run goes straight to the output.
-template <bool kF32, int V>
-__global__ void __launch_bounds__(512)
-    residual_norm_backward_kernel(const ResidualNormBackward a) {
-  __shared__ float part[2][3 * 32];
+// Each unit takes a run of consecutive rows.  Where a gate's gradient is summed and
+// its rows are many, a block's runs lie within one gate group (parts_per_gate blocks
+// to a group); else a run holds whole groups and writes their dgate itself.  A
+// thread keeps its columns' sums of the run in registers; a block's units are added
+// in order and go to the block's place in the workspace, [block][kinds][D]: dn yh,
+// and T, which the join multiplies, or (several gate groups in a run, kMulti) dw_post.
+template <bool kF32, int V, int kThreads, bool kMulti>
+__global__ void __launch_bounds__(kThreads, kThreads <= 288 ? 2 : 1)
+    residual_norm_backward_kernel(const ResidualNormBackward a, const Shape shape,
+                                  unsigned int* status, unsigned long long timeout_ns) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ float parts[8][2][3 * kMaxWarps];
+  Ring<4> ring;
+  const uint32_t wide = uint32_t(a.D) * (kF32 ? 4u : 2u), narrow = uint32_t(a.D) * 2u;
+  ring.src[0] = {a.dy, a.dy ? wide : 0u};
+  ring.src[1] = {a.y, a.w_pre ? wide : 0u};
+  ring.src[2] = {a.dn, a.w_pre ? narrow : 0u};
+  ring.src[3] = {a.block, a.block ? narrow : 0u};
+  ring.init(smem, shape, status, timeout_ns);
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
-  const int pieces = a.D / 8;
-  const int run = int(blockIdx.x);
-  int row0, row1;
-  if (a.parts_per_gate) {  // a run is a part of one group
-    const int group = run / a.parts_per_gate, k = run % a.parts_per_gate;
-    row0 = group * a.rows_per_gate + k * a.rows_per_run;
-    row1 = min(row0 + a.rows_per_run, (group + 1) * a.rows_per_gate);
-  } else {
-    row0 = run * a.rows_per_run;
-    row1 = min(row0 + a.rows_per_run, a.M);
-  }
-  Vec8 dwi[V], dwo[V], dg[V];
-#pragma unroll
-  for (int i = 0; i < V; ++i) dwi[i] = dwo[i] = dg[i] = Vec8{};
-  int buf = 0;
-  for (int row = row0; row < row1; ++row) {
-    const size_t base = size_t(row) * pieces;
-    const float ry = a.w_pre ? a.rstd_pre[row] : 0.0f;
-    const float rb = a.w_post ? a.rstd_post[row] : 1.0f;
-    Vec8 t[V], yh[V], bh[V], p[V];
-    float s[3] = {0.0f, 0.0f, 0.0f};
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int c = int(threadIdx.x) + i * int(blockDim.x);
-      t[i] = yh[i] = bh[i] = p[i] = Vec8{};
-      if (c >= pieces) continue;
-      if (a.dy) {
-        Raw8<kF32> r;
-        r.load(a.dy, base + c);
-        t[i] = r.get();
-      }
-      if (a.w_pre) {
-        Raw8<kF32> r;
-        r.load(a.y, base + c);
-        yh[i] = r.get();
-        const Vec8 d = unpack8(__ldcg(static_cast<const uint4*>(a.dn) + base + c));
-        const Vec8 w = unpack8(__ldg(static_cast<const uint4*>(a.w_pre) + c));
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          yh[i].v[j] *= ry;
-          dwi[i].v[j] += d.v[j] * yh[i].v[j];
-          const float e = d.v[j] * w.v[j];
-          s[0] += e * yh[i].v[j];
-          t[i].v[j] += ry * e;
-        }
-      }
-      if (a.block) {
-        bh[i] = unpack8(__ldcg(static_cast<const uint4*>(a.block) + base + c));
-        const Vec8 w = a.w_post ? unpack8(__ldg(static_cast<const uint4*>(a.w_post) + c)) : Vec8{};
-        const Vec8 g = a.gate ? unpack8(__ldg(static_cast<const uint4*>(a.gate) +
-                                              size_t(row / a.rows_per_gate) * pieces + c))
-                              : Vec8{};
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          float f = a.scale;
-          if (a.gate) f *= g.v[j];
-          p[i].v[j] = f;
-          if (a.w_post) {
-            bh[i].v[j] *= rb;
-            s[1] += f * w.v[j] * bh[i].v[j] * t[i].v[j];
-            s[2] += f * w.v[j] * bh[i].v[j] * yh[i].v[j];
-          }
-        }
-      }
+  const int pieces = a.D / 8, threads = 32 * shape.warps;
+  int row, end;
+  {
+    int first, last;  // the block's rows
+    if (a.parts_per_gate) {
+      const int group = int(blockIdx.x) / a.parts_per_gate, k = int(blockIdx.x) % a.parts_per_gate;
+      first = group * a.rows_per_gate + k * a.rows_per_run * shape.units;
+      last = (group + 1) * a.rows_per_gate;
+    } else {
+      first = int(blockIdx.x) * a.rows_per_run * shape.units;
+      last = a.M;
     }
-    if (a.w_pre || a.w_post) block_sum(s, part[buf]);
-    buf ^= 1;
-    const float m1 = ry * s[0] / float(a.D);
-    const float m2 = (s[1] - m1 * s[2]) / float(a.D);
-    const bool flush = a.dgate && !a.parts_per_gate && (row + 1) % a.rows_per_gate == 0;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int c = int(threadIdx.x) + i * int(blockDim.x);
-      if (c >= pieces) break;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) t[i].v[j] -= m1 * yh[i].v[j];
-      store8<kF32>(a.dx, base + c, t[i]);
-      if (a.block) {
-        const Vec8 w = a.w_post ? unpack8(__ldg(static_cast<const uint4*>(a.w_post) + c)) : Vec8{};
-        Vec8 db;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float dc = p[i].v[j] * t[i].v[j];  // at the norm's output
-          const float cv = a.w_post ? bh[i].v[j] * w.v[j] : bh[i].v[j];
-          dg[i].v[j] += a.scale * t[i].v[j] * cv;
-          if (a.w_post) {
-            dwo[i].v[j] += dc * bh[i].v[j];
-            db.v[j] = rb * (dc * w.v[j] - bh[i].v[j] * m2);
-          } else {
-            db.v[j] = dc;
-          }
-        }
-        static_cast<uint4*>(a.dblock)[base + c] = pack8(db);
-        if (flush) {
-          store8<true>(a.dgate, size_t(row / a.rows_per_gate) * pieces + c, dg[i]);
-          dg[i] = Vec8{};
-        }
-      }
-    }
+    row = min(first + ring.unit * a.rows_per_run, last);
+    end = min(row + a.rows_per_run, last);
   }
-  // the run's parts: [run][kinds][D]
-  const int kinds = a.kinds;
+  const int begin = row;
+  if (ring.tid == 0)
+    for (int i = 0; i < shape.stages && row + i < end; ++i) ring.fill(row + i);
+  uint4 w_pre[V];
+  Vec8 dwi[V], T[V], dwo[kMulti ? V : 1];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    const int c = int(threadIdx.x) + i * int(blockDim.x);
-    if (c >= pieces) break;
-    size_t at = size_t(run) * kinds * pieces + c;
-    if (a.dw_pre) {
-      store8<true>(a.parts, at, dwi[i]);
-      at += pieces;
+    const int c = ring.tid + i * threads;
+    w_pre[i] = a.w_pre && c < pieces ? __ldg(static_cast<const uint4*>(a.w_pre) + c)
+                                     : make_uint4(0, 0, 0, 0);
+    dwi[i] = T[i] = zero8();
+    if constexpr (kMulti) dwo[i] = zero8();
+  }
+  // scale times the gate's row `at`, and a value times w_post, eight columns each
+  auto scale_gate = [&](int at, int c) {
+    Vec8 f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) f.v[j] = both(a.scale);
+    if (a.gate) {
+      const Vec8 g = weights8(static_cast<const uint16_t*>(a.gate) + size_t(at) * a.D, c);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) f.v[j] = ptx::mul2(f.v[j], g.v[j]);
     }
-    if (a.dw_post) {
-      store8<true>(a.parts, at, dwo[i]);
-      at += pieces;
+    return f;
+  };
+  auto times_w = [&](Vec8 f, int c) {
+    if (a.w_post) {
+      const Vec8 w = weights8(a.w_post, c);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) f.v[j] = ptx::mul2(f.v[j], w.v[j]);
     }
-    if (a.dgate && a.parts_per_gate) store8<true>(a.parts, at, dg[i]);
+    return f;
+  };
+  Vec8 p[V];
+  int gate_row = -1;
+  auto read_gate = [&](int at) {
+    gate_row = at;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = ring.tid + i * threads;
+      p[i] = a.block && c < pieces ? times_w(scale_gate(at, c), c) : zero8();
+    }
+  };
+  if (!kMulti) read_gate(row < end ? row / a.rows_per_gate : 0);
+  float(*part)[3 * kMaxWarps] = parts[ring.unit];
+  float ry = 0.0f, rb = 1.0f;
+  auto read_rstd = [&](int at) {
+    if (a.w_pre) ry = __ldg(a.rstd_pre + at);
+    if (a.w_post) rb = __ldg(a.rstd_post + at);
+  };
+  if (row < end) read_rstd(row);
+  int odd = 0;
+  for (; row < end; ++row, odd ^= 1) {
+    const size_t base = size_t(row) * pieces;
+    if (kMulti && row / a.rows_per_gate != gate_row) read_gate(row / a.rows_per_gate);
+    const float r_y = ry, r_b = rb;
+    const uint8_t* mem = ring.wait();
+    if (row + 1 < end) read_rstd(row + 1);  // a row ahead
+    const uint8_t *mem_y = mem + (a.dy ? wide : 0u), *mem_n = mem_y + wide;
+    const uint8_t* mem_b = a.w_pre ? mem_n + narrow : mem_y;
+    Vec8 u[V];
+    float2 s0 = both(0.0f), s1 = s0, s2 = s0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = ring.tid + i * threads;
+      u[i] = zero8();
+      if (c >= pieces) continue;
+      Vec8 yh = zero8();
+      if (a.dy) {
+        Raw8<kF32> d;
+        d.read(mem, c);
+        u[i] = d.get();
+      }
+      if (a.w_pre) {
+        Raw8<kF32> y;
+        y.read(mem_y, c);
+        yh = y.get();
+        const Vec8 d = unpack8(reinterpret_cast<const uint4*>(mem_n)[c]), w = unpack8(w_pre[i]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          yh.v[j] = ptx::mul2(yh.v[j], both(r_y));
+          dwi[i].v[j] = ptx::fma2(d.v[j], yh.v[j], dwi[i].v[j]);
+          const float2 e = ptx::mul2(d.v[j], w.v[j]);
+          s0 = ptx::fma2(e, yh.v[j], s0);
+          u[i].v[j] = ptx::fma2(e, both(r_y), u[i].v[j]);
+        }
+      }
+      if (a.w_post) {
+        const Vec8 b = unpack8(reinterpret_cast<const uint4*>(mem_b)[c]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          // p bh, its factor r_b left for the sums
+          const float2 pb = ptx::mul2(p[i].v[j], b.v[j]);
+          s1 = ptx::fma2(pb, u[i].v[j], s1);
+          s2 = ptx::fma2(pb, yh.v[j], s2);
+        }
+      }
+    }
+    // Behind the next barrier every thread is done with the previous row, whose stage
+    // then takes another (with one stage: at the end of the row).
+    ptx::fence_proxy_async_smem();
+    float s[3] = {s0.x + s0.y, s1.x + s1.y, s2.x + s2.y};
+    if (a.w_pre || a.w_post) ring.sum(s, part[odd]);
+    else ring.sync();
+    if (ring.tid == 0 && shape.stages > 1 && row > begin && shape.stages - 1 < end - row)
+      ring.fill(row - 1 + shape.stages);
+    const float m1 = r_y * s[0] / float(a.D);  // r_y mean(dn w_pre yh)
+    const float m2 = r_b * (s[1] - m1 * s[2]) / float(a.D);
+    const float2 ny = both(-m1 * r_y), nb = both(-m2 * r_b * r_b);
+    const bool last = kMulti && ((row + 1) % a.rows_per_gate == 0 || row + 1 == end);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = ring.tid + i * threads;
+      if (c >= pieces) break;
+      if (a.w_pre) {
+        Raw8<kF32> y;
+        y.read(mem_y, c);
+        const Vec8 v = y.get();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) u[i].v[j] = ptx::fma2(v.v[j], ny, u[i].v[j]);
+      }
+      store8<kF32>(a.dx, base + c, u[i]);
+      if (a.block) {
+        const Vec8 b = unpack8(reinterpret_cast<const uint4*>(mem_b)[c]);
+        Vec8 db;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          T[i].v[j] = ptx::fma2(u[i].v[j], ptx::mul2(b.v[j], both(r_b)), T[i].v[j]);
+          db.v[j] = ptx::mul2(p[i].v[j], u[i].v[j]);
+          if (a.w_post) db.v[j] = ptx::fma2(b.v[j], nb, ptx::mul2(db.v[j], both(r_b)));
+        }
+        static_cast<uint4*>(a.dblock)[base + c] = pack8(db);
+        if (last) {  // the gate group's end
+          const Vec8 f = scale_gate(gate_row, c);
+          Vec8 dg;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) dg.v[j] = ptx::mul2(both(a.scale), T[i].v[j]);
+          dg = times_w(dg, c);
+          if (a.dgate) store8<true>(a.dgate, size_t(gate_row) * pieces + c, dg);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if constexpr (kMulti) dwo[i].v[j] = ptx::fma2(f.v[j], T[i].v[j], dwo[i].v[j]);
+            T[i].v[j] = make_float2(0.0f, 0.0f);
+          }
+        }
+      }
+    }
+    if (shape.stages == 1 && row + 1 < end) {
+      ptx::fence_proxy_async_smem();
+      ring.sync();
+      if (ring.tid == 0) ring.fill(row + 1);
+    }
+    ring.advance();
+  }
+  ring.settle();
+  if (a.kinds == 0) return;
+  // the block's sums; the units after the first hand theirs over in the rings' place,
+  // free once every unit is done
+  __syncthreads();
+  float* hand = reinterpret_cast<float*>(smem + 128);
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    if (k == 0 ? !a.dw_pre : a.kinds == (a.dw_pre != nullptr)) continue;
+    Vec8 (&v)[V] = *reinterpret_cast<Vec8(*)[V]>(k == 0 ? dwi : kMulti ? dwo : T);
+    if (ring.unit > 0)
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int c = ring.tid + i * threads;
+        if (c < pieces) store8<true>(hand, size_t(ring.unit - 1) * pieces + c, v[i]);
+      }
+    __syncthreads();
+    if (ring.unit == 0)
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int c = ring.tid + i * threads;
+        if (c >= pieces) continue;
+        for (int n = 1; n < shape.units; ++n) {
+          Raw8<true> other;
+          other.read(reinterpret_cast<const uint8_t*>(hand), (n - 1) * pieces + c);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[i].v[j] = ptx::add2(v[i].v[j], other.a.v[j]);
+        }
+        const int kind = k == 0 || !a.dw_pre ? 0 : 1;
+        store8<true>(a.parts, (size_t(blockIdx.x) * a.kinds + kind) * pieces + c, v[i]);
+      }
+    __syncthreads();
   }
 }
 
-// Sums the runs' parts in order.  blockIdx.y: dw_pre, dw_post (all runs), then the
-// gate's groups (each its own runs).  A block takes 32 columns; 8 warps share the
-// runs and are joined in a fixed order.
-constexpr int kJoinWarps = 8;
+// Adds the blocks' parts in a fixed order.  A block takes 32 columns; blockIdx.y 0:
+// dw_pre (or, without it, what 1 does); 1: dw_post and dgate, from T of each gate
+// group's parts, or dw_post from its own parts (multi).  The warps share a group's
+// parts where there are many, else whole groups.
+constexpr int kJoinWarps = 16;
 __global__ void __launch_bounds__(32 * kJoinWarps)
-    residual_norm_join_kernel(const ResidualNormBackward a) {
+    residual_norm_join_kernel(const ResidualNormBackward a, int blocks, int multi) {
   __shared__ float sum[kJoinWarps][32];
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
-  const int norms = (a.dw_pre != nullptr) + (a.dw_post != nullptr);
-  const int kind = min(int(blockIdx.y), norms), group = int(blockIdx.y) - norms;
-  float* out = kind == norms ? a.dgate + size_t(group) * a.D
-                             : (kind == 0 && a.dw_pre ? a.dw_pre : a.dw_post);
-  const int first = kind == norms ? group * a.parts_per_gate : 0;
-  const int count = kind == norms ? a.parts_per_gate : a.runs;
-  const int col = int(blockIdx.x) * 32 + int(threadIdx.x & 31), warp = int(threadIdx.x) >> 5;
-  float s = 0.0f;
-  if (col < a.D) {
-    const float* src = a.parts + (size_t(first) * a.kinds + kind) * a.D + col;
-    const size_t step = size_t(a.kinds) * a.D;
-#pragma unroll 4
-    for (int r = warp; r < count; r += kJoinWarps) s += __ldcg(src + r * step);
+  const int lane = int(threadIdx.x) & 31, warp = int(threadIdx.x) >> 5;
+  const int col = int(blockIdx.x) * 32 + lane;
+  const bool live = col < a.D;
+  const int kind = int(blockIdx.y);
+  const size_t step = size_t(a.kinds) * a.D;
+  const float* src = a.parts + size_t(kind) * a.D + col;
+  auto range = [&](int from, int to, int by) {
+    float s = 0.0f;
+    if (live) {
+#pragma unroll 8
+      for (int r = from; r < to; r += by) s += __ldcg(src + size_t(r) * step);
+    }
+    return s;
+  };
+  // the warps' values, added in order; warp 0 gets the sum
+  auto join = [&](float s) {
+    __syncthreads();
+    sum[warp][lane] = s;
+    __syncthreads();
+    if (warp == 0)
+      for (int w = 1; w < kJoinWarps; ++w) s += sum[w][lane];
+    return s;
+  };
+  if ((kind == 0 && a.dw_pre) || multi) {
+    const float s = join(range(warp, blocks, kJoinWarps));
+    if (warp == 0 && live) (kind == 0 && a.dw_pre ? a.dw_pre : a.dw_post)[col] = s;
+    return;
   }
-  sum[warp][threadIdx.x & 31] = s;
-  __syncthreads();
-  if (warp == 0 && col < a.D) {
-#pragma unroll
-    for (int w = 1; w < kJoinWarps; ++w) s += sum[w][threadIdx.x];
-    out[col] = s;
-  }
-}
-
-// Threads of a row: 8 V values each.
-struct RowShape {
-  int threads, V;
-};
-RowShape row_shape(int D, int most_threads, int most_v) {
-  const int pieces = D / 8;
-  int v = 1;
-  while (v < most_v && (pieces + v - 1) / v > most_threads / 2) v *= 2;
-  const int threads = ((pieces + v - 1) / v + 31) / 32 * 32;
-  return {threads, v};
-}
-
-// Backward: runs of rows, about two per SM.
-constexpr int kRuns = 304;
-struct RunPlan {
-  int runs, rows_per_run, kinds, parts_per_gate;
-};
-RunPlan make_runs(int M, int rows_per_gate, int weights, bool gates) {
-  RunPlan q{};
-  q.kinds = weights;
-  int rows = (M + kRuns - 1) / kRuns;
-  if (gates && rows_per_gate >= rows) {
-    const int parts = (rows_per_gate + rows - 1) / rows;
-    rows = (rows_per_gate + parts - 1) / parts;
-    q.parts_per_gate = (rows_per_gate + rows - 1) / rows;
-    q.runs = M / rows_per_gate * q.parts_per_gate;
-    ++q.kinds;
+  const int per = a.parts_per_gate ? a.parts_per_gate : blocks, groups = blocks / per;
+  const float w = live && a.w_post ? __uint_as_float(uint32_t(__ldg(static_cast<const uint16_t*>(a.w_post) + col)) << 16) : 1.0f;
+  float dwo = 0.0f;
+  auto group_done = [&](int g, float s) {
+    if (!live) return;
+    if (a.dgate) a.dgate[size_t(g) * a.D + col] = a.scale * w * s;
+    const float f = a.gate ? __uint_as_float(uint32_t(__ldg(static_cast<const uint16_t*>(a.gate) + size_t(g) * a.D + col)) << 16) : 1.0f;
+    dwo += a.scale * f * s;
+  };
+  if (per >= kJoinWarps) {
+    for (int g = 0; g < groups; ++g) {
+      const float s = join(range(g * per + warp, (g + 1) * per, kJoinWarps));
+      if (warp == 0) group_done(g, s);
+    }
   } else {
+    for (int g = warp; g < groups; g += kJoinWarps) group_done(g, range(g * per, (g + 1) * per, 1));
+    dwo = join(dwo);
+  }
+  if (warp == 0 && live && a.dw_post) a.dw_post[col] = dwo;
+}
+
+// ---------------------------------------------------------------- host
+// A row of D / 8 pieces: a warp or more with one, two or (past 8192 values) four
+// pieces a thread.  Two blocks per SM where their registers allow (up to 288
+// threads), each with about 100 KB of rows on their way.
+Shape make_shape(int D, int row_bytes) {
+  Shape s{};
+  const int pieces = D / 8;
+  s.V = pieces <= 32 ? 1 : pieces <= 1024 ? 2 : 4;
+  s.warps = (pieces + 32 * s.V - 1) / (32 * s.V);
+  s.units = std::max(1, 8 / s.warps);
+  s.stage_bytes = (row_bytes + 127) / 128 * 128;
+  const bool two = s.threads() <= 288;
+  const int room = two ? 104 << 10 : 208 << 10;
+  s.stages = std::min(8, std::max(1, room / (s.units * (s.stage_bytes + 8))));
+  s.ctas = two ? 304 : 152;
+  return s;
+}
+
+// How the backward pass's rows are divided; depends on the sizes alone.
+struct RunPlan {
+  int blocks, rows_per_run, parts_per_gate;
+  bool multi;
+};
+RunPlan make_runs(int M, int rows_per_gate, bool gates, const Shape& s) {
+  RunPlan q{};
+  const int most = s.ctas * s.units;
+  int rows = (M + most - 1) / most;
+  const int per_block = rows * s.units;
+  // one group for all rows needs no care
+  if (rows_per_gate >= M) {
+    q.blocks = (M + per_block - 1) / per_block;
+  } else if (gates && rows_per_gate >= per_block) {
+    q.parts_per_gate = (rows_per_gate + per_block - 1) / per_block;
+    const int units = q.parts_per_gate * s.units;
+    rows = (rows_per_gate + units - 1) / units;
+    q.parts_per_gate = (rows_per_gate + rows * s.units - 1) / (rows * s.units);
+    q.blocks = M / rows_per_gate * q.parts_per_gate;
+  } else {
+    q.multi = true;
     if (gates) rows = (rows + rows_per_gate - 1) / rows_per_gate * rows_per_gate;
-    q.runs = (M + rows - 1) / rows;
+    q.blocks = (M + rows * s.units - 1) / (rows * s.units);
   }
   q.rows_per_run = rows;
   return q;
 }
 
+template <class Kernel, class... Args>
+int launch_rows(Kernel kernel, const Shape& s, int blocks, std::atomic<int> (&ready)[64],
+                const DeviceInfo& dev, cudaStream_t stream, Args... args) {
+  if (!ready[dev.device & 63].load()) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 220 << 10) !=
+        cudaSuccess) {
+      cudaGetLastError();
+      return GEMM_ERR_LAUNCH;
+    }
+    ready[dev.device & 63].store(1);
+  }
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(s.threads());
+  cfg.dynamicSmemBytes = s.smem();
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kernel, args..., s, dev.status, wait_timeout_ns()) != cudaSuccess) {
+    cudaGetLastError();
+    return GEMM_ERR_LAUNCH;
+  }
+  return GEMM_OK;
+}
+
+template <bool kF32, int V, int kThreads>
+int run_forward(const ResidualNorm& a, const Shape& s, const DeviceInfo& dev, cudaStream_t stream) {
+  static std::atomic<int> ready[64];
+  const int blocks = std::min((a.M + s.units - 1) / s.units, s.ctas);
+  return launch_rows(residual_norm_kernel<kF32, V, kThreads>, s, blocks, ready, dev, stream, a);
+}
+
+template <bool kF32, int V, int kThreads, bool kMulti>
+int run_backward(const ResidualNormBackward& a, const Shape& s, int blocks, const DeviceInfo& dev,
+                 cudaStream_t stream) {
+  static std::atomic<int> ready[64];
+  return launch_rows(residual_norm_backward_kernel<kF32, V, kThreads, kMulti>, s, blocks, ready, dev,
+                     stream, a);
+}
+
+int backward_row_bytes(int D, bool f32, bool dy, bool pre, bool block) {
+  const int wide = D * (f32 ? 4 : 2);
+  return (dy ? wide : 0) + (pre ? wide + 2 * D : 0) + (block ? 2 * D : 0);
+}
+
 }  // namespace
 
+// The shape's units and blocks do not depend on the stages, so the matrices that a
+// call has make no difference here.
 size_t residual_norm_backward_workspace(int M, int D, int rows_per_gate, int weights, bool gates) {
-  const RunPlan q = make_runs(M, rows_per_gate, weights, gates);
-  return size_t(q.runs) * q.kinds * D * sizeof(float);
+  const Shape s = make_shape(D, 128);
+  const RunPlan q = make_runs(M, rows_per_gate, gates, s);
+  return size_t(q.blocks) * (weights + (gates && !q.multi)) * D * sizeof(float);
 }
 
 int launch_residual_norm(const ResidualNorm& a, const DeviceInfo& dev, cudaStream_t stream) {
-  const RowShape s = row_shape(a.D, 1024, 4);
-  const int per_sm = std::max(1, 2048 / s.threads);
-  const dim3 grid(std::min(a.M, dev.num_sms * per_sm));
-  auto go = [&](auto kernel) { return launch_dependent(kernel, grid, s.threads, stream, a); };
-  if (a.x_f32)
-    return s.V == 1 ? go(residual_norm_kernel<true, 1>)
-                    : s.V == 2 ? go(residual_norm_kernel<true, 2>) : go(residual_norm_kernel<true, 4>);
-  return s.V == 1 ? go(residual_norm_kernel<false, 1>)
-                  : s.V == 2 ? go(residual_norm_kernel<false, 2>) : go(residual_norm_kernel<false, 4>);
+  const Shape s = make_shape(a.D, a.D * (a.x_f32 ? 4 : 2) + (a.block ? 2 * a.D : 0));
+  auto go = [&](auto f32) {
+    constexpr bool kF32 = decltype(f32)::value;
+    if (s.V == 1) return run_forward<kF32, 1, 256>(a, s, dev, stream);
+    if (s.V == 4) return run_forward<kF32, 4, 512>(a, s, dev, stream);
+    return s.threads() <= 256   ? run_forward<kF32, 2, 256>(a, s, dev, stream)
+           : s.threads() <= 288 ? run_forward<kF32, 2, 288>(a, s, dev, stream)
+                                : run_forward<kF32, 2, 512>(a, s, dev, stream);
+  };
+  return a.x_f32 ? go(std::true_type{}) : go(std::false_type{});
 }
 
 int launch_residual_norm_backward(const ResidualNormBackward& args, const DeviceInfo& dev,
                                   cudaStream_t stream) {
   ResidualNormBackward a = args;
-  const int weights = (a.dw_pre != nullptr) + (a.dw_post != nullptr);
-  const RunPlan q = make_runs(a.M, a.rows_per_gate, weights, a.dgate != nullptr);
-  a.runs = q.runs;
+  const Shape s = make_shape(a.D, backward_row_bytes(a.D, a.x_f32, a.dy, a.w_pre, a.block));
+  const RunPlan q = make_runs(a.M, a.rows_per_gate, a.dgate != nullptr, s);
   a.rows_per_run = q.rows_per_run;
-  a.kinds = q.kinds;
   a.parts_per_gate = q.parts_per_gate;
-  const RowShape s = row_shape(a.D, 1024, 4);
-  (void)dev;
-  auto go = [&](auto kernel) {
-    return launch_dependent(kernel, dim3(a.runs), s.threads, stream, a);
+  a.kinds = (a.dw_pre != nullptr) + (a.dw_post != nullptr || (a.dgate && !q.multi));
+  auto go = [&](auto f32, auto multi) {
+    constexpr bool kF32 = decltype(f32)::value, kMulti = decltype(multi)::value;
+    if (s.V == 1) return run_backward<kF32, 1, 256, kMulti>(a, s, q.blocks, dev, stream);
+    if (s.V == 4) return run_backward<kF32, 4, 512, kMulti>(a, s, q.blocks, dev, stream);
+    return s.threads() <= 256   ? run_backward<kF32, 2, 256, kMulti>(a, s, q.blocks, dev, stream)
+           : s.threads() <= 288 ? run_backward<kF32, 2, 288, kMulti>(a, s, q.blocks, dev, stream)
+                                : run_backward<kF32, 2, 512, kMulti>(a, s, q.blocks, dev, stream);
   };
-  int rc;
-  if (a.x_f32)
-    rc = s.V == 1 ? go(residual_norm_backward_kernel<true, 1>)
-                  : s.V == 2 ? go(residual_norm_backward_kernel<true, 2>)
-                             : go(residual_norm_backward_kernel<true, 4>);
-  else
-    rc = s.V == 1 ? go(residual_norm_backward_kernel<false, 1>)
-                  : s.V == 2 ? go(residual_norm_backward_kernel<false, 2>)
-                             : go(residual_norm_backward_kernel<false, 4>);
-  const int joins = weights + (a.parts_per_gate ? a.M / a.rows_per_gate : 0);
-  if (rc != GEMM_OK || joins == 0) return rc;
-  return launch_dependent(residual_norm_join_kernel, dim3((a.D + 31) / 32, joins), 32 * kJoinWarps,
-                          stream, a);
+  const int rc = a.x_f32 ? (q.multi ? go(std::true_type{}, std::true_type{}) : go(std::true_type{}, std::false_type{}))
+                         : (q.multi ? go(std::false_type{}, std::true_type{}) : go(std::false_type{}, std::false_type{}));
+  if (rc != GEMM_OK || a.kinds == 0) return rc;
+  return launch_dependent(residual_norm_join_kernel, dim3((a.D + 31) / 32, a.kinds),
+                          32 * kJoinWarps, stream, a, q.blocks, int(q.multi));
 }
 
 }  // namespace gb300
