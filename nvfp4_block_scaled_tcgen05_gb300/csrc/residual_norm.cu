@@ -100,7 +100,7 @@ __device__ __forceinline__ float inverse_rms(float sum, int D, float eps) {
 // How a kernel's blocks are laid out: `units` of `warps` warps each, a unit with a
 // ring of `stages` rows of stage_bytes; a thread has V pieces of eight values.
 struct Shape {
-  int V, warps, units, stages, ctas;
+  int V, warps, units, stages;
   int stage_bytes;
   int threads() const { return 32 * warps * units; }
   int smem() const { return 128 + units * stages * (stage_bytes + 8); }
@@ -211,11 +211,11 @@ struct Ring {
 
 // ---------------------------------------------------------------- forward
 template <bool kF32, int V, int kThreads>
-__global__ void __launch_bounds__(kThreads, kThreads <= 288 ? 2 : 1)
+__global__ void __launch_bounds__(kThreads, 1)
     residual_norm_kernel(const ResidualNorm a, const Shape shape, unsigned int* status,
                          unsigned long long timeout_ns) {
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ float parts[8][2][2][kMaxWarps];
+  __shared__ float parts[kMaxWarps][2][2][kMaxWarps];
   Ring<2> ring;
   ring.src[0] = {a.x, uint32_t(a.D) * (kF32 ? 4u : 2u)};
   ring.src[1] = {a.block, a.block ? uint32_t(a.D) * 2u : 0u};
@@ -332,11 +332,11 @@ __global__ void __launch_bounds__(kThreads, kThreads <= 288 ? 2 : 1)
 // in order and go to the block's place in the workspace, [block][kinds][D]: dn yh,
 // and T, which the join multiplies, or (several gate groups in a run, kMulti) dw_post.
 template <bool kF32, int V, int kThreads, bool kMulti>
-__global__ void __launch_bounds__(kThreads, kThreads <= 288 ? 2 : 1)
+__global__ void __launch_bounds__(kThreads, 1)
     residual_norm_backward_kernel(const ResidualNormBackward a, const Shape shape,
                                   unsigned int* status, unsigned long long timeout_ns) {
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ float parts[8][2][3 * kMaxWarps];
+  __shared__ float parts[kMaxWarps][2][3 * kMaxWarps];
   Ring<4> ring;
   const uint32_t wide = uint32_t(a.D) * (kF32 ? 4u : 2u), narrow = uint32_t(a.D) * 2u;
   ring.src[0] = {a.dy, a.dy ? wide : 0u};
@@ -611,19 +611,18 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
 
 // ---------------------------------------------------------------- host
 // A row of D / 8 pieces: a warp or more with one, two or (past 8192 values) four
-// pieces a thread.  Two blocks per SM where their registers allow (up to 288
-// threads), each with about 100 KB of rows on their way.
+// pieces a thread.  One block per SM, as many units as 16 warps hold (18, for rows
+// of nine warps, whose single unit would leave half of the SM waiting at barriers),
+// about 200 KB of rows on their way.
+constexpr int kBlocks = 152;
 Shape make_shape(int D, int row_bytes) {
   Shape s{};
   const int pieces = D / 8;
   s.V = pieces <= 32 ? 1 : pieces <= 1024 ? 2 : 4;
   s.warps = (pieces + 32 * s.V - 1) / (32 * s.V);
-  s.units = std::max(1, 8 / s.warps);
+  s.units = s.warps == 9 ? 2 : std::max(1, kMaxWarps / s.warps);
   s.stage_bytes = (row_bytes + 127) / 128 * 128;
-  const bool two = s.threads() <= 288;
-  const int room = two ? 104 << 10 : 208 << 10;
-  s.stages = std::min(8, std::max(1, room / (s.units * (s.stage_bytes + 8))));
-  s.ctas = two ? 304 : 152;
+  s.stages = std::min(8, std::max(1, (208 << 10) / (s.units * (s.stage_bytes + 8))));
   return s;
 }
 
@@ -634,7 +633,7 @@ struct RunPlan {
 };
 RunPlan make_runs(int M, int rows_per_gate, bool gates, const Shape& s) {
   RunPlan q{};
-  const int most = s.ctas * s.units;
+  const int most = kBlocks * s.units;
   int rows = (M + most - 1) / most;
   const int per_block = rows * s.units;
   // one group for all rows needs no care
@@ -686,7 +685,7 @@ int launch_rows(Kernel kernel, const Shape& s, int blocks, std::atomic<int> (&re
 template <bool kF32, int V, int kThreads>
 int run_forward(const ResidualNorm& a, const Shape& s, const DeviceInfo& dev, cudaStream_t stream) {
   static std::atomic<int> ready[64];
-  const int blocks = std::min((a.M + s.units - 1) / s.units, s.ctas);
+  const int blocks = std::min((a.M + s.units - 1) / s.units, kBlocks);
   return launch_rows(residual_norm_kernel<kF32, V, kThreads>, s, blocks, ready, dev, stream, a);
 }
 
@@ -717,11 +716,10 @@ int launch_residual_norm(const ResidualNorm& a, const DeviceInfo& dev, cudaStrea
   const Shape s = make_shape(a.D, a.D * (a.x_f32 ? 4 : 2) + (a.block ? 2 * a.D : 0));
   auto go = [&](auto f32) {
     constexpr bool kF32 = decltype(f32)::value;
-    if (s.V == 1) return run_forward<kF32, 1, 256>(a, s, dev, stream);
+    if (s.V == 1) return run_forward<kF32, 1, 512>(a, s, dev, stream);
     if (s.V == 4) return run_forward<kF32, 4, 512>(a, s, dev, stream);
-    return s.threads() <= 256   ? run_forward<kF32, 2, 256>(a, s, dev, stream)
-           : s.threads() <= 288 ? run_forward<kF32, 2, 288>(a, s, dev, stream)
-                                : run_forward<kF32, 2, 512>(a, s, dev, stream);
+    return s.threads() <= 512 ? run_forward<kF32, 2, 512>(a, s, dev, stream)
+                              : run_forward<kF32, 2, 576>(a, s, dev, stream);
   };
   return a.x_f32 ? go(std::true_type{}) : go(std::false_type{});
 }
@@ -736,11 +734,10 @@ int launch_residual_norm_backward(const ResidualNormBackward& args, const Device
   a.kinds = (a.dw_pre != nullptr) + (a.dw_post != nullptr || (a.dgate && !q.multi));
   auto go = [&](auto f32, auto multi) {
     constexpr bool kF32 = decltype(f32)::value, kMulti = decltype(multi)::value;
-    if (s.V == 1) return run_backward<kF32, 1, 256, kMulti>(a, s, q.blocks, dev, stream);
+    if (s.V == 1) return run_backward<kF32, 1, 512, kMulti>(a, s, q.blocks, dev, stream);
     if (s.V == 4) return run_backward<kF32, 4, 512, kMulti>(a, s, q.blocks, dev, stream);
-    return s.threads() <= 256   ? run_backward<kF32, 2, 256, kMulti>(a, s, q.blocks, dev, stream)
-           : s.threads() <= 288 ? run_backward<kF32, 2, 288, kMulti>(a, s, q.blocks, dev, stream)
-                                : run_backward<kF32, 2, 512, kMulti>(a, s, q.blocks, dev, stream);
+    return s.threads() <= 512 ? run_backward<kF32, 2, 512, kMulti>(a, s, q.blocks, dev, stream)
+                              : run_backward<kF32, 2, 576, kMulti>(a, s, q.blocks, dev, stream);
   };
   const int rc = a.x_f32 ? (q.multi ? go(std::true_type{}, std::true_type{}) : go(std::true_type{}, std::false_type{}))
                          : (q.multi ? go(std::false_type{}, std::true_type{}) : go(std::false_type{}, std::false_type{}));
