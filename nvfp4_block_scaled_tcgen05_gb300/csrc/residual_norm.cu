@@ -521,10 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // free once every unit is done
   __syncthreads();
   float* hand = reinterpret_cast<float*>(smem + 128);
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    if (k == 0 ? !a.dw_pre : a.kinds == (a.dw_pre != nullptr)) continue;
-    Vec8 (&v)[V] = *reinterpret_cast<Vec8(*)[V]>(k == 0 ? dwi : kMulti ? dwo : T);
+  auto give = [&](Vec8* v, int kind) {
     if (ring.unit > 0)
 #pragma unroll
       for (int i = 0; i < V; ++i) {
@@ -543,11 +540,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int j = 0; j < 4; ++j) v[i].v[j] = ptx::add2(v[i].v[j], other.a.v[j]);
         }
-        const int kind = k == 0 || !a.dw_pre ? 0 : 1;
         store8<true>(a.parts, (size_t(blockIdx.x) * a.kinds + kind) * pieces + c, v[i]);
       }
     __syncthreads();
-  }
+  };
+  if (a.dw_pre) give(dwi, 0);
+  if (a.kinds > (a.dw_pre != nullptr)) give(kMulti ? dwo : T, a.dw_pre != nullptr);
 }
 
 // Adds the blocks' parts in a fixed order.  A block takes 32 columns; blockIdx.y 0:
@@ -610,17 +608,24 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
 }
 
 // ---------------------------------------------------------------- host
-// A row of D / 8 pieces: a warp or more with one, two or (past 8192 values) four
-// pieces a thread.  One block per SM, as many units as 16 warps hold (18, for rows
-// of nine warps, whose single unit would leave half of the SM waiting at barriers),
-// about 200 KB of rows on their way.
+// A row of D / 8 pieces with V pieces a thread.  One block per SM, of as many units
+// as the registers of V pieces leave warps for (backward: about 36 V + 35); two units
+// or more, so that one works while another waits at its barrier, with two pieces a
+// thread where that allows it, else three or four.  About 200 KB of rows on their way.
 constexpr int kBlocks = 152;
+constexpr int kThreadsOf[5] = {0, 512, 512, 384, 320};
 Shape make_shape(int D, int row_bytes) {
   Shape s{};
   const int pieces = D / 8;
-  s.V = pieces <= 32 ? 1 : pieces <= 1024 ? 2 : 4;
-  s.warps = (pieces + 32 * s.V - 1) / (32 * s.V);
-  s.units = s.warps == 9 ? 2 : std::max(1, kMaxWarps / s.warps);
+  auto take = [&](int v) {
+    s.V = v;
+    s.warps = (pieces + 32 * v - 1) / (32 * v);
+    s.units = kThreadsOf[v] / (32 * s.warps);
+    return s.units >= 2;
+  };
+  if (pieces <= 32) take(1);
+  else if (!take(2) && !take(3) && !take(4) && !take(2)) take(pieces <= 1024 ? 2 : 4);
+  s.units = std::max(1, s.units);
   s.stage_bytes = (row_bytes + 127) / 128 * 128;
   s.stages = std::min(8, std::max(1, (208 << 10) / (s.units * (s.stage_bytes + 8))));
   return s;
@@ -717,9 +722,10 @@ int launch_residual_norm(const ResidualNorm& a, const DeviceInfo& dev, cudaStrea
   auto go = [&](auto f32) {
     constexpr bool kF32 = decltype(f32)::value;
     if (s.V == 1) return run_forward<kF32, 1, 512>(a, s, dev, stream);
-    if (s.V == 4) return run_forward<kF32, 4, 512>(a, s, dev, stream);
-    return s.threads() <= 512 ? run_forward<kF32, 2, 512>(a, s, dev, stream)
-                              : run_forward<kF32, 2, 576>(a, s, dev, stream);
+    if (s.V == 2) return run_forward<kF32, 2, 512>(a, s, dev, stream);
+    if (s.V == 3) return run_forward<kF32, 3, 384>(a, s, dev, stream);
+    return s.threads() <= 320 ? run_forward<kF32, 4, 320>(a, s, dev, stream)
+                              : run_forward<kF32, 4, 512>(a, s, dev, stream);
   };
   return a.x_f32 ? go(std::true_type{}) : go(std::false_type{});
 }
@@ -735,9 +741,10 @@ int launch_residual_norm_backward(const ResidualNormBackward& args, const Device
   auto go = [&](auto f32, auto multi) {
     constexpr bool kF32 = decltype(f32)::value, kMulti = decltype(multi)::value;
     if (s.V == 1) return run_backward<kF32, 1, 512, kMulti>(a, s, q.blocks, dev, stream);
-    if (s.V == 4) return run_backward<kF32, 4, 512, kMulti>(a, s, q.blocks, dev, stream);
-    return s.threads() <= 512 ? run_backward<kF32, 2, 512, kMulti>(a, s, q.blocks, dev, stream)
-                              : run_backward<kF32, 2, 576, kMulti>(a, s, q.blocks, dev, stream);
+    if (s.V == 2) return run_backward<kF32, 2, 512, kMulti>(a, s, q.blocks, dev, stream);
+    if (s.V == 3) return run_backward<kF32, 3, 384, kMulti>(a, s, q.blocks, dev, stream);
+    return s.threads() <= 320 ? run_backward<kF32, 4, 320, kMulti>(a, s, q.blocks, dev, stream)
+                              : run_backward<kF32, 4, 512, kMulti>(a, s, q.blocks, dev, stream);
   };
   const int rc = a.x_f32 ? (q.multi ? go(std::true_type{}, std::true_type{}) : go(std::true_type{}, std::false_type{}))
                          : (q.multi ? go(std::false_type{}, std::true_type{}) : go(std::false_type{}, std::false_type{}));
