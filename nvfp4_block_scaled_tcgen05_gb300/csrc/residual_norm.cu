@@ -90,7 +90,7 @@ __device__ __forceinline__ Vec8 store8(void* p, size_t i, const Vec8& v) {
   }
 }
 __device__ __forceinline__ Vec8 weights8(const void* w, size_t i) {
-  return unpack8(__ldg(static_cast<const uint4*>(w) + i));
+  return unpack8(static_cast<const uint4*>(w)[i]);
 }
 
 __device__ __forceinline__ float inverse_rms(float sum, int D, float eps) {
@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int c = ring.tid + i * threads;
-      w[i] = p && c < pieces ? __ldg(static_cast<const uint4*>(p) + c) : make_uint4(0, 0, 0, 0);
+      w[i] = p && c < pieces ? static_cast<const uint4*>(p)[c] : make_uint4(0, 0, 0, 0);
     }
   };
   read_weights(a.w_post, w_post);
@@ -369,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int c = ring.tid + i * threads;
-    w_pre[i] = a.w_pre && c < pieces ? __ldg(static_cast<const uint4*>(a.w_pre) + c)
+    w_pre[i] = a.w_pre && c < pieces ? static_cast<const uint4*>(a.w_pre)[c]
                                      : make_uint4(0, 0, 0, 0);
     dwi[i] = T[i] = zero8();
     if constexpr (kMulti) dwo[i] = zero8();
@@ -408,8 +408,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   float(*part)[3 * kMaxWarps] = parts[ring.unit];
   float ry = 0.0f, rb = 1.0f;
   auto read_rstd = [&](int at) {
-    if (a.w_pre) ry = __ldg(a.rstd_pre + at);
-    if (a.w_post) rb = __ldg(a.rstd_post + at);
+    if (a.w_pre) ry = __ldcg(a.rstd_pre + at);
+    if (a.w_post) rb = __ldcg(a.rstd_post + at);
   };
   if (row < end) read_rstd(row);
   int odd = 0;
@@ -587,12 +587,12 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
     return;
   }
   const int per = a.parts_per_gate ? a.parts_per_gate : blocks, groups = blocks / per;
-  const float w = live && a.w_post ? __uint_as_float(uint32_t(__ldg(static_cast<const uint16_t*>(a.w_post) + col)) << 16) : 1.0f;
+  const float w = live && a.w_post ? __uint_as_float(uint32_t(static_cast<const uint16_t*>(a.w_post)[col]) << 16) : 1.0f;
   float dwo = 0.0f;
   auto group_done = [&](int g, float s) {
     if (!live) return;
     if (a.dgate) a.dgate[size_t(g) * a.D + col] = a.scale * w * s;
-    const float f = a.gate ? __uint_as_float(uint32_t(__ldg(static_cast<const uint16_t*>(a.gate) + size_t(g) * a.D + col)) << 16) : 1.0f;
+    const float f = a.gate ? __uint_as_float(uint32_t(static_cast<const uint16_t*>(a.gate)[size_t(g) * a.D + col]) << 16) : 1.0f;
     dwo += a.scale * f * s;
   };
   if (per >= kJoinWarps) {

@@ -82,3 +82,34 @@ def test_nonfinite_values_stay_in_their_rows(g):
     keep = [n for n in range(40) if n != 5]
     assert torch.equal(got[0, keep], clean[0, keep]) and torch.equal(got[2, keep], clean[2, keep])
     assert not got[1].isfinite().any()
+
+
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("M,N,K,spread", [(1, 40, 256, 30), (3, 40, 1024, 60), (9, 33, 2048, 120), (16, 100, 4096, 126), (2, 2048, 2048, 40)])
+def test_tokens_of_any_magnitude(g, M, N, K, spread, gated):
+    """Values from 2^-spread up to 2^spread in one row, some below the normal range: products stay exact."""
+    gen = torch.Generator(device="cuda").manual_seed(K + spread)
+    r = lambda *s: torch.rand(*s, generator=gen, device="cuda")
+    A = ((1 + r(M, K)) * torch.exp2(torch.floor((2 * r(M, K) - 1) * spread)) * torch.where(r(M, K) < 0.5, -1.0, 1.0)).to(BF16)
+    A[:, ::7] = 0
+    A[0, 1] = 2.0 ** -130  # a subnormal
+    (b, sf), (b2, sf2) = weights(N, K, 8), weights(N, K, 9)
+    # the large values meet weights of zero in half of the rows: what is left is small
+    big = A.abs().amax(dim=0) > 2.0 ** (spread / 3)
+    codes = torch.stack([b % 16, b // 16], dim=2).reshape(N, K)
+    codes[::2][:, big] = 0
+    b = codes[:, ::2] + 16 * codes[:, 1::2]
+    if gated:
+        s = 2.0 ** -spread
+        want, e = ref.few_tokens_gated(A, b, sf, s, b2, sf2, s * 2.0 ** -8, "silu")
+        ref.check(g.gemv_w4a16_gated(A, b, sf, s, b2, sf2, s * 2.0 ** -8), want, e + 2.0 ** -130, "H")
+    else:
+        s = 2.0 ** -20  # results stay within BF16's range
+        want, e = ref.few_tokens(A, b, sf, s)
+        # below the normal ranges: half of FP32's and of BF16's least steps
+        ref.check(g.gemv_w4a16(A, b, sf, s), want, e * (1 + ref.BF16_HALF) + ref.BF16_HALF * want.abs() + 2.0 ** -133, "C")
+
+
+def test_all_zero_tokens(g):
+    b, sf = weights(40, 512, 10)
+    assert (g.gemv_w4a16(torch.zeros(4, 512, dtype=BF16, device="cuda"), b, sf, 1.0) == 0).all()
