@@ -19,10 +19,12 @@
 // with a scale of their own: one pass for tokens as they come, up to eight for tokens
 // that span the whole BF16 range.  So products are exact and sums FP32.
 //
-// A block takes RT tiles of 16 weight rows (gated: half of them of each matrix), KS
-// warps to a tile, which take its 256-K steps in turn; the blocks of a cluster divide
-// K further where there are few rows, and add their sums through distributed shared
-// memory.  Sums are joined in a fixed order.
+// A tile is 16 weight rows (gated: 8 of each matrix, so that a lane gets both products
+// of its outputs).  One block per SM takes a run of tiles; it turns its tokens into FP16
+// in shared memory once, then its 16 warps share the run's 256-K steps evenly, each a
+// consecutive part of (tile, step), and stream without meeting.  Their sums of a tile
+// are joined at the end in a fixed order.  Where there are few tiles, or the tokens do
+// not fit, the blocks of a cluster divide K and join through distributed shared memory.
 #include <algorithm>
 
 #include "chain.cuh"
@@ -33,10 +35,11 @@ namespace gb300 {
 
 namespace {
 
-constexpr int kThreads = 256;    // RT * KS = 8 warps
-constexpr int kDepth = 2;        // 256-K steps that a warp has in flight
+constexpr int kWarps = 16, kThreads = 32 * kWarps;
+constexpr int kDepth = 2;          // 256-K steps that a warp has in flight
 constexpr int kMaxCluster = 8;
-constexpr int kTokenBytes = 96 << 10;  // of A in shared memory at a time, at most
+constexpr int kBatch = 16;         // tiles of a block at a time
+constexpr int kTokenBytes = 160 << 10;  // of tokens in shared memory at a time, at most
 
 __device__ __forceinline__ void mma_16x8x16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                             uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -59,26 +62,6 @@ __device__ __forceinline__ uint32_t weights2(uint32_t w, uint32_t s) {
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
-// BF16 values as biased exponents: the place that the lowest of their eight bits has.
-__device__ __forceinline__ uint32_t place(uint32_t bf16) { return max((bf16 >> 7) & 0xFFu, 1u); }
-constexpr uint32_t kSpan = 32;
-
-// Four token values in [low, high] of place() (and infinities and NaN with `special`)
-// times `scale` as FP16, zeros for the others.
-__device__ __forceinline__ uint2 to_f16(uint2 v, uint32_t low, uint32_t high, bool special, float scale) {
-  uint32_t o[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t b = ((i < 2 ? v.x : v.y) >> (16 * (i & 1))) & 0xFFFFu;
-    const uint32_t p = place(b);
-    const bool take = p == 255u ? special : p >= low && p <= high;
-    o[i] = take ? b << 16 : 0u;
-  }
-  const __half2 lo = __floats2half2_rn(__uint_as_float(o[0]) * scale, __uint_as_float(o[1]) * scale);
-  const __half2 hi = __floats2half2_rn(__uint_as_float(o[2]) * scale, __uint_as_float(o[3]) * scale);
-  return make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-}
-
 // A lane's part of a 256-K step of 16 rows: of rows g and g + 8, two runs of 32 codes
 // (k 128 j + 32 t ..) with their two block scales each.
 struct Step {
@@ -86,267 +69,330 @@ struct Step {
   uint16_t s[2][2];
 };
 
-// NT: groups of 8 tokens.
-template <int NT, int RT, bool kGated>
-__global__ void __launch_bounds__(kThreads, 2)
-    gemv_w4a16_kernel(const GemvW4 a, int splits, int chunk) {
-  constexpr int KS = kThreads / 32 / RT, kRows = 16 * RT, kOuts = kGated ? kRows / 2 : kRows;
-  static_assert(!kGated || RT % 2 == 0, "tiles of both matrices");
-  extern __shared__ uint2 tokens[];  // [step][i][token group][t][token]: 4 k of a token
-  __shared__ float sums[KS][kRows][8 * NT + 1];
-  __shared__ uint32_t range[2][kThreads / 32];
-  const int warp = int(threadIdx.x) >> 5, lane = int(threadIdx.x) & 31;
-  const int g = lane >> 2, t = lane & 3, tile = warp % RT, part = warp / RT;
-  const int rank = splits > 1 ? int(ptx::cluster_ctarank()) : 0;
-  const int first = int(blockIdx.x) / splits * kOuts;
-  // this warp's rows: matrix, and first row of the tile
-  const bool which = kGated && tile >= RT / 2;
-  const int row0 = first + 16 * (kGated ? tile % (RT / 2) : tile);
-  const int steps = a.K / 256;
-  const int s0 = int((long long)steps * rank / splits), s1 = int((long long)steps * (rank + 1) / splits);
+// A BF16 value's place: that of the lowest of its eight bits, as a biased exponent.
+__device__ __forceinline__ uint32_t place(uint32_t magnitude) { return max(magnitude >> 7, 1u); }
+constexpr uint32_t kSpan = 32;          // places that FP16 holds exactly
+constexpr uint32_t kInf = 0x7F80u;      // BF16 infinity; NaN above
 
-  // rows past the end read the last row again; nothing of them is stored
-  const uint8_t *pb[2], *ps[2];
+// Eight token values times `scale` as FP16.  kAll: all of them; else those whose
+// magnitude is in [low, high] (infinities and NaN with `special`), zeros for the others.
+template <bool kAll>
+__device__ __forceinline__ uint4 to_f16(uint4 v, uint32_t low, uint32_t high, bool special, float scale) {
+  uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const size_t row = size_t(min(row0 + g + 8 * h, a.N - 1));
-    pb[h] = (which ? a.b[1] : a.b[0]) + row * size_t(a.K / 2) + t * 16;
-    ps[h] = (which ? a.sf[1] : a.sf[0]) + row * size_t(a.K / 16) + t * 2;
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (!kAll) {
+      auto keep = [&](uint32_t b) { return b >= kInf ? special : b >= low && b <= high; };
+      w[i] &= (keep(w[i] & 0x7FFFu) ? 0xFFFFu : 0u) | (keep(w[i] >> 16 & 0x7FFFu) ? 0xFFFF0000u : 0u);
+    }
+    const __half2 h = __floats2half2_rn(bf16_lo(w[i]) * scale, bf16_hi(w[i]) * scale);
+    w[i] = *reinterpret_cast<const uint32_t*>(&h);
   }
-  auto load = [&](Step& x, int s) {
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// A tile's sums: [16 rows][8 NT tokens], one more for the banks.
+template <int NT>
+struct Tile {
+  float v[16][8 * NT + 1];
+};
+
+// NT: groups of 8 tokens.  `chunk`: steps whose tokens shared memory holds.
+template <int NT, bool kGated>
+__global__ void __launch_bounds__(kThreads, 1)
+    gemv_w4a16_kernel(const GemvW4 a, int splits, int chunk) {
+  constexpr int kOuts = kGated ? 8 : 16;
+  __shared__ Tile<NT> joined[kBatch];
+  __shared__ uint32_t range[2][kWarps];
+  // [tile + warp]: a warp's part of a tile's sums (warps take parts in order, so two of
+  // them share at most one tile and no two pairs have the same place); then the tokens,
+  // [128 K][token][t][chunk]: the 32 k of lane column t in four chunks of 8, chunk c at
+  // c ^ (place / 2 % 4) of place 4 token + t, so that eight lanes read different banks
+  extern __shared__ uint4 dynamic[];
+  Tile<NT>* parts = reinterpret_cast<Tile<NT>*>(dynamic);
+  const int warp = int(threadIdx.x) >> 5, lane = int(threadIdx.x) & 31;
+  const int g = lane >> 2, t = lane & 3;
+  const int rank = splits > 1 ? int(ptx::cluster_ctarank()) : 0;
+  const int cluster = int(blockIdx.x) / splits, clusters = int(gridDim.x) / splits;
+  const int all_tiles = (a.N + kOuts - 1) / kOuts;
+  const int tile0 = int((long long)all_tiles * cluster / clusters);
+  const int tile1 = int((long long)all_tiles * (cluster + 1) / clusters);
+  uint4* tokens = reinterpret_cast<uint4*>(parts + (min(kBatch, tile1 - tile0) + kWarps - 1));
+  const int all_steps = a.K / 256;
+  const int s0 = int((long long)all_steps * rank / splits);
+  const int s1 = int((long long)all_steps * (rank + 1) / splits);
+
+  // This lane's place in each 128 K of the tokens, of token 8 n + g; past the last
+  // token the last one again: those columns of the product are not stored.
+  int mine[NT];
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+  for (int n = 0; n < NT; ++n) {
+    const int at = 4 * min(8 * n + g, a.M - 1) + t;
+    mine[n] = at * 4 + (at >> 1 & 3);
+  }
+  // The lane's rows of a tile: g and g + 8, or row g of both matrices.  Rows past the
+  // end read the last row again; nothing of them is stored.
+  auto load = [&](Step& x, int tile, int s) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const size_t row = size_t(min(tile * kOuts + g + (kGated ? 0 : 8 * h), a.N - 1));
+      const uint8_t* b = (kGated && h ? a.b[1] : a.b[0]) + row * size_t(a.K / 2) + size_t(s) * 128 + t * 16;
+      const uint8_t* f = (kGated && h ? a.sf[1] : a.sf[0]) + row * size_t(a.K / 16) + size_t(s) * 16 + t * 2;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        x.c[h][j] = __ldcs(reinterpret_cast<const uint4*>(pb[h] + size_t(s) * 128 + j * 64));
-        x.s[h][j] = *reinterpret_cast<const uint16_t*>(ps[h] + size_t(s) * 16 + j * 8);
+        x.c[h][j] = __ldcs(reinterpret_cast<const uint4*>(b + j * 64));
+        x.s[h][j] = *reinterpret_cast<const uint16_t*>(f + j * 8);
       }
+    }
   };
 
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
-  Step ring[kDepth];
-#pragma unroll
-  for (int d = 0; d < kDepth; ++d)
-    if (s0 + part + KS * d < s1) load(ring[d], s0 + part + KS * d);
-
-  float total_acc[NT][4];
-#pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) total_acc[n][i] = 0.0f;
-  // tokens of each group of 8
-  const int m0 = min(a.M, 8), m1 = a.M - m0;
-  // this block's part of the tokens
-  const uint16_t* A = static_cast<const uint16_t*>(a.A) + size_t(s0) * 256;
-  const int part_k = (s1 - s0) * 256;
-
-  uint32_t below = 255;  // places that are still due: below this one
-  for (bool first_pass = true;; first_pass = false) {
-    // the largest and the smallest place among them, zeros aside
-    uint32_t high = 0, low = 255;
-    for (int m = 0; m < a.M; ++m) {
-      const uint4* src = reinterpret_cast<const uint4*>(A + size_t(m) * a.K);
-#pragma unroll 4
-      for (int q = int(threadIdx.x); q < part_k / 8; q += kThreads) {
-        const uint4 v = src[q];
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint32_t b = (w[i / 2] >> (16 * (i & 1))) & 0x7FFFu, p = place(b);
-          if (b != 0 && p < below) {
-            high = max(high, p);
-            low = min(low, p);
-          }
-        }
-      }
-    }
-    high = __reduce_max_sync(0xffffffffu, high);
-    low = __reduce_min_sync(0xffffffffu, low);
-    if (!first_pass) __syncthreads();
-    if (lane == 0) {
-      range[0][warp] = high;
-      range[1][warp] = low;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kThreads / 32; ++i) {
-      high = max(high, range[0][i]);
-      low = min(low, range[1][i]);
-    }
-    if (!first_pass && high == 0) break;
-    const uint32_t from = high > kSpan ? high - kSpan : 0u;
-    // 2^(142 - high) brings the largest to 2^15; at most 2^127
-    const int e = min(142 - int(high), 127);
-    const float scale = __uint_as_float(uint32_t(max(e + 127, 1)) << 23);
-    float acc[NT][4];
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[n][i] = 0.0f;
-    if (!first_pass) {
-#pragma unroll
-      for (int d = 0; d < kDepth; ++d)
-        if (s0 + part + KS * d < s1) load(ring[d], s0 + part + KS * d);
-    }
-
-    // `chunk` is a multiple of KS * kDepth: a chunk ends where the ring starts over
+  bool ready = false;  // shared memory holds the tokens of a single pass
+  float scale_back[2] = {1.0f, 1.0f};  // of the pass
+  for (int batch = tile0; batch < tile1; batch += kBatch) {
+    const int tiles = min(kBatch, tile1 - batch);
+    bool first_pass = true;  // of this batch
     for (int c0 = s0; c0 < s1; c0 += chunk) {
-      const int here = min(chunk, s1 - c0);
-      if (c0 > s0) __syncthreads();
-      for (int m = 0; m < a.M; ++m) {
-        const uint2* src = reinterpret_cast<const uint2*>(A + size_t(m) * a.K + size_t(c0 - s0) * 256);
-        const int col = m < 8 ? m : 4 * m0 + m - 8, cols = m < 8 ? m0 : m1;
-#pragma unroll 4
-        for (int q = int(threadIdx.x); q < here * 64; q += kThreads) {
-          // 4 k of 128-K half step q / 32
-          const int blk = q >> 5, qt = (q >> 3) & 3, i = q & 7;
-          tokens[(blk * 8 + i) * 4 * a.M + qt * cols + col] = to_f16(src[q], from, high, first_pass, scale);
-        }
-      }
-      __syncthreads();
-#pragma unroll 1
-      for (int sb = c0 + part; sb < c0 + here; sb += KS * kDepth) {
+      const int steps = min(chunk, s1 - c0);
+      // this warp's part of the (tile, step) pairs, and its first loads
+      const int u0 = tiles * steps * warp / kWarps, u1 = tiles * steps * (warp + 1) / kWarps;
+      Step ring[kDepth];
+      int tile_in = u0 / steps, step_in = u0 - tile_in * steps;  // of the next load
+      auto start = [&]() {
+        tile_in = u0 / steps;
+        step_in = u0 - tile_in * steps;
 #pragma unroll
-        for (int d = 0; d < kDepth; ++d) {
-          const int s = sb + KS * d;
-          if (s >= c0 + here) break;
-          const Step x = ring[d];
-          if (s + KS * kDepth < s1) load(ring[d], s + KS * kDepth);
+        for (int d = 0; d < kDepth; ++d)
+          if (u0 + d < u1) {
+            load(ring[d], batch + tile_in, c0 + step_in);
+            if (++step_in == steps) step_in = 0, ++tile_in;
+          }
+      };
+      start();
+      const uint16_t* A = static_cast<const uint16_t*>(a.A) + size_t(c0) * 256;
+      uint32_t below = 0x8000u;  // magnitudes that are still due: below this one
+      for (bool first_plane = true, more = true; more; first_plane = false) {
+        uint32_t from = 0;
+        if (!ready) {
+          // the largest and the smallest magnitude that are due, zeros aside (less 1,
+          // so that zeros come last)
+          uint32_t high2 = 0, low2 = 0xFFFFFFFFu;
+          for (int m = 0; m < a.M; ++m) {
+            const uint4* src = reinterpret_cast<const uint4*>(A + size_t(m) * a.K);
+#pragma unroll 2
+            for (int q = int(threadIdx.x); q < steps * 32; q += kThreads) {
+              const uint4 v = src[q];
+              const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            uint32_t sc[2][2];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              uint32_t s16;
-              asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(s16) : "h"(x.s[h][j]));
-              sc[h][0] = prmt(s16, 0u, 0x1010u);
-              sc[h][1] = prmt(s16, 0u, 0x3232u);
+              for (int i = 0; i < 4; ++i) {
+                uint32_t b = w[i] & 0x7FFF7FFFu;
+                if (!first_plane) b &= __vcmpltu2(b, below | below << 16);
+                high2 = __vmaxu2(high2, b);
+                low2 = __vminu2(low2, __vsub2(b, 0x00010001u));
+              }
             }
-            const uint2* tok = tokens + ((s - c0) * 2 + j) * 32 * a.M;
+          }
+          uint32_t high = __reduce_max_sync(0xffffffffu, max(high2 & 0xFFFFu, high2 >> 16));
+          uint32_t low = __reduce_min_sync(0xffffffffu, min(low2 & 0xFFFFu, low2 >> 16));
+          if (lane == 0) {
+            range[0][warp] = high;
+            range[1][warp] = low;
+          }
+          __syncthreads();
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              uint32_t w[2][2];
+          for (int i = 0; i < kWarps; ++i) {
+            high = max(high, range[0][i]);
+            low = min(low, range[1][i]);
+          }
+          const bool special = high >= kInf;
+          if (special) high = kInf - 1;
+          // the magnitudes of this pass: [from, high]
+          const uint32_t top = place(high);
+          from = top > kSpan + 1 ? (top - kSpan) << 7 : 0u;
+          more = low != 0xFFFFu && low + 1 < from;
+          // 2^(142 - top) brings the largest to 2^15; at most 2^127
+          const int e = min(142 - int(top), 127);
+          const float scale = __uint_as_float(uint32_t(e + 127) << 23);
+          // 2^-e in two factors, since it may lie below the FP32 range, and scale2, so
+          // that a sum that lies above it comes back before it is stored
+          const float back2 = __uint_as_float(uint32_t(127 - (e - e / 2)) << 23);
+          scale_back[0] = __uint_as_float(uint32_t(127 - e / 2) << 23);
+          scale_back[1] = back2;
+          const bool all = first_plane && !special && !more;
+          for (int m = 0; m < a.M; ++m) {
+            const uint4* src = reinterpret_cast<const uint4*>(A + size_t(m) * a.K);
+            auto fill = [&](auto whole) {
+#pragma unroll 2
+              for (int q = int(threadIdx.x); q < steps * 32; q += kThreads) {
+                const int at = 4 * m + (q >> 2 & 3);  // q / 16: 128 K, q / 4 % 4: t, q % 4: chunk
+                tokens[((q >> 4) * 4 * a.M + at) * 4 + ((q & 3) ^ (at >> 1 & 3))] =
+                    to_f16<decltype(whole)::value>(src[q], from, high, first_plane, scale);
+              }
+            };
+            if (all) fill(std::true_type{});
+            else fill(std::false_type{});
+          }
+          __syncthreads();
+        } else {
+          more = false;
+        }
+        if (!first_plane) start();
+
+        float acc[NT][4];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[n][i] = 0.0f;
+        int tile = u0 / steps, step = u0 - tile * steps;
+#pragma unroll 1
+        for (int ub = u0; ub < u1; ub += kDepth) {
+#pragma unroll
+          for (int d = 0; d < kDepth; ++d) {
+            if (ub + d >= u1) break;
+            const Step x = ring[d];
+            if (ub + d + kDepth < u1) {
+              load(ring[d], batch + tile_in, c0 + step_in);
+              if (++step_in == steps) step_in = 0, ++tile_in;
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              uint32_t sc[2][2];
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
-                const uint32_t word = (&x.c[h][j].x)[i >> 1];
-                w[h][0] = i & 1 ? weights2<2>(word, sc[h][i >> 2]) : weights2<0>(word, sc[h][i >> 2]);
-                w[h][1] = i & 1 ? weights2<3>(word, sc[h][i >> 2]) : weights2<1>(word, sc[h][i >> 2]);
+                uint32_t s16;
+                asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(s16) : "h"(x.s[h][j]));
+                sc[h][0] = prmt(s16, 0u, 0x1010u);
+                sc[h][1] = prmt(s16, 0u, 0x3232u);
               }
+              const uint4* tok = tokens + (step * 2 + j) * 16 * a.M;
 #pragma unroll
-              for (int n = 0; n < NT; ++n) {
-                uint2 v = make_uint2(0, 0);
-                if (g < (n ? m1 : m0)) v = tok[i * 4 * a.M + (n ? 4 * m0 + t * m1 : t * m0) + g];
-                mma_16x8x16(acc[n], w[0][0], w[1][0], w[0][1], w[1][1], v.x, v.y);
+              for (int c = 0; c < 4; ++c) {
+                uint4 v[NT];
+#pragma unroll
+                for (int n = 0; n < NT; ++n) v[n] = tok[mine[n] ^ c];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                  uint32_t w[2][2];
+#pragma unroll
+                  for (int h = 0; h < 2; ++h) {
+                    const uint32_t word = (&x.c[h][j].x)[c], s2 = sc[h][c >> 1];
+                    w[h][0] = i ? weights2<2>(word, s2) : weights2<0>(word, s2);
+                    w[h][1] = i ? weights2<3>(word, s2) : weights2<1>(word, s2);
+                  }
+#pragma unroll
+                  for (int n = 0; n < NT; ++n)
+                    mma_16x8x16(acc[n], w[0][0], w[1][0], w[0][1], w[1][1], i ? v[n].z : v[n].x,
+                                i ? v[n].w : v[n].y);
+                }
               }
+            }
+            if (++step == steps || ub + d + 1 == u1) {  // the warp's part of this tile is done
+#pragma unroll
+              for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const float back = scale_back[1] * (kGated && i >= 2 ? a.scale2[1] : a.scale2[0]);
+                  parts[tile + warp].v[g + 8 * (i >> 1)][8 * n + 2 * t + (i & 1)] =
+                      acc[n][i] * scale_back[0] * back;
+                  acc[n][i] = 0.0f;
+                }
+              step = 0;
+              ++tile;
             }
           }
         }
-      }
-    }
-    // 2^-e in two factors, since it may lie below the FP32 range, and scale2, so that
-    // a sum that lies above it comes back before it is stored
-    const float back = __uint_as_float(uint32_t(127 - e / 2) << 23);
-    const float back2 = __uint_as_float(uint32_t(127 - (e - e / 2)) << 23) * (which ? a.scale2[1] : a.scale2[0]);
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) total_acc[n][i] += acc[n][i] * back * back2;
-    if (low >= from || from == 0) break;
-    below = from;
-    __syncthreads();
-  }
-#pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      sums[part][16 * tile + g + 8 * (i >> 1)][8 * n + 2 * t + (i & 1)] = total_acc[n][i];
-  if (splits > 1) ptx::cluster_sync();
-  else __syncthreads();
-
-  // the blocks of a cluster share the outputs; sums in the order of the splits
-  const int per = kOuts / splits;
-  for (int i = int(threadIdx.x); i < per * a.M; i += kThreads) {
-    const int r = rank * per + i % per, m = i / per;
-    auto total = [&](int row) {
-      float s = 0.0f;
-      for (int c = 0; c < splits; ++c)
-#pragma unroll
-        for (int h = 0; h < KS; ++h) {
-          const float* p = &sums[h][row][m];
-          s += splits > 1 ? ptx::ld_cluster_f32(ptx::mapa_shared(ptx::smem_u32(p), uint32_t(c))) : *p;
+        __syncthreads();
+        // joins the warps' parts of each tile in order
+        for (int i = int(threadIdx.x); i < tiles * 16 * a.M; i += kThreads) {
+          const int r = i % 16, m = i / 16 % a.M, k = i / 16 / a.M;
+          float s = first_pass ? 0.0f : joined[k].v[r][m];
+          // warps that have a step of the tile
+          for (int w = 0; w < kWarps; ++w) {
+            const int w0 = tiles * steps * w / kWarps, w1 = tiles * steps * (w + 1) / kWarps;
+            if (w0 < w1 && w0 < (k + 1) * steps && w1 > k * steps) s += parts[k + w].v[r][m];
+          }
+          joined[k].v[r][m] = s;
         }
-      return s;
-    };
-    float v = total(r);
-    if constexpr (kGated) {
-      v = a.act == GEMM_ACT_SILU ? gate_act<GEMM_ACT_SILU>(v) : gate_act<GEMM_ACT_GELU_TANH>(v);
-      v *= total(r + kOuts);
-    }
-    if (first + r < a.N)
-      static_cast<__nv_bfloat16*>(a.C)[size_t(m) * a.N + first + r] = __float2bfloat16_rn(v);
-  }
-  // a block's sums are read by the others until here
-  if (splits > 1) ptx::cluster_sync();
-}
-
-// How a product is divided: 16-row tiles per block and blocks per cluster.
-struct Plan {
-  int rt, splits;
-};
-// The SM that gets the most blocks takes their weights and tokens and, per block, what
-// an SM could read while one starts and ends.
-Plan make_plan(const GemvW4& a) {
-  const bool gated = a.b[1] != nullptr;
-  const int steps = a.K / 256;
-  Plan best{4, 1};
-  double best_cost = 1e300;
-  for (int rt = gated ? 2 : 1; rt <= 4; rt *= 2)
-    for (int splits = 1; splits <= kMaxCluster && splits <= steps; splits *= 2) {
-      const int outs = gated ? 8 * rt : 16 * rt;
-      const long long blocks = ((long long)a.N + outs - 1) / outs * splits;
-      const double k = double((steps + splits - 1) / splits) * 256;
-      const double bytes = k * (16 * rt * 0.5625 + 2.0 * a.M);
-      const double cost = double((blocks + 151) / 152) * (bytes + 40e3) + (splits > 1 ? 20e3 : 0.0);
-      if (cost < best_cost) {
-        best_cost = cost;
-        best = {rt, splits};
+        first_pass = false;
+        if (more) below = from;
+        else if (first_plane && s1 - s0 <= chunk) ready = true;
+        __syncthreads();
       }
     }
-  return best;
+    if (splits > 1) ptx::cluster_sync();
+    // the blocks of a cluster share the outputs; sums in the order of the splits
+    for (int i = int(threadIdx.x) * splits + rank; i < tiles * kOuts * a.M; i += kThreads * splits) {
+      const int r = i % kOuts, k = i / kOuts % tiles, m = i / kOuts / tiles;
+      auto total = [&](int row) {
+        const float* p = &joined[k].v[row][m];
+        if (splits == 1) return *p;
+        float s = 0.0f;
+        for (int c = 0; c < splits; ++c)
+          s += ptx::ld_cluster_f32(ptx::mapa_shared(ptx::smem_u32(p), uint32_t(c)));
+        return s;
+      };
+      float v = total(r);
+      if constexpr (kGated) {
+        v = a.act == GEMM_ACT_SILU ? gate_act<GEMM_ACT_SILU>(v) : gate_act<GEMM_ACT_GELU_TANH>(v);
+        v *= total(r + 8);
+      }
+      const int n = (batch + k) * kOuts + r;
+      if (n < a.N) static_cast<__nv_bfloat16*>(a.C)[size_t(m) * a.N + n] = __float2bfloat16_rn(v);
+    }
+    // `joined` is read until here, by the other blocks too
+    if (splits > 1) ptx::cluster_sync();
+    else __syncthreads();
+  }
 }
 
-template <int NT, int RT, bool kGated>
-int run(const GemvW4& a, int splits, const DeviceInfo& dev, cudaStream_t stream) {
-  constexpr int kOuts = kGated ? 8 * RT : 16 * RT, kGroup = kThreads / 32 / RT * kDepth;
-  const int tiles = (a.N + kOuts - 1) / kOuts;
-  const int steps = (a.K / 256 + splits - 1) / splits;
-  const int step_bytes = 512 * a.M;
-  int chunk = std::max(1, kTokenBytes / step_bytes / kGroup) * kGroup;
-  const size_t smem = size_t(std::min(steps, chunk)) * step_bytes;
-  auto kernel = gemv_w4a16_kernel<NT, RT, kGated>;
-  static std::atomic<bool> ready[64];
-  if (!ready[dev.device & 63].load()) {
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             std::max(kTokenBytes, kGroup * 512 * 8 * NT)) != cudaSuccess) {
+template <int NT, bool kGated>
+int run(const GemvW4& a, const DeviceInfo& dev, cudaStream_t stream) {
+  constexpr int kOuts = kGated ? 8 : 16;
+  const int tiles = (a.N + kOuts - 1) / kOuts, steps = a.K / 256, step_bytes = 512 * a.M;
+  // K is divided where the tokens do not fit, or the tiles leave SMs without work that
+  // have a step for each warp
+  int splits = 1;
+  while (splits < kMaxCluster && ((steps + splits - 1) / splits * step_bytes > kTokenBytes ||
+                                  (tiles * splits * 2 <= dev.num_sms && steps >= 2 * splits * kWarps)))
+    splits *= 2;
+  auto kernel = gemv_w4a16_kernel<NT, kGated>;
+  const int parts = int(sizeof(Tile<NT>)) * (kBatch + kWarps - 1);
+  cudaLaunchConfig_t cfg{};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = splits;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = parts + kTokenBytes;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  // clusters of each size that the device holds at a time
+  static std::atomic<int> capacity[64][4];
+  const int log2 = splits == 1 ? 0 : splits == 2 ? 1 : splits == 4 ? 2 : 3;
+  int cap = capacity[dev.device & 63][log2].load();
+  if (cap == 0) {
+    cfg.gridDim = dim3(dev.num_sms / splits * splits);
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, parts + kTokenBytes) !=
+        cudaSuccess) {
       cudaGetLastError();
       return GEMM_ERR_LAUNCH;
     }
-    ready[dev.device & 63].store(true);
+    if (cudaOccupancyMaxActiveClusters(&cap, kernel, &cfg) != cudaSuccess || cap <= 0) {
+      cudaGetLastError();
+      cap = dev.num_sms / splits;
+    }
+    capacity[dev.device & 63][log2].store(cap);
   }
-  cudaLaunchConfig_t cfg{};
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = splits;
-  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  cfg.gridDim = dim3(unsigned(tiles) * splits);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = splits > 1 ? 2 : 1;
+  const int clusters = std::min(tiles, cap);
+  const int chunk = std::max(1, std::min((steps + splits - 1) / splits, kTokenBytes / step_bytes));
+  const int most = std::min(kBatch, (tiles + clusters - 1) / clusters);
+  cfg.gridDim = dim3(unsigned(clusters) * splits);
+  cfg.dynamicSmemBytes = sizeof(Tile<NT>) * (most + kWarps - 1) + size_t(chunk) * step_bytes;
+  cfg.numAttrs = 2;
   if (cudaLaunchKernelEx(&cfg, kernel, a, splits, chunk) != cudaSuccess) {
     cudaGetLastError();
     return GEMM_ERR_LAUNCH;
@@ -357,17 +403,8 @@ int run(const GemvW4& a, int splits, const DeviceInfo& dev, cudaStream_t stream)
 }  // namespace
 
 int launch_gemv_w4a16(const GemvW4& a, const DeviceInfo& dev, cudaStream_t stream) {
-  const Plan q = make_plan(a);
-  auto go = [&](auto nt) {
-    constexpr int NT = decltype(nt)::value;
-    if (a.b[1])
-      return q.rt == 2 ? run<NT, 2, true>(a, q.splits, dev, stream)
-                       : run<NT, 4, true>(a, q.splits, dev, stream);
-    return q.rt == 1   ? run<NT, 1, false>(a, q.splits, dev, stream)
-           : q.rt == 2 ? run<NT, 2, false>(a, q.splits, dev, stream)
-                       : run<NT, 4, false>(a, q.splits, dev, stream);
-  };
-  return a.M <= 8 ? go(std::integral_constant<int, 1>{}) : go(std::integral_constant<int, 2>{});
+  if (a.b[1]) return a.M <= 8 ? run<1, true>(a, dev, stream) : run<2, true>(a, dev, stream);
+  return a.M <= 8 ? run<1, false>(a, dev, stream) : run<2, false>(a, dev, stream);
 }
 
 }  // namespace gb300

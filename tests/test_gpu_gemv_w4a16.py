@@ -36,8 +36,9 @@ def tokens(M, K, seed):
     return torch.randn(M, K, generator=gen, device="cuda").to(BF16)
 
 
-# rows: one, a tile's edges, more than a wave of blocks; K: the least, odd multiples, past a chunk
-SIZES = [(1, 1, 256), (1, 8, 256), (2, 15, 512), (3, 16, 768), (5, 17, 256), (7, 63, 1280), (8, 64, 2048), (9, 65, 2304), (1, 2048, 11008),
+# rows: one, a tile's edges, several tiles to an SM, more than a block holds at a time;
+# K: the least, odd multiples, more than a block's tokens
+SIZES = [(1, 70001, 256), (16, 40003, 256), (1, 24, 131072), (3, 50, 98304), (16, 9, 65536), (1, 1, 256), (1, 8, 256), (2, 15, 512), (3, 16, 768), (5, 17, 256), (7, 63, 1280), (8, 64, 2048), (9, 65, 2304), (1, 2048, 11008),
          (16, 127, 16384), (11, 130, 3328), (15, 1000, 4096), (4, 10008, 512), (16, 20000, 768), (12, 33, 256)]
 
 
