@@ -175,22 +175,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (bool first_plane = true, more = true; more; first_plane = false) {
         uint32_t from = 0;
         if (!ready) {
+          // the tokens as they are, 8 k at a time: q / 16: 128 K, q / 4 % 4: t, q % 4: chunk
+          const int per_token = steps * 32, pieces = per_token * a.M;
+          for (int q = int(threadIdx.x), m = 0; m < a.M; q += kThreads) {
+            while (q >= per_token) q -= per_token, ++m;
+            if (m >= a.M) break;
+            const int at = 4 * m + (q >> 2 & 3);
+            ptx::cp_async_16(&tokens[((q >> 4) * 4 * a.M + at) * 4 + ((q & 3) ^ (at >> 1 & 3))],
+                             A + size_t(m) * a.K + q * 8);
+          }
+          ptx::cp_async_wait_all();
           // the largest and the smallest magnitude that are due, zeros aside (less 1,
           // so that zeros come last)
+          __syncthreads();
           uint32_t high2 = 0, low2 = 0xFFFFFFFFu;
-          for (int m = 0; m < a.M; ++m) {
-            const uint4* src = reinterpret_cast<const uint4*>(A + size_t(m) * a.K);
-#pragma unroll 2
-            for (int q = int(threadIdx.x); q < steps * 32; q += kThreads) {
-              const uint4 v = src[q];
-              const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll 4
+          for (int q = int(threadIdx.x); q < pieces; q += kThreads) {
+            const uint4 v = tokens[q];
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                uint32_t b = w[i] & 0x7FFF7FFFu;
-                if (!first_plane) b &= __vcmpltu2(b, below | below << 16);
-                high2 = __vmaxu2(high2, b);
-                low2 = __vminu2(low2, __vsub2(b, 0x00010001u));
-              }
+            for (int i = 0; i < 4; ++i) {
+              uint32_t b = w[i] & 0x7FFF7FFFu;
+              if (!first_plane) b &= __vcmpltu2(b, below | below << 16);
+              high2 = __vmaxu2(high2, b);
+              low2 = __vminu2(low2, __vsub2(b, 0x00010001u));
             }
           }
           uint32_t high = __reduce_max_sync(0xffffffffu, max(high2 & 0xFFFFu, high2 >> 16));
@@ -220,19 +228,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           scale_back[0] = __uint_as_float(uint32_t(127 - e / 2) << 23);
           scale_back[1] = back2;
           const bool all = first_plane && !special && !more;
-          for (int m = 0; m < a.M; ++m) {
-            const uint4* src = reinterpret_cast<const uint4*>(A + size_t(m) * a.K);
-            auto fill = [&](auto whole) {
-#pragma unroll 2
-              for (int q = int(threadIdx.x); q < steps * 32; q += kThreads) {
-                const int at = 4 * m + (q >> 2 & 3);  // q / 16: 128 K, q / 4 % 4: t, q % 4: chunk
-                tokens[((q >> 4) * 4 * a.M + at) * 4 + ((q & 3) ^ (at >> 1 & 3))] =
-                    to_f16<decltype(whole)::value>(src[q], from, high, first_plane, scale);
-              }
-            };
-            if (all) fill(std::true_type{});
-            else fill(std::false_type{});
-          }
+          auto convert = [&](auto whole) {
+#pragma unroll 4
+            for (int q = int(threadIdx.x); q < pieces; q += kThreads)
+              tokens[q] = to_f16<decltype(whole)::value>(tokens[q], from, high, first_plane, scale);
+          };
+          if (all) convert(std::true_type{});
+          else convert(std::false_type{});
           __syncthreads();
         } else {
           more = false;
