@@ -38,12 +38,13 @@ namespace {
 constexpr int kWarps = 16, kThreads = 32 * kWarps;
 constexpr int kDepth = 2;          // 256-K steps that a warp has in flight
 constexpr int kMaxCluster = 8;
+constexpr int kChains = 1;
 constexpr int kBatch = 16;         // tiles of a block at a time
 constexpr int kTokenBytes = 160 << 10;  // of tokens in shared memory at a time, at most
 
 __device__ __forceinline__ void mma_16x8x16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                             uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7},"
       " {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -103,7 +104,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     gemv_w4a16_kernel(const GemvW4 a, int splits, int chunk) {
   constexpr int kOuts = kGated ? 8 : 16;
   __shared__ Tile<NT> joined[kBatch];
-  __shared__ uint32_t range[2][kWarps];
+  __shared__ uint32_t range[2][kWarps], with[kBatch];
   // [tile + warp]: a warp's part of a tile's sums (warps take parts in order, so two of
   // them share at most one tile and no two pairs have the same place); then the tokens,
   // [128 K][token][t][chunk]: the 32 k of lane column t in four chunks of 8, chunk c at
@@ -124,26 +125,43 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // This lane's place in each 128 K of the tokens, of token 8 n + g; past the last
   // token the last one again: those columns of the product are not stored.
-  int mine[NT];
+  int mine[NT][4];
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     const int at = 4 * min(8 * n + g, a.M - 1) + t;
-    mine[n] = at * 4 + (at >> 1 & 3);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) mine[n][c] = at * 4 + (c ^ (at >> 1 & 3));
   }
-  // The lane's rows of a tile: g and g + 8, or row g of both matrices.  Rows past the
-  // end read the last row again; nothing of them is stored.
-  auto load = [&](Step& x, int tile, int s) {
+  // The lane's rows of a tile: g and g + 8, or row g of both matrices; where their next
+  // step lies.  Rows past the end read the last row again; nothing of them is stored.
+  const uint8_t *codes[2], *scales[2];
+  auto go_to = [&](int tile, int s) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const size_t row = size_t(min(tile * kOuts + g + (kGated ? 0 : 8 * h), a.N - 1));
-      const uint8_t* b = (kGated && h ? a.b[1] : a.b[0]) + row * size_t(a.K / 2) + size_t(s) * 128 + t * 16;
-      const uint8_t* f = (kGated && h ? a.sf[1] : a.sf[0]) + row * size_t(a.K / 16) + size_t(s) * 16 + t * 2;
+      codes[h] = (kGated && h ? a.b[1] : a.b[0]) + row * size_t(a.K / 2) + size_t(s) * 128 + t * 16;
+      scales[h] = (kGated && h ? a.sf[1] : a.sf[0]) + row * size_t(a.K / 16) + size_t(s) * 16 + t * 2;
+    }
+  };
+  auto load = [&](Step& x) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        x.c[h][j] = __ldcs(reinterpret_cast<const uint4*>(b + j * 64));
-        x.s[h][j] = *reinterpret_cast<const uint16_t*>(f + j * 8);
+        x.c[h][j] = __ldcs(reinterpret_cast<const uint4*>(codes[h] + j * 64));
+        x.s[h][j] = *reinterpret_cast<const uint16_t*>(scales[h] + j * 8);
       }
+      codes[h] += 128;
+      scales[h] += 16;
     }
+  };
+
+  // the output of row r of tile k and token m, from its sum (gated: both)
+  auto store = [&](int k, int r, int m, float v, float u, int batch) {
+    if constexpr (kGated)
+      v = u * (a.act == GEMM_ACT_SILU ? gate_act<GEMM_ACT_SILU>(v) : gate_act<GEMM_ACT_GELU_TANH>(v));
+    const int n = (batch + k) * kOuts + r;
+    if (n < a.N) static_cast<__nv_bfloat16*>(a.C)[size_t(m) * a.N + n] = __float2bfloat16_rn(v);
   };
 
   ptx::griddep_launch_dependents();
@@ -152,24 +170,39 @@ __global__ void __launch_bounds__(kThreads, 1)
   float scale_back[2] = {1.0f, 1.0f};  // of the pass
   for (int batch = tile0; batch < tile1; batch += kBatch) {
     const int tiles = min(kBatch, tile1 - batch);
-    bool first_pass = true;  // of this batch
+    bool first_pass = true, done = false;  // of this batch
     for (int c0 = s0; c0 < s1; c0 += chunk) {
       const int steps = min(chunk, s1 - c0);
       // this warp's part of the (tile, step) pairs, and its first loads
       const int u0 = tiles * steps * warp / kWarps, u1 = tiles * steps * (warp + 1) / kWarps;
+      // the warps that have a step of each tile (one lane per warp), for the join
+      for (int k = warp; k < tiles; k += kWarps) {
+        const int from_u = tiles * steps * lane / kWarps, to_u = tiles * steps * (lane + 1) / kWarps;
+        const uint32_t b = __ballot_sync(0xffffffffu, lane < kWarps && from_u < to_u &&
+                                                          from_u < (k + 1) * steps && to_u > k * steps);
+        if (lane == 0) with[k] = b;
+      }
       Step ring[kDepth];
-      int tile_in = u0 / steps, step_in = u0 - tile_in * steps;  // of the next load
-      auto start = [&]() {
-        tile_in = u0 / steps;
-        step_in = u0 - tile_in * steps;
+      int tile_in = 0, step_in = 0;  // of the next load
+      auto load_next = [&](Step& x) {
+        load(x);
+        if (++step_in == steps) {
+          step_in = 0;
+          go_to(batch + ++tile_in, c0);
+        }
+      };
+      // (the first loads go out between the steps of the tokens' preparation: all at once
+      // they would hold up the tokens)
+      auto start = [&](int d0, int d1) {
+        if (d0 == 0) {
+          tile_in = u0 / steps;
+          step_in = u0 - tile_in * steps;
+          go_to(batch + tile_in, c0 + step_in);
+        }
 #pragma unroll
         for (int d = 0; d < kDepth; ++d)
-          if (u0 + d < u1) {
-            load(ring[d], batch + tile_in, c0 + step_in);
-            if (++step_in == steps) step_in = 0, ++tile_in;
-          }
+          if (d >= d0 && d < d1 && u0 + d < u1) load_next(ring[d]);
       };
-      start();
       const uint16_t* A = static_cast<const uint16_t*>(a.A) + size_t(c0) * 256;
       uint32_t below = 0x8000u;  // magnitudes that are still due: below this one
       for (bool first_plane = true, more = true; more; first_plane = false) {
@@ -184,10 +217,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::cp_async_16(&tokens[((q >> 4) * 4 * a.M + at) * 4 + ((q & 3) ^ (at >> 1 & 3))],
                              A + size_t(m) * a.K + q * 8);
           }
+          start(0, 1);
           ptx::cp_async_wait_all();
           // the largest and the smallest magnitude that are due, zeros aside (less 1,
           // so that zeros come last)
           __syncthreads();
+          start(1, 2);
           uint32_t high2 = 0, low2 = 0xFFFFFFFFu;
 #pragma unroll 4
           for (int q = int(threadIdx.x); q < pieces; q += kThreads) {
@@ -228,6 +263,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           scale_back[0] = __uint_as_float(uint32_t(127 - e / 2) << 23);
           scale_back[1] = back2;
           const bool all = first_plane && !special && !more;
+          start(2, kDepth);
           auto convert = [&](auto whole) {
 #pragma unroll 4
             for (int q = int(threadIdx.x); q < pieces; q += kThreads)
@@ -238,25 +274,21 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncthreads();
         } else {
           more = false;
+          start(0, kDepth);
         }
-        if (!first_plane) start();
 
-        float acc[NT][4];
+        float acc[NT][kChains][4];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) acc[n][i] = 0.0f;
+          for (int i = 0; i < 4 * kChains; ++i) acc[n][i / 4][i % 4] = 0.0f;
         int tile = u0 / steps, step = u0 - tile * steps;
 #pragma unroll 1
         for (int ub = u0; ub < u1; ub += kDepth) {
 #pragma unroll
           for (int d = 0; d < kDepth; ++d) {
             if (ub + d >= u1) break;
-            const Step x = ring[d];
-            if (ub + d + kDepth < u1) {
-              load(ring[d], batch + tile_in, c0 + step_in);
-              if (++step_in == steps) step_in = 0, ++tile_in;
-            }
+            Step& x = ring[d];
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
               uint32_t sc[2][2];
@@ -272,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int c = 0; c < 4; ++c) {
                 uint4 v[NT];
 #pragma unroll
-                for (int n = 0; n < NT; ++n) v[n] = tok[mine[n] ^ c];
+                for (int n = 0; n < NT; ++n) v[n] = tok[mine[n][c]];
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                   uint32_t w[2][2];
@@ -284,11 +316,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                   }
 #pragma unroll
                   for (int n = 0; n < NT; ++n)
-                    mma_16x8x16(acc[n], w[0][0], w[1][0], w[0][1], w[1][1], i ? v[n].z : v[n].x,
+                    mma_16x8x16(acc[n][i % kChains], w[0][0], w[1][0], w[0][1], w[1][1], i ? v[n].z : v[n].x,
                                 i ? v[n].w : v[n].y);
                 }
               }
             }
+            if (ub + d + kDepth < u1) load_next(x);
             if (++step == steps || ub + d + 1 == u1) {  // the warp's part of this tile is done
 #pragma unroll
               for (int n = 0; n < NT; ++n)
@@ -296,8 +329,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int i = 0; i < 4; ++i) {
                   const float back = scale_back[1] * (kGated && i >= 2 ? a.scale2[1] : a.scale2[0]);
                   parts[tile + warp].v[g + 8 * (i >> 1)][8 * n + 2 * t + (i & 1)] =
-                      acc[n][i] * scale_back[0] * back;
-                  acc[n][i] = 0.0f;
+                      (kChains == 2 ? acc[n][0][i] + acc[n][kChains - 1][i] : acc[n][0][i]) * scale_back[0] * back;
+#pragma unroll
+                  for (int c = 0; c < kChains; ++c) acc[n][c][i] = 0.0f;
                 }
               step = 0;
               ++tile;
@@ -305,42 +339,46 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         __syncthreads();
-        // joins the warps' parts of each tile in order
-        for (int i = int(threadIdx.x); i < tiles * 16 * a.M; i += kThreads) {
-          const int r = i % 16, m = i / 16 % a.M, k = i / 16 / a.M;
-          float s = first_pass ? 0.0f : joined[k].v[r][m];
-          // warps that have a step of the tile
-          for (int w = 0; w < kWarps; ++w) {
-            const int w0 = tiles * steps * w / kWarps, w1 = tiles * steps * (w + 1) / kWarps;
-            if (w0 < w1 && w0 < (k + 1) * steps && w1 > k * steps) s += parts[k + w].v[r][m];
-          }
-          joined[k].v[r][m] = s;
+        // Joins the warps' parts of each tile in order.  The sums are the result where
+        // nothing else is added, and wait in `joined` otherwise.
+        const bool whole = first_plane && !more && splits == 1 && s1 - s0 <= chunk;
+        const int rows = whole ? kOuts : 16;
+        for (int i = int(threadIdx.x); i < tiles * rows * 8 * NT; i += kThreads) {
+          const int r = i % rows, m = i / rows % (8 * NT), k = i / rows / (8 * NT);
+          if (m >= a.M) continue;
+          auto sum = [&](int row) {
+            float s = first_pass ? 0.0f : joined[k].v[row][m];
+            for (uint32_t b = with[k]; b; b &= b - 1) s += parts[k + __ffs(int(b)) - 1].v[row][m];
+            return s;
+          };
+          if (whole) store(k, r, m, sum(r), kGated ? sum(r + 8) : 0.0f, batch);
+          else joined[k].v[r][m] = sum(r);
         }
+        done = whole;
         first_pass = false;
         if (more) below = from;
         else if (first_plane && s1 - s0 <= chunk) ready = true;
         __syncthreads();
       }
     }
+    if (done) continue;
     if (splits > 1) ptx::cluster_sync();
     // the blocks of a cluster share the outputs; sums in the order of the splits
-    for (int i = int(threadIdx.x) * splits + rank; i < tiles * kOuts * a.M; i += kThreads * splits) {
-      const int r = i % kOuts, k = i / kOuts % tiles, m = i / kOuts / tiles;
+    for (int i = int(threadIdx.x) * splits + rank; i < tiles * kOuts * 8 * NT; i += kThreads * splits) {
+      const int r = i % kOuts, m = i / kOuts % (8 * NT), k = i / kOuts / (8 * NT);
+      if (m >= a.M) continue;
       auto total = [&](int row) {
         const float* p = &joined[k].v[row][m];
         if (splits == 1) return *p;
-        float s = 0.0f;
-        for (int c = 0; c < splits; ++c)
-          s += ptx::ld_cluster_f32(ptx::mapa_shared(ptx::smem_u32(p), uint32_t(c)));
+        float v[kMaxCluster], s = 0.0f;
+#pragma unroll
+        for (int c = 0; c < kMaxCluster; ++c)
+          v[c] = c < splits ? ptx::ld_cluster_f32(ptx::mapa_shared(ptx::smem_u32(p), uint32_t(c))) : 0.0f;
+#pragma unroll
+        for (int c = 0; c < kMaxCluster; ++c) s += v[c];
         return s;
       };
-      float v = total(r);
-      if constexpr (kGated) {
-        v = a.act == GEMM_ACT_SILU ? gate_act<GEMM_ACT_SILU>(v) : gate_act<GEMM_ACT_GELU_TANH>(v);
-        v *= total(r + 8);
-      }
-      const int n = (batch + k) * kOuts + r;
-      if (n < a.N) static_cast<__nv_bfloat16*>(a.C)[size_t(m) * a.N + n] = __float2bfloat16_rn(v);
+      store(k, r, m, total(r), kGated ? total(r + 8) : 0.0f, batch);
     }
     // `joined` is read until here, by the other blocks too
     if (splits > 1) ptx::cluster_sync();
