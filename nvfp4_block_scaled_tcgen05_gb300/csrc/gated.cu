@@ -26,6 +26,11 @@ namespace gb300 {
 namespace {
 
 using FwdPair = GatedCfg<TileCfg<Operand::kBF16, 2, 256, 3, 4, 2, true, false, 2>>;
+// Forward of few tokens: the weights on the MMA's M side, half of a tile's rows of each
+// matrix, the tokens on the N side, so that the kernel streams the weights.
+template <int BN, int STAGES>
+using FwdFew = PairedRowsCfg<
+    FewTokensCfg<TileCfg<Operand::kBF16, 2, BN, STAGES, 4, 1, true, false, 2>, true>>;
 template <bool kAmn>
 using ChainPair =
     TrimCfg<TileCfg<Operand::kBF16, 2, 256, 3, 4, 2, true, false, 2, true, false, kAmn, true>>;
@@ -52,6 +57,22 @@ int setup_gated(const void* X, const void* Wg, const void* Wu, int act, int M, i
   p.total_tiles = p.num_m_blocks * p.num_n_blocks;
   p.act = act;
   return rc;
+}
+
+template <class Cfg>
+int run_forward_few(const GatedForward& a, const DeviceInfo& dev, cudaStream_t stream) {
+  CUtensorMap tx, tg, tu;
+  const int rows = few_rows(2 * a.F, Cfg::BN) / 2;  // of each matrix, per CTA and tile
+  int rc = encode_rows(&tx, a.X, a.M, a.K, Cfg::B_ROWS);
+  if (rc == GEMM_OK) rc = encode_rows(&tg, a.Wg, a.F, a.K, rows);
+  if (rc == GEMM_OK) rc = encode_rows(&tu, a.Wu, a.F, a.K, rows);
+  if (rc != GEMM_OK) return rc;
+  GemmParams p = base_params<Cfg>(a.F, a.M, a.K, dev);
+  set_few_rows(p, rows);
+  p.act = a.act;
+  p.c_ptr = a.H;
+  p.gates_ptr = static_cast<uint16_t*>(a.gates);
+  return launch_tcgen05<Cfg, Epilogue::kGatedTBF16>(tg, tx, tg, tu, tg, p, dev, stream);
 }
 
 // dG and dU [2][n] from the stored gates [2][n]: three values read and two written
@@ -201,6 +222,8 @@ size_t gated_backward_workspace(int M, int F, int K) {
 }
 
 int launch_gated_forward(const GatedForward& a, const DeviceInfo& dev, cudaStream_t stream) {
+  if (a.M <= 64) return run_forward_few<FwdFew<64, 5>>(a, dev, stream);
+  if (a.M <= 128) return run_forward_few<FwdFew<128, 4>>(a, dev, stream);
   using Cfg = FwdPair;
   CUtensorMap tx, tg, tu, th, tk;
   GemmParams p;

@@ -57,6 +57,8 @@ enum class Operand : int { kBF16 = 0, kNVFP4 = 1, kW4A16 = 2 };
 //   column; the row is the vocabulary's)
 // kGatedBF16 (GATED tiles): C = bf16(act(gate) * up), and with p.gates_out both
 //   factors as BF16 through the A-scale map
+// kGatedTBF16 (PAIRED_ROWS tiles): kGatedBF16 with the roles swapped (rows of D are the
+//   weights', columns the tokens)
 // kGatedGradBF16: C[0] = bf16(dH * up * act'(gate)), C[1] = bf16(dH * act(gate))
 enum class Epilogue : int {
   kStoreBF16 = 0,
@@ -70,7 +72,8 @@ enum class Epilogue : int {
   kXentStatsT = 8,
   kXentGradTBF16 = 9,
   kGatedBF16 = 10,
-  kGatedGradBF16 = 11
+  kGatedGradBF16 = 11,
+  kGatedTBF16 = 12
 };
 
 struct GemmParams {
@@ -109,6 +112,7 @@ struct GemmParams {
   int act;                        // GEMM_ACT_*
   int gates_out;                  // kGatedBF16: store the factors too
   const uint16_t* dh;             // kGatedGradBF16: gradient of the output, [M][N]
+  uint16_t* gates_ptr;            // kGatedTBF16: the factors' place, or null
   int k_half;                     // DUAL_K: K blocks of the first pair of operands
 };
 
@@ -157,6 +161,8 @@ struct TileCfg {
   static constexpr bool TRIM_N = false;
   // GATED, DUAL_K, DUAL_OUT: see GatedCfg, DualKCfg, DualOutCfg.
   static constexpr bool GATED = false, DUAL_K = false, DUAL_OUT = false;
+  // PAIRED_ROWS: see PairedRowsCfg.
+  static constexpr bool PAIRED_ROWS = false;
   // C_T: the output is D transposed (the swapped-operand decode GEMM, whose
   // M role holds the weights and N role the few activation rows)
   static constexpr bool C_T = C_T_;
@@ -322,6 +328,19 @@ template <class Base>
 struct GatedCfg : Base {
   static constexpr bool GATED = true;
   static_assert(Base::CG == 2 && !Base::B_MN && !Base::kFP4 && !Base::kW4, "CTA pairs, NT layout");
+};
+
+// Few tokens (FewTokensCfg) against two weight matrices: rows 0 .. m_rows - 1 of A are
+// rows of the one (gate), rows 64 .. the same rows of the other (up, the A-scale map);
+// m_rows <= 64.  Epilogue warps q and q + 2 hold the two products of the same outputs.
+// (16 rows of each in turn, 16 lanes apart in one warp, loaded in boxes of 2 KB: 11008 x
+// 2048, one token, 29.9 us.)
+template <class Base>
+struct PairedRowsCfg : Base {
+  static constexpr bool PAIRED_ROWS = true;
+  static_assert(Base::CG == 2 && Base::VAR_ROWS && !Base::B_MN && !Base::A_MN && Base::EPI_WARPS == 4 &&
+                    Base::EPI_BUFS == 1,
+                "few tokens, NT layout, a box per warp");
 };
 
 // One K loop over two products, A0 B0 + A1 B1: K blocks from k_half on come from
@@ -591,11 +610,12 @@ __device__ __forceinline__ void xent_grad_t(const float (&x)[32], uint32_t (&v)[
   }
 }
 
-// Gated projection: 32 columns of a row, FP32 bits.  g <- act(g) u.
+// Gated projection: the first kCols columns of a row, FP32 bits.  g <- act(g) u.
+template <int kCols = 32>
 __device__ __forceinline__ void gated_product(int act, uint32_t (&g)[32], const uint32_t (&u)[32]) {
   auto all = [&](auto kind) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
+    for (int i = 0; i < kCols; ++i) {
       const float x = __uint_as_float(g[i]);
       g[i] = __float_as_uint(gate_act<decltype(kind)::value>(x) * __uint_as_float(u[i]));
     }
@@ -857,7 +877,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
       ptx::prefetch_tmap(&tmap_sfb);
     } else if constexpr (Cfg::kW4) {
       ptx::prefetch_tmap(&tmap_sfb);  // the block scales (tmap_b: the codes)
-    } else if (p.sk || Cfg::DUAL_K || Cfg::DUAL_OUT || p.gates_out) {
+    } else if (p.sk || Cfg::DUAL_K || Cfg::DUAL_OUT || Cfg::PAIRED_ROWS || p.gates_out) {
       ptx::prefetch_tmap(&tmap_sfa);  // the stream-K workspace, or a second matrix
     }
     if constexpr (Cfg::GATED || Cfg::DUAL_K) ptx::prefetch_tmap(&tmap_sfb);
@@ -881,6 +901,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
           for (int sub = 0; sub < Cfg::KSUB; ++sub) {
             const int x = kb * Cfg::KX * Cfg::KSUB + sub * Cfg::KX;
             if constexpr (!Cfg::A_MN && !Cfg::DUAL_K) ptx::tma_prefetch_3d(&tmap_a, x, a_row, l);
+            if constexpr (Cfg::PAIRED_ROWS) ptx::tma_prefetch_3d(&tmap_sfa, x, a_row, l);
             if constexpr (!Cfg::kW4 && !Cfg::B_MN) ptx::tma_prefetch_3d(map_b, x, b_row, l);
           }
           if constexpr (kFP4 && Cfg::SFA_REP)
@@ -989,7 +1010,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         int sfb_atoms = 0;
         if constexpr (kFP4) sfb_atoms = min(Cfg::SFB_ATOMS, p.rest_n - nb * Cfg::SFB_ATOMS);
         const uint32_t tx =
-            uint32_t(CG) * (uint32_t(m_rows) * 128 * Cfg::KSUB + (Cfg::kW4 ? 0u : b_bytes) +
+            uint32_t(CG) * (uint32_t(m_rows) * (Cfg::PAIRED_ROWS ? 256 : 128) * Cfg::KSUB + (Cfg::kW4 ? 0u : b_bytes) +
                             Cfg::SFA_BYTES + uint32_t(sfb_atoms) * Cfg::SFB_ATOM_BYTES);
         // split-K: the batch slot holds batch * k_splits + split
         const int kb_begin = sg.kb0;
@@ -1082,6 +1103,10 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                     if (!Cfg::TRIM_N || at < b_atoms)
                       ptx::tma_load_3d_pair_hint(stage_b(stage) + at * Cfg::B_ATOM_BYTES, map_b,
                                                  fb, b_row + 64 * at, kb_x * Cfg::BK, l_b, pol_ab);
+              } else if constexpr (Cfg::PAIRED_ROWS) {
+                ptx::tma_load_3d_pair_hint(da, &tmap_a, fb, x, a_row, l, pol_a);
+                ptx::tma_load_3d_pair_hint(da + 64 * 128, &tmap_sfa, fb, x, a_row, l, pol_a);
+                ptx::tma_load_3d_pair_hint(db, map_b, fb, x, b_row, l, pol_ab);
               } else if constexpr (kHintLoads) {
                 ptx::tma_load_3d_pair_hint(da, &tmap_a, fb, x, a_row, l, pol_a);
                 ptx::tma_load_3d_pair_hint(db, map_b, fb, x, b_row, l, pol_ab);
@@ -2086,6 +2111,63 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
             sbuf = next_box();
             write_box_row<Epilogue::kStoreBF16>(smem + (sbuf - sbase) + lane * 128, lane, u0, u1, 0.0f);
             send(&tmap_c, sbuf, col0, 1);
+          }
+        }
+      } else if constexpr (EPI == Epilogue::kGatedTBF16) {
+        // Warps q and q + 2 hold the gate and the up row of a lane's output: each gives
+        // the other half of its tokens through the two halves of its box in turn, and
+        // takes the other half of the outputs.  Two-byte stores, 64 bytes of a token's
+        // row together: the outputs are few beside the weights.
+        const bool gate = q < 2;
+        const int in_tile = (q & 1) * 32 + lane, f = (mb * CG + int(peer)) * m_rows + in_tile;
+        const bool some = (q & 1) * 32 < m_rows && f - lane < p.M;  // warp-uniform, for both warps
+        const bool live = in_tile < m_rows && f < p.M;
+        const int partner = e ^ 2;
+#pragma unroll 1
+        for (int c = 0; c < Cfg::EPI_COLS / 32; ++c) {
+          uint32_t r[32];
+          ptx::tmem_ld_32x32b_x32(tacc + uint32_t(32 * c), r);
+          ptx::tmem_ld_wait_regs(r);
+          if (c == Cfg::EPI_COLS / 32 - 1) release_acc(acc);
+          const int tok0 = nb * BN + col_base + 32 * c;
+          if (!some || tok0 >= p.N) continue;  // for both warps
+          const uint32_t half = (chunk_ctr & 1u) * 2048u;
+          uint32_t* mine = reinterpret_cast<uint32_t*>(smem + (buf0 - sbase) + half);
+          const uint32_t* other =
+              reinterpret_cast<const uint32_t*>(smem + (epi_base + partner * Cfg::EPI_BOX_BYTES - sbase) + half);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) mine[i * 32 + lane] = gate ? r[16 + i] : r[i];
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(epi_bar(partner, 0));
+          const bool got = wait_bar(epi_bar(e, 0), chunk_ctr & 1u, w, 13);
+          ++chunk_ctr;
+          if (!__all_sync(0xffffffffu, got)) {
+            ok = false;
+            break;
+          }
+          uint32_t g[32], u[32];  // the first 16 count
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const uint32_t v = other[i * 32 + lane];
+            g[i] = gate ? r[i] : v;
+            u[i] = gate ? v : r[16 + i];
+          }
+          const int tok = tok0 + (gate ? 0 : 16);
+          const size_t at = size_t(tok) * p.M + f, all = size_t(p.N) * p.M;
+          if (p.gates_ptr && live) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if (tok + i < p.N) {
+                p.gates_ptr[at + size_t(i) * p.M] = uint16_t(pack_bf16x2(g[i], 0u));
+                p.gates_ptr[all + at + size_t(i) * p.M] = uint16_t(pack_bf16x2(u[i], 0u));
+              }
+          }
+          gated_product<16>(p.act, g, u);
+          if (live) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if (tok + i < p.N)
+                static_cast<uint16_t*>(p.c_ptr)[at + size_t(i) * p.M] = uint16_t(pack_bf16x2(g[i], 0u));
           }
         }
       } else if constexpr (EPI == Epilogue::kStoreF32 || EPI == Epilogue::kAddF32) {
