@@ -93,6 +93,28 @@ __device__ __forceinline__ Vec8 weights8(const void* w, size_t i) {
   return unpack8(static_cast<const uint4*>(w)[i]);
 }
 
+// Piece `at` of a gate (ones where there is none) times `scale`; piece c of a weight
+// (ones) times v.
+__device__ __forceinline__ Vec8 scaled_gate(float scale, const void* gate, size_t at) {
+  Vec8 f;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) f.v[j] = both(scale);
+  if (gate) {
+    const Vec8 g = weights8(gate, at);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) f.v[j] = ptx::mul2(f.v[j], g.v[j]);
+  }
+  return f;
+}
+__device__ __forceinline__ Vec8 times_weight(Vec8 v, const void* weight, int c) {
+  if (weight) {
+    const Vec8 w = weights8(weight, c);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v.v[j] = ptx::mul2(v.v[j], w.v[j]);
+  }
+  return v;
+}
+
 __device__ __forceinline__ float inverse_rms(float sum, int D, float eps) {
   return 1.0f / sqrtf(sum / float(D) + eps);
 }
@@ -226,16 +248,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int first = int(blockIdx.x) * shape.units + ring.unit;
   if (ring.tid == 0)
     for (int i = 0, row = first; i < shape.stages && row < a.M; ++i, row += step) ring.fill(row);
-  uint4 w_post[V], w_pre[V], gate[V];
-  auto read_weights = [&](const void* p, uint4 (&w)[V]) {
+  uint4 w_pre[V];
+  Vec8 p[V];  // scale * gate * w_post
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int c = ring.tid + i * threads;
-      w[i] = p && c < pieces ? static_cast<const uint4*>(p)[c] : make_uint4(0, 0, 0, 0);
-    }
-  };
-  read_weights(a.w_post, w_post);
-  read_weights(a.w_pre, w_pre);
+  for (int i = 0; i < V; ++i) {
+    const int c = ring.tid + i * threads;
+    w_pre[i] = a.w_pre && c < pieces ? static_cast<const uint4*>(a.w_pre)[c] : make_uint4(0, 0, 0, 0);
+    p[i] = a.block && !a.gate && c < pieces ? times_weight(scaled_gate(a.scale, nullptr, 0), a.w_post, c)
+                                            : zero8();
+  }
   int gate_row = -1;
   float(*part)[2][kMaxWarps] = parts[ring.unit];
   int odd = 0;
@@ -243,26 +264,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     const size_t base = size_t(row) * pieces;
     if (a.gate && row / a.rows_per_gate != gate_row) {
       gate_row = row / a.rows_per_gate;
-      read_weights(static_cast<const uint16_t*>(a.gate) + size_t(gate_row) * a.D, gate);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int c = ring.tid + i * threads;
+        if (c < pieces)
+          p[i] = times_weight(scaled_gate(a.scale, a.gate, size_t(gate_row) * pieces + c), a.w_post, c);
+      }
     }
     const uint8_t* mem = ring.wait();
-    Vec8 y[V];
-    uint4 b[V];
+    Vec8 y[V], b[V];
     float2 s2 = both(0.0f);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int c = ring.tid + i * threads;
-      y[i] = zero8();
-      b[i] = make_uint4(0, 0, 0, 0);
+      y[i] = b[i] = zero8();
       if (c < pieces) {
         Raw8<kF32> x;
         x.read(mem, c);
         y[i] = x.get();
-        if (a.block) b[i] = reinterpret_cast<const uint4*>(mem + ring.src[0].bytes)[c];
+        if (a.block) b[i] = unpack8(reinterpret_cast<const uint4*>(mem + ring.src[0].bytes)[c]);
       }
-      const Vec8 v = unpack8(b[i]);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) s2 = ptx::fma2(v.v[j], v.v[j], s2);
+      for (int j = 0; j < 4; ++j) s2 = ptx::fma2(b[i].v[j], b[i].v[j], s2);
     }
     // the row is in registers: after the next barrier its stage takes another
     ptx::fence_proxy_async_smem();
@@ -282,19 +305,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int c = ring.tid + i * threads;
       if (c >= pieces) break;
       if (a.block) {
-        Vec8 v = unpack8(b[i]);
-        if (a.w_post) {
-          const Vec8 w = unpack8(w_post[i]);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) v.v[j] = ptx::mul2(ptx::mul2(v.v[j], both(r)), w.v[j]);
-        }
-        if (a.gate) {
-          const Vec8 w = unpack8(gate[i]);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) v.v[j] = ptx::mul2(v.v[j], w.v[j]);
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) y[i].v[j] = ptx::fma2(both(a.scale), v.v[j], y[i].v[j]);
+        for (int j = 0; j < 4; ++j)
+          y[i].v[j] = ptx::fma2(ptx::mul2(b[i].v[j], both(r)), p[i].v[j], y[i].v[j]);
         y[i] = store8<kF32>(a.y, base + c, y[i]);
       }
 #pragma unroll
@@ -374,26 +387,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     dwi[i] = T[i] = zero8();
     if constexpr (kMulti) dwo[i] = zero8();
   }
-  // scale times the gate's row `at`, and a value times w_post, eight columns each
-  auto scale_gate = [&](int at, int c) {
-    Vec8 f;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) f.v[j] = both(a.scale);
-    if (a.gate) {
-      const Vec8 g = weights8(static_cast<const uint16_t*>(a.gate) + size_t(at) * a.D, c);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) f.v[j] = ptx::mul2(f.v[j], g.v[j]);
-    }
-    return f;
-  };
-  auto times_w = [&](Vec8 f, int c) {
-    if (a.w_post) {
-      const Vec8 w = weights8(a.w_post, c);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) f.v[j] = ptx::mul2(f.v[j], w.v[j]);
-    }
-    return f;
-  };
   Vec8 p[V];
   int gate_row = -1;
   auto read_gate = [&](int at) {
@@ -401,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int c = ring.tid + i * threads;
-      p[i] = a.block && c < pieces ? times_w(scale_gate(at, c), c) : zero8();
+      p[i] = a.block && c < pieces ? times_weight(scaled_gate(a.scale, a.gate, size_t(at) * pieces + c), a.w_post, c) : zero8();
     }
   };
   if (!kMulti) read_gate(row < end ? row / a.rows_per_gate : 0);
@@ -494,11 +487,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         static_cast<uint4*>(a.dblock)[base + c] = pack8(db);
         if (last) {  // the gate group's end
-          const Vec8 f = scale_gate(gate_row, c);
+          const Vec8 f = scaled_gate(a.scale, a.gate, size_t(gate_row) * pieces + c);
           Vec8 dg;
 #pragma unroll
           for (int j = 0; j < 4; ++j) dg.v[j] = ptx::mul2(both(a.scale), T[i].v[j]);
-          dg = times_w(dg, c);
+          dg = times_weight(dg, a.w_post, c);
           if (a.dgate) store8<true>(a.dgate, size_t(gate_row) * pieces + c, dg);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
@@ -617,25 +610,29 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
 
 // ---------------------------------------------------------------- host
 // A row of D / 8 pieces with V pieces a thread.  One block per SM, of as many units
-// as the registers of V pieces leave warps for (backward: about 36 V + 35); two units
-// or more, so that one works while another waits at its barrier, with two pieces a
-// thread where that allows it, else three or four.  About 200 KB of rows on their way.
+// as the registers of V pieces leave warps for; two units or more where two or three
+// pieces a thread allow it, so that one works while another waits at its barrier.
+// (Four pieces a thread spill: 6553 x 5120 backward took 139 us with two units of them,
+// with one unit of two pieces it takes 89 us at 5461 x 6144.)
 constexpr int kBlocks = 152;
-constexpr int kThreadsOf[5] = {0, 512, 512, 384, 320};
-Shape make_shape(int D, int row_bytes) {
+// Rows on their way, per SM: the backward pass needs the 200 KB (100 KB: 8192 x 4096
+// 76 -> 106 us), the forward pass is a little faster with half of it (56 -> 54 us).
+constexpr int kThreadsOf[5] = {0, 512, 512, 384, 512};
+constexpr int kForwardBytes = 104 << 10, kBackwardBytes = 208 << 10;
+Shape make_shape(int D, int row_bytes, int ring_bytes) {
   Shape s{};
   const int pieces = D / 8;
   auto take = [&](int v) {
     s.V = v;
     s.warps = (pieces + 32 * v - 1) / (32 * v);
-    s.units = kThreadsOf[v] / (32 * s.warps);
+    s.units = std::min(kMaxWarps, kThreadsOf[v] / (32 * s.warps));
     return s.units >= 2;
   };
   if (pieces <= 32) take(1);
-  else if (!take(2) && !take(3) && !take(4) && !take(2)) take(pieces <= 1024 ? 2 : 4);
+  else if (!take(2) && !take(3)) take(pieces <= 1024 ? 2 : 4);
   s.units = std::max(1, s.units);
   s.stage_bytes = (row_bytes + 127) / 128 * 128;
-  s.stages = std::min(8, std::max(1, (208 << 10) / (s.units * (s.stage_bytes + 8))));
+  s.stages = std::min(8, std::max(1, ring_bytes / (s.units * (s.stage_bytes + 8))));
   return s;
 }
 
@@ -720,20 +717,19 @@ int backward_row_bytes(int D, bool f32, bool dy, bool pre, bool block) {
 // The shape's units and blocks do not depend on the stages, so the matrices that a
 // call has make no difference here.
 size_t residual_norm_backward_workspace(int M, int D, int rows_per_gate, int weights, bool gates) {
-  const Shape s = make_shape(D, 128);
+  const Shape s = make_shape(D, 128, kBackwardBytes);
   const RunPlan q = make_runs(M, rows_per_gate, gates, s);
   return size_t(q.blocks) * (weights + (gates && !q.multi)) * D * sizeof(float);
 }
 
 int launch_residual_norm(const ResidualNorm& a, const DeviceInfo& dev, cudaStream_t stream) {
-  const Shape s = make_shape(a.D, a.D * (a.x_f32 ? 4 : 2) + (a.block ? 2 * a.D : 0));
+  const Shape s = make_shape(a.D, a.D * (a.x_f32 ? 4 : 2) + (a.block ? 2 * a.D : 0), kForwardBytes);
   auto go = [&](auto f32) {
     constexpr bool kF32 = decltype(f32)::value;
-    if (s.V == 1) return run_forward<kF32, 1, 512>(a, s, dev, stream);
-    if (s.V == 2) return run_forward<kF32, 2, 512>(a, s, dev, stream);
-    if (s.V == 3) return run_forward<kF32, 3, 384>(a, s, dev, stream);
-    return s.threads() <= 320 ? run_forward<kF32, 4, 320>(a, s, dev, stream)
-                              : run_forward<kF32, 4, 512>(a, s, dev, stream);
+    if (s.V == 1) return run_forward<kF32, 1, kThreadsOf[1]>(a, s, dev, stream);
+    if (s.V == 2) return run_forward<kF32, 2, kThreadsOf[2]>(a, s, dev, stream);
+    if (s.V == 3) return run_forward<kF32, 3, kThreadsOf[3]>(a, s, dev, stream);
+    return run_forward<kF32, 4, kThreadsOf[4]>(a, s, dev, stream);
   };
   return a.x_f32 ? go(std::true_type{}) : go(std::false_type{});
 }
@@ -741,18 +737,17 @@ int launch_residual_norm(const ResidualNorm& a, const DeviceInfo& dev, cudaStrea
 int launch_residual_norm_backward(const ResidualNormBackward& args, const DeviceInfo& dev,
                                   cudaStream_t stream) {
   ResidualNormBackward a = args;
-  const Shape s = make_shape(a.D, backward_row_bytes(a.D, a.x_f32, a.dy, a.w_pre, a.block));
+  const Shape s = make_shape(a.D, backward_row_bytes(a.D, a.x_f32, a.dy, a.w_pre, a.block), kBackwardBytes);
   const RunPlan q = make_runs(a.M, a.rows_per_gate, a.dgate != nullptr, s);
   a.rows_per_run = q.rows_per_run;
   a.parts_per_gate = q.parts_per_gate;
   a.kinds = (a.dw_pre != nullptr) + (a.dw_post != nullptr || (a.dgate && !q.multi));
   auto go = [&](auto f32, auto multi) {
     constexpr bool kF32 = decltype(f32)::value, kMulti = decltype(multi)::value;
-    if (s.V == 1) return run_backward<kF32, 1, 512, kMulti>(a, s, q.blocks, dev, stream);
-    if (s.V == 2) return run_backward<kF32, 2, 512, kMulti>(a, s, q.blocks, dev, stream);
-    if (s.V == 3) return run_backward<kF32, 3, 384, kMulti>(a, s, q.blocks, dev, stream);
-    return s.threads() <= 320 ? run_backward<kF32, 4, 320, kMulti>(a, s, q.blocks, dev, stream)
-                              : run_backward<kF32, 4, 512, kMulti>(a, s, q.blocks, dev, stream);
+    if (s.V == 1) return run_backward<kF32, 1, kThreadsOf[1], kMulti>(a, s, q.blocks, dev, stream);
+    if (s.V == 2) return run_backward<kF32, 2, kThreadsOf[2], kMulti>(a, s, q.blocks, dev, stream);
+    if (s.V == 3) return run_backward<kF32, 3, kThreadsOf[3], kMulti>(a, s, q.blocks, dev, stream);
+    return run_backward<kF32, 4, kThreadsOf[4], kMulti>(a, s, q.blocks, dev, stream);
   };
   const int rc = a.x_f32 ? (q.multi ? go(std::true_type{}, std::true_type{}) : go(std::true_type{}, std::false_type{}))
                          : (q.multi ? go(std::false_type{}, std::true_type{}) : go(std::false_type{}, std::false_type{}));
