@@ -537,7 +537,7 @@ GB300GEMM_API int router_topk_backward(const float* logits, const int* experts, 
  *   X      bf16 [M][K], Wg, Wu bf16 [F][K]                       (read)
  *   H      bf16 [M][F]                                           (written)
  *   gates  bf16 [2][M][F], or NULL: G and U rounded, for the backward call
- *   M, F, K >= 1, at most 2^30; F % 8 == 0 and K % 8 == 0; every pointer 16-byte
+ *   M, F, K >= 1, at most 2^30 (F: 2^29); F % 8 == 0 and K % 8 == 0; every pointer 16-byte
  *   aligned; the outputs overlap no input and not each other.
  * A gate of -inf gives NaN, as the formula does.
  * Errors: GEMM_ERR_NULL, _SHAPE (also an unknown act), _ALIGN, _ALIAS, _ARCH,

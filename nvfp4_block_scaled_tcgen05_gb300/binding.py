@@ -426,7 +426,7 @@ def _context(device, stream):
         if not isinstance(stream, torch.cuda.Stream):
             stream = torch.cuda.ExternalStream(_stream_ptr(stream), device=device)
         return torch.cuda.stream(stream)
-    if torch.cuda.current_device() != device.index:
+    if torch._C._cuda_getDevice() != device.index:
         return torch.cuda.device(device)
     return None
 
@@ -803,36 +803,39 @@ def _stream_rows(t, name: str):
     """(M, D, 1 if FP32) of the residual stream or its gradient."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype not in (torch.bfloat16, torch.float32):
-        raise TypeError(f"{name} must be bfloat16 or float32, got {t.dtype}")
-    _mat(t, t.dtype, name)
-    M, D = t.shape
+    dtype, shape = t.dtype, t.shape
+    if dtype is not torch.bfloat16 and dtype is not torch.float32:
+        raise TypeError(f"{name} must be bfloat16 or float32, got {dtype}")
+    if len(shape) != 2 or not (t.is_cuda and t.is_contiguous()):
+        _mat(t, dtype, name)
+    M, D = shape
     if M > _INT_MAX or D > _INT_MAX:
         raise ValueError(f"sizes past 2^31 - 1: M {M}, D {D}")
-    return M, D, 1 if t.dtype == torch.float32 else 0
+    return M, D, 1 if dtype is torch.float32 else 0
 
 
 def _norm_inputs(M, D, device, block, w_post, gate, w_pre):
     """Checks what residual_norm and its gradient share; rows per gate (M without one)."""
-    bf16 = torch.bfloat16
-    if block is None and (w_post is not None or gate is not None):
-        raise ValueError("w_post and gate belong to a block: give block")
-    if block is None and w_pre is None:
-        raise ValueError("neither a block nor w_pre: nothing to do")
+    bf16, row = torch.bfloat16, (D,)
     if block is not None:
         _on_device("block", device, block, bf16, (M, D))
+    elif w_post is not None or gate is not None:
+        raise ValueError("w_post and gate belong to a block: give block")
+    elif w_pre is None:
+        raise ValueError("neither a block nor w_pre: nothing to do")
     if w_post is not None:
-        _on_device("w_post", device, w_post, bf16, (D,))
+        _on_device("w_post", device, w_post, bf16, row)
     if w_pre is not None:
-        _on_device("w_pre", device, w_pre, bf16, (D,))
+        _on_device("w_pre", device, w_pre, bf16, row)
     if gate is None:
         return M
-    groups = 1
-    if isinstance(gate, torch.Tensor) and gate.dim() == 2:
-        groups = gate.shape[0]
-        if groups == 0 or M % groups:
-            raise ValueError(f"gate has {groups} rows, which do not divide {M}")
-    _on_device("gate", device, gate, bf16, (D,) if groups == 1 and gate.dim() == 1 else (groups, D))
+    if isinstance(gate, torch.Tensor) and gate.dim() == 1:
+        _on_device("gate", device, gate, bf16, row)
+        return M
+    groups = gate.shape[0] if isinstance(gate, torch.Tensor) and gate.dim() == 2 else 1
+    if groups == 0 or M % groups:
+        raise ValueError(f"gate has {groups} rows, which do not divide {M}")
+    _on_device("gate", device, gate, bf16, (groups, D))
     return M // groups
 
 
@@ -864,15 +867,26 @@ def residual_norm(x: torch.Tensor, block: torch.Tensor | None = None,
     if elsewhere is not None:
         with elsewhere:
             return residual_norm(x, block, w_post, gate, w_pre, scale, eps, y, n)
-    empty, F32 = torch.empty, torch.float32
-    if y is None and block is not None:
-        y = empty((M, D), dtype=x.dtype, device=device)
-    if n is None and w_pre is not None:
-        n = empty((M, D), dtype=torch.bfloat16, device=device)
-    rstd_post = None if w_post is None else empty((M,), dtype=F32, device=device)
-    rstd_pre = None if w_pre is None else empty((M,), dtype=F32, device=device)
-    _run("residual_norm", device, x.data_ptr(), _ptr(block), _ptr(w_post), _ptr(gate), _ptr(w_pre),
-         _ptr(y), _ptr(n), _ptr(rstd_post), _ptr(rstd_pre), float(scale), float(eps), f32, M, D, rows)
+    # (pointers without a call to _ptr each: the host's time is what a few rows take)
+    empty, F32, like, post, pre = torch.empty, torch.float32, torch.empty_like, None, None
+    if block is not None:
+        if y is None:
+            y = like(x)
+        y_ptr, block_ptr = y.data_ptr(), block.data_ptr()
+    else:
+        y_ptr = block_ptr = None
+    rstd_post = rstd_pre = n_ptr = post_ptr = pre_ptr = None
+    if w_post is not None:
+        rstd_post = empty((M,), dtype=F32, device=device)
+        post, post_ptr = w_post.data_ptr(), rstd_post.data_ptr()
+    if w_pre is not None:
+        if n is None:
+            n = like(x) if f32 == 0 else empty((M, D), dtype=torch.bfloat16, device=device)
+        rstd_pre = empty((M,), dtype=F32, device=device)
+        pre, n_ptr, pre_ptr = w_pre.data_ptr(), n.data_ptr(), rstd_pre.data_ptr()
+    _run("residual_norm", device, x.data_ptr(), block_ptr, post,
+         None if gate is None else gate.data_ptr(), pre, y_ptr, n_ptr, post_ptr, pre_ptr,
+         float(scale), float(eps), f32, M, D, rows)
     return ResidualNorm(x if block is None else y, n, rstd_post, rstd_pre)
 
 
@@ -946,18 +960,20 @@ def _gemv_inputs(A, *weights):
     """(M, N, K) of few tokens A and NVFP4 weight matrices of one shape: (b, sfb, names)."""
     _mat(A, torch.bfloat16, "A")
     M, K = A.shape
-    first = weights[0][0]
-    _mat(first, torch.uint8, weights[0][2])
-    N = first.shape[0]
+    b, _, name_b, _ = weights[0]
+    if not isinstance(b, torch.Tensor) or b.dim() != 2:
+        _mat(b, torch.uint8, name_b)
+    N = b.shape[0]
     if M > _INT_MAX or N > _INT_MAX or K > _INT_MAX:
         raise ValueError(f"sizes past 2^31 - 1: M {M}, N {N}, K {K}")
     if K % 256:
         raise ValueError(f"K must be a multiple of 256, got {K}")
     if not 1 <= M <= 16:
         raise ValueError(f"1 to 16 tokens, got {M}: gemm_w4a16 takes more")
+    device, u8, codes, scales = A.device, torch.uint8, (N, K // 2), (N, K // 16)
     for b, sf, name_b, name_sf in weights:
-        _on_device(name_b, A.device, b, torch.uint8, (N, K // 2))
-        _on_device(name_sf, A.device, sf, torch.uint8, (N, K // 16))
+        _on_device(name_b, device, b, u8, codes)
+        _on_device(name_sf, device, sf, u8, scales)
     return M, N, K
 
 

@@ -241,7 +241,7 @@ int check_xent(const void* X, const void* W, int M, int V, int K) {
 int check_gated(const void* X, const void* Wg, const void* Wu, int act, int M, int F, int K) {
   if (!X || !Wg || !Wu) return GEMM_ERR_NULL;
   if (M <= 0 || F <= 0 || K <= 0) return GEMM_ERR_SHAPE;
-  if (M > kMaxDim || F > kMaxDim || K > kMaxDim) return GEMM_ERR_SHAPE;
+  if (M > kMaxDim || F > kMaxDim / 2 || K > kMaxDim) return GEMM_ERR_SHAPE;  // dX's K loop: 2 F
   if (act != GEMM_ACT_SILU && act != GEMM_ACT_GELU_TANH) return GEMM_ERR_SHAPE;
   // tiles of every product, both directions; K blocks of dX's loop over 2 F
   const long long mb = ((long long)M + 127) / 128, fb = ((long long)F + 63) / 64,
@@ -648,7 +648,7 @@ int gemm_bf16_nt_gated(const void* X, const void* Wg, const void* Wu, void* H, v
 }
 
 size_t gemm_bf16_nt_gated_backward_workspace_bytes(int M, int F, int K) {
-  if (M <= 0 || F <= 0 || K <= 0 || M > kMaxDim || F > kMaxDim || K > kMaxDim) return 0;
+  if (M <= 0 || F <= 0 || K <= 0 || M > kMaxDim || F > kMaxDim / 2 || K > kMaxDim) return 0;
   return gated_backward_workspace(M, F, K);
 }
 
