@@ -115,7 +115,7 @@ inline HeadStart head_start(GridTiles before, long long tiles, double tile_kb, i
   return h;
 }
 template <class Cfg, Epilogue EPI>
-void set_head_start(GemmParams& p, GridTiles before, double tile_kb, const DeviceInfo& dev) {
+static void set_head_start(GemmParams& p, GridTiles before, double tile_kb, const DeviceInfo& dev) {
   const int pairs = tcgen05_cluster_capacity<Cfg, EPI>(dev);
   if (before.tiles == 0 || pairs <= 0 || p.total_tiles < pairs) return;
   const HeadStart h = head_start(before, p.total_tiles, tile_kb, pairs);
@@ -151,7 +151,7 @@ int launch_dependent(Kernel kernel, dim3 grid, int threads, cudaStream_t stream,
   return GEMM_OK;
 }
 
-inline int launch_sum_slots(const float* acc, void* out, size_t n, int slots, const DeviceInfo& dev,
+static inline int launch_sum_slots(const float* acc, void* out, size_t n, int slots, const DeviceInfo& dev,
                             cudaStream_t stream) {
   const long long grid = std::min<long long>((n / 4 + kSumThreads - 1) / kSumThreads,
                                              (long long)dev.num_sms * 16);

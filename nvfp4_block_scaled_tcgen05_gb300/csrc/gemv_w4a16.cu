@@ -17,7 +17,9 @@
 // brings a block's largest to 2^15, if it is at least 2^-32 of that (its eight bits are
 // then multiples of 2^-24).  Values below that wait for another pass over the weights
 // with a scale of their own: one pass for tokens as they come, up to eight for tokens
-// that span the whole BF16 range.  So products are exact and sums FP32.
+// that span the whole BF16 range.  So products are exact and sums FP32; they are scaled
+// back, and by scale2, before they are stored, so that a sum beyond the FP32 range whose
+// result is not comes back.
 //
 // A tile is 16 weight rows (gated: 8 of each matrix, so that a lane gets both products
 // of its outputs).  One block per SM takes a run of tiles; it turns its tokens into FP16
@@ -74,6 +76,20 @@ struct Step {
 __device__ __forceinline__ uint32_t place(uint32_t magnitude) { return max(magnitude >> 7, 1u); }
 constexpr uint32_t kSpan = 32;          // places that FP16 holds exactly
 constexpr uint32_t kInf = 0x7F80u;      // BF16 infinity; NaN above
+
+// Joins the magnitudes below `below` of eight token values into the largest and the
+// smallest so far, zeros aside (the smallest less 1, so that zeros come last); two values
+// per word.
+__device__ __forceinline__ void span_of(uint4 v, uint32_t below, uint32_t& high2, uint32_t& low2) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t b = w[i] & 0x7FFF7FFFu;
+    if (below != 0x8000u) b &= __vcmpltu2(b, below | below << 16);
+    high2 = __vmaxu2(high2, b);
+    low2 = __vminu2(low2, __vsub2(b, 0x00010001u));
+  }
+}
 
 // Eight token values times `scale` as FP16.  kAll: all of them; else those whose
 // magnitude is in [low, high] (infinities and NaN with `special`), zeros for the others.
@@ -204,38 +220,67 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (d >= d0 && d < d1 && u0 + d < u1) load_next(ring[d]);
       };
       const uint16_t* A = static_cast<const uint16_t*>(a.A) + size_t(c0) * 256;
-      uint32_t below = 0x8000u;  // magnitudes that are still due: below this one
-      for (bool first_plane = true, more = true; more; first_plane = false) {
-        uint32_t from = 0;
-        if (!ready) {
-          // the tokens as they are, 8 k at a time: q / 16: 128 K, q / 4 % 4: t, q % 4: chunk
-          const int per_token = steps * 32, pieces = per_token * a.M;
-          for (int q = int(threadIdx.x), m = 0; m < a.M; q += kThreads) {
-            while (q >= per_token) q -= per_token, ++m;
-            if (m >= a.M) break;
-            const int at = 4 * m + (q >> 2 & 3);
-            ptx::cp_async_16(&tokens[((q >> 4) * 4 * a.M + at) * 4 + ((q & 3) ^ (at >> 1 & 3))],
-                             A + size_t(m) * a.K + q * 8);
-          }
-          start(0, 1);
-          ptx::cp_async_wait_all();
-          // the largest and the smallest magnitude that are due, zeros aside (less 1,
-          // so that zeros come last)
-          __syncthreads();
-          start(1, 2);
-          uint32_t high2 = 0, low2 = 0xFFFFFFFFu;
-#pragma unroll 4
-          for (int q = int(threadIdx.x); q < pieces; q += kThreads) {
-            const uint4 v = tokens[q];
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      const int per_token = steps * 32, pieces = per_token * a.M;  // of 8 k
+      // what(place, piece of token m) for this thread's pieces, kAhead at a time: `get`
+      // first for all of them
+      auto each_piece = [&](auto get, auto what) {
+        constexpr int kAhead = 4;
+        int q = int(threadIdx.x), m = 0;
+        while (true) {
+          int at[kAhead];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              uint32_t b = w[i] & 0x7FFF7FFFu;
-              if (!first_plane) b &= __vcmpltu2(b, below | below << 16);
-              high2 = __vmaxu2(high2, b);
-              low2 = __vminu2(low2, __vsub2(b, 0x00010001u));
+          for (int b = 0; b < kAhead; ++b) {
+            while (q >= per_token && m < a.M) q -= per_token, ++m;
+            at[b] = -1;
+            if (m < a.M) {
+              // q / 16: 128 K, q / 4 % 4: t, q % 4: chunk
+              const int row = 4 * m + (q >> 2 & 3);
+              at[b] = ((q >> 4) * 4 * a.M + row) * 4 + ((q & 3) ^ (row >> 1 & 3));
+              get(b, at[b], reinterpret_cast<const uint4*>(A + size_t(m) * a.K) + q);
             }
+            q += kThreads;
           }
+#pragma unroll
+          for (int b = 0; b < kAhead; ++b)
+            if (at[b] >= 0) what(b, at[b]);
+          if (m >= a.M) break;
+        }
+      };
+      uint32_t below = 0x8000u;  // magnitudes that are still due: below this one
+      bool more = true;
+      for (int plane = 0; more; ++plane) {
+        uint32_t from = 0;
+        const bool first_plane = plane == 0;
+        more = false;
+        if (ready) {
+          start(0, kDepth);
+        } else if (first_plane) {
+          // Tokens as they come are zero or between 2^-25 and 2^8: converted on their
+          // way, with one scale.  A value outside is seen at the end, and the tokens then
+          // go the long way.
+          constexpr uint32_t kLeast = (127 - 25) << 7, kMost = ((127 + 8) << 7) - 1;
+          start(0, 1);
+          uint32_t high2 = 0, low2 = 0xFFFFFFFFu;
+          uint4 v[4];
+          each_piece([&](int b, int, const uint4* src) { v[b] = __ldcg(src); },
+                     [&](int b, int at) {
+                       span_of(v[b], 0x8000u, high2, low2);
+                       tokens[at] = to_f16<true>(v[b], 0u, 0u, false, 256.0f);
+                     });
+          start(1, kDepth);
+          scale_back[0] = 1.0f / 256.0f;
+          scale_back[1] = 1.0f;
+          more = __syncthreads_or(max(high2 & 0xFFFFu, high2 >> 16) > kMost ||
+                                  min(low2 & 0xFFFFu, low2 >> 16) < kLeast - 1);
+        }
+        if (!ready && (more || !first_plane)) {
+          if (!first_plane) start(0, kDepth);
+          // the tokens as they are
+          each_piece([&](int, int at, const uint4* src) { ptx::cp_async_16(&tokens[at], src); }, [](int, int) {});
+          ptx::cp_async_wait_all();
+          __syncthreads();
+          uint32_t high2 = 0, low2 = 0xFFFFFFFFu;
+          for (int q = int(threadIdx.x); q < pieces; q += kThreads) span_of(tokens[q], below, high2, low2);
           uint32_t high = __reduce_max_sync(0xffffffffu, max(high2 & 0xFFFFu, high2 >> 16));
           uint32_t low = __reduce_min_sync(0xffffffffu, min(low2 & 0xFFFFu, low2 >> 16));
           if (lane == 0) {
@@ -248,8 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             high = max(high, range[0][i]);
             low = min(low, range[1][i]);
           }
-          const bool special = high >= kInf;
-          if (special) high = kInf - 1;
+          if (high >= kInf) high = kInf - 1;
           // the magnitudes of this pass: [from, high]
           const uint32_t top = place(high);
           from = top > kSpan + 1 ? (top - kSpan) << 7 : 0u;
@@ -257,24 +301,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           // 2^(142 - top) brings the largest to 2^15; at most 2^127
           const int e = min(142 - int(top), 127);
           const float scale = __uint_as_float(uint32_t(e + 127) << 23);
-          // 2^-e in two factors, since it may lie below the FP32 range, and scale2, so
-          // that a sum that lies above it comes back before it is stored
-          const float back2 = __uint_as_float(uint32_t(127 - (e - e / 2)) << 23);
+          // 2^-e in two factors, since it may lie below the FP32 range
           scale_back[0] = __uint_as_float(uint32_t(127 - e / 2) << 23);
-          scale_back[1] = back2;
-          const bool all = first_plane && !special && !more;
-          start(2, kDepth);
-          auto convert = [&](auto whole) {
-#pragma unroll 4
-            for (int q = int(threadIdx.x); q < pieces; q += kThreads)
-              tokens[q] = to_f16<decltype(whole)::value>(tokens[q], from, high, first_plane, scale);
-          };
-          if (all) convert(std::true_type{});
-          else convert(std::false_type{});
+          scale_back[1] = __uint_as_float(uint32_t(127 - (e - e / 2)) << 23);
+          for (int q = int(threadIdx.x); q < pieces; q += kThreads)
+            tokens[q] = to_f16<false>(tokens[q], from, high, first_plane, scale);
           __syncthreads();
-        } else {
-          more = false;
-          start(0, kDepth);
         }
 
         float acc[NT][kChains][4];

@@ -1,6 +1,10 @@
 // Host-side launch of tcgen05_gemm_kernel instantiations: one-time per-device
 // attributes, co-resident cluster count, cudaLaunchKernelEx with the cluster
 // dimension of the configuration (its CTA group).
+//
+// The functions that name a kernel are static: each translation unit has its own copy
+// of a kernel that two of them instantiate, with attributes of its own, so one unit
+// must not take the other's word that they are set.
 #pragma once
 
 #include <algorithm>
@@ -32,7 +36,7 @@ void fill_launch_config(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr, cuda
 // most one per SM group); sets the kernel's shared-memory attribute on first
 // use.  Returns 0 when the attribute cannot be set.
 template <class Cfg, Epilogue EPI>
-int tcgen05_cluster_capacity(const DeviceInfo& dev) {
+static int tcgen05_cluster_capacity(const DeviceInfo& dev) {
   static std::atomic<int> max_clusters[64];  // 0: not yet configured
   const int d = dev.device & 63;
   int cap = max_clusters[d].load();
@@ -61,7 +65,7 @@ int tcgen05_cluster_capacity(const DeviceInfo& dev) {
 // fewer tiles.  A stream-K schedule (p.sk) divides its tail over exactly
 // `clusters` clusters, so the caller passes the count it planned with.
 template <class Cfg, Epilogue EPI>
-int launch_tcgen05(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& tc,
+static int launch_tcgen05(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& tc,
                    const CUtensorMap& tsfa, const CUtensorMap& tsfb, const GemmParams& p,
                    const DeviceInfo& dev, cudaStream_t stream, int clusters = 0) {
   const int cap = tcgen05_cluster_capacity<Cfg, EPI>(dev);
