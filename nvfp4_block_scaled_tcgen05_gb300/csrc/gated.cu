@@ -44,16 +44,44 @@ int encode_two(CUtensorMap* m, const void* base, int rows, int cols, int box_row
                         uint64_t(rows), 2, 64, uint32_t(box_rows), CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+// N blocks of full width (128 outputs) of `mb` M blocks, the rest being of 64: so that
+// the pair with the most tiles has the least.  A tile of half the width takes about 0.6
+// of the time.
+constexpr double kNarrowTile = 0.6;
+int wide_blocks(int mb, int F) {
+  const int all = (F + 127) / 128;
+  int best = all;
+  double best_cost = 1e300;
+  // whole rounds of wide tiles, from all of them downward
+  for (long long rounds = ((long long)mb * all + kPairs - 1) / kPairs; rounds >= 0; --rounds) {
+    const int wide = int(std::min<long long>(all, rounds * kPairs / mb));
+    const long long tw = (long long)mb * wide;
+    const long long tn = (long long)mb * ((std::max(0, F - wide * 128) + 63) / 64);
+    double cost = 0.0;
+    for (int c = 0; c < kPairs; ++c) {
+      const long long w = (tw - c + kPairs - 1) / kPairs, t = (tw + tn - c + kPairs - 1) / kPairs;
+      cost = std::max(cost, double(w) + kNarrowTile * double(t - w));
+    }
+    if (cost < best_cost - 0.05) {
+      best_cost = cost;
+      best = wide;
+    }
+    if (rounds + 2 < ((long long)mb * all + kPairs - 1) / kPairs) break;
+  }
+  return best;
+}
+
 // Maps and schedule of the gated tiles: X, both weight matrices.
 template <class Cfg>
 int setup_gated(const void* X, const void* Wg, const void* Wu, int act, int M, int F, int K,
                 const DeviceInfo& dev, CUtensorMap& tx, CUtensorMap& tg, CUtensorMap& tu,
                 GemmParams& p) {
   int rc = encode_rows(&tx, X, M, K, Cfg::BM);
-  if (rc == GEMM_OK) rc = encode_rows(&tg, Wg, F, K, Cfg::B_ROWS);
-  if (rc == GEMM_OK) rc = encode_rows(&tu, Wu, F, K, Cfg::B_ROWS);
+  if (rc == GEMM_OK) rc = encode_rows(&tg, Wg, F, K, Cfg::BN / 4);
+  if (rc == GEMM_OK) rc = encode_rows(&tu, Wu, F, K, Cfg::BN / 4);
   p = base_params<Cfg>(M, F, K, dev);
-  p.num_n_blocks = (F + Cfg::B_ROWS - 1) / Cfg::B_ROWS;  // outputs per tile: half its columns
+  p.n_wide = wide_blocks(p.num_m_blocks, F);
+  p.num_n_blocks = p.n_wide + (std::max(0, F - p.n_wide * 128) + 63) / 64;
   p.total_tiles = p.num_m_blocks * p.num_n_blocks;
   p.act = act;
   return rc;

@@ -114,6 +114,7 @@ struct GemmParams {
   const uint16_t* dh;             // kGatedGradBF16: gradient of the output, [M][N]
   uint16_t* gates_ptr;            // kGatedTBF16: the factors' place, or null
   int k_half;                     // DUAL_K: K blocks of the first pair of operands
+  int n_wide;                     // GATED: N blocks of full width
 };
 
 template <Operand OP, int CG_, int BN_, int STAGES_, int EPI_WARPS_ = 4, int EPI_BUFS_ = 2,
@@ -323,7 +324,9 @@ struct TrimCfg : Base {
 // Two weight matrices share a tile: the first CTA of the pair stages BN / 2 rows
 // of B (gate), the second the same rows of another matrix (up, the B-scale map),
 // so that column c of the accumulator's first half and of its second belong to
-// one output.
+// one output.  The N blocks from n_wide on are half as wide (BN / 4 rows of each
+// matrix, half of the MMA's columns): the last round of tiles then leaves fewer
+// pairs idle, and few tiles spread over more of them.
 template <class Base>
 struct GatedCfg : Base {
   static constexpr bool GATED = true;
@@ -860,7 +863,12 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
   const int m_rows = Cfg::VAR_ROWS ? p.m_rows : Cfg::BM;  // rows of A per CTA and tile
   // columns of N block nb's MMAs
   auto tile_n = [&](int nb) {
+    if (Cfg::GATED) return nb < p.n_wide ? BN : BN / 2;
     return Cfg::TRIM_N && nb + 1 == p.num_n_blocks ? p.n_last : BN;
+  };
+  // GATED: N block nb's first output
+  auto gated_col = [&](int nb) {
+    return min(nb, p.n_wide) * (BN / 2) + max(nb - p.n_wide, 0) * (BN / 4);
   };
   // The producer's first segment, found before the dependency wait: the
   // schedule arithmetic run for the first time cost ~0.7 us between the
@@ -892,7 +900,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         decode_tile<Cfg>(s0.tile, p, l0, mb0, nb0);
         const int l = (p.k_splits > 1) ? l0 / p.k_splits : l0;
         const int a_row = (mb0 * CG + int(peer)) * m_rows;
-        const int b_row = Cfg::GATED ? nb0 * Cfg::B_ROWS : nb0 * BN + int(peer) * Cfg::B_ROWS;
+        const int b_row = Cfg::GATED ? gated_col(nb0) : nb0 * BN + int(peer) * Cfg::B_ROWS;
         const void* map_b = Cfg::GATED && peer ? &tmap_sfb : &tmap_b;
         (void)map_b, (void)b_row;
         const int kend = min(s0.kb1, s0.kb0 + STAGES);
@@ -1001,12 +1009,13 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
           decode_tile<Cfg>(sg.tile, p, l, mb, nb);
         }
         const int a_row = (mb * CG + int(peer)) * m_rows;
-        const int b_row = Cfg::GATED ? nb * Cfg::B_ROWS
+        const int b_row = Cfg::GATED ? gated_col(nb)
                                      : nb * BN + int(peer) * (Cfg::TRIM_N ? tile_n(nb) / 2 : Cfg::B_ROWS);
         // TRIM_N: 64-column atoms of B that the tile needs
         const int b_atoms = Cfg::TRIM_N ? (tile_n(nb) / 2 + 63) / 64 : Cfg::B_ROWS / 64;
-        const uint32_t b_bytes =
-            Cfg::TRIM_N ? uint32_t(b_atoms) * Cfg::B_ATOM_BYTES : uint32_t(Cfg::B_BYTES);
+        const uint32_t b_bytes = Cfg::TRIM_N  ? uint32_t(b_atoms) * Cfg::B_ATOM_BYTES
+                                 : Cfg::GATED ? uint32_t(tile_n(nb) / 2) * 128 * Cfg::KSUB
+                                              : uint32_t(Cfg::B_BYTES);
         int sfb_atoms = 0;
         if constexpr (kFP4) sfb_atoms = min(Cfg::SFB_ATOMS, p.rest_n - nb * Cfg::SFB_ATOMS);
         const uint32_t tx =
@@ -1107,6 +1116,12 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                 ptx::tma_load_3d_pair_hint(da, &tmap_a, fb, x, a_row, l, pol_a);
                 ptx::tma_load_3d_pair_hint(da + 64 * 128, &tmap_sfa, fb, x, a_row, l, pol_a);
                 ptx::tma_load_3d_pair_hint(db, map_b, fb, x, b_row, l, pol_ab);
+              } else if constexpr (Cfg::GATED) {
+                // boxes of BN / 4 rows
+                ptx::tma_load_3d_pair_hint(da, &tmap_a, fb, x, a_row, l, pol_a);
+                ptx::tma_load_3d_pair_hint(db, map_b, fb, x, b_row, l, pol_ab);
+                if (nb < p.n_wide)
+                  ptx::tma_load_3d_pair_hint(db + (BN / 4) * 128, map_b, fb, x, b_row + BN / 4, l, pol_ab);
               } else if constexpr (kHintLoads) {
                 ptx::tma_load_3d_pair_hint(da, &tmap_a, fb, x, a_row, l, pol_a);
                 ptx::tma_load_3d_pair_hint(db, map_b, fb, x, b_row, l, pol_ab);
@@ -1241,7 +1256,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
           break;
         }
         ptx::tc_fence_after();
-        if constexpr (Cfg::TRIM_N) {
+        if constexpr (Cfg::TRIM_N || Cfg::GATED) {
           int l, mb, nb;
           decode_tile<Cfg>(sg.tile, p, l, mb, nb);
           idesc = (Cfg::idesc() & ~(0x3Fu << 17)) | (uint32_t(tile_n(nb) >> 3) << 17);
@@ -2037,7 +2052,8 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         // The CTA's last tile puts each box in a place of its own in the freed
         // stage memory (as in the other epilogues).
         static_assert(Cfg::EPI_COLS == 256, "one warp holds both halves");
-        constexpr int NCH = Cfg::BN / 128;     // 64-column chunks of a tile's outputs
+        constexpr int NCH = Cfg::BN / 128;     // 64-column chunks of a wide tile's outputs
+        const int chunks = tile_n(nb) / 128, col_first = gated_col(nb);
         constexpr int kBoxesMost = EPI == Epilogue::kGatedBF16 ? 3 : 2;  // per chunk
         static_assert(Cfg::EPI_WARPS * NCH * kBoxesMost * Cfg::EPI_BOX_BYTES <=
                           Cfg::STAGES * Cfg::STAGE_BYTES,
@@ -2062,8 +2078,8 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
           }
         };
 #pragma unroll 1
-        for (int c = 0; c < NCH; ++c) {
-          const int col0 = nb * (BN / 2) + c * 64;
+        for (int c = 0; c < chunks; ++c) {
+          const int col0 = col_first + c * 64;
           const bool live = rows_live && col0 < p.N;  // warp-uniform
           uint4 dh[8];
           if constexpr (EPI == Epilogue::kGatedGradBF16) {
@@ -2076,7 +2092,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                           : make_uint4(0, 0, 0, 0);
           }
           uint32_t g0[32], g1[32], u0[32], u1[32];
-          const uint32_t tg = tacc + uint32_t(c * 64), tu = tg + BN / 2;
+          const uint32_t tg = tacc + uint32_t(c * 64), tu = tg + uint32_t(chunks * 64);
           ptx::tmem_ld_32x32b_x32(tg, g0);
           ptx::tmem_ld_32x32b_x32(tg + 32, g1);
           ptx::tmem_ld_32x32b_x32(tu, u0);
@@ -2085,7 +2101,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
           ptx::tmem_ld_wait_regs(g1);
           ptx::tmem_ld_wait_regs(u0);
           ptx::tmem_ld_wait_regs(u1);
-          if (c == NCH - 1) release_acc(acc);
+          if (c == chunks - 1) release_acc(acc);
           if (!live) continue;
           if constexpr (EPI == Epilogue::kGatedBF16) {
             if (p.gates_out) {
