@@ -585,12 +585,18 @@ GB300GEMM_API size_t gemm_bf16_nt_gated_backward_workspace_bytes(int M, int F, i
  *
  *   A bf16 [K][M], B bf16 [K][N] (read), C bf16 [M][N] (written), row-major;
  *   M, N, K >= 1; M % 8 == 0 and N % 8 == 0 (16-byte row pitches; any K); every
- *   pointer 16-byte aligned; C must not overlap A or B.
+ *   pointer 16-byte aligned; C and the workspace overlap no input and not each other.
+ *   workspace  at least gemm_bf16_tn_workspace_bytes(M, N, K) bytes (0, then NULL will
+ *   do, but where few tiles have a long K, which is divided and summed in order);
+ *   contents on entry ignored, on return unspecified.
  * Errors: GEMM_ERR_NULL, _SHAPE, _ALIGN, _ALIAS, _ARCH, _LAUNCH, _NO_DEVICE,
  * _CAPTURE.
  */
-GB300GEMM_API int gemm_bf16_tn(const void* A, const void* B, void* C, int M, int N, int K,
-                               void* stream);
+GB300GEMM_API int gemm_bf16_tn(const void* A, const void* B, void* C, void* workspace,
+                               size_t workspace_bytes, int M, int N, int K, void* stream);
+
+/* Workspace bytes gemm_bf16_tn needs (0 for none or invalid arguments). */
+GB300GEMM_API size_t gemm_bf16_tn_workspace_bytes(int M, int N, int K);
 
 /*
  * residual_norm - the residual step between two blocks of a transformer: the norm

@@ -91,7 +91,9 @@ def load() -> ctypes.CDLL:
             lib.gemm_bf16_nt_gated_backward.argtypes = [vp] * 9 + [ctypes.c_size_t] + [i] * 4 + [vp]
             lib.gemm_bf16_nt_gated_backward_workspace_bytes.argtypes = [i] * 3
             lib.gemm_bf16_nt_gated_backward_workspace_bytes.restype = ctypes.c_size_t
-            lib.gemm_bf16_tn.argtypes = [vp] * 3 + [i] * 3 + [vp]
+            lib.gemm_bf16_tn.argtypes = [vp] * 4 + [ctypes.c_size_t] + [i] * 3 + [vp]
+            lib.gemm_bf16_tn_workspace_bytes.argtypes = [i] * 3
+            lib.gemm_bf16_tn_workspace_bytes.restype = ctypes.c_size_t
             lib.residual_norm.argtypes = [vp] * 9 + [f] * 2 + [i] * 4 + [vp]
             lib.residual_norm_backward.argtypes = [vp] * 15 + [ctypes.c_size_t, f] + [i] * 4 + [vp]
             lib.residual_norm_backward_workspace_bytes.argtypes = [i] * 5
@@ -757,7 +759,14 @@ def gemm_bf16_nt_gated_backward(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Ten
     return dX, dWg, dWu
 
 
-def gemm_bf16_tn(A: torch.Tensor, B: torch.Tensor, C: torch.Tensor | None = None, stream=None):
+def gemm_bf16_tn_workspace_bytes(M: int, N: int, K: int) -> int:
+    if not (0 <= M <= _INT_MAX and 0 <= N <= _INT_MAX and 0 <= K <= _INT_MAX):
+        return 0
+    return int((_lib or load()).gemm_bf16_tn_workspace_bytes(M, N, K))
+
+
+def gemm_bf16_tn(A: torch.Tensor, B: torch.Tensor, C: torch.Tensor | None = None,
+                 workspace: torch.Tensor | None = None, stream=None):
     """C[M,N] = bf16(A[K,M]^T . B[K,N]), FP32 accumulation: a weight gradient dY^T X."""
     _mat(A, torch.bfloat16, "A")
     _mat(B, torch.bfloat16, "B")
@@ -773,12 +782,13 @@ def gemm_bf16_tn(A: torch.Tensor, B: torch.Tensor, C: torch.Tensor | None = None
     elsewhere = _context(device, stream)
     if elsewhere is not None:
         with elsewhere:
-            return gemm_bf16_tn(A, B, C)
+            return gemm_bf16_tn(A, B, C, workspace)
     if C is None:
         C = torch.empty((M, N), dtype=torch.bfloat16, device=device)
     else:
         _on_device("C", device, C, torch.bfloat16, (M, N))
-    _run("gemm_bf16_tn", device, A.data_ptr(), B.data_ptr(), C.data_ptr(), M, N, K)
+    ws, nbytes, _alive = _workspace(workspace, gemm_bf16_tn_workspace_bytes(M, N, K), device)
+    _run("gemm_bf16_tn", device, A.data_ptr(), B.data_ptr(), C.data_ptr(), ws, nbytes, M, N, K)
     return C
 
 

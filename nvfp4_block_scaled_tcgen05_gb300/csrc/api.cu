@@ -675,20 +675,30 @@ int gemm_bf16_nt_gated_backward(const void* X, const void* Wg, const void* Wu, c
   return launch_gated_backward(a, dev, static_cast<cudaStream_t>(stream));
 }
 
-int gemm_bf16_tn(const void* A, const void* B, void* C, int M, int N, int K, void* stream) {
+size_t gemm_bf16_tn_workspace_bytes(int M, int N, int K) {
+  if (M <= 0 || N <= 0 || K <= 0 || M > kMaxDim || N > kMaxDim || K > kMaxDim) return 0;
+  return gemm_bf16_tn_workspace(M, N, K);
+}
+
+int gemm_bf16_tn(const void* A, const void* B, void* C, void* workspace, size_t workspace_bytes,
+                 int M, int N, int K, void* stream) {
   if (!A || !B || !C) return GEMM_ERR_NULL;
   if (M <= 0 || N <= 0 || K <= 0) return GEMM_ERR_SHAPE;
   if (M > kMaxDim || N > kMaxDim || K > kMaxDim) return GEMM_ERR_SHAPE;
   const long long tiles = ((long long)M + 127) / 128 * (((long long)N + 63) / 64);
   if (tiles > kMaxTiles) return GEMM_ERR_SHAPE;
-  if (!aligned16(A) || !aligned16(B) || !aligned16(C)) return GEMM_ERR_ALIGN;
+  if (!aligned16(A) || !aligned16(B) || !aligned16(C) || !aligned16(workspace)) return GEMM_ERR_ALIGN;
   if (M % 8 != 0 || N % 8 != 0) return GEMM_ERR_ALIGN;  // 16-byte row pitch of A, B and C
-  const size_t sa = size_t(K) * M * 2, sb = size_t(K) * N * 2, sc = size_t(M) * N * 2;
-  if (overlaps(C, sc, A, sa) || overlaps(C, sc, B, sb)) return GEMM_ERR_ALIAS;
+  const size_t need = gemm_bf16_tn_workspace(M, N, K);
+  if (need && !workspace) return GEMM_ERR_NULL;
+  if (workspace_bytes < need) return GEMM_ERR_SHAPE;
+  const Span in[] = {{A, size_t(K) * M * 2}, {B, size_t(K) * N * 2}};
+  const Span out[] = {{C, size_t(M) * N * 2}, {workspace, need}};
+  if (any_overlap(in, 2, out, 2)) return GEMM_ERR_ALIAS;
   DeviceInfo dev;
   const int rc = current_device(&dev, stream);
   if (rc != GEMM_OK) return rc;
-  return launch_gemm_bf16_tn(A, B, C, M, N, K, dev, static_cast<cudaStream_t>(stream));
+  return launch_gemm_bf16_tn(A, B, C, workspace, M, N, K, dev, static_cast<cudaStream_t>(stream));
 }
 
 int residual_norm(const void* x, const void* block, const void* w_post, const void* gate,

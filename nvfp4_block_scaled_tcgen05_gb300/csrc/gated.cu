@@ -26,11 +26,17 @@ namespace gb300 {
 namespace {
 
 using FwdPair = GatedCfg<TileCfg<Operand::kBF16, 2, 256, 3, 4, 2, true, false, 2>>;
-// Forward of few tokens: the weights on the MMA's M side, half of a tile's rows of each
-// matrix, the tokens on the N side, so that the kernel streams the weights.
+// Few tokens: the weights on the MMA's M side, half of a tile's rows of each matrix, the
+// tokens on the N side, so that the kernel streams the weights.  (11008 x 2048: one token
+// 42 us on the tiles above, 20.8 on these, 128 tokens 23.5, 129 on the others 28.)
+// Their gradient reads dH two bytes at a time, which pays up to 32 tokens (5504 x 2048,
+// all gradients from X: one token 56 -> 44.7 us, 16 tokens 49 -> 41, 128 50.8 -> 52.8).
+constexpr int kFewTokens = 128, kFewTokensGrad = 32;
 template <int BN, int STAGES>
-using FwdFew = PairedRowsCfg<
+using Few = PairedRowsCfg<
     FewTokensCfg<TileCfg<Operand::kBF16, 2, BN, STAGES, 4, 1, true, false, 2>, true>>;
+using Few64 = Few<64, 5>;
+using Few128 = Few<128, 4>;
 template <bool kAmn>
 using ChainPair =
     TrimCfg<TileCfg<Operand::kBF16, 2, 256, 3, 4, 2, true, false, 2, true, false, kAmn, true>>;
@@ -87,20 +93,23 @@ int setup_gated(const void* X, const void* Wg, const void* Wu, int act, int M, i
   return rc;
 }
 
-template <class Cfg>
-int run_forward_few(const GatedForward& a, const DeviceInfo& dev, cudaStream_t stream) {
+// The few tokens' form of both: H (and the gates), or with dH the two gradients.
+template <class Cfg, Epilogue EPI>
+int run_few(const void* X, const void* Wg, const void* Wu, const void* dH, void* out, void* gates,
+            int act, int M, int F, int K, const DeviceInfo& dev, cudaStream_t stream) {
   CUtensorMap tx, tg, tu;
-  const int rows = few_rows(2 * a.F, Cfg::BN) / 2;  // of each matrix, per CTA and tile
-  int rc = encode_rows(&tx, a.X, a.M, a.K, Cfg::B_ROWS);
-  if (rc == GEMM_OK) rc = encode_rows(&tg, a.Wg, a.F, a.K, rows);
-  if (rc == GEMM_OK) rc = encode_rows(&tu, a.Wu, a.F, a.K, rows);
+  const int rows = few_rows(2 * F, Cfg::BN) / 2;  // of each matrix, per CTA and tile
+  int rc = encode_rows(&tx, X, M, K, Cfg::B_ROWS);
+  if (rc == GEMM_OK) rc = encode_rows(&tg, Wg, F, K, rows);
+  if (rc == GEMM_OK) rc = encode_rows(&tu, Wu, F, K, rows);
   if (rc != GEMM_OK) return rc;
-  GemmParams p = base_params<Cfg>(a.F, a.M, a.K, dev);
+  GemmParams p = base_params<Cfg>(F, M, K, dev);
   set_few_rows(p, rows);
-  p.act = a.act;
-  p.c_ptr = a.H;
-  p.gates_ptr = static_cast<uint16_t*>(a.gates);
-  return launch_tcgen05<Cfg, Epilogue::kGatedTBF16>(tg, tx, tg, tu, tg, p, dev, stream);
+  p.act = act;
+  p.c_ptr = out;
+  p.dh = static_cast<const uint16_t*>(dH);
+  p.gates_ptr = static_cast<uint16_t*>(gates);
+  return launch_tcgen05<Cfg, EPI>(tg, tx, tg, tu, tg, p, dev, stream);
 }
 
 // dG and dU [2][n] from the stored gates [2][n]: three values read and two written
@@ -170,6 +179,32 @@ GatedPlan make_plan(int M, int F, int K) {
   return q;
 }
 
+// Divides the K loop in `splits` parts, none of them empty, that are summed later.
+void split_k(GemmParams& p, int splits) {
+  p.kb_per_split = (p.num_k_blocks + splits - 1) / splits;
+  p.k_splits = p.L = splits;
+  p.total_tiles *= splits;
+}
+
+// Parts of A^T B's K loop, where its tiles leave CTA pairs idle: cost in K blocks as in
+// make_plan, four for the second grid.
+int tn_splits(int M, int N, int K) {
+  const long long tiles = (long long)((M + 255) / 256) * ((N + 255) / 256);
+  const int nkb = (K + TnPair::BK - 1) / TnPair::BK;
+  int splits = 1;
+  double best = 1e300;
+  for (int want = 1; want <= std::max(1, nkb / 4) && want * tiles <= 2 * kPairs + tiles; ++want) {
+    const int per = (nkb + want - 1) / want, s = (nkb + per - 1) / per;
+    const double parts = s > 1 ? double(s) * M * double(N) * 8.0 / 3.4e6 + 4.0 : 0.0;
+    const double cost = double((tiles * s + kPairs - 1) / kPairs) * (per + 2) + parts;
+    if (cost < 0.95 * best) {
+      best = cost;
+      splits = s;
+    }
+  }
+  return splits;
+}
+
 int run_grad(const GatedBackward& a, uint16_t* grad, const DeviceInfo& dev, cudaStream_t stream) {
   if (a.gates) {
     const size_t n = size_t(a.M) * a.F;
@@ -181,6 +216,9 @@ int run_grad(const GatedBackward& a, uint16_t* grad, const DeviceInfo& dev, cuda
                             static_cast<const uint16_t*>(a.gates),
                             static_cast<const uint16_t*>(a.dH), grad, n);
   }
+  if (a.M <= kFewTokensGrad)
+    return run_few<Few64, Epilogue::kGatedGradTBF16>(a.X, a.Wg, a.Wu, a.dH, grad, nullptr, a.act, a.M,
+                                                     a.F, a.K, dev, stream);
   using Cfg = FwdPair;
   CUtensorMap tx, tg, tu, tc;
   GemmParams p;
@@ -217,9 +255,7 @@ int run_dx(const GatedBackward& a, const GatedPlan& q, const uint16_t* grad, flo
   rc = encode_tmap_3d(&tc, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, parts, uint64_t(a.K),
                       uint64_t(a.M), uint64_t(q.splits), 32, 32, CU_TENSOR_MAP_SWIZZLE_128B);
   if (rc != GEMM_OK) return rc;
-  p.kb_per_split = (p.num_k_blocks + q.splits - 1) / q.splits;
-  p.k_splits = p.L = q.splits;
-  p.total_tiles *= q.splits;
+  split_k(p, q.splits);
   *grid = {p.total_tiles, p.kb_per_split + 2.0};
   return launch_tcgen05<Cfg, Epilogue::kAddF32>(tdg, tg, tc, tdu, tu, p, dev, stream);
 }
@@ -250,8 +286,10 @@ size_t gated_backward_workspace(int M, int F, int K) {
 }
 
 int launch_gated_forward(const GatedForward& a, const DeviceInfo& dev, cudaStream_t stream) {
-  if (a.M <= 64) return run_forward_few<FwdFew<64, 5>>(a, dev, stream);
-  if (a.M <= 128) return run_forward_few<FwdFew<128, 4>>(a, dev, stream);
+  if (a.M <= kFewTokens) {
+    const auto few = a.M <= 64 ? run_few<Few64, Epilogue::kGatedTBF16> : run_few<Few128, Epilogue::kGatedTBF16>;
+    return few(a.X, a.Wg, a.Wu, nullptr, a.H, a.gates, a.act, a.M, a.F, a.K, dev, stream);
+  }
   using Cfg = FwdPair;
   CUtensorMap tx, tg, tu, th, tk;
   GemmParams p;
@@ -277,16 +315,29 @@ int launch_gated_backward(const GatedBackward& a, const DeviceInfo& dev, cudaStr
   return rc;
 }
 
-int launch_gemm_bf16_tn(const void* A, const void* B, void* C, int M, int N, int K,
+size_t gemm_bf16_tn_workspace(int M, int N, int K) {
+  const int splits = tn_splits(M, N, K);
+  return splits == 1 ? 0 : size_t(splits) * M * size_t(N) * 4;
+}
+
+int launch_gemm_bf16_tn(const void* A, const void* B, void* C, void* workspace, int M, int N, int K,
                         const DeviceInfo& dev, cudaStream_t stream) {
   using Cfg = TnPair;
   CUtensorMap ta, tb, tc;
+  const int splits = tn_splits(M, N, K);
   int rc = encode_rows(&ta, A, K, M, Cfg::BK);
   if (rc == GEMM_OK) rc = encode_rows(&tb, B, K, N, Cfg::BK);
-  if (rc == GEMM_OK) rc = encode_rows(&tc, C, M, N, 32);
+  if (rc == GEMM_OK)
+    rc = splits == 1 ? encode_rows(&tc, C, M, N, 32)
+                     : encode_tmap_3d(&tc, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, workspace, uint64_t(N),
+                                      uint64_t(M), uint64_t(splits), 32, 32, CU_TENSOR_MAP_SWIZZLE_128B);
   if (rc != GEMM_OK) return rc;
-  const GemmParams p = base_params<Cfg>(M, N, K, dev);
-  return launch_tcgen05<Cfg, Epilogue::kStoreBF16>(ta, tb, tc, ta, ta, p, dev, stream);
+  GemmParams p = base_params<Cfg>(M, N, K, dev);
+  if (splits == 1) return launch_tcgen05<Cfg, Epilogue::kStoreBF16>(ta, tb, tc, ta, ta, p, dev, stream);
+  split_k(p, splits);
+  rc = launch_tcgen05<Cfg, Epilogue::kAddF32>(ta, tb, tc, ta, ta, p, dev, stream);
+  if (rc != GEMM_OK) return rc;
+  return launch_sum_slots(static_cast<const float*>(workspace), C, size_t(M) * N, splits, dev, stream);
 }
 
 }  // namespace gb300

@@ -158,7 +158,8 @@ struct GatedBackward {
 size_t gated_backward_workspace(int M, int F, int K);
 int launch_gated_forward(const GatedForward& a, const DeviceInfo& dev, cudaStream_t stream);
 int launch_gated_backward(const GatedBackward& a, const DeviceInfo& dev, cudaStream_t stream);
-int launch_gemm_bf16_tn(const void* A, const void* B, void* C, int M, int N, int K,
+size_t gemm_bf16_tn_workspace(int M, int N, int K);
+int launch_gemm_bf16_tn(const void* A, const void* B, void* C, void* workspace, int M, int N, int K,
                         const DeviceInfo& dev, cudaStream_t stream);
 
 // Few tokens times NVFP4 weights (gemv_w4a16.cu), M <= kGemvMaxM; with b[1] the

@@ -60,6 +60,7 @@ enum class Operand : int { kBF16 = 0, kNVFP4 = 1, kW4A16 = 2 };
 // kGatedTBF16 (PAIRED_ROWS tiles): kGatedBF16 with the roles swapped (rows of D are the
 //   weights', columns the tokens)
 // kGatedGradBF16: C[0] = bf16(dH * up * act'(gate)), C[1] = bf16(dH * act(gate))
+// kGatedGradTBF16 (PAIRED_ROWS tiles): the same with the roles swapped
 enum class Epilogue : int {
   kStoreBF16 = 0,
   kScaledAccBF16 = 1,
@@ -73,7 +74,8 @@ enum class Epilogue : int {
   kXentGradTBF16 = 9,
   kGatedBF16 = 10,
   kGatedGradBF16 = 11,
-  kGatedTBF16 = 12
+  kGatedTBF16 = 12,
+  kGatedGradTBF16 = 13
 };
 
 struct GemmParams {
@@ -111,7 +113,7 @@ struct GemmParams {
   // gated projection (kGated*)
   int act;                        // GEMM_ACT_*
   int gates_out;                  // kGatedBF16: store the factors too
-  const uint16_t* dh;             // kGatedGradBF16: gradient of the output, [M][N]
+  const uint16_t* dh;             // kGatedGrad*: gradient of the output, [rows][F]
   uint16_t* gates_ptr;            // kGatedTBF16: the factors' place, or null
   int k_half;                     // DUAL_K: K blocks of the first pair of operands
   int n_wide;                     // GATED: N blocks of full width
@@ -627,12 +629,13 @@ __device__ __forceinline__ void gated_product(int act, uint32_t (&g)[32], const 
   else all(ActKind<GEMM_ACT_GELU_TANH>{});
 }
 
-// g <- dh u act'(g), u <- dh act(g); dh: the 32 values of the output's gradient.
+// g <- dh u act'(g), u <- dh act(g); dh: the values of the output's gradient.
+template <int kCols = 32>
 __device__ __forceinline__ void gated_gradient(int act, uint32_t (&g)[32], uint32_t (&u)[32],
-                                               const uint4 (&dh)[4]) {
+                                               const uint4 (&dh)[kCols / 8]) {
   auto all = [&](auto kind) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
+    for (int i = 0; i < kCols; ++i) {
       const uint32_t w = (&dh[i / 8].x)[(i % 8) / 2];
       const float d = i % 2 ? bf16_hi(w) : bf16_lo(w);
       const float2 a = gate_act_slope<decltype(kind)::value>(__uint_as_float(g[i]));
@@ -2129,7 +2132,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
             send(&tmap_c, sbuf, col0, 1);
           }
         }
-      } else if constexpr (EPI == Epilogue::kGatedTBF16) {
+      } else if constexpr (EPI == Epilogue::kGatedTBF16 || EPI == Epilogue::kGatedGradTBF16) {
         // Warps q and q + 2 hold the gate and the up row of a lane's output: each gives
         // the other half of its tokens through the two halves of its box in turn, and
         // takes the other half of the outputs.  Two-byte stores, 64 bytes of a token's
@@ -2170,6 +2173,27 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
           }
           const int tok = tok0 + (gate ? 0 : 16);
           const size_t at = size_t(tok) * p.M + f, all = size_t(p.N) * p.M;
+          uint16_t* out = static_cast<uint16_t*>(p.c_ptr);
+          if constexpr (EPI == Epilogue::kGatedGradTBF16) {
+            uint4 dh[2];  // of the 16 tokens
+            uint32_t* d = &dh[0].x;
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) {
+              const uint32_t lo = live && tok + i < p.N ? __ldcg(p.dh + at + size_t(i) * p.M) : 0;
+              const uint32_t hi = live && tok + i + 1 < p.N ? __ldcg(p.dh + at + size_t(i + 1) * p.M) : 0;
+              d[i / 2] = lo | hi << 16;
+            }
+            gated_gradient<16>(p.act, g, u, dh);
+            if (live) {
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                if (tok + i < p.N) {
+                  out[at + size_t(i) * p.M] = uint16_t(pack_bf16x2(g[i], 0u));
+                  out[all + at + size_t(i) * p.M] = uint16_t(pack_bf16x2(u[i], 0u));
+                }
+            }
+            continue;
+          }
           if (p.gates_ptr && live) {
 #pragma unroll
             for (int i = 0; i < 16; ++i)
@@ -2183,7 +2207,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
 #pragma unroll
             for (int i = 0; i < 16; ++i)
               if (tok + i < p.N)
-                static_cast<uint16_t*>(p.c_ptr)[at + size_t(i) * p.M] = uint16_t(pack_bf16x2(g[i], 0u));
+                out[at + size_t(i) * p.M] = uint16_t(pack_bf16x2(g[i], 0u));
           }
         }
       } else if constexpr (EPI == Epilogue::kStoreF32 || EPI == Epilogue::kAddF32) {

@@ -48,14 +48,20 @@ def test_gated_backward_rejects_bad_arguments(lib, kw, expect):  # noqa: F811
     assert gated_backward(lib, **kw) == expect
 
 
-@pytest.mark.parametrize("args,expect", [
-    ((0, 2 * P, 3 * P, 8, 8, 8), 1), ((P, 0, 3 * P, 8, 8, 8), 1), ((P, 2 * P, 0, 8, 8, 8), 1),
-    ((P, 2 * P, 3 * P, 0, 8, 8), 2), ((P, 2 * P, 3 * P, 8, -8, 8), 2), ((P, 2 * P, 3 * P, 8, 8, 0), 2), ((P, 2 * P, 3 * P, 1 << 30, 1 << 30, 8), 2),
-    ((P + 8, 2 * P, 3 * P, 8, 8, 8), 3), ((P, 2 * P, 3 * P, 12, 8, 8), 3), ((P, 2 * P, 3 * P, 8, 4, 8), 3),
-    ((P, 2 * P, P + 16, 8, 8, 8), 4), ((P, 2 * P, 2 * P, 8, 8, 8), 4),
+def tn(lib, **kw):
+    a = dict(A=P, B=2 * P, C=3 * P, ws=4 * P, n=BIG, M=64, N=72, K=4096)
+    a.update(kw)
+    return lib.gemm_bf16_tn(a["A"], a["B"], a["C"], a["ws"], a["n"], a["M"], a["N"], a["K"], None)
+
+
+@pytest.mark.parametrize("kw,expect", [
+    ({"A": 0}, 1), ({"B": 0}, 1), ({"C": 0}, 1), ({"ws": 0}, 1),
+    ({"M": 0}, 2), ({"N": -8}, 2), ({"K": 0}, 2), ({"M": 1 << 30, "N": 1 << 30}, 2), ({"n": 64 * 72 * 4}, 2),
+    ({"A": P + 8}, 3), ({"B": 2 * P + 2}, 3), ({"C": 3 * P + 4}, 3), ({"ws": 4 * P + 8}, 3), ({"M": 60}, 3), ({"N": 76}, 3),
+    ({"C": P + 16}, 4), ({"C": 2 * P}, 4), ({"ws": P}, 4), ({"ws": 3 * P + 16}, 4),
 ])
-def test_tn_rejects_bad_arguments(lib, args, expect):  # noqa: F811
-    assert lib.gemm_bf16_tn(*args, None) == expect
+def test_tn_rejects_bad_arguments(lib, kw, expect):  # noqa: F811
+    assert tn(lib, **kw) == expect
 
 
 def norm(lib, **kw):
@@ -133,6 +139,9 @@ def test_workspace_sizes(lib):  # noqa: F811
     assert f(5120, 11008, 2048) >= 5120 * 11008 * 4
     # dX of few tokens is summed from parts of a long K loop
     assert f(1, 11008, 2048) > 11008 * 4 + 2048 * 4
+    t = lib.gemm_bf16_tn_workspace_bytes
+    assert t(0, 8, 8) == 0 and t(2048, 11008, 5120) == 0   # tiles enough
+    assert t(64, 72, 4096) >= 2 * 64 * 72 * 4              # one tile, a long K
     n = lib.residual_norm_backward_workspace_bytes
     assert n(100, 64, 100, 0, 0) == 0                            # no gradient of a weight: none
     assert n(100, 60, 100, 1, 0) == 0 and n(100, 64, 30, 1, 1) == 0  # invalid

@@ -69,7 +69,8 @@ def test_backward(g, M, F, K, kind, kept):
 
 
 @pytest.mark.parametrize("M,N,K", [(8, 8, 1), (136, 72, 1), (128, 256, 3), (264, 520, 100), (256, 256, 128), (1000, 248, 129),
-                                   (520, 2056, 777), (2048, 1032, 4096)])
+                                   (520, 2056, 777), (2048, 1032, 4096), (8, 16, 5000), (512, 520, 4097),
+                                   (1024, 1288, 2500)])
 def test_tn(g, M, N, K):
     A, B = randn(3, K, M), randn(4, K, N)
     want = A.to(ref.F64).T @ B.to(ref.F64)
