@@ -75,17 +75,19 @@ struct Raw8<true> {
   }
   __device__ __forceinline__ Vec8 get() const { return a; }
 };
-// Stores piece i of eight values and returns them as they are stored.
+// Stores piece i of eight values, where `live`, and returns them as they are stored.
 template <bool kF32>
-__device__ __forceinline__ Vec8 store8(void* p, size_t i, const Vec8& v) {
+__device__ __forceinline__ Vec8 store8(void* p, size_t i, const Vec8& v, bool live = true) {
   if constexpr (kF32) {
     float4* q = static_cast<float4*>(p) + 2 * i;
-    q[0] = make_float4(v.v[0].x, v.v[0].y, v.v[1].x, v.v[1].y);
-    q[1] = make_float4(v.v[2].x, v.v[2].y, v.v[3].x, v.v[3].y);
+    if (live) {
+      q[0] = make_float4(v.v[0].x, v.v[0].y, v.v[1].x, v.v[1].y);
+      q[1] = make_float4(v.v[2].x, v.v[2].y, v.v[3].x, v.v[3].y);
+    }
     return v;
   } else {
     const uint4 w = pack8(v);
-    static_cast<uint4*>(p)[i] = w;
+    if (live) static_cast<uint4*>(p)[i] = w;
     return unpack8(w);
   }
 }
@@ -232,15 +234,18 @@ struct Ring {
 };
 
 // ---------------------------------------------------------------- forward
-template <bool kF32, int V, int kThreads>
+// kFull: there are a block and both norms, the usual call, whose choices are then made
+// at compile time (below: `has_*`).
+template <bool kF32, int V, int kThreads, bool kFull>
 __global__ void __launch_bounds__(kThreads, 1)
     residual_norm_kernel(const ResidualNorm a, const Shape shape, unsigned int* status,
                          unsigned long long timeout_ns) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float parts[kMaxWarps][2][2][kMaxWarps];
+  const bool has_block = kFull || a.block, has_post = kFull || a.w_post, has_pre = kFull || a.w_pre;
   Ring<2> ring;
   ring.src[0] = {a.x, uint32_t(a.D) * (kF32 ? 4u : 2u)};
-  ring.src[1] = {a.block, a.block ? uint32_t(a.D) * 2u : 0u};
+  ring.src[1] = {a.block, has_block ? uint32_t(a.D) * 2u : 0u};
   ring.init(smem, shape, status, timeout_ns);
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
@@ -248,15 +253,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int first = int(blockIdx.x) * shape.units + ring.unit;
   if (ring.tid == 0)
     for (int i = 0, row = first; i < shape.stages && row < a.M; ++i, row += step) ring.fill(row);
+  // This thread's pieces.  A place past the row's end reads the last piece again; its
+  // values are set to zero, and not stored.
+  int at[V];
   uint4 w_pre[V];
   Vec8 p[V];  // scale * gate * w_post
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int c = ring.tid + i * threads;
-    w_pre[i] = a.w_pre && c < pieces ? static_cast<const uint4*>(a.w_pre)[c] : make_uint4(0, 0, 0, 0);
-    p[i] = a.block && !a.gate && c < pieces ? times_weight(scaled_gate(a.scale, nullptr, 0), a.w_post, c)
-                                            : zero8();
+    at[i] = min(c, pieces - 1);
+    w_pre[i] = has_pre ? static_cast<const uint4*>(a.w_pre)[at[i]] : make_uint4(0, 0, 0, 0);
+    p[i] = has_block && !a.gate ? times_weight(scaled_gate(a.scale, nullptr, 0), a.w_post, at[i]) : zero8();
   }
+  auto live = [&](int i) { return ring.tid + i * threads < pieces; };
   int gate_row = -1;
   float(*part)[2][kMaxWarps] = parts[ring.unit];
   int odd = 0;
@@ -265,25 +274,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (a.gate && row / a.rows_per_gate != gate_row) {
       gate_row = row / a.rows_per_gate;
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int c = ring.tid + i * threads;
-        if (c < pieces)
-          p[i] = times_weight(scaled_gate(a.scale, a.gate, size_t(gate_row) * pieces + c), a.w_post, c);
-      }
+      for (int i = 0; i < V; ++i)
+        p[i] = times_weight(scaled_gate(a.scale, a.gate, size_t(gate_row) * pieces + at[i]), a.w_post, at[i]);
     }
     const uint8_t* mem = ring.wait();
     Vec8 y[V], b[V];
     float2 s2 = both(0.0f);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int c = ring.tid + i * threads;
-      y[i] = b[i] = zero8();
-      if (c < pieces) {
-        Raw8<kF32> x;
-        x.read(mem, c);
-        y[i] = x.get();
-        if (a.block) b[i] = unpack8(reinterpret_cast<const uint4*>(mem + ring.src[0].bytes)[c]);
-      }
+      Raw8<kF32> x;
+      x.read(mem, at[i]);
+      y[i] = x.get();
+      b[i] = zero8();
+      if (has_block) b[i] = unpack8(reinterpret_cast<const uint4*>(mem + ring.src[0].bytes)[at[i]]);
+      if (!live(i)) y[i] = b[i] = zero8();
 #pragma unroll
       for (int j = 0; j < 4; ++j) s2 = ptx::fma2(b[i].v[j], b[i].v[j], s2);
     }
@@ -292,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int ahead = row + shape.stages * step;
     const bool refill = ring.tid == 0 && ahead < a.M && ahead > row;
     float r = 1.0f;
-    if (a.w_post) {
+    if (has_post) {
       float s[1] = {s2.x + s2.y};
       ring.sum(s, part[odd][0]);
       if (refill) ring.fill(ahead);
@@ -302,33 +306,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     s2 = both(0.0f);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int c = ring.tid + i * threads;
-      if (c >= pieces) break;
-      if (a.block) {
+      if (has_block) {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
           y[i].v[j] = ptx::fma2(ptx::mul2(b[i].v[j], both(r)), p[i].v[j], y[i].v[j]);
-        y[i] = store8<kF32>(a.y, base + c, y[i]);
+        y[i] = store8<kF32>(a.y, base + at[i], y[i], live(i));
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j) s2 = ptx::fma2(y[i].v[j], y[i].v[j], s2);
     }
-    if (a.w_pre) {
+    if (has_pre) {
       float s[1] = {s2.x + s2.y};
       ring.sum(s, part[odd][1]);
-      if (refill && !a.w_post) ring.fill(ahead);
+      if (refill && !has_post) ring.fill(ahead);
       const float ry = inverse_rms(s[0], a.D, a.eps);
       if (ring.tid == 0 && a.rstd_pre) a.rstd_pre[row] = ry;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        const int c = ring.tid + i * threads;
-        if (c >= pieces) break;
         const Vec8 w = unpack8(w_pre[i]);
 #pragma unroll
         for (int j = 0; j < 4; ++j) y[i].v[j] = ptx::mul2(ptx::mul2(y[i].v[j], both(ry)), w.v[j]);
-        static_cast<uint4*>(a.n)[base + c] = pack8(y[i]);
+        store8<false>(a.n, base + at[i], y[i], live(i));
       }
-    } else if (!a.w_post) {
+    } else if (!has_post) {
       ring.sync();
       if (refill) ring.fill(ahead);
     }
@@ -344,18 +344,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 // thread keeps its columns' sums of the run in registers; a block's units are added
 // in order and go to the block's place in the workspace, [block][kinds][D]: dn yh,
 // and T, which the join multiplies, or (several gate groups in a run, kMulti) dw_post.
-template <bool kF32, int V, int kThreads, bool kMulti>
+template <bool kF32, int V, int kThreads, bool kMulti, bool kFull>
 __global__ void __launch_bounds__(kThreads, 1)
     residual_norm_backward_kernel(const ResidualNormBackward a, const Shape shape,
                                   unsigned int* status, unsigned long long timeout_ns) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float parts[kMaxWarps][2][3 * kMaxWarps];
+  const bool has_dy = kFull || a.dy, has_block = kFull || a.block, has_post = kFull || a.w_post,
+             has_pre = kFull || a.w_pre;
   Ring<4> ring;
   const uint32_t wide = uint32_t(a.D) * (kF32 ? 4u : 2u), narrow = uint32_t(a.D) * 2u;
-  ring.src[0] = {a.dy, a.dy ? wide : 0u};
-  ring.src[1] = {a.y, a.w_pre ? wide : 0u};
-  ring.src[2] = {a.dn, a.w_pre ? narrow : 0u};
-  ring.src[3] = {a.block, a.block ? narrow : 0u};
+  ring.src[0] = {a.dy, has_dy ? wide : 0u};
+  ring.src[1] = {a.y, has_pre ? wide : 0u};
+  ring.src[2] = {a.dn, has_pre ? narrow : 0u};
+  ring.src[3] = {a.block, has_block ? narrow : 0u};
   ring.init(smem, shape, status, timeout_ns);
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
@@ -377,32 +379,35 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int begin = row;
   if (ring.tid == 0)
     for (int i = 0; i < shape.stages && row + i < end; ++i) ring.fill(row + i);
+  // This thread's pieces.  A place past the row's end reads the last piece again, and
+  // neither joins the row's sums nor is stored.
+  int at[V];
+  auto live = [&](int i) { return ring.tid + i * threads < pieces; };
   uint4 w_pre[V];
   Vec8 dwi[V], T[V], dwo[kMulti ? V : 1];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    const int c = ring.tid + i * threads;
-    w_pre[i] = a.w_pre && c < pieces ? static_cast<const uint4*>(a.w_pre)[c]
-                                     : make_uint4(0, 0, 0, 0);
+    at[i] = min(ring.tid + i * threads, pieces - 1);
+    w_pre[i] = has_pre && live(i) ? static_cast<const uint4*>(a.w_pre)[at[i]] : make_uint4(0, 0, 0, 0);
     dwi[i] = T[i] = zero8();
     if constexpr (kMulti) dwo[i] = zero8();
   }
   Vec8 p[V];
   int gate_row = -1;
-  auto read_gate = [&](int at) {
-    gate_row = at;
+  auto read_gate = [&](int gate) {
+    gate_row = gate;
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int c = ring.tid + i * threads;
-      p[i] = a.block && c < pieces ? times_weight(scaled_gate(a.scale, a.gate, size_t(at) * pieces + c), a.w_post, c) : zero8();
-    }
+    for (int i = 0; i < V; ++i)
+      p[i] = has_block && live(i)
+                 ? times_weight(scaled_gate(a.scale, a.gate, size_t(gate) * pieces + at[i]), a.w_post, at[i])
+                 : zero8();
   };
   if (!kMulti) read_gate(row < end ? row / a.rows_per_gate : 0);
   float(*part)[3 * kMaxWarps] = parts[ring.unit];
   float ry = 0.0f, rb = 1.0f;
-  auto read_rstd = [&](int at) {
-    if (a.w_pre) ry = __ldcg(a.rstd_pre + at);
-    if (a.w_post) rb = __ldcg(a.rstd_post + at);
+  auto read_rstd = [&](int of) {
+    if (has_pre) ry = __ldcg(a.rstd_pre + of);
+    if (has_post) rb = __ldcg(a.rstd_post + of);
   };
   if (row < end) read_rstd(row);
   int odd = 0;
@@ -412,51 +417,55 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float r_y = ry, r_b = rb;
     const uint8_t* mem = ring.wait();
     if (row + 1 < end) read_rstd(row + 1);  // a row ahead
-    const uint8_t *mem_y = mem + (a.dy ? wide : 0u), *mem_n = mem_y + wide;
-    const uint8_t* mem_b = a.w_pre ? mem_n + narrow : mem_y;
+    const uint8_t *mem_y = mem + (has_dy ? wide : 0u), *mem_n = mem_y + wide;
+    const uint8_t* mem_b = has_pre ? mem_n + narrow : mem_y;
     Vec8 u[V];
     float2 s0 = both(0.0f), s1 = s0, s2 = s0;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int c = ring.tid + i * threads;
       u[i] = zero8();
-      if (c >= pieces) continue;
       Vec8 yh = zero8();
-      if (a.dy) {
+      float2 q0 = both(0.0f), q1 = q0, q2 = q0;
+      if (has_dy) {
         Raw8<kF32> d;
-        d.read(mem, c);
+        d.read(mem, at[i]);
         u[i] = d.get();
       }
-      if (a.w_pre) {
+      if (has_pre) {
         Raw8<kF32> y;
-        y.read(mem_y, c);
+        y.read(mem_y, at[i]);
         yh = y.get();
-        const Vec8 d = unpack8(reinterpret_cast<const uint4*>(mem_n)[c]), w = unpack8(w_pre[i]);
+        const Vec8 d = unpack8(reinterpret_cast<const uint4*>(mem_n)[at[i]]), w = unpack8(w_pre[i]);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           yh.v[j] = ptx::mul2(yh.v[j], both(r_y));
           dwi[i].v[j] = ptx::fma2(d.v[j], yh.v[j], dwi[i].v[j]);
           const float2 e = ptx::mul2(d.v[j], w.v[j]);
-          s0 = ptx::fma2(e, yh.v[j], s0);
+          q0 = ptx::fma2(e, yh.v[j], q0);
           u[i].v[j] = ptx::fma2(e, both(r_y), u[i].v[j]);
         }
       }
-      if (a.w_post) {
-        const Vec8 b = unpack8(reinterpret_cast<const uint4*>(mem_b)[c]);
+      if (has_post) {
+        const Vec8 b = unpack8(reinterpret_cast<const uint4*>(mem_b)[at[i]]);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           // p bh, its factor r_b left for the sums
           const float2 pb = ptx::mul2(p[i].v[j], b.v[j]);
-          s1 = ptx::fma2(pb, u[i].v[j], s1);
-          s2 = ptx::fma2(pb, yh.v[j], s2);
+          q1 = ptx::fma2(pb, u[i].v[j], q1);
+          q2 = ptx::fma2(pb, yh.v[j], q2);
         }
+      }
+      if (live(i)) {
+        s0 = ptx::add2(s0, q0);
+        s1 = ptx::add2(s1, q1);
+        s2 = ptx::add2(s2, q2);
       }
     }
     // Behind the next barrier every thread is done with the previous row, whose stage
     // then takes another (with one stage: at the end of the row).
     ptx::fence_proxy_async_smem();
     float s[3] = {s0.x + s0.y, s1.x + s1.y, s2.x + s2.y};
-    if (a.w_pre || a.w_post) ring.sum(s, part[odd]);
+    if (has_pre || has_post) ring.sum(s, part[odd]);
     else ring.sync();
     if (ring.tid == 0 && shape.stages > 1 && row > begin && shape.stages - 1 < end - row)
       ring.fill(row - 1 + shape.stages);
@@ -466,33 +475,31 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool last = kMulti && ((row + 1) % a.rows_per_gate == 0 || row + 1 == end);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int c = ring.tid + i * threads;
-      if (c >= pieces) break;
-      if (a.w_pre) {
+      if (has_pre) {
         Raw8<kF32> y;
-        y.read(mem_y, c);
+        y.read(mem_y, at[i]);
         const Vec8 v = y.get();
 #pragma unroll
         for (int j = 0; j < 4; ++j) u[i].v[j] = ptx::fma2(v.v[j], ny, u[i].v[j]);
       }
-      store8<kF32>(a.dx, base + c, u[i]);
-      if (a.block) {
-        const Vec8 b = unpack8(reinterpret_cast<const uint4*>(mem_b)[c]);
+      store8<kF32>(a.dx, base + at[i], u[i], live(i));
+      if (has_block) {
+        const Vec8 b = unpack8(reinterpret_cast<const uint4*>(mem_b)[at[i]]);
         Vec8 db;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           T[i].v[j] = ptx::fma2(u[i].v[j], ptx::mul2(b.v[j], both(r_b)), T[i].v[j]);
           db.v[j] = ptx::mul2(p[i].v[j], u[i].v[j]);
-          if (a.w_post) db.v[j] = ptx::fma2(b.v[j], nb, ptx::mul2(db.v[j], both(r_b)));
+          if (has_post) db.v[j] = ptx::fma2(b.v[j], nb, ptx::mul2(db.v[j], both(r_b)));
         }
-        static_cast<uint4*>(a.dblock)[base + c] = pack8(db);
+        store8<false>(a.dblock, base + at[i], db, live(i));
         if (last) {  // the gate group's end
-          const Vec8 f = scaled_gate(a.scale, a.gate, size_t(gate_row) * pieces + c);
+          const Vec8 f = scaled_gate(a.scale, a.gate, size_t(gate_row) * pieces + at[i]);
           Vec8 dg;
 #pragma unroll
           for (int j = 0; j < 4; ++j) dg.v[j] = ptx::mul2(both(a.scale), T[i].v[j]);
-          dg = times_weight(dg, a.w_post, c);
-          if (a.dgate) store8<true>(a.dgate, size_t(gate_row) * pieces + c, dg);
+          dg = times_weight(dg, a.w_post, at[i]);
+          if (a.dgate) store8<true>(a.dgate, size_t(gate_row) * pieces + at[i], dg, live(i));
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             if constexpr (kMulti) dwo[i].v[j] = ptx::fma2(f.v[j], T[i].v[j], dwo[i].v[j]);
@@ -692,19 +699,19 @@ int launch_rows(Kernel kernel, const Shape& s, int blocks, std::atomic<int> (&re
   return GEMM_OK;
 }
 
-template <bool kF32, int V, int kThreads>
+template <bool kF32, int V, bool kFull>
 int run_forward(const ResidualNorm& a, const Shape& s, const DeviceInfo& dev, cudaStream_t stream) {
   static std::atomic<int> ready[64];
   const int blocks = std::min((a.M + s.units - 1) / s.units, kBlocks);
-  return launch_rows(residual_norm_kernel<kF32, V, kThreads>, s, blocks, ready, dev, stream, a);
+  return launch_rows(residual_norm_kernel<kF32, V, kThreadsOf[V], kFull>, s, blocks, ready, dev, stream, a);
 }
 
-template <bool kF32, int V, int kThreads, bool kMulti>
+template <bool kF32, int V, bool kMulti, bool kFull>
 int run_backward(const ResidualNormBackward& a, const Shape& s, int blocks, const DeviceInfo& dev,
                  cudaStream_t stream) {
   static std::atomic<int> ready[64];
-  return launch_rows(residual_norm_backward_kernel<kF32, V, kThreads, kMulti>, s, blocks, ready, dev,
-                     stream, a);
+  return launch_rows(residual_norm_backward_kernel<kF32, V, kThreadsOf[V], kMulti, kFull>, s, blocks,
+                     ready, dev, stream, a);
 }
 
 int backward_row_bytes(int D, bool f32, bool dy, bool pre, bool block) {
@@ -724,14 +731,16 @@ size_t residual_norm_backward_workspace(int M, int D, int rows_per_gate, int wei
 
 int launch_residual_norm(const ResidualNorm& a, const DeviceInfo& dev, cudaStream_t stream) {
   const Shape s = make_shape(a.D, a.D * (a.x_f32 ? 4 : 2) + (a.block ? 2 * a.D : 0), kForwardBytes);
-  auto go = [&](auto f32) {
-    constexpr bool kF32 = decltype(f32)::value;
-    if (s.V == 1) return run_forward<kF32, 1, kThreadsOf[1]>(a, s, dev, stream);
-    if (s.V == 2) return run_forward<kF32, 2, kThreadsOf[2]>(a, s, dev, stream);
-    if (s.V == 3) return run_forward<kF32, 3, kThreadsOf[3]>(a, s, dev, stream);
-    return run_forward<kF32, 4, kThreadsOf[4]>(a, s, dev, stream);
+  auto go = [&](auto f32, auto full) {
+    constexpr bool kF32 = decltype(f32)::value, kFull = decltype(full)::value;
+    if (s.V == 1) return run_forward<kF32, 1, kFull>(a, s, dev, stream);
+    if (s.V == 2) return run_forward<kF32, 2, kFull>(a, s, dev, stream);
+    if (s.V == 3) return run_forward<kF32, 3, kFull>(a, s, dev, stream);
+    return run_forward<kF32, 4, false>(a, s, dev, stream);
   };
-  return a.x_f32 ? go(std::true_type{}) : go(std::false_type{});
+  const bool full = a.block && a.w_post && a.w_pre;
+  if (a.x_f32) return full ? go(std::true_type{}, std::true_type{}) : go(std::true_type{}, std::false_type{});
+  return full ? go(std::false_type{}, std::true_type{}) : go(std::false_type{}, std::false_type{});
 }
 
 int launch_residual_norm_backward(const ResidualNormBackward& args, const DeviceInfo& dev,
@@ -742,15 +751,18 @@ int launch_residual_norm_backward(const ResidualNormBackward& args, const Device
   a.rows_per_run = q.rows_per_run;
   a.parts_per_gate = q.parts_per_gate;
   a.kinds = (a.dw_pre != nullptr) + (a.dw_post != nullptr || (a.dgate && !q.multi));
-  auto go = [&](auto f32, auto multi) {
-    constexpr bool kF32 = decltype(f32)::value, kMulti = decltype(multi)::value;
-    if (s.V == 1) return run_backward<kF32, 1, kThreadsOf[1], kMulti>(a, s, q.blocks, dev, stream);
-    if (s.V == 2) return run_backward<kF32, 2, kThreadsOf[2], kMulti>(a, s, q.blocks, dev, stream);
-    if (s.V == 3) return run_backward<kF32, 3, kThreadsOf[3], kMulti>(a, s, q.blocks, dev, stream);
-    return run_backward<kF32, 4, kThreadsOf[4], kMulti>(a, s, q.blocks, dev, stream);
+  auto go = [&](auto f32, auto multi, auto full) {
+    constexpr bool kF32 = decltype(f32)::value, kMulti = decltype(multi)::value, kFull = decltype(full)::value;
+    if (s.V == 1) return run_backward<kF32, 1, kMulti, kFull>(a, s, q.blocks, dev, stream);
+    if (s.V == 2) return run_backward<kF32, 2, kMulti, kFull>(a, s, q.blocks, dev, stream);
+    if (s.V == 3) return run_backward<kF32, 3, kMulti, kFull>(a, s, q.blocks, dev, stream);
+    return run_backward<kF32, 4, kMulti, false>(a, s, q.blocks, dev, stream);
   };
-  const int rc = a.x_f32 ? (q.multi ? go(std::true_type{}, std::true_type{}) : go(std::true_type{}, std::false_type{}))
-                         : (q.multi ? go(std::false_type{}, std::true_type{}) : go(std::false_type{}, std::false_type{}));
+  const bool full = a.dy && a.block && a.w_post && a.w_pre;
+  constexpr std::true_type yes{};
+  constexpr std::false_type no{};
+  const int rc = a.x_f32 ? (q.multi ? go(yes, yes, no) : full ? go(yes, no, yes) : go(yes, no, no))
+                         : (q.multi ? go(no, yes, no) : full ? go(no, no, yes) : go(no, no, no));
   if (rc != GEMM_OK || a.kinds == 0) return rc;
   return launch_dependent(residual_norm_join_kernel, dim3((a.D + 31) / 32, a.kinds),
                           32 * kJoinWarps, stream, a, q.blocks, int(q.multi));

@@ -127,6 +127,37 @@ def test_rows_with_nan_inf_and_zeros_stay_apart(g):
         assert torch.equal(out.y[row], clean.y[row]) and torch.equal(out.n[row], clean.n[row])
 
 
+@pytest.mark.parametrize("D", [8, 264, 520, 4104, 5000])
+@pytest.mark.parametrize("where", [0, -1])
+def test_infinite_and_nan_gradients_as_the_formula_has_them(g, D, where):
+    """A row with an infinity in its first or last place: the same places are infinite, of the
+    same sign, and NaN as in the formula; the other rows keep their bits."""
+    s, grads = make(3, D, F32, True, True, None)
+    out = g.residual_norm(**s)
+    back = lambda: g.residual_norm_backward(grads["dy"], grads["dn"], out.y, s["block"], out.rstd_post, out.rstd_pre, w_post=s["w_post"],
+                                            w_pre=s["w_pre"], need_dw=False)
+    clean = back()
+    for value in (float("inf"), float("nan")):
+        for name in ("dy", "dn"):
+            keep = grads[name].clone()
+            grads[name][1, where] = value
+            got = back()
+            grads[name].copy_(keep)
+            assert torch.equal(got.dx[::2], clean.dx[::2]) and torch.equal(got.dblock[::2], clean.dblock[::2])
+            # t is infinite or NaN where dy is; an infinite mean reaches every place of the row
+            if name == "dy":
+                assert not got.dx[1, where].isfinite() and int((~got.dx[1].isfinite()).sum()) == 1
+            elif value == float("inf"):
+                yhat = out.y[1].double() * out.rstd_pre[1].double()
+                e = float(s["w_pre"][where]) * float("inf")
+                want = -yhat * (e * float(yhat[where]))
+                want[where] = float("nan") if float(yhat[where]) ** 2 > 0 else e
+                fine = torch.isinf(got.dx[1]) & (torch.sign(got.dx[1]) == torch.sign(want))
+                assert bool(fine[torch.arange(D, device="cuda") != where % D].all())
+            else:
+                assert got.dx[1].isnan().all()
+
+
 def test_against_differences(g):
     """The gradients against central differences of the forward formula in 64 bits."""
     s, grads = make(4, 16, F32, True, True, 2, seed=5)
