@@ -626,7 +626,8 @@ constexpr int kBlocks = 152;
 // 76 -> 106 us), the forward pass is a little faster with half of it (56 -> 54 us).
 constexpr int kThreadsOf[5] = {0, 512, 512, 384, 512};
 constexpr int kForwardBytes = 104 << 10, kBackwardBytes = 208 << 10;
-Shape make_shape(int D, int row_bytes, int ring_bytes) {
+Shape make_shape(int D, int row_bytes, bool forward) {
+  const int ring_bytes = forward ? kForwardBytes : kBackwardBytes;
   Shape s{};
   const int pieces = D / 8;
   auto take = [&](int v) {
@@ -635,8 +636,14 @@ Shape make_shape(int D, int row_bytes, int ring_bytes) {
     s.units = std::min(kMaxWarps, kThreadsOf[v] / (32 * s.warps));
     return s.units >= 2;
   };
-  if (pieces <= 32) take(1);
-  else if (!take(2) && !take(3)) take(pieces <= 1024 ? 2 : 4);
+  if (pieces <= 32) {
+    take(1);
+  } else if (!take(2) && !take(3)) {
+    // the forward pass needs fewer registers: two units of three pieces a thread still
+    // fit, spilling a little (6553 x 5120: 64 us with one unit, 45 with two)
+    if (forward && s.warps <= 8) s.units = 2;
+    else take(pieces <= 1024 ? 2 : 4);
+  }
   s.units = std::max(1, s.units);
   s.stage_bytes = (row_bytes + 127) / 128 * 128;
   s.stages = std::min(8, std::max(1, ring_bytes / (s.units * (s.stage_bytes + 8))));
@@ -699,11 +706,11 @@ int launch_rows(Kernel kernel, const Shape& s, int blocks, std::atomic<int> (&re
   return GEMM_OK;
 }
 
-template <bool kF32, int V, bool kFull>
+template <bool kF32, int V, bool kFull, int kThreads = kThreadsOf[V]>
 int run_forward(const ResidualNorm& a, const Shape& s, const DeviceInfo& dev, cudaStream_t stream) {
   static std::atomic<int> ready[64];
   const int blocks = std::min((a.M + s.units - 1) / s.units, kBlocks);
-  return launch_rows(residual_norm_kernel<kF32, V, kThreadsOf[V], kFull>, s, blocks, ready, dev, stream, a);
+  return launch_rows(residual_norm_kernel<kF32, V, kThreads, kFull>, s, blocks, ready, dev, stream, a);
 }
 
 template <bool kF32, int V, bool kMulti, bool kFull>
@@ -724,18 +731,20 @@ int backward_row_bytes(int D, bool f32, bool dy, bool pre, bool block) {
 // The shape's units and blocks do not depend on the stages, so the matrices that a
 // call has make no difference here.
 size_t residual_norm_backward_workspace(int M, int D, int rows_per_gate, int weights, bool gates) {
-  const Shape s = make_shape(D, 128, kBackwardBytes);
+  const Shape s = make_shape(D, 128, false);
   const RunPlan q = make_runs(M, rows_per_gate, gates, s);
   return size_t(q.blocks) * (weights + (gates && !q.multi)) * D * sizeof(float);
 }
 
 int launch_residual_norm(const ResidualNorm& a, const DeviceInfo& dev, cudaStream_t stream) {
-  const Shape s = make_shape(a.D, a.D * (a.x_f32 ? 4 : 2) + (a.block ? 2 * a.D : 0), kForwardBytes);
+  const Shape s = make_shape(a.D, a.D * (a.x_f32 ? 4 : 2) + (a.block ? 2 * a.D : 0), true);
   auto go = [&](auto f32, auto full) {
     constexpr bool kF32 = decltype(f32)::value, kFull = decltype(full)::value;
     if (s.V == 1) return run_forward<kF32, 1, kFull>(a, s, dev, stream);
     if (s.V == 2) return run_forward<kF32, 2, kFull>(a, s, dev, stream);
-    if (s.V == 3) return run_forward<kF32, 3, kFull>(a, s, dev, stream);
+    if (s.V == 3)
+      return s.threads() <= kThreadsOf[3] ? run_forward<kF32, 3, kFull>(a, s, dev, stream)
+                                          : run_forward<kF32, 3, kFull, 512>(a, s, dev, stream);
     return run_forward<kF32, 4, false>(a, s, dev, stream);
   };
   const bool full = a.block && a.w_post && a.w_pre;
@@ -746,7 +755,7 @@ int launch_residual_norm(const ResidualNorm& a, const DeviceInfo& dev, cudaStrea
 int launch_residual_norm_backward(const ResidualNormBackward& args, const DeviceInfo& dev,
                                   cudaStream_t stream) {
   ResidualNormBackward a = args;
-  const Shape s = make_shape(a.D, backward_row_bytes(a.D, a.x_f32, a.dy, a.w_pre, a.block), kBackwardBytes);
+  const Shape s = make_shape(a.D, backward_row_bytes(a.D, a.x_f32, a.dy, a.w_pre, a.block), false);
   const RunPlan q = make_runs(a.M, a.rows_per_gate, a.dgate != nullptr, s);
   a.rows_per_run = q.rows_per_run;
   a.parts_per_gate = q.parts_per_gate;

@@ -32,7 +32,7 @@ def make(M, D, dtype, post, pre, groups, seed=0):
 
 
 # rows: one, fewer and more than the grid; D: one piece, a warp's edge, odd, the most
-SHAPES = [(1, 8), (1, 4096), (3, 248), (7, 256), (33, 264), (130, 2056), (304, 1032), (305, 8), (701, 4104), (16, 8192), (12, 12296), (9, 16384)]
+SHAPES = [(1, 8), (1, 4096), (3, 248), (7, 256), (33, 264), (130, 2056), (40, 5120), (25, 6008), (304, 1032), (305, 8), (701, 4104), (16, 8192), (12, 12296), (9, 16384)]
 # with a gate: none (None), one vector (0), groups
 KINDS = [(True, True, 0), (True, True, 1), (True, False, None), (False, True, None), (False, True, 0), (False, False, 1)]
 
