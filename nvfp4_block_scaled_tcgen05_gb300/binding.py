@@ -9,6 +9,7 @@ is no fallback path.  A missing library raises immediately.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 from typing import NamedTuple
@@ -711,6 +712,7 @@ def gemm_bf16_nt_gated(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, act:
     return H, gates
 
 
+@functools.lru_cache(maxsize=1024)  # a size is asked for with every call
 def gemm_bf16_nt_gated_backward_workspace_bytes(M: int, F: int, K: int) -> int:
     if not (0 <= M <= _INT_MAX and 0 <= F <= _INT_MAX and 0 <= K <= _INT_MAX):
         return 0
@@ -759,6 +761,7 @@ def gemm_bf16_nt_gated_backward(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Ten
     return dX, dWg, dWu
 
 
+@functools.lru_cache(maxsize=1024)  # a size is asked for with every call
 def gemm_bf16_tn_workspace_bytes(M: int, N: int, K: int) -> int:
     if not (0 <= M <= _INT_MAX and 0 <= N <= _INT_MAX and 0 <= K <= _INT_MAX):
         return 0
@@ -900,6 +903,7 @@ def residual_norm(x: torch.Tensor, block: torch.Tensor | None = None,
     return ResidualNorm(x if block is None else y, n, rstd_post, rstd_pre)
 
 
+@functools.lru_cache(maxsize=1024)  # a size is asked for with every call
 def residual_norm_backward_workspace_bytes(M: int, D: int, rows_per_gate: int, weights: int,
                                            gates: int) -> int:
     if not (0 <= M <= _INT_MAX and 0 <= D <= _INT_MAX and 0 <= rows_per_gate <= _INT_MAX):
