@@ -7,7 +7,9 @@
 //
 // Forward: 256-row tiles whose accumulator holds 128 gate columns beside the 128
 // up columns of the same outputs (GatedCfg), so the two products, the activation
-// and their product take one pass over X and the weights.
+// and their product take one pass over X and the weights.  Bound by the tensor cores:
+// 5120 x 11008 x 2048 with the gates stored 249 us, 1860 TFLOP/s (280 us where calls
+// follow each other and the power limit lowers the clock).
 //
 // Backward: dG and dU as BF16 (the operand type of the products that follow: one
 // rounding of relative size at most 2^-8 per term), from the stored gates by a
@@ -16,7 +18,11 @@
 // as one grid (DualOutCfg).  Order of the grids: dX's grid waits for dG and dU and
 // only then lets the weight gradients' grid start, on the SM pairs that dX's last
 // round leaves idle; that grid reads what was complete before it could start, and
-// waits for dX at its end.
+// waits for dX at its end.  5120 x 11008 x 2048 from the stored gates: 571 us, 77 of
+// them the streaming kernel's (7.3 TB/s), the products 1870 TFLOP/s.
+//
+// C = A^T B: both operands with their K as the rows, as dWg and dWu have them; 2048 x
+// 11008 x 5120 129 us, 1800 TFLOP/s.
 #include <algorithm>
 
 #include "chain.cuh"
@@ -26,11 +32,11 @@ namespace gb300 {
 namespace {
 
 using FwdPair = GatedCfg<TileCfg<Operand::kBF16, 2, 256, 3, 4, 2, true, false, 2>>;
-// Few tokens: the weights on the MMA's M side, half of a tile's rows of each matrix, the
-// tokens on the N side, so that the kernel streams the weights.  (11008 x 2048: one token
-// 42 us on the tiles above, 20.8 on these, 128 tokens 23.5, 129 on the others 28.)
+// Few tokens that gated_few.cu does not take: the weights on the MMA's M side, half of a
+// tile's rows of each matrix, the tokens on the N side, so that the kernel streams the
+// weights.  (11008 x 2048: 32 tokens 20.5 us, 128 tokens 23.5, 129 on the tiles above 28.)
 // Their gradient reads dH two bytes at a time, which pays up to 32 tokens (5504 x 2048,
-// all gradients from X: one token 56 -> 44.7 us, 16 tokens 49 -> 41, 128 50.8 -> 52.8).
+// all gradients from X: 17 tokens 49 -> 41 us, 128 50.8 -> 52.8).
 constexpr int kFewTokens = 128, kFewTokensGrad = 32;
 template <int BN, int STAGES>
 using Few = PairedRowsCfg<
@@ -113,7 +119,7 @@ int run_few(const void* X, const void* Wg, const void* Wu, const void* dH, void*
 }
 
 // dG and dU [2][n] from the stored gates [2][n]: three values read and two written
-// per output, bound by memory.
+// per output, bound by memory (5120 x 11008: 564 MB, 77 us).
 constexpr int kGradThreads = 256;
 template <int kAct>
 __global__ void __launch_bounds__(kGradThreads)
@@ -216,6 +222,7 @@ int run_grad(const GatedBackward& a, uint16_t* grad, const DeviceInfo& dev, cuda
                             static_cast<const uint16_t*>(a.gates),
                             static_cast<const uint16_t*>(a.dH), grad, n);
   }
+  if (gated_few_takes(a.M, a.F, a.K)) return launch_gated_few_grad(a, grad, dev, stream);
   if (a.M <= kFewTokensGrad)
     return run_few<Few64, Epilogue::kGatedGradTBF16>(a.X, a.Wg, a.Wu, a.dH, grad, nullptr, a.act, a.M,
                                                      a.F, a.K, dev, stream);
@@ -286,6 +293,7 @@ size_t gated_backward_workspace(int M, int F, int K) {
 }
 
 int launch_gated_forward(const GatedForward& a, const DeviceInfo& dev, cudaStream_t stream) {
+  if (gated_few_takes(a.M, a.F, a.K)) return launch_gated_few(a, dev, stream);
   if (a.M <= kFewTokens) {
     const auto few = a.M <= 64 ? run_few<Few64, Epilogue::kGatedTBF16> : run_few<Few128, Epilogue::kGatedTBF16>;
     return few(a.X, a.Wg, a.Wu, nullptr, a.H, a.gates, a.act, a.M, a.F, a.K, dev, stream);

@@ -158,6 +158,10 @@ struct GatedBackward {
 size_t gated_backward_workspace(int M, int F, int K);
 int launch_gated_forward(const GatedForward& a, const DeviceInfo& dev, cudaStream_t stream);
 int launch_gated_backward(const GatedBackward& a, const DeviceInfo& dev, cudaStream_t stream);
+// Few tokens (gated_few.cu): whether it takes a call, H (and the gates), dG and dU.
+bool gated_few_takes(int M, int F, int K);
+int launch_gated_few(const GatedForward& a, const DeviceInfo& dev, cudaStream_t stream);
+int launch_gated_few_grad(const GatedBackward& a, uint16_t* grad, const DeviceInfo& dev, cudaStream_t stream);
 size_t gemm_bf16_tn_workspace(int M, int N, int K);
 int launch_gemm_bf16_tn(const void* A, const void* B, void* C, void* workspace, int M, int N, int K,
                         const DeviceInfo& dev, cudaStream_t stream);

@@ -35,6 +35,10 @@ def inputs(M, F, K, seed=0):
 # one token, few, a tile's edges, odd sizes; K below, at and past a stage of 128
 SIZES = [(1, 8, 8), (1, 136, 72), (5, 1032, 256), (33, 264, 2056), (64, 248, 640), (65, 504, 136), (127, 128, 64),
          (128, 264, 392), (129, 248, 136), (256, 256, 128), (300, 1032, 520), (513, 392, 1000), (1100, 2568, 264)]
+# few tokens: warps with no step, part of a tile, whole tiles; every count of token groups;
+# tokens that shared memory holds, and not; long runs with more than 16 tokens, and not
+SIZES += [(2, 136, 1032), (3, 9736, 1096), (8, 2056, 520), (9, 16392, 264), (16, 264, 5816), (16, 264, 6008),
+          (17, 136, 72), (20, 9736, 1096), (32, 1032, 2824), (32, 520, 3064)]
 
 
 @pytest.mark.parametrize("kind", ["silu", "gelu_tanh"])
