@@ -19,7 +19,7 @@
 // only then lets the weight gradients' grid start, on the SM pairs that dX's last
 // round leaves idle; that grid reads what was complete before it could start, and
 // waits for dX at its end.  5120 x 11008 x 2048 from the stored gates: 571 us, 77 of
-// them the streaming kernel's (7.3 TB/s), the products 1870 TFLOP/s.
+// them the streaming kernel's, the products 1870 TFLOP/s.
 //
 // C = A^T B: both operands with their K as the rows, as dWg and dWu have them; 2048 x
 // 11008 x 5120 129 us, 1800 TFLOP/s.
@@ -119,7 +119,8 @@ int run_few(const void* X, const void* Wg, const void* Wu, const void* dH, void*
 }
 
 // dG and dU [2][n] from the stored gates [2][n]: three values read and two written
-// per output, bound by memory (5120 x 11008: 564 MB, 77 us).
+// per output, bound by memory (5120 x 11008: 564 MB, 77 us,
+// part of them still in the second-level cache).
 constexpr int kGradThreads = 256;
 template <int kAct>
 __global__ void __launch_bounds__(kGradThreads)
