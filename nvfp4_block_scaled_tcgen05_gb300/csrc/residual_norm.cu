@@ -98,26 +98,27 @@ __device__ __forceinline__ Vec8 weights8(const void* w, size_t i) {
   return unpack8(static_cast<const uint4*>(w)[i]);
 }
 
+__device__ __forceinline__ Vec8 weighted(Vec8 v, const Vec8& w) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) v.v[j] = ptx::mul2(v.v[j], w.v[j]);
+  return v;
+}
+__device__ __forceinline__ Vec8 scaled(float scale, Vec8 v) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) v.v[j] = ptx::mul2(both(scale), v.v[j]);
+  return v;
+}
 // Piece `at` of a gate (ones where there is none) times `scale`; piece c of a weight
 // (ones) times v.
 __device__ __forceinline__ Vec8 scaled_gate(float scale, const void* gate, size_t at) {
+  if (gate) return scaled(scale, weights8(gate, at));
   Vec8 f;
 #pragma unroll
   for (int j = 0; j < 4; ++j) f.v[j] = both(scale);
-  if (gate) {
-    const Vec8 g = weights8(gate, at);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) f.v[j] = ptx::mul2(f.v[j], g.v[j]);
-  }
   return f;
 }
-__device__ __forceinline__ Vec8 times_weight(Vec8 v, const void* weight, int c) {
-  if (weight) {
-    const Vec8 w = weights8(weight, c);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) v.v[j] = ptx::mul2(v.v[j], w.v[j]);
-  }
-  return v;
+__device__ __forceinline__ Vec8 times_weight(const Vec8& v, const void* weight, int c) {
+  return weight ? weighted(v, weights8(weight, c)) : v;
 }
 
 __device__ __forceinline__ float inverse_rms(float sum, int D, float eps) {
@@ -135,10 +136,11 @@ struct Shape {
 
 constexpr int kMaxWarps = 16;  // of a unit: D = 16384 with V = 4
 
-// Rows of up to four matrices through a unit's ring.
+// Rows of up to five matrices through a unit's ring.
 struct Source {
   const void* p;
   uint32_t bytes;  // per row; 0: no such matrix
+  int rows = 1;    // that share a row of it
 };
 template <int N>
 struct Ring {
@@ -182,8 +184,8 @@ struct Ring {
 #pragma unroll
     for (int i = 0; i < N; ++i)
       if (src[i].bytes) {
-        ptx::bulk_load(dst, static_cast<const uint8_t*>(src[i].p) + size_t(row) * src[i].bytes,
-                       src[i].bytes, bar);
+        const int of = src[i].rows == 1 ? row : row / src[i].rows;
+        ptx::bulk_load(dst, static_cast<const uint8_t*>(src[i].p) + size_t(of) * src[i].bytes, src[i].bytes, bar);
         dst += src[i].bytes;
       }
     if (++next_stage == stages) next_stage = 0;
@@ -238,17 +240,19 @@ struct Ring {
 
 // ---------------------------------------------------------------- forward
 // kFull: there are a block and both norms, the usual call, whose choices are then made
-// at compile time (below: `has_*`).
-template <bool kF32, int V, int kThreads, bool kFull>
+// at compile time (below: `has_*`).  kGates: and nearly every row of a unit has another
+// gate, which then comes through the ring (8192 x 4096, a gate for each row: 74 -> 55 us).
+template <bool kF32, int V, int kThreads, bool kFull, bool kGates>
 __global__ void __launch_bounds__(kThreads, 1)
     residual_norm_kernel(const ResidualNorm a, const Shape shape, unsigned int* status,
                          unsigned long long timeout_ns) {
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float parts[kMaxWarps][2][2][kMaxWarps];
   const bool has_block = kFull || a.block, has_post = kFull || a.w_post, has_pre = kFull || a.w_pre;
-  Ring<2> ring;
+  Ring<kGates ? 3 : 2> ring;
   ring.src[0] = {a.x, uint32_t(a.D) * (kF32 ? 4u : 2u)};
   ring.src[1] = {a.block, has_block ? uint32_t(a.D) * 2u : 0u};
+  if constexpr (kGates) ring.src[2] = {a.gate, uint32_t(a.D) * 2u, a.rows_per_gate};
   ring.init(smem, shape, status, timeout_ns);
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
@@ -259,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // This thread's pieces.  A place past the row's end reads the last piece again; its
   // values are set to zero, and not stored.
   int at[V];
-  uint4 w_pre[V];
+  uint4 w_pre[V], w_post[V];
   Vec8 p[V];  // scale * gate * w_post
 #pragma unroll
   for (int i = 0; i < V; ++i) {
@@ -267,6 +271,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     at[i] = min(c, pieces - 1);
     w_pre[i] = has_pre ? static_cast<const uint4*>(a.w_pre)[at[i]] : make_uint4(0, 0, 0, 0);
     p[i] = has_block && !a.gate ? times_weight(scaled_gate(a.scale, nullptr, 0), a.w_post, at[i]) : zero8();
+    if (kGates) w_post[i] = static_cast<const uint4*>(a.w_post)[at[i]];
   }
   auto live = [&](int i) { return ring.tid + i * threads < pieces; };
   int gate_row = -1;
@@ -274,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   int odd = 0;
   for (int row = first; row < a.M; row += step, odd ^= 1) {
     const size_t base = size_t(row) * pieces;
-    if (a.gate && row / a.rows_per_gate != gate_row) {
+    if (!kGates && a.gate && row / a.rows_per_gate != gate_row) {
       gate_row = row / a.rows_per_gate;
 #pragma unroll
       for (int i = 0; i < V; ++i)
@@ -282,6 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     const uint8_t* mem = ring.wait();
     Vec8 y[V], b[V];
+    uint4 gate[V];
     float2 s2 = both(0.0f);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -290,6 +296,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       y[i] = x.get();
       b[i] = zero8();
       if (has_block) b[i] = unpack8(reinterpret_cast<const uint4*>(mem + ring.src[0].bytes)[at[i]]);
+      if constexpr (kGates)
+        gate[i] = reinterpret_cast<const uint4*>(mem + ring.src[0].bytes + ring.src[1].bytes)[at[i]];
       if (!live(i)) y[i] = b[i] = zero8();
 #pragma unroll
       for (int j = 0; j < 4; ++j) s2 = ptx::fma2(b[i].v[j], b[i].v[j], s2);
@@ -310,6 +318,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       if (has_block) {
+        if constexpr (kGates) p[i] = weighted(scaled(a.scale, unpack8(gate[i])), unpack8(w_post[i]));
 #pragma unroll
         for (int j = 0; j < 4; ++j)
           y[i].v[j] = ptx::fma2(ptx::mul2(b[i].v[j], both(r)), p[i].v[j], y[i].v[j]);
@@ -347,7 +356,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 // thread keeps its columns' sums of the run in registers; a block's units are added
 // in order and go to the block's place in the workspace, [block][kinds][D]: dn yh,
 // and T, which the join multiplies, or (several gate groups in a run, kMulti) dw_post.
-template <bool kF32, int V, int kThreads, bool kMulti, bool kFull>
+// kGates: every row has its own gate, which comes through the ring, and T is the row's
+// (8192 x 4096: read when at hand 165 us, so 107; FP32 stream 196 and 148).
+template <bool kF32, int V, int kThreads, bool kMulti, bool kFull, bool kGates>
 __global__ void __launch_bounds__(kThreads, 1)
     residual_norm_backward_kernel(const ResidualNormBackward a, const Shape shape,
                                   unsigned int* status, unsigned long long timeout_ns) {
@@ -355,12 +366,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ float parts[kMaxWarps][2][3 * kMaxWarps];
   const bool has_dy = kFull || a.dy, has_block = kFull || a.block, has_post = kFull || a.w_post,
              has_pre = kFull || a.w_pre;
-  Ring<4> ring;
+  static_assert(!kGates || (kMulti && kFull), "a run of many gates, every part");
+  Ring<kGates ? 5 : 4> ring;
   const uint32_t wide = uint32_t(a.D) * (kF32 ? 4u : 2u), narrow = uint32_t(a.D) * 2u;
   ring.src[0] = {a.dy, has_dy ? wide : 0u};
   ring.src[1] = {a.y, has_pre ? wide : 0u};
   ring.src[2] = {a.dn, has_pre ? narrow : 0u};
   ring.src[3] = {a.block, has_block ? narrow : 0u};
+  if constexpr (kGates) ring.src[4] = {a.gate, narrow};
   ring.init(smem, shape, status, timeout_ns);
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
@@ -386,12 +399,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   // neither joins the row's sums nor is stored.
   int at[V];
   auto live = [&](int i) { return ring.tid + i * threads < pieces; };
-  uint4 w_pre[V];
+  uint4 w_pre[V], w_post[V];
   Vec8 dwi[V], T[V], dwo[kMulti ? V : 1];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     at[i] = min(ring.tid + i * threads, pieces - 1);
     w_pre[i] = has_pre && live(i) ? static_cast<const uint4*>(a.w_pre)[at[i]] : make_uint4(0, 0, 0, 0);
+    if (kGates) w_post[i] = static_cast<const uint4*>(a.w_post)[at[i]];
     dwi[i] = T[i] = zero8();
     if constexpr (kMulti) dwo[i] = zero8();
   }
@@ -416,12 +430,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   int odd = 0;
   for (; row < end; ++row, odd ^= 1) {
     const size_t base = size_t(row) * pieces;
-    if (kMulti && row / a.rows_per_gate != gate_row) read_gate(row / a.rows_per_gate);
+    if (kMulti && !kGates && row / a.rows_per_gate != gate_row) read_gate(row / a.rows_per_gate);
     const float r_y = ry, r_b = rb;
     const uint8_t* mem = ring.wait();
     if (row + 1 < end) read_rstd(row + 1);  // a row ahead
     const uint8_t *mem_y = mem + (has_dy ? wide : 0u), *mem_n = mem_y + wide;
     const uint8_t* mem_b = has_pre ? mem_n + narrow : mem_y;
+    // piece i of the row's gate, and of scale * gate * w_post
+    auto own_gate = [&](int i) { return scaled(a.scale, unpack8(reinterpret_cast<const uint4*>(mem_b + narrow)[at[i]])); };
+    auto factor = [&](int i) {
+      if constexpr (kGates) return weighted(own_gate(i), unpack8(w_post[i]));
+      else return p[i];
+    };
     Vec8 u[V];
     float2 s0 = both(0.0f), s1 = s0, s2 = s0;
 #pragma unroll
@@ -449,11 +469,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (has_post) {
-        const Vec8 b = unpack8(reinterpret_cast<const uint4*>(mem_b)[at[i]]);
+        const Vec8 b = unpack8(reinterpret_cast<const uint4*>(mem_b)[at[i]]), f = factor(i);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           // p bh, its factor r_b left for the sums
-          const float2 pb = ptx::mul2(p[i].v[j], b.v[j]);
+          const float2 pb = ptx::mul2(f.v[j], b.v[j]);
           q1 = ptx::fma2(pb, u[i].v[j], q1);
           q2 = ptx::fma2(pb, yh.v[j], q2);
         }
@@ -475,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const float m1 = r_y * s[0] / float(a.D);  // r_y mean(dn w_pre yh)
     const float m2 = r_b * (s[1] - m1 * s[2]) / float(a.D);
     const float2 ny = both(-m1 * r_y), nb = both(-m2 * r_b * r_b);
-    const bool last = kMulti && ((row + 1) % a.rows_per_gate == 0 || row + 1 == end);
+    const bool last = kGates || (kMulti && ((row + 1) % a.rows_per_gate == 0 || row + 1 == end));
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       if (has_pre) {
@@ -487,25 +507,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       store8<kF32>(a.dx, base + at[i], u[i], live(i));
       if (has_block) {
-        const Vec8 b = unpack8(reinterpret_cast<const uint4*>(mem_b)[at[i]]);
+        const Vec8 b = unpack8(reinterpret_cast<const uint4*>(mem_b)[at[i]]), f = factor(i);
         Vec8 db;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           T[i].v[j] = ptx::fma2(u[i].v[j], ptx::mul2(b.v[j], both(r_b)), T[i].v[j]);
-          db.v[j] = ptx::mul2(p[i].v[j], u[i].v[j]);
+          db.v[j] = ptx::mul2(f.v[j], u[i].v[j]);
           if (has_post) db.v[j] = ptx::fma2(b.v[j], nb, ptx::mul2(db.v[j], both(r_b)));
         }
         store8<false>(a.dblock, base + at[i], db, live(i));
         if (last) {  // the gate group's end
-          const Vec8 f = scaled_gate(a.scale, a.gate, size_t(gate_row) * pieces + at[i]);
-          Vec8 dg;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) dg.v[j] = ptx::mul2(both(a.scale), T[i].v[j]);
-          dg = times_weight(dg, a.w_post, at[i]);
-          if (a.dgate) store8<true>(a.dgate, size_t(gate_row) * pieces + at[i], dg, live(i));
+          const size_t to = kGates ? base : size_t(gate_row) * pieces;
+          const Vec8 gate = kGates ? own_gate(i) : scaled_gate(a.scale, a.gate, to + at[i]);
+          Vec8 dg = scaled(a.scale, T[i]);
+          dg = kGates ? weighted(dg, unpack8(w_post[i])) : times_weight(dg, a.w_post, at[i]);
+          if (a.dgate) store8<true>(a.dgate, to + at[i], dg, live(i));
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            if constexpr (kMulti) dwo[i].v[j] = ptx::fma2(f.v[j], T[i].v[j], dwo[i].v[j]);
+            if constexpr (kMulti) dwo[i].v[j] = ptx::fma2(gate.v[j], T[i].v[j], dwo[i].v[j]);
             T[i].v[j] = make_float2(0.0f, 0.0f);
           }
         }
@@ -709,18 +728,18 @@ int launch_rows(Kernel kernel, const Shape& s, int blocks, std::atomic<int> (&re
   return GEMM_OK;
 }
 
-template <bool kF32, int V, bool kFull, int kThreads = kThreadsOf[V]>
+template <bool kF32, int V, bool kFull, bool kGates, int kThreads = kThreadsOf[V]>
 int run_forward(const ResidualNorm& a, const Shape& s, const DeviceInfo& dev, cudaStream_t stream) {
   static std::atomic<int> ready[64];
   const int blocks = std::min((a.M + s.units - 1) / s.units, kBlocks);
-  return launch_rows(residual_norm_kernel<kF32, V, kThreads, kFull>, s, blocks, ready, dev, stream, a);
+  return launch_rows(residual_norm_kernel<kF32, V, kThreads, kFull, kGates>, s, blocks, ready, dev, stream, a);
 }
 
-template <bool kF32, int V, bool kMulti, bool kFull>
+template <bool kF32, int V, bool kMulti, bool kFull, bool kGates>
 int run_backward(const ResidualNormBackward& a, const Shape& s, int blocks, const DeviceInfo& dev,
                  cudaStream_t stream) {
   static std::atomic<int> ready[64];
-  return launch_rows(residual_norm_backward_kernel<kF32, V, kThreadsOf[V], kMulti, kFull>, s, blocks,
+  return launch_rows(residual_norm_backward_kernel<kF32, V, kThreadsOf[V], kMulti, kFull, kGates>, s, blocks,
                      ready, dev, stream, a);
 }
 
@@ -740,41 +759,54 @@ size_t residual_norm_backward_workspace(int M, int D, int rows_per_gate, int wei
 }
 
 int launch_residual_norm(const ResidualNorm& a, const DeviceInfo& dev, cudaStream_t stream) {
-  const Shape s = make_shape(a.D, a.D * (a.x_f32 ? 4 : 2) + (a.block ? 2 * a.D : 0), true);
-  auto go = [&](auto f32, auto full) {
-    constexpr bool kF32 = decltype(f32)::value, kFull = decltype(full)::value;
-    if (s.V == 1) return run_forward<kF32, 1, kFull>(a, s, dev, stream);
-    if (s.V == 2) return run_forward<kF32, 2, kFull>(a, s, dev, stream);
+  // (a unit's rows are at most kBlocks units apart; with V = 4 the kernel has no registers
+  // for choices made at compile time)
+  const bool full = a.block && a.w_post && a.w_pre && a.D <= 8192;
+  const int row_bytes = a.D * (a.x_f32 ? 4 : 2) + (a.block ? 2 * a.D : 0);
+  Shape s = make_shape(a.D, row_bytes, true);
+  const bool gates = full && a.gate && a.rows_per_gate < kBlocks * s.units;
+  if (gates) s = make_shape(a.D, row_bytes + 2 * a.D, true);
+  auto go = [&](auto f32, auto kind) {
+    constexpr bool kF32 = decltype(f32)::value, kFull = decltype(kind)::value > 0, kGates = decltype(kind)::value > 1;
+    if (s.V == 1) return run_forward<kF32, 1, kFull, kGates>(a, s, dev, stream);
+    if (s.V == 2) return run_forward<kF32, 2, kFull, kGates>(a, s, dev, stream);
     if (s.V == 3)
-      return s.threads() <= kThreadsOf[3] ? run_forward<kF32, 3, kFull>(a, s, dev, stream)
-                                          : run_forward<kF32, 3, kFull, 512>(a, s, dev, stream);
-    return run_forward<kF32, 4, false>(a, s, dev, stream);
+      return s.threads() <= kThreadsOf[3] ? run_forward<kF32, 3, kFull, kGates>(a, s, dev, stream)
+                                          : run_forward<kF32, 3, kFull, kGates, 512>(a, s, dev, stream);
+    return run_forward<kF32, 4, false, false>(a, s, dev, stream);
   };
-  const bool full = a.block && a.w_post && a.w_pre;
-  if (a.x_f32) return full ? go(std::true_type{}, std::true_type{}) : go(std::true_type{}, std::false_type{});
-  return full ? go(std::false_type{}, std::true_type{}) : go(std::false_type{}, std::false_type{});
+  auto go_kind = [&](auto f32) {
+    if (gates) return go(f32, std::integral_constant<int, 2>{});
+    return full ? go(f32, std::integral_constant<int, 1>{}) : go(f32, std::integral_constant<int, 0>{});
+  };
+  return a.x_f32 ? go_kind(std::true_type{}) : go_kind(std::false_type{});
 }
 
 int launch_residual_norm_backward(const ResidualNormBackward& args, const DeviceInfo& dev,
                                   cudaStream_t stream) {
   ResidualNormBackward a = args;
-  const Shape s = make_shape(a.D, backward_row_bytes(a.D, a.x_f32, a.dy, a.w_pre, a.block), false);
+  const bool full = a.dy && a.block && a.w_post && a.w_pre && a.D <= 8192;
+  const bool gates = full && a.gate && a.rows_per_gate == 1 && a.M > 1;
+  const Shape s = make_shape(a.D, backward_row_bytes(a.D, a.x_f32, a.dy, a.w_pre, a.block) + (gates ? 2 * a.D : 0), false);
   const RunPlan q = make_runs(a.M, a.rows_per_gate, a.dgate != nullptr, s);
   a.rows_per_run = q.rows_per_run;
   a.parts_per_gate = q.parts_per_gate;
   a.kinds = (a.dw_pre != nullptr) + (a.dw_post != nullptr || (a.dgate && !q.multi));
-  auto go = [&](auto f32, auto multi, auto full) {
-    constexpr bool kF32 = decltype(f32)::value, kMulti = decltype(multi)::value, kFull = decltype(full)::value;
-    if (s.V == 1) return run_backward<kF32, 1, kMulti, kFull>(a, s, q.blocks, dev, stream);
-    if (s.V == 2) return run_backward<kF32, 2, kMulti, kFull>(a, s, q.blocks, dev, stream);
-    if (s.V == 3) return run_backward<kF32, 3, kMulti, kFull>(a, s, q.blocks, dev, stream);
-    return run_backward<kF32, 4, kMulti, false>(a, s, q.blocks, dev, stream);
+  // kinds: any call; every part (0, 1), of one gate or (2) several per run; 3: a gate per row
+  auto go = [&](auto f32, auto kind) {
+    constexpr int k = decltype(kind)::value;
+    constexpr bool kF32 = decltype(f32)::value, kMulti = k >= 2, kFull = k == 1 || k == 3, kGates = k == 3;
+    if (s.V == 1) return run_backward<kF32, 1, kMulti, kFull, kGates>(a, s, q.blocks, dev, stream);
+    if (s.V == 2) return run_backward<kF32, 2, kMulti, kFull, kGates>(a, s, q.blocks, dev, stream);
+    if (s.V == 3) return run_backward<kF32, 3, kMulti, kFull, kGates>(a, s, q.blocks, dev, stream);
+    return run_backward<kF32, 4, kMulti, false, false>(a, s, q.blocks, dev, stream);
   };
-  const bool full = a.dy && a.block && a.w_post && a.w_pre;
-  constexpr std::true_type yes{};
-  constexpr std::false_type no{};
-  const int rc = a.x_f32 ? (q.multi ? go(yes, yes, no) : full ? go(yes, no, yes) : go(yes, no, no))
-                         : (q.multi ? go(no, yes, no) : full ? go(no, no, yes) : go(no, no, no));
+  auto go_kind = [&](auto f32) {
+    if (q.multi)
+      return gates ? go(f32, std::integral_constant<int, 3>{}) : go(f32, std::integral_constant<int, 2>{});
+    return full ? go(f32, std::integral_constant<int, 1>{}) : go(f32, std::integral_constant<int, 0>{});
+  };
+  const int rc = a.x_f32 ? go_kind(std::true_type{}) : go_kind(std::false_type{});
   if (rc != GEMM_OK || a.kinds == 0) return rc;
   return launch_dependent(residual_norm_join_kernel, dim3((a.D + 31) / 32, a.kinds),
                           32 * kJoinWarps, stream, a, q.blocks, int(q.multi));

@@ -46,7 +46,9 @@ def test_forward_and_backward(g, M, D, post, pre, groups, dtype):
 
 # groups that lie within a run, hold several runs, or are rows
 @pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
-@pytest.mark.parametrize("M,D,groups", [(12, 264, 12), (12, 264, 3), (1000, 72, 500), (1000, 72, 8), (1000, 72, 1000), (2432, 40, 2), (3648, 16, 304)])
+@pytest.mark.parametrize("M,D,groups", [(12, 264, 12), (12, 264, 3), (1000, 72, 500), (1000, 72, 8), (1000, 72, 1000), (2432, 40, 2), (3648, 16, 304),
+                                        (460, 1032, 460), (500, 4104, 500), (320, 2056, 160), (701, 3592, 701), (33, 5120, 33),
+                                        (40, 8192, 40), (40, 6008, 20), (20, 12296, 20)])
 def test_gate_groups(g, M, D, groups, dtype):
     run(g, M, D, True, True, groups, dtype)
     run(g, M, D, False, True, groups, dtype)
