@@ -131,6 +131,11 @@ def calls(g, seed=0):
     yield "tn", [dH], lambda: [g.gemm_bf16_tn(dH, X)]
     yield "norm", [x, blk], lambda: g.residual_norm(x, blk, w_post=w, gate=gate, w_pre=w)
     yield "norm backward", [x, blk], lambda: g.residual_norm_backward(x, blk, x, blk, r, r, w_post=w, gate=gate, w_pre=w)
+    X3, dH3, row_gate = randn(gen, 11, 264), randn(gen, 11, 520), randn(gen, 90, 520)
+    yield "gated, fewer", [X3], lambda: g.gemm_bf16_nt_gated(X3, Wg, Wu, act="gelu_tanh", save_gates=True)
+    yield "gated backward, fewer", [X3, dH3], lambda: g.gemm_bf16_nt_gated_backward(X3, Wg, Wu, dH3)
+    yield "norm, a gate per row", [x, blk], lambda: g.residual_norm(x, blk, w_post=w, gate=row_gate, w_pre=w)
+    yield "norm backward, a gate per row", [x, blk], lambda: g.residual_norm_backward(x, blk, x, blk, r, r, w_post=w, gate=row_gate, w_pre=w)
     yield "gemv", [A], lambda: [g.gemv_w4a16(A, b, sf, 0.1)]
     yield "gemv gated", [A], lambda: [g.gemv_w4a16_gated(A, b, sf, 0.01, b2, sf2, 0.02)]
 
@@ -229,7 +234,7 @@ def guarded(shape, dtype, fill):
     return buf[pad:pad + n].view(shape), buf, pad
 
 
-@pytest.mark.parametrize("M", [1, 65, 130, 257])
+@pytest.mark.parametrize("M", [1, 20, 65, 130, 257])
 def test_nothing_outside_the_outputs_is_written(g, M):
     gen = torch.Generator(device="cuda").manual_seed(M)
     X, Wg, Wu, dH = randn(gen, M, 136), randn(gen, 264, 136), randn(gen, 264, 136), randn(gen, M, 264)
@@ -348,6 +353,13 @@ def test_past_32_bit_offsets(g):
     ref.check(back.dx[pick], *want["dx"], "dx")
     ref.check(back.dblock[pick], *want["dblock"], "dblock")
     del H, out, back
+    F, K = 300000, 8192  # 2.5e9 weights
+    Wg, X = torch.empty(F, K, dtype=BF16, device="cuda"), randn(gen, 3, K)
+    Wg.view(-1).view(torch.int16).random_(0x3C00, 0x3D00, generator=gen)  # 2^-7 to 2^-5
+    at = torch.tensor([0, 131071, 262144, F - 1], device="cuda")
+    want, _, _, e, _, _ = ref.gated(X, Wg[at], Wg[at], "silu")
+    ref.check(g.gemm_bf16_nt_gated(X, Wg, Wg)[0][:, at], want, e, "H of few tokens")
+    del Wg
     N, K = 560000, 8192  # 2.3e9 code bytes
     b = torch.randint(0, 256, (N, K // 2), device="cuda", dtype=torch.uint8)
     sf = torch.full((N, K // 16), 56, device="cuda", dtype=torch.uint8)
