@@ -11,9 +11,9 @@
 // so that all stream to the end whatever the sizes.  A warp that began a tile joins the
 // parts of those that went on with it, in order, at the end.
 //
-// 11008 x 2048, one token: 16.6 us, 90 MB at 5.4 TB/s (tcgen05 tiles of 128 weight rows,
-// whose rounds do not fit the sizes, 20.8); 1024 x 1024, 4 tokens: 3.1 (7.1); 512 x 4096,
-// 16 tokens: 6.3 (17.1).  What shared memory takes, the first-level cache lacks for the
+// 11008 x 2048, one token: 15.0 us, 90 MB at 6.0 TB/s (tcgen05 tiles of 128 weight rows,
+// whose rounds do not fit the sizes, 20.8); 1024 x 1024, 4 tokens: 3.2 (7.1); 512 x 4096,
+// 16 tokens: 5.9 (17.1).  What shared memory takes, the first-level cache lacks for the
 // loads in flight (16 x 4096 x 5120 with 35 KB more of it: 29 us, as it is 19).
 #include <algorithm>
 #include <type_traits>
@@ -124,6 +124,21 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
   }
   ptx::fence_mbar_init();
   __syncthreads();
+  // The weights' first steps on their way into L2 while the previous grid ends (11008 x
+  // 2048, one token 16.2 -> 14.9 us; three steps 15.0, four 15.7).  Rows that do not begin
+  // on a cache line lose by it (5512 x 2056 10.0 -> 10.5), and the shortest runs (1024 x
+  // 1024, 4 tokens 3.2 -> 3.4).
+  if (a.K % 64 == 0 && u1 - u0 >= kDepth) {
+    const long long end = u0 + kDepth;
+    for (long long u = u0; u < end;) {
+      const int k = int(u / steps), st = int(u - (long long)k * steps), n = int(min((long long)(steps - st), end - u));
+      const void* W = lane & 8 ? a.Wu : a.Wg;
+      if (lane < 16)
+        ptx::bulk_prefetch(static_cast<const uint16_t*>(W) + (size_t(tile0 + k) * 8 + (lane & 7)) * a.K + st * 128,
+                           uint32_t(min(n * 128, a.K - st * 128)) * 2u);
+      u += n;
+    }
+  }
   ptx::griddep_launch_dependents();
   ptx::griddep_wait();
   // The weights' first loads, then the tokens: the weights are what takes long (16 x 2048

@@ -144,6 +144,11 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
       : "memory");
 }
 
+// Brings `bytes` (a multiple of 16, from a multiple of 16) into L2.
+__device__ __forceinline__ void bulk_prefetch(const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
+}
+
 // Asynchronous copy of 16 bytes into this block's shared memory (through L2), and the
 // wait for all of the thread's.
 __device__ __forceinline__ void cp_async_16(void* dst, const void* src) {
