@@ -856,14 +856,15 @@ def residual_norm(x: torch.Tensor, block: torch.Tensor | None = None,
                   w_post: torch.Tensor | None = None, gate: torch.Tensor | None = None,
                   w_pre: torch.Tensor | None = None, scale: float = 1.0, eps: float = 1e-6,
                   y: torch.Tensor | None = None, n: torch.Tensor | None = None,
-                  stream=None) -> ResidualNorm:
+                  stream=None, need_rstd: bool = True) -> ResidualNorm:
     """The residual step between two blocks: y = x + scale * gate * norm(block, w_post) and
     n = norm(y, w_pre), root-mean-square norms, in one pass.
 
     x [M,D], the stream, bf16 or float32; block bf16 [M,D], or None: no block
     yet (y is x); gate bf16 [D], or [G,D] with G a divisor of M: row m has gate
     row m // (M // G); w_post, w_pre bf16 [D], or None: no such norm.  y may be
-    x: the stream is updated in place.
+    x: the stream is updated in place.  need_rstd False leaves out what only the
+    gradient needs (one token: a quarter of the host's time).
     """
     M, D, f32 = _stream_rows(x, "x")
     device = x.device
@@ -879,7 +880,7 @@ def residual_norm(x: torch.Tensor, block: torch.Tensor | None = None,
     elsewhere = _context(device, stream)
     if elsewhere is not None:
         with elsewhere:
-            return residual_norm(x, block, w_post, gate, w_pre, scale, eps, y, n)
+            return residual_norm(x, block, w_post, gate, w_pre, scale, eps, y, n, need_rstd=need_rstd)
     # (pointers without a call to _ptr each: the host's time is what a few rows take)
     empty, F32, like, post, pre = torch.empty, torch.float32, torch.empty_like, None, None
     if block is not None:
@@ -890,13 +891,17 @@ def residual_norm(x: torch.Tensor, block: torch.Tensor | None = None,
         y_ptr = block_ptr = None
     rstd_post = rstd_pre = n_ptr = post_ptr = pre_ptr = None
     if w_post is not None:
-        rstd_post = empty((M,), dtype=F32, device=device)
-        post, post_ptr = w_post.data_ptr(), rstd_post.data_ptr()
+        post = w_post.data_ptr()
+        if need_rstd:
+            rstd_post = empty((M,), dtype=F32, device=device)
+            post_ptr = rstd_post.data_ptr()
     if w_pre is not None:
         if n is None:
             n = like(x) if f32 == 0 else empty((M, D), dtype=torch.bfloat16, device=device)
-        rstd_pre = empty((M,), dtype=F32, device=device)
-        pre, n_ptr, pre_ptr = w_pre.data_ptr(), n.data_ptr(), rstd_pre.data_ptr()
+        pre, n_ptr = w_pre.data_ptr(), n.data_ptr()
+        if need_rstd:
+            rstd_pre = empty((M,), dtype=F32, device=device)
+            pre_ptr = rstd_pre.data_ptr()
     _run("residual_norm", device, x.data_ptr(), block_ptr, post,
          None if gate is None else gate.data_ptr(), pre, y_ptr, n_ptr, post_ptr, pre_ptr,
          float(scale), float(eps), f32, M, D, rows)

@@ -96,6 +96,15 @@ def test_first_norm_without_a_block(g, dtype):
         ref.check(got.dw_pre, *want["dw_pre"], "dw_pre")
 
 
+@pytest.mark.parametrize("kind", [(True, True), (True, False), (False, True)])
+def test_without_what_the_gradient_needs(g, kind):
+    s, _ = make(9, 264, BF16, *kind, 0)
+    out, less = g.residual_norm(**s), g.residual_norm(**s, need_rstd=False)
+    assert less.rstd_post is None and less.rstd_pre is None
+    assert torch.equal(less.y, out.y) and (out.n is None) == (less.n is None)
+    assert out.n is None or torch.equal(less.n, out.n)
+
+
 def test_in_place(g):
     s, grads = make(77, 1032, BF16, True, True, 0)
     out = g.residual_norm(**s)
