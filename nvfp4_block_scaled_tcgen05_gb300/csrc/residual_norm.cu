@@ -261,7 +261,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (ring.tid == 0)
     for (int i = 0, row = first; i < shape.stages && row < a.M; ++i, row += step) ring.fill(row);
   // This thread's pieces.  A place past the row's end reads the last piece again; its
-  // values are set to zero, and not stored.
+  // values are set to zero before each sum (an infinite weight or gate makes them NaN in
+  // between), and not stored.
   int at[V];
   uint4 w_pre[V], w_post[V];
   Vec8 p[V];  // scale * gate * w_post
@@ -298,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (has_block) b[i] = unpack8(reinterpret_cast<const uint4*>(mem + ring.src[0].bytes)[at[i]]);
       if constexpr (kGates)
         gate[i] = reinterpret_cast<const uint4*>(mem + ring.src[0].bytes + ring.src[1].bytes)[at[i]];
-      if (!live(i)) y[i] = b[i] = zero8();
+      if (!live(i)) b[i] = zero8();
 #pragma unroll
       for (int j = 0; j < 4; ++j) s2 = ptx::fma2(b[i].v[j], b[i].v[j], s2);
     }
@@ -324,6 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           y[i].v[j] = ptx::fma2(ptx::mul2(b[i].v[j], both(r)), p[i].v[j], y[i].v[j]);
         y[i] = store8<kF32>(a.y, base + at[i], y[i], live(i));
       }
+      if (!live(i)) y[i] = zero8();
 #pragma unroll
       for (int j = 0; j < 4; ++j) s2 = ptx::fma2(y[i].v[j], y[i].v[j], s2);
     }
