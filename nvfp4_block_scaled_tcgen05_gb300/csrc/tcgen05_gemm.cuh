@@ -40,6 +40,7 @@
 #include "epilogue_math.cuh"
 #include "e2m1.cuh"
 #include "gate_act.cuh"
+#include "pair_exchange.cuh"
 #include "ptx.cuh"
 #include "watchdog.cuh"
 
@@ -109,7 +110,8 @@ struct GemmParams {
   int col_offset, col_total;      // first column of this launch, columns in all
   int k_chunk, chunks;            // CHUNKED: K blocks per chunk, chunks per tile
   int n_last;                     // TRIM_N: columns of the last N block, rounded up to 32
-  int m_rows;                     // VAR_ROWS: rows of A per CTA and tile (a multiple of 32, <= 128)
+  int m_rows;                     // VAR_ROWS: rows of A per CTA and tile (a multiple of 32, <= 128;
+                                  // PAIRED_ROWS: of each matrix, a multiple of 16, <= 64)
   // gated projection (kGated*)
   int act;                        // GEMM_ACT_*
   int gates_out;                  // kGatedBF16: store the factors too
@@ -849,7 +851,8 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
       ptx::mbar_init(acc_empty(b), Cfg::EPI_WARPS * CG);
     }
     for (int e = 0; e < Cfg::EPI_WARPS; ++e)
-      for (int b = 0; b < Cfg::EPI_BUFS; ++b) ptx::mbar_init(epi_bar(e, b), 1);
+      for (int b = 0; b < Cfg::EPI_BUFS; ++b)
+        ptx::mbar_init(epi_bar(e, b), Cfg::PAIRED_ROWS ? PairExchange::kArrivals : 1);
     ptx::mbar_init(mma_done, 1);
     if constexpr (Cfg::SF_WARP)
       for (int s = 0; s < STAGES; ++s) ptx::mbar_init(sf_full(s), Cfg::SF_WARPS);
@@ -2134,8 +2137,8 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
         }
       } else if constexpr (EPI == Epilogue::kGatedTBF16 || EPI == Epilogue::kGatedGradTBF16) {
         // Warps q and q + 2 hold the gate and the up row of a lane's output: each gives
-        // the other half of its tokens through the two halves of its box in turn, and
-        // takes the other half of the outputs.  Two-byte stores, 64 bytes of a token's
+        // the other half of its tokens through the two halves of its box in turn
+        // (PairExchange), and takes the other half of the outputs.  Two-byte stores, 64 bytes of a token's
         // row together: the outputs are few beside the weights.
         const bool gate = q < 2;
         const int in_tile = (q & 1) * 32 + lane, f = (mb * CG + int(peer)) * m_rows + in_tile;
@@ -2150,15 +2153,16 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
           if (c == Cfg::EPI_COLS / 32 - 1) release_acc(acc);
           const int tok0 = nb * BN + col_base + 32 * c;
           if (!some || tok0 >= p.N) continue;  // for both warps
-          const uint32_t half = (chunk_ctr & 1u) * 2048u;
+          const uint32_t half = PairExchange::half(chunk_ctr) * 2048u;
           uint32_t* mine = reinterpret_cast<uint32_t*>(smem + (buf0 - sbase) + half);
           const uint32_t* other =
               reinterpret_cast<const uint32_t*>(smem + (epi_base + partner * Cfg::EPI_BOX_BYTES - sbase) + half);
 #pragma unroll
           for (int i = 0; i < 16; ++i) mine[i * 32 + lane] = gate ? r[16 + i] : r[i];
           __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(epi_bar(partner, 0));
-          const bool got = wait_bar(epi_bar(e, 0), chunk_ctr & 1u, w, 13);
+          const uint32_t bar = epi_bar(PairExchange::bar(e), 0);
+          if (lane == 0) ptx::mbar_arrive(bar);
+          const bool got = wait_bar(bar, PairExchange::parity(chunk_ctr), w, 13);
           ++chunk_ctr;
           if (!__all_sync(0xffffffffu, got)) {
             ok = false;
