@@ -19,7 +19,8 @@
 // with a scale of their own: one pass for tokens as they come, up to eight for tokens
 // that span the whole BF16 range.  So products are exact and sums FP32; they are scaled
 // back, and by scale2, before they are stored, so that a sum beyond the FP32 range whose
-// result is not comes back.
+// result is not comes back; the largest token may be another one than the sum's, so the
+// factors alone stay within the range too.
 //
 // A tile is 16 weight rows (gated: 8 of each matrix, so that a lane gets both products
 // of its outputs).  One block per SM takes a run of tiles; it turns its tokens into FP16
@@ -111,6 +112,15 @@ __device__ __forceinline__ uint4 to_f16(uint4 v, uint32_t low, uint32_t high, bo
     w[i] = *reinterpret_cast<const uint32_t*>(&h);
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// acc * back0 * back1 * scale2, in an order in which nothing leaves the FP32 range unless the
+// result does: 2^-34 <= |acc| <= 2^57, the factors back both in [2^-64, 1] or in [1, 2^56],
+// and back1 and scale2 are multiplied with each other where one grows and one shrinks.
+__device__ __forceinline__ float scaled_back(float acc, float back0, float back1, float scale2) {
+  const bool together = (back1 <= 1.0f) == (fabsf(scale2) >= 1.0f);
+  const float first = together ? back1 * scale2 : scale2, second = together ? 1.0f : back1;
+  return acc * back0 * first * second;
 }
 
 // A tile's sums: [16 rows][8 NT tokens], one more for the banks.
@@ -364,8 +374,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                  const float back = scale_back[1] * (kGated && i >= 2 ? a.scale2[1] : a.scale2[0]);
-                  parts[tile + warp].v[g + 8 * (i >> 1)][8 * n + 2 * t + (i & 1)] = acc[n][i] * scale_back[0] * back;
+                  parts[tile + warp].v[g + 8 * (i >> 1)][8 * n + 2 * t + (i & 1)] =
+                      scaled_back(acc[n][i], scale_back[0], scale_back[1], kGated && i >= 2 ? a.scale2[1] : a.scale2[0]);
                   acc[n][i] = 0.0f;
                 }
               step = 0;
