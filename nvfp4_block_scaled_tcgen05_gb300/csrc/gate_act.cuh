@@ -37,8 +37,9 @@ template <int kAct>
 __device__ __forceinline__ float2 gate_act_slope(float x) {
   const float s = ptx::rcp(1.0f + ptx::ex2(gate_exponent<kAct>(x)));
   float dz = 1.0f;
+  // (past |x| = 100, where s (1 - s) is zero, z' stays finite)
   if constexpr (kAct == GEMM_ACT_GELU_TANH)
-    dz = 1.5957691216057308f * (1.0f + 3.0f * 0.044715f * (x * x));
+    dz = 1.5957691216057308f * (1.0f + 3.0f * 0.044715f * fminf(x * x, 1e4f));
   return make_float2(x * s, s + x * s * (1.0f - s) * dz);
 }
 
