@@ -565,6 +565,8 @@ GB300GEMM_API int gemm_bf16_nt_gated(const void* X, const void* Wg, const void* 
  *          bytes, 16-byte aligned; contents on entry ignored, on return unspecified
  *   Every pointer 16-byte aligned; the outputs and the workspace overlap no input
  *   and not each other.
+ * Finite gates of any size have a finite slope; an infinite one gives NaN in dG, as
+ * the formula does.
  * Errors: as gemm_bf16_nt_gated; GEMM_ERR_SHAPE also for a workspace that is too
  * small.
  */
@@ -625,7 +627,8 @@ GB300GEMM_API size_t gemm_bf16_tn_workspace_bytes(int M, int N, int K);
  *   M >= 1, at most 2^30; 8 <= D <= 16384, D % 8 == 0; eps >= 0; rows_per_gate >= 1
  *   divides M (used with a gate); matrices and weights 16-byte, rstd 4-byte aligned;
  *   an output overlaps no input (but y == x) and no other output.
- * A row whose values are all zero has r = 1 / sqrt(eps), and NaN for eps = 0.
+ * A row whose values are all zero has r = 1 / sqrt(eps), and NaN for eps = 0.  An
+ * infinite weight or gate value makes its own column of y infinite; r(y) is then 0.
  * Errors: GEMM_ERR_NULL, _SHAPE, _ALIGN, _ALIAS, _ARCH, _LAUNCH, _NO_DEVICE,
  * _CAPTURE.
  */
@@ -687,7 +690,9 @@ GB300GEMM_API size_t residual_norm_backward_workspace_bytes(int M, int D, int ro
  * extension.
  *
  *   A bf16 [M][K], b uint8 [N][K/2], sfb uint8 [N][K/16] e4m3, scale2: as for
- *   gemm_w4a16 (read);  C bf16 [M][N] (written; must not overlap A, b or sfb)
+ *   gemm_w4a16 (read);  C bf16 [M][N] (written; must not overlap A, b or sfb).
+ *   Any finite scale2: a result that fits is not lost to the size of other tokens.
+ *   Token values below 2^-32 of a block's largest take further passes over the weights.
  *   1 <= M <= 16; N >= 1 (any N), K >= 1, K % 256 == 0, at most 2^30 each; A, b and
  *   sfb 16-byte, C 2-byte aligned.
  * Errors: GEMM_ERR_NULL, _SHAPE, _ALIGN (also K % 256), _ALIAS, _ARCH, _LAUNCH,

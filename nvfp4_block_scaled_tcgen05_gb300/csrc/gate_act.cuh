@@ -3,9 +3,11 @@
 //   gelu_tanh  z = 2 sqrt(2 / pi) (x + 0.044715 x^3), since
 //              (1 + tanh(z / 2)) / 2 = s(z)
 // and their slopes s + x s (1 - s) z'.  Two special-function operations each, in
-// FP32: relative error of s below 2^-21, far below the BF16 rounding of what
-// follows (tanh.approx would take one, but is off by 2^-11).  -inf as a gate
-// gives NaN (0 times inf), as the formula does.
+// FP32, far below the BF16 rounding of what follows (tanh.approx would take one,
+// but is off by 2^-11).  z's roundings move s by (1 - s) 2^-21 |z|, relative to s, at most
+// (silu: a quarter of that), the two operations and the sum by 2^-21 more: a gate of -1
+// has s to 2^-19, the last ones whose s is a normal number (z = -87) to 2^-14.  -inf as a
+// gate gives NaN (0 times inf), as the formula does; so does the slope of +inf.
 #pragma once
 
 #include "gb300gemm.h"

@@ -23,6 +23,11 @@
 //
 // C = A^T B: both operands with their K as the rows, as dWg and dWu have them; 2048 x
 // 11008 x 5120 129 us, 1800 TFLOP/s.
+//
+// Rows of an odd multiple of 16 bytes take five 32-byte sectors per 128 bytes on the way
+// from L2.  1016 tokens, forward: 5504 x 2048 33.7 us, 5512 x 2048 34.0, 5504 x 2056 42.6;
+// gradients from X: 100.9, 110.8 (dG and dU, whose rows in the workspace are F long) and
+// 115.5, both odd 129.7.
 #include <algorithm>
 
 #include "chain.cuh"
@@ -34,7 +39,7 @@ namespace {
 using FwdPair = GatedCfg<TileCfg<Operand::kBF16, 2, 256, 3, 4, 2, true, false, 2>>;
 // Few tokens that gated_few.cu does not take: the weights on the MMA's M side, half of a
 // tile's rows of each matrix, the tokens on the N side, so that the kernel streams the
-// weights.  (11008 x 2048: 32 tokens 20.5 us, 128 tokens 23.5, 129 on the tiles above 28.)
+// weights.  (11008 x 2048: 32 tokens 20.4 us, 128 tokens 23.6, 129 on the tiles above 26.)
 // Their gradient reads dH two bytes at a time, which pays up to 32 tokens (5504 x 2048,
 // all gradients from X: 17 tokens 49 -> 41 us, 128 50.8 -> 52.8).
 constexpr int kFewTokens = 128, kFewTokensGrad = 32;
@@ -268,7 +273,9 @@ int run_dx(const GatedBackward& a, const GatedPlan& q, const uint16_t* grad, flo
   return launch_tcgen05<Cfg, Epilogue::kAddF32>(tdg, tg, tc, tdu, tu, p, dev, stream);
 }
 
-// dWg = dG^T X and dWu = dU^T X.
+// dWg = dG^T X and dWu = dU^T X.  Their K loop, the tokens, is not divided: with few weight
+// tiles and many tokens most pairs are idle (8192 tokens, 512 x 512: 43 us of both, where
+// gemm_bf16_tn, which divides it, takes 12.5 us of each).
 int run_dw(const GatedBackward& a, const uint16_t* grad, bool after_dx, GridTiles before,
            const DeviceInfo& dev, cudaStream_t stream) {
   using Cfg = DwPair;

@@ -16,11 +16,16 @@
 // one token 14.4 us).  A BF16 token value is exact in FP16 after a power of two that
 // brings a block's largest to 2^15, if it is at least 2^-32 of that (its eight bits are
 // then multiples of 2^-24).  Values below that wait for another pass over the weights
-// with a scale of their own: one pass for tokens as they come, up to eight for tokens
-// that span the whole BF16 range.  So products are exact and sums FP32; they are scaled
-// back, and by scale2, before they are stored, so that a sum beyond the FP32 range whose
-// result is not comes back; the largest token may be another one than the sum's, so the
-// factors alone stay within the range too.
+// with a scale of their own: one pass for normally distributed tokens, up to eight for
+// tokens that span the whole BF16 range.  So products are exact and sums FP32; they are
+// scaled back, and by scale2, before they are stored, so that a sum beyond the FP32 range
+// whose result is not comes back; the largest token may be another one than the sum's, so
+// the factors alone stay within the range too.
+//
+// The output of a gated projection spans more the larger its negative gates are, and one
+// value is enough for another pass of the blocks whose K holds it.  2048 x 11008, one token
+// (11): normal tokens 6.9 us (11.7), SiLU of normal gates 6.9 (14.7), GELU 6.9 (15.5), SiLU
+// of gates of eight times that size 15.5 (35.8), GELU of four times 27.8 (65).
 //
 // A tile is 16 weight rows (gated: 8 of each matrix, so that a lane gets both products
 // of its outputs).  One block per SM takes a run of tiles; it turns its tokens into FP16

@@ -17,8 +17,8 @@
 // bytes in flight do not depend on how many threads wait.  Sums are FP32 in a fixed
 // order (results repeat bit for bit).
 //
-// Forward 16384 x 4096 with an FP32 stream 128 us (805 MB at 6.3 TB/s; without
-// the ring 184 us), 8192 x 4096 BF16 45 us; backward 8128 x 4104 74.6 us (400 MB, 5.4 TB/s).
+// Forward 16384 x 4096 with an FP32 stream 126 us (805 MB at 6.4 TB/s; without
+// the ring 184 us), 8192 x 4096 BF16 46 us; backward 8128 x 4104 74.6 us (400 MB, 5.4 TB/s).
 #include <algorithm>
 
 #include "chain.cuh"
@@ -643,11 +643,14 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
 // A row of D / 8 pieces with V pieces a thread.  One block per SM, of as many units
 // as the registers of V pieces leave warps for; two units or more where two or three
 // pieces a thread allow it, so that one works while another waits at its barrier.
-// (Four pieces a thread spill: 6553 x 5120 backward took 139 us with two units of them,
-// with one unit of two pieces it takes 89 us at 5461 x 6144.)
+// (One unit of two pieces a thread: backward 76 us at 6553 x 5120 and 5461 x 6144, 74 at
+// 4096 x 8192; two units of four pieces, which spill, took 139 us at the first.  Rows of more
+// than 8192 values need four pieces, and spill: 2736 x 12288 forward 80, backward 167 us,
+// floors 40 and 59.)
 constexpr int kBlocks = 152;
 // Rows on their way, per SM: the backward pass needs the 200 KB (100 KB: 8192 x 4096
-// 76 -> 106 us), the forward pass is a little faster with half of it (56 -> 54 us).
+// 76 -> 106 us), the forward pass was a little faster with half of it (56 -> 54 us, before
+// the choices at compile time).
 constexpr int kThreadsOf[5] = {0, 512, 512, 384, 512};
 constexpr int kForwardBytes = 104 << 10, kBackwardBytes = 208 << 10;
 Shape make_shape(int D, int row_bytes, bool forward) {
@@ -664,7 +667,7 @@ Shape make_shape(int D, int row_bytes, bool forward) {
     take(1);
   } else if (!take(2) && !take(3)) {
     // the forward pass needs fewer registers: two units of three pieces a thread still
-    // fit, spilling a little (6553 x 5120: 64 us with one unit, 45 with two)
+    // fit, spilling a little (6553 x 5120: 64 us with one unit, 46 with two)
     if (forward && s.warps <= 8) s.units = 2;
     else take(pieces <= 1024 ? 2 : 4);
   }
@@ -674,7 +677,12 @@ Shape make_shape(int D, int row_bytes, bool forward) {
   return s;
 }
 
-// How the backward pass's rows are divided; depends on the sizes alone.
+// How the backward pass's rows are divided; depends on the sizes alone.  Where a gate's
+// gradient is summed, no run crosses a group's end unless it holds whole groups, whatever
+// that leaves of the SMs.  8192 x 4096: one to eight gates 74 us (8 x 19 blocks), 16 and 32
+// gates 107 (160 blocks: a second round for eight of them), 64 99 (192); 32768 x 1024 with
+// 128 rows to a gate 439 us (each unit a whole group, on 32 SMs), 65536 x 512 with 256 rows
+// 817 (16 SMs), against 80 with one gate.
 struct RunPlan {
   int blocks, rows_per_run, parts_per_gate;
   bool multi;
